@@ -1,0 +1,34 @@
+// Device helpers shared by the cache's kernels.
+#pragma once
+#include "cache_internal.h"
+#include "ci_common.cuh"
+#include "ci_internal.h"
+
+namespace ci {
+
+// The request of row t; -1 (reported) where the row starts name none.
+__device__ __forceinline__ int row_request(const CacheArgs& c, int t) {
+  if (c.layout == kLayoutDecode) return t;
+  if (c.layout == kLayoutPrefill) return 0;
+  int lo = 0, hi = c.num_req;  // the last r with req_start[r] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.req_start[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  if (c.req_start[lo] <= t && t < c.req_start[lo + 1]) return lo;
+  report(c.dev_err, kDevErrReq);
+  return -1;
+}
+
+template <bool kFp8>
+__host__ __device__ constexpr int64_t cache_page_bytes(int d) {
+  return kFp8 ? kPage * d + kPage * 4 : kPage * d * 2;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+}  // namespace ci
