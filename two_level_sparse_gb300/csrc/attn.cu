@@ -1,108 +1,125 @@
-// Attention of query rows over the paged cache (contract in include/ci_cache.h).
-//
-// One warp per (row, query head): the positions one after another, the
-// softmax's maximum and sum carried along.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "cache_common.cuh"
+// Attention over the paged cache: dispatch, the workspace's layout, and the
+// join of units that several CTAs worked on (contract in include/ci_cache.h;
+// the main kernel is in attn.cuh).
+#include "attn.cuh"
 
 namespace ci {
 namespace {
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(128) attn_kernel(const AttnArgs a) {
-  constexpr int kPer = D / 32;
-  const CacheArgs& c = a.c;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(a.rows) * c.num_q_heads) return;
-  const int t = static_cast<int>(w / c.num_q_heads), h = static_cast<int>(w % c.num_q_heads);
-  const int kvh = h / (c.num_q_heads / c.num_kv_heads);
-  int len = a.seq_len[t];
-  if (len < 0 || len > a.max_len) {
-    if (lane == 0) report(c.dev_err, kDevErrLen);
-    len = 0;
-  }
-  const int req = row_request(c, t);
-  if (req < 0) len = 0;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    q[j] = __uint_as_float(static_cast<uint32_t>(a.q[t * a.q_stride + h * D + j * 32 + lane]) << 16);
-    o[j] = 0.f;
-  }
-  const int n = a.pos != nullptr ? a.npos : len;
-  for (int i = 0; i < n; ++i) {
-    const int s = a.pos != nullptr ? a.pos[t * a.pos_stride + i] : i;
-    if (s < 0 || s >= len) {
-      if (s != -1 && lane == 0) report(c.dev_err, kDevErrPos);
-      continue;
-    }
-    const int page = c.page_table[static_cast<int64_t>(req) * c.max_pages + s / kPage];
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) report(c.dev_err, kDevErrPage);
-      continue;
-    }
-    const int64_t at = (static_cast<int64_t>(page) * c.num_kv_heads + kvh) * cache_page_bytes<kFp8>(D);
-    const int slot = s % kPage;
-    float ks = 1.f, vs = 1.f, k[kPer], v[kPer];
-    if (kFp8) {
-      ks = reinterpret_cast<const float*>(c.k_pool + at + kPage * D)[slot];
-      vs = reinterpret_cast<const float*>(c.v_pool + at + kPage * D)[slot];
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = slot * D + j * 32 + lane;
-      if (kFp8) {
-        k[j] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(c.k_pool + at)[e]);
-        v[j] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(c.v_pool + at)[e]);
-      } else {
-        k[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(c.k_pool + at)[e]);
-        v[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(c.v_pool + at)[e]);
-      }
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) x = fmaf(q[j], k[j], x);
-#pragma unroll
-    for (int b = 16; b > 0; b >>= 1) x += __shfl_xor_sync(0xffffffffu, x, b);
-    x *= ks * a.scale;
-    const float top = fmaxf(m, x), keep = m == -INFINITY ? 0.f : __expf(m - top);
-    const float p = x == -INFINITY ? 0.f : __expf(x - top);
-    l = l * keep + p;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] = o[j] * keep + p * vs * v[j];
-    m = top;
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    a.out[t * a.out_stride + h * D + j * 32 + lane] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o[j] / l));
-  if (a.lse != nullptr && lane == 0) a.lse[w] = l == 0.f ? -INFINITY : m + logf(l);
+using attn::Args;
+using attn::Layout;
+using attn::Part;
+
+constexpr int kJoinHeads = 4, kJoinWays = 4;  // heads per CTA, warps per head
+
+Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const int group = num_q_heads / num_kv_heads;
+  const int heads = group <= 8 ? 8 : group <= 16 ? 16 : group <= 32 ? 32 : 64;
+  return Layout{device_sm_count() * (head_dim == 256 ? 1 : 2), heads, (group + heads - 1) / heads, group};
 }
 
+// With the parts' maxima m_i, sums l_i and unnormalised sums o_i:
+//   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
+// One CTA per (CTA in whose range a split unit starts, four heads); a head's
+// parts are dealt to four warps, whose sums are added in order.  Bound by the
+// latency of its loads: the parts of a unit are few and sit in L2.
 template <int D>
-void launch_d(const AttnArgs& a, unsigned grid, cudaStream_t stream) {
-  if (a.c.fp8)
-    attn_kernel<D, true><<<grid, 128, 0, stream>>>(a);
-  else
-    attn_kernel<D, false><<<grid, 128, 0, stream>>>(a);
+__global__ void __launch_bounds__(32 * kJoinHeads * kJoinWays) join_kernel(const Args k) {
+  constexpr int kPer = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Part p = k.part[blockIdx.x];
+  if (p.last < 0) return;
+  __shared__ float sums[kJoinWays][kJoinHeads][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hw = warp / kJoinWays, way = warp % kJoinWays;
+  const int h = blockIdx.y * kJoinHeads + hw, heads = k.l.heads;
+  const int head = p.unit / k.l.blocks, hb = p.unit - head * k.l.blocks;
+  const bool live = hb * heads + h < k.l.group;
+  const int first = blockIdx.x, n = p.last - first + 1;
+  auto slot = [&](int i) -> int64_t { return i == 0 ? 2ll * first + 1 : 2ll * (first + i); };
+  float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) o[j] = 0.f;
+  if (live) {
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, k.stat[(slot(i) * heads + h) * 2]);
+#pragma unroll
+    for (int b = 16; b > 0; b >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < n; i += 32) {
+      const float2 st = *reinterpret_cast<const float2*>(k.stat + (slot(i) * heads + h) * 2);
+      l += st.y * attn::exp2_approx(st.x - ref);
+    }
+#pragma unroll
+    for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+#pragma unroll 4
+    for (int i = way; i < n; i += kJoinWays) {
+      const float f = attn::exp2_approx(k.stat[(slot(i) * heads + h) * 2] - ref);
+      const float* src = k.sum + (slot(i) * heads + h) * D + lane;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[j] += f * src[32 * j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) sums[way][hw][32 * j + lane] = o[j];
+  __syncthreads();
+  if (!live || way != 0) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t qh = static_cast<int64_t>(head) * k.l.group + hb * heads + h;
+  uint16_t* dst = k.a.out + p.row * k.a.out_stride + qh * D;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    float v = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoinWays; ++x) v += sums[x][hw][32 * j + lane];
+    dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v * inv));
+  }
+  if (k.a.lse != nullptr && lane == 0)
+    k.a.lse[static_cast<int64_t>(p.row) * k.a.c.num_q_heads + qh] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+int64_t part_bytes(const Layout& l) { return (static_cast<int64_t>(l.ctas) * sizeof(Part) + 15) / 16 * 16; }
+int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.heads * 2 * 4; }
+
+template <int D>
+cudaError_t launch_join(const Args& k, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(k.l.ctas, (k.l.heads < k.l.group ? k.l.heads : k.l.group) / kJoinHeads +
+                                   ((k.l.heads < k.l.group ? k.l.heads : k.l.group) % kJoinHeads != 0));
+  cfg.blockDim = dim3(32 * kJoinHeads * kJoinWays);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, k);
 }
 
 }  // namespace
 
-int64_t attn_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 16; }
+int64_t attn_workspace_bytes(int32_t, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const Layout l = layout_of(num_q_heads, num_kv_heads, head_dim);
+  return part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.heads * head_dim * 4;
+}
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.rows) * a.c.num_q_heads + 3) / 4);
-  if (a.c.head_dim == 64)
-    launch_d<64>(a, grid, stream);
-  else if (a.c.head_dim == 128)
-    launch_d<128>(a, grid, stream);
-  else
-    launch_d<256>(a, grid, stream);
-  return cudaGetLastError();
+  const CacheArgs& c = a.c;
+  Args k{a, layout_of(c.num_q_heads, c.num_kv_heads, c.head_dim), nullptr, nullptr, nullptr};
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  k.part = reinterpret_cast<Part*>(ws);
+  k.stat = reinterpret_cast<float*>(ws + part_bytes(k.l));
+  k.sum = reinterpret_cast<float*>(ws + part_bytes(k.l) + stat_bytes(k.l));
+  const int row = c.fp8 ? c.head_dim : 2 * c.head_dim;
+  const int per_page = static_cast<int>((c.fp8 ? cache_page_bytes<true>(c.head_dim) : cache_page_bytes<false>(c.head_dim)) / row);
+  CUtensorMap kmap, vmap;
+  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, a.pos != nullptr ? 1 : attn::kTile);
+  if (e == cudaSuccess)
+    e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, a.pos != nullptr ? 1 : attn::kTile);
+  if (e == cudaSuccess) e = c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
+  if (e != cudaSuccess) return e;
+  return c.head_dim == 64    ? launch_join<64>(k, stream)
+         : c.head_dim == 128 ? launch_join<128>(k, stream)
+                             : launch_join<256>(k, stream);
 }
 
 }  // namespace ci

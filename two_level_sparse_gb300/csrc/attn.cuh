@@ -1,0 +1,763 @@
+// The attention kernel over a paged cache (contract in include/ci_cache.h);
+// instances per cache format in attn_bf16.cu and attn_fp8.cu, dispatch and the
+// join in attn.cu.
+//
+// Work.  A row's positions are cut into tiles of 64 (a page, or 64 entries of
+// its list); a unit is (row, key-value head, block of up to 64 query heads).
+// The units' tiles, in order, are one long list that is split evenly over the
+// CTAs of one wave, so ragged batches and a single long row fill the card
+// alike.  A CTA whose range covers a whole unit writes its result; where a
+// range ends inside a unit, each part leaves its unnormalised sum and softmax
+// statistics in the workspace (two parts per CTA at most), and the join kernel
+// adds them in order.
+//
+// A tile.  One producer warp fetches K and V by TMA into a ring of stages
+// (128-byte swizzled rows): one box of 64 rows per page, or, for listed
+// positions, gathers of four rows each.  WP x WH consumer warps compute, WP
+// along the positions and WH along the heads:
+//   S^T = K Q^T   A = K from shared memory (ldmatrix), B = Q in registers;
+//   online softmax per head, a column of S^T: its maximum over the warp's
+//                 positions is a reduction over registers and three shuffles;
+//   O^T += V^T P^T  A = V transposed by ldmatrix, B = P transposed in
+//                 registers (movmatrix).
+// Positions sit on the 16-wide side of the MMA and heads on the 8-wide one, so
+// that a group of 8 query heads wastes nothing; a cache read at the HBM's rate
+// (64 positions x D = 128 in bf16 per 1400 cycles and SM) needs 128 x G / 8 of
+// these instructions, which legacy tensor throughput covers up to G = 64.
+//
+// FP8 pages.  An e4m3 code's exponent and mantissa, moved into the low bits of
+// a bf16's, are the value x 2^-120, subnormals included: three logic operations
+// per pair instead of conversions, and exact.  The powers of two come back
+// through the query (x 2^64, exact), the logit's factor and the final division.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "cache_common.cuh"
+
+namespace ci {
+namespace attn {
+
+constexpr int kTile = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTwo56 = 72057594037927936.f, kTwo60 = 1152921504606846976.f, kTwo64 = 18446744073709551616.f;
+
+// What the main kernel and the join agree on.
+struct Part {  // the unit that goes on past the end of a CTA's range; last < 0: none
+  int32_t row, unit, last, pad;
+};
+struct Layout {
+  int32_t ctas;      // CTAs that share the list of tiles
+  int32_t heads;     // query heads of a unit, padded (HB)
+  int32_t blocks;    // head blocks per key-value head
+  int32_t group;     // query heads per key-value head
+};
+struct Args {
+  AttnArgs a;
+  Layout l;
+  Part* part;    // [ctas]
+  float* stat;   // [2 ctas][heads][2]: maximum (base 2) and sum
+  float* sum;    // [2 ctas][heads][D]
+};
+
+template <int D, bool kFp8, int NT, int WP, int WH>
+struct Config {
+  static constexpr int kRow = kFp8 ? D : 2 * D;           // bytes of a position
+  static constexpr int kBox = kRow < 128 ? kRow : 128;    // bytes of a TMA box's rows
+  static constexpr int kBoxes = kRow / kBox;
+  static constexpr int kSub = kTile * kBox;               // bytes of one box in shared memory
+  static constexpr int kMat = kTile * kRow;               // K or V of a tile
+  static constexpr int kScale = kFp8 ? kTile * 4 : 0;
+  static constexpr int kStage = 2 * kMat;                 // a multiple of the swizzle's 1024 bytes
+  static constexpr int kHeadsU = 8 * NT * WH;
+  static constexpr int kAccStride = D + 4;                // floats; the pad spreads the heads over the banks
+  static constexpr int kAcc = kHeadsU * kAccStride * 4;
+  static constexpr int kStat = WP * kHeadsU * 2 * 4;
+  static constexpr int kMisc = 1024;                      // barriers, masks, the range
+  static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+  static constexpr int kBudget = kCtasPerSm == 1 ? 226 * 1024 : 112 * 1024;
+  static constexpr int kFit = (kBudget - 1024 - kAcc - kStat - kMisc) / (kStage + 2 * kScale);
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static_assert(kStages >= 2, "a ring needs two stages");
+  static constexpr int kSmem = 1024 + kStages * (kStage + 2 * kScale) + kAcc + kStat + kMisc;
+  static constexpr int kConsumers = 32 * WP * WH;
+  static constexpr int kThreads = kConsumers + 32;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes of r (bytes picked by sel into the upper byte of each half)
+// as bf16 of value x 2^-120.
+__device__ __forceinline__ uint32_t widen2(uint32_t r, uint32_t sel) {
+  const uint32_t x = __byte_perm(r, 0, sel);
+  return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+}
+
+// Byte offset of 16-byte chunk `chunk` of position `p` in a matrix of a tile:
+// boxes of 128-byte (64-byte) rows, the chunk index XOR-ed as the TMA swizzle does.
+template <class C>
+__device__ __forceinline__ uint32_t tile_offset(int p, int chunk) {
+  constexpr int kPer = C::kBox / 16;
+  const int box = chunk / kPer, c = chunk % kPer;
+  const int x = C::kBox == 128 ? c ^ (p & 7) : c ^ ((p >> 1) & 3);
+  return box * C::kSub + p * C::kBox + x * 16;
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// The tiles of row t (0: nothing to read).
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, int t) {
+  const int len = a.seq_len[t];
+  if (len <= 0 || len > a.max_len) return 0;
+  return ((a.pos != nullptr ? a.npos : len) + kTile - 1) / kTile;
+}
+
+// A CTA's way through the list: segment by segment (tiles [i0, i1) of a unit).
+struct Walk {
+  int64_t x, end, base;  // next tile, end of the range, first tile of the row
+  int row, n, units;     // n: tiles of the row
+  int unit, i0, i1;
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    if (x >= end) return false;
+    while (x >= base + static_cast<int64_t>(n) * units) {
+      base += static_cast<int64_t>(n) * units;
+      n = row_tiles(a, ++row);
+    }
+    const int64_t off = x - base;
+    unit = static_cast<int>(off / n);
+    i0 = static_cast<int>(off - static_cast<int64_t>(unit) * n);
+    i1 = static_cast<int>(min(static_cast<int64_t>(n), i0 + (end - x)));
+    x += i1 - i0;
+    return true;
+  }
+};
+
+struct Range {
+  int64_t first, end, base, total;
+  int32_t row, ctas;  // ctas: how many share the list (every one of them has a tile)
+};
+
+struct Shared {
+  uint64_t full[8], empty[8];
+  uint32_t mask[8][2];  // per stage: which of the 64 positions count
+  Range range;
+  int64_t warp_sum[9];
+  int32_t abort;
+};
+static_assert(sizeof(Shared) <= 1024, "");
+
+// The CTA's range of the list and the row it starts in: every thread adds up
+// a run of rows, a scan over the threads gives the total, and the thread whose
+// run holds the range's first tile walks to its row.
+template <int kThreads>
+__device__ void find_range(const Args& k, Shared& sh, int units) {
+  const AttnArgs& a = k.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.rows + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int len = a.seq_len[r];
+    if (blockIdx.x == 0 && (len < 0 || len > a.max_len)) report(a.c.dev_err, kDevErrLen);
+    mine += row_tiles(a, r);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+  }
+  total *= units;
+  const int64_t ctas = min(static_cast<int64_t>(k.l.ctas), total);
+  const int64_t first = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
+  const int64_t end = blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
+  if (tid == 0)
+    sh.range.first = first, sh.range.end = end, sh.range.total = total, sh.range.ctas = static_cast<int32_t>(ctas);
+  int64_t at = before * units;
+  if (first < end && at <= first && first < at + mine * units) {
+    int r = r0;
+    for (;; ++r) {
+      const int64_t n = static_cast<int64_t>(row_tiles(a, r)) * units;
+      if (first < at + n) break;
+      at += n;
+    }
+    sh.range.row = r;
+    sh.range.base = at;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ producer
+template <class C, int D, bool kFp8>
+__device__ void produce(const Args& k, Shared& sh, Walk w, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                        uint32_t stages) {
+  const AttnArgs& a = k.a;
+  const CacheArgs& c = a.c;
+  constexpr int kRowsPerPage = cache_page_bytes<kFp8>(D) / C::kRow;
+  const int lane = threadIdx.x & 31;
+  int stage = 0;
+  uint32_t phase = 1;  // the first round of stages is free
+  uint32_t used = 0;
+  bool alive = true;
+  while (w.next(a)) {
+    const int req = row_request(c, w.row);
+    const int head = w.unit / k.l.blocks;
+    const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
+    const int len = table != nullptr ? a.seq_len[w.row] : 0;
+    int ids = 0, s0 = -1, s1 = -1;
+    if (a.pos != nullptr) {
+      const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + w.i0 * kTile;
+      s0 = w.i0 * kTile + lane < a.npos ? list[lane] : -1;
+      s1 = w.i0 * kTile + 32 + lane < a.npos ? list[32 + lane] : -1;
+    }
+    for (int i = w.i0; i < w.i1; ++i) {
+      // ---- which positions, and where they are
+      uint32_t m0, m1;
+      int row0 = 0, row1 = 0, page = 0;
+      if (a.pos == nullptr) {
+        const int j = (i - w.i0) & 31;
+        if (j == 0) {  // the next 32 tiles' pages, one per lane
+          ids = -1;
+          if (i + lane < w.i1 && table != nullptr) ids = table[i + lane];
+        }
+        page = __shfl_sync(0xffffffffu, ids, j);
+        const bool ok = page >= 0 && page < c.num_pages;
+        if (!ok && lane == 0 && table != nullptr) report(c.dev_err, kDevErrPage);
+        const int left = ok ? len - i * kTile : 0;
+        m0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+        m1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1 : 0;
+      } else {
+        const bool in0 = s0 >= 0 && s0 < len, in1 = s1 >= 0 && s1 < len;
+        if (table != nullptr && ((!in0 && s0 != -1) || (!in1 && s1 != -1))) report(c.dev_err, kDevErrPos);
+        const int p0 = in0 ? table[s0 / kPage] : 0, p1 = in1 ? table[s1 / kPage] : 0;
+        const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
+        if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
+        // a position that does not count fetches the pool's first row instead
+        row0 = ok0 ? (p0 * c.num_kv_heads + head) * kRowsPerPage + s0 % kPage : 0;
+        row1 = ok1 ? (p1 * c.num_kv_heads + head) * kRowsPerPage + s1 % kPage : 0;
+        m0 = __ballot_sync(0xffffffffu, ok0);
+        m1 = __ballot_sync(0xffffffffu, ok1);
+        if (i + 1 < w.i1) {  // the next tile's list entries
+          const int at = (i + 1) * kTile + lane;
+          const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
+          s0 = at < a.npos ? list[0] : -1;
+          s1 = at + 32 < a.npos ? list[32] : -1;
+        }
+      }
+      // ---- the copies
+      alive = alive && warp_wait_lane0(&sh.empty[stage], phase, &sh.abort);
+      if (!alive) {
+        if (lane == 0) {
+          if (atomicExch(&sh.abort, 1) == 0) report(c.dev_err, kDevErrTimeout);
+        }
+      } else {
+        const uint32_t bar = smem_u32(&sh.full[stage]);
+        const uint32_t kdst = stages + stage * C::kStage, vdst = kdst + C::kMat;
+        const uint32_t sdst = stages + C::kStages * C::kStage + stage * 2 * C::kScale;
+        const bool any = (m0 | m1) != 0;
+        const bool lists = a.pos != nullptr;
+        if (lane == 0) {
+          sh.mask[stage][0] = m0;
+          sh.mask[stage][1] = m1;
+          if (any)
+            mbar_arrive_expect_tx(&sh.full[stage], lists ? C::kStage : C::kStage + 2 * C::kScale);
+          else
+            mbar_arrive(&sh.full[stage]);
+        }
+        __syncwarp();
+        if (any && !lists) {
+          const int row = (page * c.num_kv_heads + head) * kRowsPerPage;
+          if (lane < 2 * C::kBoxes) {
+            const int b = lane % C::kBoxes;
+            tma_box((lane < C::kBoxes ? kdst : vdst) + b * C::kSub, lane < C::kBoxes ? kmap : vmap, b * C::kBox, row,
+                    bar);
+          }
+          if (kFp8 && (lane == 16 || lane == 17)) {
+            const int64_t at = (static_cast<int64_t>(page) * c.num_kv_heads + head) * cache_page_bytes<kFp8>(D) + kPage * D;
+            bulk_load(sdst + (lane - 16) * C::kScale, (lane == 16 ? c.k_pool : c.v_pool) + at, C::kScale, bar);
+          }
+        }
+        if (lists) {
+          if (any) {
+            // lanes 0..15 gather K, lanes 16..31 V, four positions each
+            const int g = lane & 15;
+            int r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int x = __shfl_sync(0xffffffffu, row0, (4 * g + j) & 31);
+              const int y = __shfl_sync(0xffffffffu, row1, (4 * g + j) & 31);
+              r[j] = g < 8 ? x : y;
+            }
+            const uint32_t dst = (lane < 16 ? kdst : vdst) + g * 4 * C::kBox;
+#pragma unroll
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_gather4(dst + b * C::kSub, lane < 16 ? kmap : vmap, b * C::kBox, r[0], r[1], r[2], r[3], bar);
+            if (kFp8) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                if ((((hh ? m1 : m0) >> lane) & 1) == 0) continue;
+                const int row = hh ? row1 : row0, slot = row % kRowsPerPage;
+                const int64_t at = static_cast<int64_t>(row / kRowsPerPage) * cache_page_bytes<kFp8>(D) + kPage * D + slot * 4;
+                const uint32_t to = sdst + (hh * 32 + lane) * 4;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(c.k_pool + at) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + C::kScale), "l"(c.v_pool + at)
+                             : "memory");
+              }
+            }
+          }
+          if (kFp8) cp_async_arrive_noinc(&sh.full[stage]);
+        }
+        used |= 1u << stage;
+      }
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+  }
+  if (!alive) {  // gave up: what is in flight lands before the CTA's memory goes
+    for (int st = 0; st < C::kStages; ++st) {
+      const uint32_t last = st < stage ? phase ^ 1 : phase;  // parity of the stage's last fill
+      if ((used >> st) & 1) mbar_wait(&sh.full[st], last, nullptr, 1000000ull);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ consumers
+template <class C, int D, bool kFp8, int NT, int WP, int WH>
+__device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, float* acc, float* stat) {
+  constexpr int kM = D / 16, kK = D / 16, MT = 4 / WP;
+  const AttnArgs& a = k.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int wp = warp % WP, wh = warp / WP, p0 = wp * 16 * MT;
+  const int tid = threadIdx.x;
+  const float factor = a.scale * kLog2e * (kFp8 ? kTwo56 : 1.f);
+  const Range range = sh.range;
+  int stage = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  while (w.next(a)) {
+    const int head = w.unit / k.l.blocks, hb = w.unit - head * k.l.blocks;
+    const int h0 = hb * C::kHeadsU;                                // first head of the unit, within its group
+    const int live = min(C::kHeadsU, k.l.group - h0);              // heads of the unit that exist
+    // ---- the queries, as B fragments
+    uint32_t qf[NT][kK][2];
+    {
+      const uint16_t* row = a.q + w.row * a.q_stride + (static_cast<int64_t>(head) * k.l.group + h0) * D;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = wh * 8 * NT + nt * 8 + g;
+        const uint16_t* src = row + static_cast<int64_t>(h < live ? h : 0) * D;
+#pragma unroll
+        for (int kk = 0; kk < kK; ++kk) {
+          uint32_t b0, b1;
+          if (kFp8) {  // the order of the 16 dims that the widened codes come in: 4q, 4q + 1 | 4q + 2, 4q + 3
+            const uint2 v = *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * q);
+            b0 = bf16x2(bf16_lo(v.x) * kTwo64, bf16_hi(v.x) * kTwo64);
+            b1 = bf16x2(bf16_lo(v.y) * kTwo64, bf16_hi(v.y) * kTwo64);
+          } else {
+            b0 = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * q);
+            b1 = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * q);
+          }
+          qf[nt][kk][0] = h < live ? b0 : 0;
+          qf[nt][kk][1] = h < live ? b1 : 0;
+        }
+      }
+    }
+    float o[NT][kM][4], top[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.f;
+      top[nt][0] = top[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    for (int i = w.i0; i < w.i1; ++i) {
+      alive = alive && warp_wait_fast(&sh.full[stage], phase, &sh.abort);
+      if (!alive && lane == 0) {
+        if (atomicExch(&sh.abort, 1) == 0) report(a.c.dev_err, kDevErrTimeout);
+      }
+      const uint32_t kbase = stages + stage * C::kStage, vbase = kbase + C::kMat;
+      const uint32_t sbase = stages + C::kStages * C::kStage + stage * 2 * C::kScale;
+      const uint64_t mask = static_cast<uint64_t>(sh.mask[stage][1]) << 32 | sh.mask[stage][0];
+      constexpr uint64_t kOnes = MT == 4 ? ~0ull : (1ull << (16 * MT & 63)) - 1;
+      const uint64_t here = (mask >> p0) & kOnes;  // the warp's positions
+      if (alive && here != 0) {
+        // ---- S^T
+        float s[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+          const int p = p0 + mt * 16;
+          if (kFp8) {
+#pragma unroll
+            for (int kk = 0; kk < kK; kk += 2) {
+              uint32_t r[4];  // positions 0-7 | 8-15 of dims 0-15, then of dims 16-31
+              ldsm4(r, kbase + tile_offset<C>(p + (lane & 15), kk + (lane >> 4)));
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t x = r[2 * hh], y = r[2 * hh + 1];
+                const uint32_t a0 = widen2(x, 0x1404), a1 = widen2(y, 0x1404), a2 = widen2(x, 0x3424), a3 = widen2(y, 0x3424);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(s[mt][nt], a0, a1, a2, a3, qf[nt][kk + hh][0], qf[nt][kk + hh][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kK; ++kk) {
+              uint32_t r[4];
+              ldsm4(r, kbase + tile_offset<C>(p + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16(s[mt][nt], r[0], r[1], r[2], r[3], qf[nt][kk][0], qf[nt][kk][1]);
+            }
+          }
+        }
+        // ---- logits in base 2, the new maxima
+        const bool all = here == kOnes;
+        float now[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) now[nt][0] = top[nt][0], now[nt][1] = top[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int pa = p0 + mt * 16 + g;
+          float fa = factor, fb = factor;
+          if (kFp8) {
+            fa *= lds_f32(sbase + pa * 4);
+            fb *= lds_f32(sbase + (pa + 8) * 4);
+          }
+          const bool ina = all || ((mask >> pa) & 1), inb = all || ((mask >> (pa + 8)) & 1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&v)[4] = s[mt][nt];
+            v[0] = ina ? v[0] * fa : -INFINITY;
+            v[1] = ina ? v[1] * fa : -INFINITY;
+            v[2] = inb ? v[2] * fb : -INFINITY;
+            v[3] = inb ? v[3] * fb : -INFINITY;
+            now[nt][0] = fmaxf(now[nt][0], fmaxf(v[0], v[2]));
+            now[nt][1] = fmaxf(now[nt][1], fmaxf(v[1], v[3]));
+          }
+        }
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) now[nt][e] = fmaxf(now[nt][e], __shfl_xor_sync(0xffffffffu, now[nt][e], b));
+            grew |= now[nt][e] > top[nt][e];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              keep[e] = now[nt][e] > top[nt][e] ? exp2_approx(top[nt][e] - now[nt][e]) : 1.f;
+              top[nt][e] = now[nt][e];
+              l[nt][e] *= keep[e];
+            }
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              o[nt][m][0] *= keep[0], o[nt][m][1] *= keep[1];
+              o[nt][m][2] *= keep[0], o[nt][m][3] *= keep[1];
+            }
+          }
+        }
+        if (!kFp8 && !all) {  // a position that does not count: its value must not reach a product with 0
+          for (int e = lane; e < 16 * MT * (C::kRow / 16); e += 32) {
+            const int p = p0 + e / (C::kRow / 16);
+            if ((mask >> p) & 1) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vbase + tile_offset<C>(p, e % (C::kRow / 16))),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async_smem();  // before the stage's next TMA write
+          __syncwarp();
+        }
+        // ---- probabilities; O^T += V^T P^T
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int p = p0 + mt * 16;
+          float va = 1.f, vb = 1.f;
+          if (kFp8) {
+            va = kTwo60 * lds_f32(sbase + C::kScale + (p + g) * 4);
+            vb = kTwo60 * lds_f32(sbase + C::kScale + (p + g + 8) * 4);
+            if (!all) {
+              if (!((mask >> (p + g)) & 1)) va = 0.f;
+              if (!((mask >> (p + g + 8)) & 1)) vb = 0.f;
+            }
+          }
+          uint32_t b0[NT], b1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&v)[4] = s[mt][nt];
+            // top is -inf only while every logit of the head so far is: exp2(-inf) = 0 either way
+            const float t0 = top[nt][0] == -INFINITY ? 0.f : top[nt][0], t1 = top[nt][1] == -INFINITY ? 0.f : top[nt][1];
+            v[0] = exp2_approx(v[0] - t0);
+            v[1] = exp2_approx(v[1] - t1);
+            v[2] = exp2_approx(v[2] - t0);
+            v[3] = exp2_approx(v[3] - t1);
+            l[nt][0] += v[0] + v[2];
+            l[nt][1] += v[1] + v[3];
+            if (kFp8) v[0] *= va, v[1] *= va, v[2] *= vb, v[3] *= vb;
+            b0[nt] = transpose8x8(bf16x2(v[0], v[1]));
+            b1[nt] = transpose8x8(bf16x2(v[2], v[3]));
+          }
+          if (kFp8) {
+#pragma unroll
+            for (int m = 0; m < kM; m += 2) {
+              uint32_t r[4];  // positions 0-7 | 8-15 of dims 0-15, then of dims 16-31; pairs of dims move together
+              ldsm4_t(r, vbase + tile_offset<C>(p + (lane & 15), m + (lane >> 4)));
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {  // row g of the product is dim 2g, row g + 8 dim 2g + 1
+                const uint32_t x = r[2 * hh], y = r[2 * hh + 1];
+                const uint32_t a0 = widen2(x, 0x2404), a1 = widen2(x, 0x3414), a2 = widen2(y, 0x2404), a3 = widen2(y, 0x3414);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][m + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              uint32_t r[4];
+              ldsm4_t(r, vbase + tile_offset<C>(p + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][m], r[0], r[1], r[2], r[3], b0[nt], b1[nt]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[stage]);
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+    // ---- the warps' parts of the segment into one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int b = 4; b < 32; b <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], b);
+        if (g == 0) {
+          const int h = wh * 8 * NT + nt * 8 + 2 * q + e;
+          stat[(wp * C::kHeadsU + h) * 2] = top[nt][e];
+          stat[(wp * C::kHeadsU + h) * 2 + 1] = l[nt][e];
+        }
+      }
+    named_sync(1, C::kConsumers);
+    const bool whole = w.i0 == 0 && w.i1 == w.n;
+    float keep[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = wh * 8 * NT + nt * 8 + 2 * q + e;
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < WP; ++x) m = fmaxf(m, stat[(x * C::kHeadsU + h) * 2]);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int x = 0; x < WP; ++x)
+          sum += stat[(x * C::kHeadsU + h) * 2 + 1] * exp2_approx(stat[(x * C::kHeadsU + h) * 2] - ref);
+        keep[nt][e] = exp2_approx(top[nt][e] - ref) * (kFp8 ? kTwo60 : 1.f);
+        if (whole) keep[nt][e] *= sum == 0.f ? 0.f : 1.f / sum;
+        if (wp == 0 && g == 0) {
+          if (!whole) {
+            const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
+            float* st = k.stat + (slot * C::kHeadsU + h) * 2;
+            st[0] = m;
+            st[1] = sum;
+          } else if (a.lse != nullptr && h < live) {
+            a.lse[static_cast<int64_t>(w.row) * a.c.num_q_heads + static_cast<int64_t>(head) * k.l.group + h0 + h] =
+                sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+          }
+        }
+      }
+#pragma unroll 1
+    for (int x = 0; x < WP; ++x) {
+      if (wp == x) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int h = wh * 8 * NT + nt * 8 + 2 * q + (e & 1);
+              const int d = m * 16 + (kFp8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+              float* at = acc + h * C::kAccStride + d;
+              const float v = o[nt][m][e] * keep[nt][e & 1];
+              *at = x == 0 ? v : *at + v;
+            }
+      }
+      named_sync(1, C::kConsumers);
+    }
+    if (whole) {
+      uint16_t* dst = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * D;
+      for (int e = tid; e < live * (D / 8); e += C::kConsumers) {
+        const int h = e / (D / 8), d = e % (D / 8) * 8;
+        const float4 x = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d);
+        const float4 y = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d + 4);
+        *reinterpret_cast<uint4*>(dst + h * D + d) = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+      }
+    } else {
+      const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
+      float* dst = k.sum + slot * C::kHeadsU * D;
+      for (int e = tid; e < live * (D / 4); e += C::kConsumers) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
+        *reinterpret_cast<float4*>(dst + h * D + d) = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d);
+      }
+      if (tid == 0 && w.i0 == 0) {
+        // the CTA that holds the unit's last tile
+        const int64_t end = w.base + static_cast<int64_t>(w.unit + 1) * w.n - 1;
+        const int64_t last = ((end + 1) * range.ctas - 1) / range.total;
+        k.part[blockIdx.x] = Part{w.row, w.unit, static_cast<int32_t>(last), 0};
+      }
+    }
+  }
+}
+
+template <int D, bool kFp8, int NT, int WP, int WH>
+__global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<D, kFp8, NT, WP, WH>::kCtasPerSm)
+    attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Args k) {
+  using C = Config<D, kFp8, NT, WP, WH>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;  // the swizzle is one of address bits
+  uint8_t* mem = raw + (base - smem_u32(raw));
+  float* acc = reinterpret_cast<float*>(mem + C::kStages * (C::kStage + 2 * C::kScale));
+  float* stat = acc + C::kAcc / 4;
+  Shared& sh = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(stat) + C::kStat);
+  const AttnArgs& a = k.a;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh.full[s], kFp8 && a.pos != nullptr ? 33 : 1);
+      mbar_init(&sh.empty[s], WP * WH);
+    }
+    fence_mbar_init();
+    sh.abort = 0;
+    k.part[blockIdx.x].last = -1;
+  }
+  const int units = a.c.num_kv_heads * k.l.blocks;
+  find_range<C::kThreads>(k, sh, units);
+  // rows with nothing to read
+  for (int t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    if (row_tiles(a, t) != 0) continue;
+    for (int e = tid; e < a.c.num_q_heads * (D / 8); e += C::kThreads)
+      *reinterpret_cast<uint4*>(a.out + t * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int h = tid; h < a.c.num_q_heads; h += C::kThreads)
+        a.lse[static_cast<int64_t>(t) * a.c.num_q_heads + h] = -INFINITY;
+  }
+  const Range r = sh.range;
+  if (r.first < r.end) {
+    Walk w{r.first, r.end, r.base, r.row, row_tiles(a, r.row), units, 0, 0, 0};
+    if (warp == WP * WH)
+      produce<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
+    else
+      consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int D, bool kFp8, int NT, int WP, int WH>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t stream) {
+  using C = Config<D, kFp8, NT, WP, WH>;
+  auto fn = attn_kernel<D, kFp8, NT, WP, WH>;
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set[dev]) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev] = true;
+  }
+  fn<<<k.l.ctas, C::kThreads, C::kSmem, stream>>>(kmap, vmap, k);
+  return cudaGetLastError();
+}
+
+// The instance for a head size and a padded number of heads per unit.
+template <bool kFp8>
+cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s) {
+  const int d = k.a.c.head_dim, h = k.l.heads;
+  if (d == 64) {
+    if (h == 8) return launch<64, kFp8, 1, 4, 1>(kmap, vmap, k, s);
+    if (h == 16) return launch<64, kFp8, 2, 4, 1>(kmap, vmap, k, s);
+    if (h == 32) return launch<64, kFp8, 2, 2, 2>(kmap, vmap, k, s);
+    return launch<64, kFp8, 2, 1, 4>(kmap, vmap, k, s);
+  }
+  if (d == 128) {
+    if (h == 8) return launch<128, kFp8, 1, 4, 1>(kmap, vmap, k, s);
+    if (h == 16) return launch<128, kFp8, 2, 4, 1>(kmap, vmap, k, s);
+    if (h == 32) return launch<128, kFp8, 2, 2, 2>(kmap, vmap, k, s);
+    return launch<128, kFp8, 2, 1, 4>(kmap, vmap, k, s);
+  }
+  if (h == 8) return launch<256, kFp8, 1, 4, 1>(kmap, vmap, k, s);
+  if (h == 16) return launch<256, kFp8, 1, 4, 2>(kmap, vmap, k, s);
+  if (h == 32) return launch<256, kFp8, 1, 2, 4>(kmap, vmap, k, s);
+  return launch<256, kFp8, 1, 1, 8>(kmap, vmap, k, s);
+}
+
+cudaError_t launch_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s);
+cudaError_t launch_fp8(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace ci

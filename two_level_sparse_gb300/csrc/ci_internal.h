@@ -148,5 +148,9 @@ int64_t device_l2_bytes();  // L2 cache size of the current device
 // [num_pages][64 positions][128 bytes], 128-byte swizzle, box of `box_rows`
 // positions of one page.
 cudaError_t make_pool_tmap(CUtensorMap* map, const uint8_t* k_pool, int64_t num_pages, int kv_format, int box_rows);
+// Tensor map over `rows` rows of row_bytes (64, or a multiple of 128) bytes
+// behind one another, 64- or 128-byte swizzle, box of min(row_bytes, 128)
+// bytes of box_rows rows.
+cudaError_t make_rows_tmap(CUtensorMap* map, const uint8_t* base, int64_t rows, int row_bytes, int box_rows);
 
 }  // namespace ci
