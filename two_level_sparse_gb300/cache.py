@@ -77,10 +77,11 @@ def _numel(t, n, name):
         raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(device).cuda_stream, without the object
+
+
 def _on(stream, like):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(like.device).cuda_stream
+    return stream.cuda_stream if stream is not None else _current_stream(like.get_device())
 
 
 def _check(fn, status):

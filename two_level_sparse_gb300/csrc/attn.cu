@@ -10,7 +10,7 @@ using attn::Args;
 using attn::Layout;
 using attn::Part;
 
-constexpr int kJoinHeads = 4, kJoinWays = 4;  // heads per CTA, warps per head
+constexpr int kJoinWarps = 16;
 
 Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
   const int group = num_q_heads / num_kv_heads;
@@ -20,21 +20,37 @@ Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
 
 // With the parts' maxima m_i, sums l_i and unnormalised sums o_i:
 //   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
-// One CTA per (CTA in whose range a split unit starts, four heads); a head's
-// parts are dealt to four warps, whose sums are added in order.  Bound by the
-// latency of its loads: the parts of a unit are few and sit in L2.
+// CTA (x, y) takes the x-th split unit and 16 / ways of its heads; a head's
+// parts are dealt to `ways` warps, whose sums are added in order.  Bound by
+// the latency of its loads (the parts sit in L2), so few parts per warp.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinHeads * kJoinWays) join_kernel(const Args k) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int ways) {
   constexpr int kPer = D / 32;
+  __shared__ float sums[kJoinWarps][D];
+  __shared__ int starts;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Part p = k.part[blockIdx.x];
-  if (p.last < 0) return;
-  __shared__ float sums[kJoinWays][kJoinHeads][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hw = warp / kJoinWays, way = warp % kJoinWays;
-  const int h = blockIdx.y * kJoinHeads + hw, heads = k.l.heads;
+  // the CTA in whose range the x-th split unit starts
+  if (warp == 0) {
+    int found = -1, seen = 0;
+    for (int c0 = 0; c0 < k.l.ctas && found < 0; c0 += 32) {
+      const bool starts_one = c0 + lane < k.l.ctas && k.part[c0 + lane].last >= 0;
+      const uint32_t b = __ballot_sync(0xffffffffu, starts_one);
+      const int want = blockIdx.x - seen;  // among this group's, if it has that many
+      if (want < __popc(b)) found = c0 + __fns(b, 0, want + 1);
+      seen += __popc(b);
+    }
+    if (lane == 0) starts = found;
+  }
+  __syncthreads();
+  const int first = starts;
+  if (first < 0) return;
+  const Part p = k.part[first];
+  const int hw = warp / ways, way = warp - hw * ways;
+  const int heads = k.l.heads, h = blockIdx.y * (kJoinWarps / ways) + hw;
   const int head = p.unit / k.l.blocks, hb = p.unit - head * k.l.blocks;
-  const bool live = hb * heads + h < k.l.group;
-  const int first = blockIdx.x, n = p.last - first + 1;
+  const bool live = h < heads && hb * heads + h < k.l.group;
+  const int n = p.last - first + 1;
   auto slot = [&](int i) -> int64_t { return i == 0 ? 2ll * first + 1 : 2ll * (first + i); };
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
@@ -51,7 +67,7 @@ __global__ void __launch_bounds__(32 * kJoinHeads * kJoinWays) join_kernel(const
 #pragma unroll
     for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
 #pragma unroll 4
-    for (int i = way; i < n; i += kJoinWays) {
+    for (int i = way; i < n; i += ways) {
       const float f = attn::exp2_approx(k.stat[(slot(i) * heads + h) * 2] - ref);
       const float* src = k.sum + (slot(i) * heads + h) * D + lane;
 #pragma unroll
@@ -59,7 +75,7 @@ __global__ void __launch_bounds__(32 * kJoinHeads * kJoinWays) join_kernel(const
     }
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) sums[way][hw][32 * j + lane] = o[j];
+  for (int j = 0; j < kPer; ++j) sums[warp][32 * j + lane] = o[j];
   __syncthreads();
   if (!live || way != 0) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -68,8 +84,7 @@ __global__ void __launch_bounds__(32 * kJoinHeads * kJoinWays) join_kernel(const
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     float v = 0.f;
-#pragma unroll
-    for (int x = 0; x < kJoinWays; ++x) v += sums[x][hw][32 * j + lane];
+    for (int x = 0; x < ways; ++x) v += sums[warp + x][32 * j + lane];
     dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v * inv));
   }
   if (k.a.lse != nullptr && lane == 0)
@@ -82,17 +97,22 @@ int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.heads * 2 * 4; }
 
 template <int D>
 cudaError_t launch_join(const Args& k, cudaStream_t stream) {
+  // Units number rows * kv heads * blocks; at most one starts unfinished in a
+  // CTA's range.  The fewer units, the more parts each: 16, 4 or 1 warps a head.
+  const int64_t units = static_cast<int64_t>(k.a.rows) * k.a.c.num_kv_heads * k.l.blocks;
+  const int64_t split = units < k.l.ctas ? units : k.l.ctas, parts = k.l.ctas / split + 1;
+  const int ways = parts > 16 ? 16 : parts > 4 ? 4 : 1, per = kJoinWarps / ways;
+  const int heads = k.l.heads < k.l.group ? k.l.heads : k.l.group;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(k.l.ctas, (k.l.heads < k.l.group ? k.l.heads : k.l.group) / kJoinHeads +
-                                   ((k.l.heads < k.l.group ? k.l.heads : k.l.group) % kJoinHeads != 0));
-  cfg.blockDim = dim3(32 * kJoinHeads * kJoinWays);
+  cfg.gridDim = dim3(static_cast<unsigned>(split), (heads + per - 1) / per);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, k);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, k, ways);
 }
 
 }  // namespace

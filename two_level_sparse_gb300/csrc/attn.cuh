@@ -25,10 +25,13 @@
 // (64 positions x D = 128 in bf16 per 1400 cycles and SM) needs 128 x G / 8 of
 // these instructions, which legacy tensor throughput covers up to G = 64.
 //
-// FP8 pages.  An e4m3 code's exponent and mantissa, moved into the low bits of
-// a bf16's, are the value x 2^-120, subnormals included: three logic operations
-// per pair instead of conversions, and exact.  The powers of two come back
-// through the query (x 2^64, exact), the logit's factor and the final division.
+// FP8 pages.  K: e4m3 widens to f16 exactly, one conversion per pair; the
+// query becomes f16 exactly too once each head is scaled by a power of two to
+// a largest magnitude in [2^14, 2^15) (what it loses lies 2^-39 below that).
+// V: the probabilities carry the value's scale, whose range f16 does not have,
+// so this product is bf16: an e4m3 code's exponent and mantissa, moved into the
+// low bits of a bf16's, are the value x 2^-120, subnormals included.  The
+// powers of two come back in the logit's factor and the final division.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -39,7 +42,7 @@ namespace attn {
 
 constexpr int kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTwo56 = 72057594037927936.f, kTwo60 = 1152921504606846976.f, kTwo64 = 18446744073709551616.f;
+constexpr float kTwo60 = 1152921504606846976.f;
 
 // What the main kernel and the join agree on.
 struct Part {  // the unit that goes on past the end of a CTA's range; last < 0: none
@@ -117,11 +120,28 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 codes of r (bytes picked by sel into the upper byte of each half)
-// as bf16 of value x 2^-120.
-__device__ __forceinline__ uint32_t widen2(uint32_t r, uint32_t sel) {
-  const uint32_t x = __byte_perm(r, 0, sel);
-  return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Bytes 0, 1 and bytes 2, 3 of r (e4m3) as f16 pairs.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t r, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(r));
+}
+// Bytes 0, 2 and bytes 1, 3 of r (e4m3) as bf16 pairs of the value x 2^-120.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t r, uint32_t& even, uint32_t& odd) {
+  even = ((r << 8) & 0x80008000u) | ((r << 4) & 0x07F007F0u);
+  odd = (r & 0x80008000u) | ((r >> 4) & 0x07F007F0u);
 }
 
 // Byte offset of 16-byte chunk `chunk` of position `p` in a matrix of a tile:
@@ -386,7 +406,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int wp = warp % WP, wh = warp / WP, p0 = wp * 16 * MT;
   const int tid = threadIdx.x;
-  const float factor = a.scale * kLog2e * (kFp8 ? kTwo56 : 1.f);
+  const float factor = a.scale * kLog2e;
   const Range range = sh.range;
   int stage = 0;
   uint32_t phase = 0;
@@ -397,6 +417,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
     const int live = min(C::kHeadsU, k.l.group - h0);              // heads of the unit that exist
     // ---- the queries, as B fragments
     uint32_t qf[NT][kK][2];
+    float qs[NT][2];  // FP8: what undoes the scaling of heads 2q and 2q + 1
     {
       const uint16_t* row = a.q + w.row * a.q_stride + (static_cast<int64_t>(head) * k.l.group + h0) * D;
 #pragma unroll
@@ -405,17 +426,35 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
         const uint16_t* src = row + static_cast<int64_t>(h < live ? h : 0) * D;
 #pragma unroll
         for (int kk = 0; kk < kK; ++kk) {
-          uint32_t b0, b1;
+          uint2 v;
           if (kFp8) {  // the order of the 16 dims that the widened codes come in: 4q, 4q + 1 | 4q + 2, 4q + 3
-            const uint2 v = *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * q);
-            b0 = bf16x2(bf16_lo(v.x) * kTwo64, bf16_hi(v.x) * kTwo64);
-            b1 = bf16x2(bf16_lo(v.y) * kTwo64, bf16_hi(v.y) * kTwo64);
+            v = *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * q);
           } else {
-            b0 = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * q);
-            b1 = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * q);
+            v.x = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * q);
+            v.y = *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * q);
           }
-          qf[nt][kk][0] = h < live ? b0 : 0;
-          qf[nt][kk][1] = h < live ? b1 : 0;
+          qf[nt][kk][0] = h < live ? v.x : 0;
+          qf[nt][kk][1] = h < live ? v.y : 0;
+        }
+        if (kFp8) {
+          uint32_t most = 0;  // the largest magnitude's bits, of both halves
+#pragma unroll
+          for (int kk = 0; kk < kK; ++kk) most = __vmaxu2(most, __vmaxu2(qf[nt][kk][0] & 0x7FFF7FFFu, qf[nt][kk][1] & 0x7FFF7FFFu));
+          most = max(most & 0xFFFFu, most >> 16);
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          const int e = most >> 7;  // biased exponent; 0: zeros and subnormals, 255: not finite
+          const int up = e == 0 || e == 255 ? 0 : 127 + 14 - e;  // times 2^up
+          // 2^up lies in [2^-113, 2^140]: in two steps, each a normal number
+          const float f0 = __uint_as_float((127 + up / 2) << 23), f1 = __uint_as_float((127 + up - up / 2) << 23);
+          const float back = __uint_as_float((127 - up / 2) << 23) * __uint_as_float((127 - (up - up / 2)) << 23);
+          qs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * q);
+          qs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * q + 4);
+#pragma unroll
+          for (int kk = 0; kk < kK; ++kk)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2)
+              qf[nt][kk][e2] = f16x2(bf16_lo(qf[nt][kk][e2]) * f0 * f1, bf16_hi(qf[nt][kk][e2]) * f0 * f1);
         }
       }
     }
@@ -455,9 +494,11 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
                 const uint32_t x = r[2 * hh], y = r[2 * hh + 1];
-                const uint32_t a0 = widen2(x, 0x1404), a1 = widen2(y, 0x1404), a2 = widen2(x, 0x3424), a3 = widen2(y, 0x3424);
+                uint32_t a0, a1, a2, a3;
+                e4m3_to_f16(x, a0, a2);
+                e4m3_to_f16(y, a1, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_bf16(s[mt][nt], a0, a1, a2, a3, qf[nt][kk + hh][0], qf[nt][kk + hh][1]);
+                for (int nt = 0; nt < NT; ++nt) mma_f16(s[mt][nt], a0, a1, a2, a3, qf[nt][kk + hh][0], qf[nt][kk + hh][1]);
               }
             }
           } else {
@@ -487,6 +528,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float(&v)[4] = s[mt][nt];
+            if (kFp8) v[0] *= qs[nt][0], v[1] *= qs[nt][1], v[2] *= qs[nt][0], v[3] *= qs[nt][1];
             v[0] = ina ? v[0] * fa : -INFINITY;
             v[1] = ina ? v[1] * fa : -INFINITY;
             v[2] = inb ? v[2] * fb : -INFINITY;
@@ -569,7 +611,9 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {  // row g of the product is dim 2g, row g + 8 dim 2g + 1
                 const uint32_t x = r[2 * hh], y = r[2 * hh + 1];
-                const uint32_t a0 = widen2(x, 0x2404), a1 = widen2(x, 0x3414), a2 = widen2(y, 0x2404), a3 = widen2(y, 0x3414);
+                uint32_t a0, a1, a2, a3;
+                e4m3_to_bf16(x, a0, a1);
+                e4m3_to_bf16(y, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][m + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
               }
