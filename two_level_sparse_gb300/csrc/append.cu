@@ -20,7 +20,7 @@ namespace ci {
 namespace {
 
 constexpr int kWarps = 4, kCtasPerSm = 5;
-constexpr int kBatch = 4;  // groups of heads per task
+constexpr int kBatch = 4;  // groups of 32 / (D / 8) heads per task
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
@@ -37,10 +37,11 @@ __device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
-// The heads of a task: kBatch groups of 32 / (D / 8) heads, all of q, then of k,
-// then of v (a group holds heads of one kind).
-struct Groups {
-  int q, k, all, chunks;  // groups of q; of q and k; of all; tasks per token
+// The tasks of a token: chunks of kBatch * 32 / (D / 8) heads, of q, then of k,
+// then of v.
+struct Chunks {
+  int q, k, all;              // chunks of q; of q and k; of all
+  int step_tok, step_chunk;   // a warp's stride over the tasks
 };
 
 // A task's raw heads and position.
@@ -50,37 +51,95 @@ struct Loaded {
 };
 
 template <int D>
-__device__ __forceinline__ void load_task(const AppendArgs& a, const Groups& n, int t, int chunk, int o0, int o1, int sub,
+__device__ __forceinline__ void load_task(const AppendArgs& a, const Chunks& n, int t, int chunk, int o0, int o1, int sub,
                                           Loaded& x) {
   constexpr int kPer = 32 / (D / 8);
   x.p = a.positions[t];
   x.u = a.cache_pos != nullptr ? a.cache_pos[t] : x.p;
+  const bool isq = chunk < n.q, isk = chunk < n.k;
+  const int h = (chunk - (isq ? 0 : isk ? n.q : n.k)) * kBatch * kPer + sub;
+  const int left = (isq ? a.c.num_q_heads : a.c.num_kv_heads) - h;
+  const uint16_t* src = (isq ? a.q + t * a.q_stride : isk ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D;
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
-    const int g = chunk * kBatch + i;
-    const bool isq = g < n.q, isk = g < n.k;
-    const int h = (isq ? g : isk ? g - n.q : g - n.k) * kPer + sub;
-    const uint16_t* src = (isq ? a.q + t * a.q_stride : isk ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D;
     x.lo[i] = x.hi[i] = make_uint2(0, 0);
-    if (g < n.all && h < (isq ? a.c.num_q_heads : a.c.num_kv_heads)) {
-      x.lo[i] = *reinterpret_cast<const uint2*>(src + o0);
-      x.hi[i] = *reinterpret_cast<const uint2*>(src + o1);
+    if (i * kPer < left) {
+      x.lo[i] = *reinterpret_cast<const uint2*>(src + i * kPer * D + o0);
+      x.hi[i] = *reinterpret_cast<const uint2*>(src + i * kPer * D + o1);
     }
   }
 }
 
+__device__ __forceinline__ void unpack8(uint2 lo, uint2 hi, float (&x)[8]) {
+  x[0] = bf16_lo(lo.x), x[1] = bf16_hi(lo.x), x[2] = bf16_lo(lo.y), x[3] = bf16_hi(lo.y);
+  x[4] = bf16_lo(hi.x), x[5] = bf16_hi(hi.x), x[6] = bf16_lo(hi.y), x[7] = bf16_hi(hi.y);
+}
+
+template <int D, bool kNeox>
+__device__ __forceinline__ void norm_turn(float (&x)[8], const float (&w)[8], bool norm, float eps, bool turns,
+                                          const float (&cs)[4], const float (&sn)[4]) {
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+  }
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = kNeox ? j : 2 * j, f = kNeox ? j + 4 : 2 * j + 1;
+      const float va = x[e], vb = x[f];
+      x[e] = va * cs[j] - vb * sn[j];
+      x[f] = vb * cs[j] + va * sn[j];
+    }
+  }
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* dst, int o0, int o1, const float (&x)[8]) {
+  *reinterpret_cast<uint2*>(dst + o0) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+  *reinterpret_cast<uint2*>(dst + o1) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+}
+
+// One position's entry of a (page, head) at `at`; all lanes of the head take part.
+template <int D, bool kFp8>
+__device__ __forceinline__ void store_entry(uint8_t* at, int slot, int o0, int o1, int m, bool store, float (&x)[8]) {
+  if (!kFp8) {
+    if (store) store_bf16(reinterpret_cast<uint16_t*>(at) + slot * D, o0, o1, x);
+    return;
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float scale = __fdiv_rn(max_nan(amax, 1e-10f), 448.f), inv = __frcp_rn(scale);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // x / scale: a product with the reciprocal, and Markstein's correction of it
+    const float y = x[j] * inv;
+    x[j] = fmaf(fmaf(-y, scale, x[j]), inv, y);
+  }
+  if (store) {
+    *reinterpret_cast<uint32_t*>(at + slot * D + o0) = e4m3_quad(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint32_t*>(at + slot * D + o1) = e4m3_quad(x[4], x[5], x[6], x[7]);
+    if (m == 0) reinterpret_cast<float*>(at + kPage * D)[slot] = scale;
+  }
+}
+
 template <int D, bool kFp8, bool kNeox>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, const Groups n) {
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, const Chunks n) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes per head, heads per group
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31, m = lane % kLanes, sub = lane / kLanes;
   const int half = a.rot_dim / 2;
   const bool turns = 8 * m < a.rot_dim;
   const int o0 = kNeox && turns ? 4 * m : 8 * m, o1 = kNeox && turns ? half + 4 * m : 8 * m + 4;
-  const int64_t tasks = static_cast<int64_t>(a.tokens) * n.chunks, step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (task >= tasks) return;
-  int t = static_cast<int>(task / n.chunks), chunk = static_cast<int>(task - static_cast<int64_t>(t) * n.chunks);
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  int t = static_cast<int>(task / n.all), chunk = static_cast<int>(task - static_cast<int64_t>(t) * n.all);
+  if (t >= a.tokens) return;
   Loaded now;
   load_task<D>(a, n, t, chunk, o0, o1, sub, now);
   float wq[8], wk[8];
@@ -92,20 +151,23 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
     wq[4 * j] = x.x, wq[4 * j + 1] = x.y, wq[4 * j + 2] = x.z, wq[4 * j + 3] = x.w;
     wk[4 * j] = y.x, wk[4 * j + 1] = y.y, wk[4 * j + 2] = y.z, wk[4 * j + 3] = y.w;
   }
-  while (true) {
-    // ---- this task's rotation and page; the next task's heads
-    const int p = now.p, u = now.u, g0 = chunk * kBatch, tok = t;
+  const bool qnorm = a.q_norm != nullptr, knorm = a.k_norm != nullptr;
+  bool more = true;
+  while (more) {
+    // ---- this task's rotation and page
+    const int p = now.p, u = now.u, tok = t, mine = chunk;
+    const bool isq = mine < n.q, isk = !isq && mine < n.k;
     const bool ok = p >= 0 && p < a.max_pos;
-    if (!ok && lane == 0 && chunk == 0) report(c.dev_err, kDevErrPos);
+    if (!ok && lane == 0 && mine == 0) report(c.dev_err, kDevErrPos);
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok && turns && g0 < n.k) {
+    if (ok && turns && (isq || isk)) {
       const float* at = a.cos_sin + static_cast<int64_t>(p) * a.rot_dim + 4 * m;
       const float4 x = *reinterpret_cast<const float4*>(at), y = *reinterpret_cast<const float4*>(at + half);
       cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
       sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
     }
     int page = -1;
-    if (ok && u >= 0 && g0 + kBatch > n.q) {
+    if (ok && u >= 0 && !isq) {
       const int r = row_request(c, tok);
       if (u >= static_cast<int64_t>(c.max_pages) * kPage) {
         if (lane == 0) report(c.dev_err, kDevErrPos);
@@ -117,92 +179,53 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
         }
       }
     }
+    // ---- the next task's heads
     const Loaded cur = now;
-    task += step;
-    const bool more = task < tasks;
-    if (more) {
-      t = static_cast<int>(task / n.chunks);
-      chunk = static_cast<int>(task - static_cast<int64_t>(t) * n.chunks);
-      load_task<D>(a, n, t, chunk, o0, o1, sub, now);
-    }
+    t += n.step_tok;
+    chunk += n.step_chunk;
+    if (chunk >= n.all) chunk -= n.all, ++t;
+    more = t < a.tokens;
+    if (more) load_task<D>(a, n, t, chunk, o0, o1, sub, now);
+    // ---- this task's heads
+    const int h = (mine - (isq ? 0 : isk ? n.q : n.k)) * kBatch * kPer + sub;
+    if (isq) {
+      uint16_t* dst = a.q_out + tok * a.q_out_stride + h * D;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int g = g0 + i;
-      if (g >= n.all) break;
-      const bool isq = g < n.q, isk = !isq && g < n.k;
-      const int h = (isq ? g : isk ? g - n.q : g - n.k) * kPer + sub;
-      const bool live = h < (isq ? c.num_q_heads : c.num_kv_heads);
-      float x[8] = {bf16_lo(cur.lo[i].x), bf16_hi(cur.lo[i].x), bf16_lo(cur.lo[i].y), bf16_hi(cur.lo[i].y),
-                    bf16_lo(cur.hi[i].x), bf16_hi(cur.hi[i].x), bf16_lo(cur.hi[i].y), bf16_hi(cur.hi[i].y)};
-      if (isq || isk) {
-        if ((isq ? a.q_norm : a.k_norm) != nullptr) {
-          float ss = 0.f;
+      for (int i = 0; i < kBatch; ++i) {
+        float x[8];
+        unpack8(cur.lo[i], cur.hi[i], x);
+        norm_turn<D, kNeox>(x, wq, qnorm, a.eps, turns, cs, sn);
+        if (!ok) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          if (isq) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wq[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wk[j];
-          }
+          for (int j = 0; j < 8; ++j) x[j] = 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // dims past rot_dim turn by (1, 0)
-          const int e = kNeox ? j : 2 * j, f = kNeox ? j + 4 : 2 * j + 1;
-          const float va = x[e], vb = x[f];
-          if (turns) x[e] = va * cs[j] - vb * sn[j], x[f] = vb * cs[j] + va * sn[j];
-        }
+        if (h + i * kPer < c.num_q_heads) store_bf16(dst + i * kPer * D, o0, o1, x);
       }
-      if (isq) {
-        uint16_t* dst = a.q_out + tok * a.q_out_stride + h * D;
-        if (live) {
-          const uint2 lo = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-          const uint2 hi = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-          *reinterpret_cast<uint2*>(dst + o0) = ok ? lo : make_uint2(0, 0);
-          *reinterpret_cast<uint2*>(dst + o1) = ok ? hi : make_uint2(0, 0);
-        }
-        continue;
-      }
-      const bool store = live && page >= 0;
-      const int slot = u & (kPage - 1);
+    } else {
       uint8_t* at = (isk ? c.k_pool : c.v_pool) +
-                    (static_cast<int64_t>(page) * c.num_kv_heads + h) * cache_page_bytes<kFp8>(D);
-      if (kFp8) {
-        float amax = 0.f;
+                    (static_cast<int64_t>(max(page, 0)) * c.num_kv_heads + h) * cache_page_bytes<kFp8>(D);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float scale = __fdiv_rn(max_nan(amax, 1e-10f), 448.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], scale);
-        if (store) {
-          *reinterpret_cast<uint32_t*>(at + slot * D + o0) = e4m3_quad(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint32_t*>(at + slot * D + o1) = e4m3_quad(x[4], x[5], x[6], x[7]);
-          if (m == 0) reinterpret_cast<float*>(at + kPage * D)[slot] = scale;
-        }
-      } else if (store) {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(at) + slot * D;
-        *reinterpret_cast<uint2*>(dst + o0) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-        *reinterpret_cast<uint2*>(dst + o1) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+      for (int i = 0; i < kBatch; ++i) {
+        float x[8];
+        unpack8(cur.lo[i], cur.hi[i], x);
+        if (isk) norm_turn<D, kNeox>(x, wk, knorm, a.eps, turns, cs, sn);
+        store_entry<D, kFp8>(at + i * kPer * cache_page_bytes<kFp8>(D), u & (kPage - 1), o0, o1, m,
+                             page >= 0 && h + i * kPer < c.num_kv_heads, x);
       }
     }
-    if (!more) break;
   }
 }
 
 template <int D>
 void launch_d(const AppendArgs& a, cudaStream_t stream) {
-  constexpr int kPer = 32 / (D / 8);
-  const int qg = (a.c.num_q_heads + kPer - 1) / kPer, kg = (a.c.num_kv_heads + kPer - 1) / kPer;
-  const Groups n{qg, qg + kg, qg + 2 * kg, (qg + 2 * kg + kBatch - 1) / kBatch};
-  const int64_t ctas = (static_cast<int64_t>(a.tokens) * n.chunks + kWarps - 1) / kWarps;
+  constexpr int kHeads = kBatch * (32 / (D / 8));  // of a task
+  const int qc = (a.c.num_q_heads + kHeads - 1) / kHeads, kc = (a.c.num_kv_heads + kHeads - 1) / kHeads;
+  const int all = qc + 2 * kc;
+  const int64_t ctas = (static_cast<int64_t>(a.tokens) * all + kWarps - 1) / kWarps;
   const int64_t most = static_cast<int64_t>(device_sm_count()) * kCtasPerSm;
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+  const int warps = static_cast<int>(grid) * kWarps;
+  const Chunks n{qc, qc + kc, all, warps / all, warps % all};
   if (a.c.fp8) {
     if (a.neox)
       append_kernel<D, true, true><<<grid, 32 * kWarps, 0, stream>>>(a, n);
