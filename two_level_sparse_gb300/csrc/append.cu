@@ -9,8 +9,9 @@
 // elements of every rotated pair sit in one lane (half layout: dims 4m.. and
 // rot/2 + 4m..; interleaved and unrotated dims: 8m..8m + 7): the rotation needs
 // no exchange between lanes, only the norm's sum and the FP8 maximum do.  A
-// warp's task is a token and a few of its heads; the next task's loads are in
-// flight while one is worked on, and the norm weights stay in registers.
+// warp's task is a token and a few of its heads of one kind: norm weight and
+// rotation become two factors per element once for all of them, and the next
+// task's loads are in flight while one is worked on.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -19,7 +20,7 @@
 namespace ci {
 namespace {
 
-constexpr int kWarps = 4, kCtasPerSm = 5;
+constexpr int kWarps = 4, kCtasPerSm = 6;
 constexpr int kBatch = 4;  // groups of 32 / (D / 8) heads per task
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -70,67 +71,121 @@ __device__ __forceinline__ void load_task(const AppendArgs& a, const Chunks& n, 
   }
 }
 
-__device__ __forceinline__ void unpack8(uint2 lo, uint2 hi, float (&x)[8]) {
-  x[0] = bf16_lo(lo.x), x[1] = bf16_hi(lo.x), x[2] = bf16_lo(lo.y), x[3] = bf16_hi(lo.y);
-  x[4] = bf16_lo(hi.x), x[5] = bf16_hi(hi.x), x[6] = bf16_lo(hi.y), x[7] = bf16_hi(hi.y);
+__device__ __forceinline__ void unpack8(uint2 lo, uint2 hi, float2 (&x)[4]) {
+  x[0] = make_float2(bf16_lo(lo.x), bf16_hi(lo.x)), x[1] = make_float2(bf16_lo(lo.y), bf16_hi(lo.y));
+  x[2] = make_float2(bf16_lo(hi.x), bf16_hi(hi.x)), x[3] = make_float2(bf16_lo(hi.y), bf16_hi(hi.y));
 }
+
+// Two fp32 operations per instruction, each rounded as its scalar form is.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// A lane's share of norm and rotation, as two factors per element:
+//   out_j = r (x_j own_j + x_j' other_j),  j' the pair's other element,
+// own = w cos, other = -+ w' sin, r = rsqrt(mean(x^2) + eps).  Pairs of elements
+// (2i, 2i + 1); j' is j +- 4 in the half layout, j ^ 1 in the interleaved one.
+struct Factors {
+  float2 own[4], other[4];
+};
 
 template <int D, bool kNeox>
-__device__ __forceinline__ void norm_turn(float (&x)[8], const float (&w)[8], bool norm, float eps, bool turns,
-                                          const float (&cs)[4], const float (&sn)[4]) {
-  if (norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-    for (int o = 1; o < D / 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / D) + eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+__device__ __forceinline__ Factors factors_of(const float* w, int o0, int o1, const float* cos_sin, int half, int m) {
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  const float4 wl = w != nullptr ? *reinterpret_cast<const float4*>(w + o0) : one;
+  const float4 wh = w != nullptr ? *reinterpret_cast<const float4*>(w + o1) : one;
+  float4 c = one, s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (cos_sin != nullptr) {
+    c = *reinterpret_cast<const float4*>(cos_sin + 4 * m);
+    s = *reinterpret_cast<const float4*>(cos_sin + half + 4 * m);
   }
-  if (turns) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = kNeox ? j : 2 * j, f = kNeox ? j + 4 : 2 * j + 1;
-      const float va = x[e], vb = x[f];
-      x[e] = va * cs[j] - vb * sn[j];
-      x[f] = vb * cs[j] + va * sn[j];
-    }
+  Factors f;
+  if (kNeox) {  // elements j and j + 4 are a pair, turned by angle j
+    f.own[0] = make_float2(wl.x * c.x, wl.y * c.y), f.own[1] = make_float2(wl.z * c.z, wl.w * c.w);
+    f.own[2] = make_float2(wh.x * c.x, wh.y * c.y), f.own[3] = make_float2(wh.z * c.z, wh.w * c.w);
+    f.other[0] = make_float2(-wh.x * s.x, -wh.y * s.y), f.other[1] = make_float2(-wh.z * s.z, -wh.w * s.w);
+    f.other[2] = make_float2(wl.x * s.x, wl.y * s.y), f.other[3] = make_float2(wl.z * s.z, wl.w * s.w);
+  } else {  // elements 2i and 2i + 1 are a pair, turned by angle i
+    f.own[0] = make_float2(wl.x * c.x, wl.y * c.x), f.own[1] = make_float2(wl.z * c.y, wl.w * c.y);
+    f.own[2] = make_float2(wh.x * c.z, wh.y * c.z), f.own[3] = make_float2(wh.z * c.w, wh.w * c.w);
+    f.other[0] = make_float2(-wl.y * s.x, wl.x * s.x), f.other[1] = make_float2(-wl.w * s.y, wl.z * s.y);
+    f.other[2] = make_float2(-wh.y * s.z, wh.x * s.z), f.other[3] = make_float2(-wh.w * s.w, wh.z * s.w);
   }
+  return f;
 }
 
-__device__ __forceinline__ void store_bf16(uint16_t* dst, int o0, int o1, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(dst + o0) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-  *reinterpret_cast<uint2*>(dst + o1) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+// `whole`: every dim turns.  Where one does not, its `other` is 0 and must not
+// meet an infinity of the pair's other element.
+template <int D, bool kNeox>
+__device__ __forceinline__ void norm_turn(float2 (&x)[4], const Factors& f, bool norm, float eps, bool whole, bool turns) {
+  float r = 1.f;
+  if (norm) {
+    float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) ss = fma2(x[j], x[j], ss);
+    float s = ss.x + ss.y;
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    r = rsqrtf(s * (1.f / D) + eps);
+  }
+  const float2 rr = make_float2(r, r);
+  float2 y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 mate = kNeox ? x[j ^ 2] : make_float2(x[j].y, x[j].x);
+    y[j] = mul2(fma2(mate, f.other[j], mul2(x[j], f.own[j])), rr);
+    if (!whole && !turns) y[j] = mul2(mul2(x[j], f.own[j]), rr);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = y[j];
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* dst, int o0, int o1, const float2 (&x)[4]) {
+  *reinterpret_cast<uint2*>(dst + o0) = make_uint2(bf16_pair(x[0].x, x[0].y), bf16_pair(x[1].x, x[1].y));
+  *reinterpret_cast<uint2*>(dst + o1) = make_uint2(bf16_pair(x[2].x, x[2].y), bf16_pair(x[3].x, x[3].y));
 }
 
 // One position's entry of a (page, head) at `at`; all lanes of the head take part.
 template <int D, bool kFp8>
-__device__ __forceinline__ void store_entry(uint8_t* at, int slot, int o0, int o1, int m, bool store, float (&x)[8]) {
+__device__ __forceinline__ void store_entry(uint8_t* at, int slot, int o0, int o1, int m, bool store, float2 (&x)[4]) {
   if (!kFp8) {
     if (store) store_bf16(reinterpret_cast<uint16_t*>(at) + slot * D, o0, o1, x);
     return;
   }
   float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
+  for (int j = 0; j < 4; ++j) amax = max_nan(max_nan(amax, fabsf(x[j].x)), fabsf(x[j].y));
 #pragma unroll
   for (int o = 1; o < D / 8; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float scale = __fdiv_rn(max_nan(amax, 1e-10f), 448.f), inv = __frcp_rn(scale);
+  const float2 inv2 = make_float2(inv, inv), minus = make_float2(-scale, -scale);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {  // x / scale: a product with the reciprocal, and Markstein's correction of it
-    const float y = x[j] * inv;
-    x[j] = fmaf(fmaf(-y, scale, x[j]), inv, y);
+  for (int j = 0; j < 4; ++j) {  // x / scale: a product with the reciprocal, and Markstein's correction of it
+    const float2 y = mul2(x[j], inv2);
+    x[j] = fma2(fma2(y, minus, x[j]), inv2, y);
   }
   if (store) {
-    *reinterpret_cast<uint32_t*>(at + slot * D + o0) = e4m3_quad(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint32_t*>(at + slot * D + o1) = e4m3_quad(x[4], x[5], x[6], x[7]);
+    *reinterpret_cast<uint32_t*>(at + slot * D + o0) = e4m3_quad(x[0].x, x[0].y, x[1].x, x[1].y);
+    *reinterpret_cast<uint32_t*>(at + slot * D + o1) = e4m3_quad(x[2].x, x[2].y, x[3].x, x[3].y);
     if (m == 0) reinterpret_cast<float*>(at + kPage * D)[slot] = scale;
   }
 }
 
 template <int D, bool kFp8, bool kNeox>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, const Chunks n) {
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) append_kernel(const AppendArgs a, const Chunks n) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes per head, heads per group
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31, m = lane % kLanes, sub = lane / kLanes;
@@ -142,16 +197,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
   if (t >= a.tokens) return;
   Loaded now;
   load_task<D>(a, n, t, chunk, o0, o1, sub, now);
-  float wq[8], wk[8];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 x = a.q_norm != nullptr ? *reinterpret_cast<const float4*>(a.q_norm + (j ? o1 : o0)) : one;
-    const float4 y = a.k_norm != nullptr ? *reinterpret_cast<const float4*>(a.k_norm + (j ? o1 : o0)) : one;
-    wq[4 * j] = x.x, wq[4 * j + 1] = x.y, wq[4 * j + 2] = x.z, wq[4 * j + 3] = x.w;
-    wk[4 * j] = y.x, wk[4 * j + 1] = y.y, wk[4 * j + 2] = y.z, wk[4 * j + 3] = y.w;
-  }
-  const bool qnorm = a.q_norm != nullptr, knorm = a.k_norm != nullptr;
+  const bool whole = a.rot_dim == D;
   bool more = true;
   while (more) {
     // ---- this task's rotation and page
@@ -159,13 +205,10 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
     const bool isq = mine < n.q, isk = !isq && mine < n.k;
     const bool ok = p >= 0 && p < a.max_pos;
     if (!ok && lane == 0 && mine == 0) report(c.dev_err, kDevErrPos);
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok && turns && (isq || isk)) {
-      const float* at = a.cos_sin + static_cast<int64_t>(p) * a.rot_dim + 4 * m;
-      const float4 x = *reinterpret_cast<const float4*>(at), y = *reinterpret_cast<const float4*>(at + half);
-      cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
-      sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
-    }
+    Factors f;
+    if (isq || isk)
+      f = factors_of<D, kNeox>(isq ? a.q_norm : a.k_norm, o0, o1,
+                               ok && turns ? a.cos_sin + static_cast<int64_t>(p) * a.rot_dim : nullptr, half, m);
     int page = -1;
     if (ok && u >= 0 && !isq) {
       const int r = row_request(c, tok);
@@ -192,13 +235,10 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
       uint16_t* dst = a.q_out + tok * a.q_out_stride + h * D;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        float x[8];
+        float2 x[4];
         unpack8(cur.lo[i], cur.hi[i], x);
-        norm_turn<D, kNeox>(x, wq, qnorm, a.eps, turns, cs, sn);
-        if (!ok) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        }
+        norm_turn<D, kNeox>(x, f, a.q_norm != nullptr, a.eps, whole, turns);
+        if (!ok) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
         if (h + i * kPer < c.num_q_heads) store_bf16(dst + i * kPer * D, o0, o1, x);
       }
     } else {
@@ -206,9 +246,9 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
                     (static_cast<int64_t>(max(page, 0)) * c.num_kv_heads + h) * cache_page_bytes<kFp8>(D);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        float x[8];
+        float2 x[4];
         unpack8(cur.lo[i], cur.hi[i], x);
-        if (isk) norm_turn<D, kNeox>(x, wk, knorm, a.eps, turns, cs, sn);
+        if (isk) norm_turn<D, kNeox>(x, f, a.k_norm != nullptr, a.eps, whole, turns);
         store_entry<D, kFp8>(at + i * kPer * cache_page_bytes<kFp8>(D), u & (kPage - 1), o0, o1, m,
                              page >= 0 && h + i * kPer < c.num_kv_heads, x);
       }

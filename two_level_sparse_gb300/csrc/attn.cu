@@ -27,22 +27,26 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int ways) {
   constexpr int kPer = D / 32;
   __shared__ float sums[kJoinWarps][D];
-  __shared__ int starts;
+  __shared__ int counts[kJoinWarps], starts;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) starts = -1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the CTA in whose range the x-th split unit starts
-  if (warp == 0) {
-    int found = -1, seen = 0;
-    for (int c0 = 0; c0 < k.l.ctas && found < 0; c0 += 32) {
-      const bool starts_one = c0 + lane < k.l.ctas && k.part[c0 + lane].last >= 0;
-      const uint32_t b = __ballot_sync(0xffffffffu, starts_one);
-      const int want = blockIdx.x - seen;  // among this group's, if it has that many
-      if (want < __popc(b)) found = c0 + __fns(b, 0, want + 1);
-      seen += __popc(b);
+  int seen = 0;
+  for (int c0 = 0; c0 < k.l.ctas; c0 += 32 * kJoinWarps) {
+    const bool one = c0 + tid < k.l.ctas && k.part[c0 + tid].last >= 0;
+    const uint32_t b = __ballot_sync(0xffffffffu, one);
+    if (lane == 0) counts[warp] = __popc(b);
+    __syncthreads();
+    int before = seen + __popc(b & lanemask_lt());
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) before += counts[w];
+      seen += counts[w];
     }
-    if (lane == 0) starts = found;
+    if (one && before == static_cast<int>(blockIdx.x)) starts = c0 + tid;
+    __syncthreads();
   }
-  __syncthreads();
   const int first = starts;
   if (first < 0) return;
   const Part p = k.part[first];
@@ -56,19 +60,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int
 #pragma unroll
   for (int j = 0; j < kPer; ++j) o[j] = 0.f;
   if (live) {
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, k.stat[(slot(i) * heads + h) * 2]);
-#pragma unroll
-    for (int b = 16; b > 0; b >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
-    const float ref = m == -INFINITY ? 0.f : m;
+    const float2* stat = reinterpret_cast<const float2*>(k.stat) + h;
     for (int i = lane; i < n; i += 32) {
-      const float2 st = *reinterpret_cast<const float2*>(k.stat + (slot(i) * heads + h) * 2);
-      l += st.y * attn::exp2_approx(st.x - ref);
+      const float2 st = stat[slot(i) * heads];
+      const float top = fmaxf(m, st.x), ref = top == -INFINITY ? 0.f : top;
+      l = l * attn::exp2_approx(m - ref) + st.y * attn::exp2_approx(st.x - ref);
+      m = top;
     }
+    float top = m;
+#pragma unroll
+    for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+    const float ref = top == -INFINITY ? 0.f : top;
+    l *= attn::exp2_approx(m - ref);
+    m = top;
 #pragma unroll
     for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
 #pragma unroll 4
     for (int i = way; i < n; i += ways) {
-      const float f = attn::exp2_approx(k.stat[(slot(i) * heads + h) * 2] - ref);
+      const float f = attn::exp2_approx(stat[slot(i) * heads].x - ref);
       const float* src = k.sum + (slot(i) * heads + h) * D + lane;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) o[j] += f * src[32 * j];
@@ -132,9 +141,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   const int row = c.fp8 ? c.head_dim : 2 * c.head_dim;
   const int per_page = static_cast<int>((c.fp8 ? cache_page_bytes<true>(c.head_dim) : cache_page_bytes<false>(c.head_dim)) / row);
   CUtensorMap kmap, vmap;
-  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, a.pos != nullptr ? 1 : attn::kTile);
+  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
   if (e == cudaSuccess)
-    e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, a.pos != nullptr ? 1 : attn::kTile);
+    e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
   if (e == cudaSuccess) e = c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
   if (e != cudaSuccess) return e;
   return c.head_dim == 64    ? launch_join<64>(k, stream)

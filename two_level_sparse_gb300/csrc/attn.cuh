@@ -11,9 +11,9 @@
 // statistics in the workspace (two parts per CTA at most), and the join kernel
 // adds them in order.
 //
-// A tile.  One producer warp fetches K and V by TMA into a ring of stages
-// (128-byte swizzled rows): one box of 64 rows per page, or, for listed
-// positions, gathers of four rows each.  WP x WH consumer warps compute, WP
+// A tile.  One producer warp fetches K and V into a ring of stages, pages by TMA
+// (128-byte swizzled rows), or, for listed positions, by 16-byte asynchronous
+// copies of their rows.  WP x WH consumer warps compute, WP
 // along the positions and WH along the heads:
 //   S^T = K Q^T   A = K from shared memory (ldmatrix), B = Q in registers;
 //   online softmax per head, a column of S^T: its maximum over the warp's
@@ -161,14 +161,6 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(map), "r"(x), "r"(row), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -265,85 +257,78 @@ __device__ void find_range(const Args& k, Shared& sh, int units) {
   __syncthreads();
 }
 
-// ------------------------------------------------------------------ producer
-template <class C, int D, bool kFp8>
-__device__ void produce(const Args& k, Shared& sh, Walk w, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                        uint32_t stages) {
-  const AttnArgs& a = k.a;
-  const CacheArgs& c = a.c;
-  constexpr int kRowsPerPage = cache_page_bytes<kFp8>(D) / C::kRow;
-  const int lane = threadIdx.x & 31;
+// ------------------------------------------------------------------ producers
+// The ring as the producer sees it.
+template <class C>
+struct Ring {
+  Shared& sh;
+  const Args& k;
   int stage = 0;
   uint32_t phase = 1;  // the first round of stages is free
   uint32_t used = 0;
   bool alive = true;
+
+  __device__ __forceinline__ bool acquire() {
+    alive = alive && warp_wait_lane0(&sh.empty[stage], phase, &sh.abort);
+    if (!alive && (threadIdx.x & 31) == 0 && atomicExch(&sh.abort, 1) == 0) report(k.a.c.dev_err, kDevErrTimeout);
+    return alive;
+  }
+  __device__ __forceinline__ void advance() {
+    used |= 1u << stage;
+    if (++stage == C::kStages) stage = 0, phase ^= 1;
+  }
+  // Gave up: what is in flight lands before the CTA's memory goes.
+  __device__ __forceinline__ void drain() {
+    if (alive) return;
+    for (int st = 0; st < C::kStages; ++st) {
+      const uint32_t last = st < stage ? phase ^ 1 : phase;  // parity of the stage's last fill
+      if ((used >> st) & 1) mbar_wait(&sh.full[st], last, nullptr, 1000000ull);
+    }
+  }
+};
+
+// Every position below the length: a tile is a page, fetched by TMA.
+template <class C, int D, bool kFp8>
+__device__ void produce_pages(const Args& k, Shared& sh, Walk w, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                              uint32_t stages) {
+  const AttnArgs& a = k.a;
+  const CacheArgs& c = a.c;
+  constexpr int kRowsPerPage = cache_page_bytes<kFp8>(D) / C::kRow;
+  const int lane = threadIdx.x & 31;
+  Ring<C> ring{sh, k};
   while (w.next(a)) {
     const int req = row_request(c, w.row);
     const int head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
     const int len = table != nullptr ? a.seq_len[w.row] : 0;
-    int ids = 0, s0 = -1, s1 = -1;
-    if (a.pos != nullptr) {
-      const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + w.i0 * kTile;
-      s0 = w.i0 * kTile + lane < a.npos ? list[lane] : -1;
-      s1 = w.i0 * kTile + 32 + lane < a.npos ? list[32 + lane] : -1;
-    }
+    int ids = 0;
     for (int i = w.i0; i < w.i1; ++i) {
-      // ---- which positions, and where they are
-      uint32_t m0, m1;
-      int row0 = 0, row1 = 0, page = 0;
-      if (a.pos == nullptr) {
-        const int j = (i - w.i0) & 31;
-        if (j == 0) {  // the next 32 tiles' pages, one per lane
-          ids = -1;
-          if (i + lane < w.i1 && table != nullptr) ids = table[i + lane];
-        }
-        page = __shfl_sync(0xffffffffu, ids, j);
-        const bool ok = page >= 0 && page < c.num_pages;
-        if (!ok && lane == 0 && table != nullptr) report(c.dev_err, kDevErrPage);
-        const int left = ok ? len - i * kTile : 0;
-        m0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
-        m1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1 : 0;
-      } else {
-        const bool in0 = s0 >= 0 && s0 < len, in1 = s1 >= 0 && s1 < len;
-        if (table != nullptr && ((!in0 && s0 != -1) || (!in1 && s1 != -1))) report(c.dev_err, kDevErrPos);
-        const int p0 = in0 ? table[s0 / kPage] : 0, p1 = in1 ? table[s1 / kPage] : 0;
-        const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
-        if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
-        // a position that does not count fetches the pool's first row instead
-        row0 = ok0 ? (p0 * c.num_kv_heads + head) * kRowsPerPage + s0 % kPage : 0;
-        row1 = ok1 ? (p1 * c.num_kv_heads + head) * kRowsPerPage + s1 % kPage : 0;
-        m0 = __ballot_sync(0xffffffffu, ok0);
-        m1 = __ballot_sync(0xffffffffu, ok1);
-        if (i + 1 < w.i1) {  // the next tile's list entries
-          const int at = (i + 1) * kTile + lane;
-          const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
-          s0 = at < a.npos ? list[0] : -1;
-          s1 = at + 32 < a.npos ? list[32] : -1;
-        }
+      const int j = (i - w.i0) & 31;
+      if (j == 0) {  // the next 32 tiles' pages, one per lane
+        ids = -1;
+        if (i + lane < w.i1 && table != nullptr) ids = table[i + lane];
       }
-      // ---- the copies
-      alive = alive && warp_wait_lane0(&sh.empty[stage], phase, &sh.abort);
-      if (!alive) {
-        if (lane == 0) {
-          if (atomicExch(&sh.abort, 1) == 0) report(c.dev_err, kDevErrTimeout);
-        }
-      } else {
+      const int page = __shfl_sync(0xffffffffu, ids, j);
+      const bool ok = page >= 0 && page < c.num_pages;
+      if (!ok && lane == 0 && table != nullptr) report(c.dev_err, kDevErrPage);
+      const int left = ok ? len - i * kTile : 0;
+      const uint32_t m0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+      const uint32_t m1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1 : 0;
+      if (ring.acquire()) {
+        const int stage = ring.stage;
         const uint32_t bar = smem_u32(&sh.full[stage]);
         const uint32_t kdst = stages + stage * C::kStage, vdst = kdst + C::kMat;
         const uint32_t sdst = stages + C::kStages * C::kStage + stage * 2 * C::kScale;
-        const bool any = (m0 | m1) != 0;
-        const bool lists = a.pos != nullptr;
         if (lane == 0) {
           sh.mask[stage][0] = m0;
           sh.mask[stage][1] = m1;
-          if (any)
-            mbar_arrive_expect_tx(&sh.full[stage], lists ? C::kStage : C::kStage + 2 * C::kScale);
+          if (left > 0)
+            mbar_arrive_expect_tx(&sh.full[stage], C::kStage + 2 * C::kScale);
           else
             mbar_arrive(&sh.full[stage]);
         }
         __syncwarp();
-        if (any && !lists) {
+        if (left > 0) {
           const int row = (page * c.num_kv_heads + head) * kRowsPerPage;
           if (lane < 2 * C::kBoxes) {
             const int b = lane % C::kBoxes;
@@ -355,47 +340,110 @@ __device__ void produce(const Args& k, Shared& sh, Walk w, const CUtensorMap* km
             bulk_load(sdst + (lane - 16) * C::kScale, (lane == 16 ? c.k_pool : c.v_pool) + at, C::kScale, bar);
           }
         }
-        if (lists) {
-          if (any) {
-            // lanes 0..15 gather K, lanes 16..31 V, four positions each
-            const int g = lane & 15;
-            int r[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int x = __shfl_sync(0xffffffffu, row0, (4 * g + j) & 31);
-              const int y = __shfl_sync(0xffffffffu, row1, (4 * g + j) & 31);
-              r[j] = g < 8 ? x : y;
-            }
-            const uint32_t dst = (lane < 16 ? kdst : vdst) + g * 4 * C::kBox;
-#pragma unroll
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_gather4(dst + b * C::kSub, lane < 16 ? kmap : vmap, b * C::kBox, r[0], r[1], r[2], r[3], bar);
-            if (kFp8) {
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                if ((((hh ? m1 : m0) >> lane) & 1) == 0) continue;
-                const int row = hh ? row1 : row0, slot = row % kRowsPerPage;
-                const int64_t at = static_cast<int64_t>(row / kRowsPerPage) * cache_page_bytes<kFp8>(D) + kPage * D + slot * 4;
-                const uint32_t to = sdst + (hh * 32 + lane) * 4;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(c.k_pool + at) : "memory");
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + C::kScale), "l"(c.v_pool + at)
-                             : "memory");
-              }
-            }
-          }
-          if (kFp8) cp_async_arrive_noinc(&sh.full[stage]);
-        }
-        used |= 1u << stage;
       }
-      if (++stage == C::kStages) stage = 0, phase ^= 1;
+      ring.advance();
     }
   }
-  if (!alive) {  // gave up: what is in flight lands before the CTA's memory goes
-    for (int st = 0; st < C::kStages; ++st) {
-      const uint32_t last = st < stage ? phase ^ 1 : phase;  // parity of the stage's last fill
-      if ((used >> st) & 1) mbar_wait(&sh.full[st], last, nullptr, 1000000ull);
+  ring.drain();
+}
+
+// Listed positions: every row is copied by 16-byte asynchronous copies, its
+// chunks put where the TMA swizzle would have put them (a TMA gather of four
+// rows took 55 cycles of the SM's copy engine, 1.9 us per tile of 64 positions
+// in bf16; these copies pass through the load path instead).  Two tiles of
+// look-ahead: the list entries of the second next tile and the page ids of the
+// next one are on their way while a tile is copied.
+struct ListTile {
+  const int32_t* table;  // null: the row has no request
+  int head, len;
+  int s0, s1;  // the list's entries lane and 32 + lane of the tile
+  bool live;
+};
+
+template <class C, int D, bool kFp8>
+__device__ void produce_list(const Args& k, Shared& sh, Walk w, uint32_t stages) {
+  const AttnArgs& a = k.a;
+  const CacheArgs& c = a.c;
+  constexpr int64_t kPageBytes = cache_page_bytes<kFp8>(D);
+  constexpr int kChunks = C::kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows per warp and copy
+  const int lane = threadIdx.x & 31, chunk = lane % kChunks;
+  Ring<C> ring{sh, k};
+  int i = 0, end = 0;  // the next tile of the walk's segment
+  ListTile seg{nullptr, 0, 0, -1, -1, false};
+  auto fetch = [&]() {  // the next tile, its list entries under way
+    ListTile x{nullptr, 0, 0, -1, -1, false};
+    if (i >= end) {
+      if (!w.next(a)) return x;
+      i = w.i0, end = w.i1;
+      const int req = row_request(c, w.row);
+      seg.table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
+      seg.len = seg.table != nullptr ? a.seq_len[w.row] : 0;
+      seg.head = w.unit / k.l.blocks;
     }
+    x = seg;
+    x.live = true;
+    const int at = i * kTile + lane;
+    const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
+    if (at < a.npos) x.s0 = list[0];
+    if (at + 32 < a.npos) x.s1 = list[32];
+    ++i;
+    return x;
+  };
+  // page ids of a tile's entries (0 where an entry does not count)
+  auto look_up = [&](const ListTile& x, int& p0, int& p1) {
+    p0 = x.s0 >= 0 && x.s0 < x.len ? x.table[x.s0 / kPage] : 0;
+    p1 = x.s1 >= 0 && x.s1 < x.len ? x.table[x.s1 / kPage] : 0;
+  };
+  ListTile now = fetch(), next = fetch();
+  int p0, p1;
+  look_up(now, p0, p1);
+  while (now.live) {
+    int n0, n1;
+    look_up(next, n0, n1);
+    const ListTile after = fetch();
+    const bool in0 = now.s0 >= 0 && now.s0 < now.len, in1 = now.s1 >= 0 && now.s1 < now.len;
+    if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
+    const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
+    if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
+    const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
+    // byte offset of the (page, head), and the slot
+    const int64_t at0 = (static_cast<int64_t>(p0) * c.num_kv_heads + now.head) * kPageBytes;
+    const int64_t at1 = (static_cast<int64_t>(p1) * c.num_kv_heads + now.head) * kPageBytes;
+    const int64_t row0 = at0 + (now.s0 & (kPage - 1)) * C::kRow, row1 = at1 + (now.s1 & (kPage - 1)) * C::kRow;
+    if (ring.acquire()) {
+      const int stage = ring.stage;
+      const uint32_t kdst = stages + stage * C::kStage, vdst = kdst + C::kMat;
+      if (lane == 0) {
+        sh.mask[stage][0] = m0;
+        sh.mask[stage][1] = m1;
+      }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll 8
+        for (int r = 0; r < 32; r += kRows) {
+          const int src = r + lane / kChunks;
+          const int64_t row = __shfl_sync(0xffffffffu, hh ? row1 : row0, src) + chunk * 16;
+          if ((((hh ? m1 : m0) >> src) & 1) == 0) continue;
+          const uint32_t to = tile_offset<C>(hh * 32 + src, chunk);
+          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(kdst + to), "l"(c.k_pool + row) : "memory");
+          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(vdst + to), "l"(c.v_pool + row) : "memory");
+        }
+        if (kFp8 && (((hh ? m1 : m0) >> lane) & 1)) {
+          const int64_t at = (hh ? at1 : at0) + kPage * D + ((hh ? now.s1 : now.s0) & (kPage - 1)) * 4;
+          const uint32_t to = stages + C::kStages * C::kStage + stage * 2 * C::kScale + (hh * 32 + lane) * 4;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(c.k_pool + at) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + C::kScale), "l"(c.v_pool + at) : "memory");
+        }
+      }
+      cp_async_arrive_noinc(&sh.full[stage]);
+      if (lane == 0) mbar_arrive(&sh.full[stage]);  // the mask
+    }
+    ring.advance();
+    now = next;
+    next = after;
+    p0 = n0, p1 = n1;
   }
+  ring.drain();
 }
 
 // ------------------------------------------------------------------ consumers
@@ -732,7 +780,7 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh.full[s], kFp8 && a.pos != nullptr ? 33 : 1);
+      mbar_init(&sh.full[s], a.pos != nullptr ? 33 : 1);
       mbar_init(&sh.empty[s], WP * WH);
     }
     fence_mbar_init();
@@ -753,10 +801,12 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
   const Range r = sh.range;
   if (r.first < r.end) {
     Walk w{r.first, r.end, r.base, r.row, row_tiles(a, r.row), units, 0, 0, 0};
-    if (warp == WP * WH)
-      produce<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
-    else
+    if (warp != WP * WH)
       consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
+    else if (a.pos != nullptr)
+      produce_list<C, D, kFp8>(k, sh, w, base);
+    else
+      produce_pages<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
