@@ -167,6 +167,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// 16 bytes to shared memory, asynchronously: from src, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
 // The tiles of row t (0: nothing to read).
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int t) {
   const int len = a.seq_len[t];
@@ -366,7 +371,9 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk w, uint32_t stages)
   const CacheArgs& c = a.c;
   constexpr int64_t kPageBytes = cache_page_bytes<kFp8>(D);
   constexpr int kChunks = C::kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows per warp and copy
+  constexpr int kRowsPerPage = kPageBytes / C::kRow;
   const int lane = threadIdx.x & 31, chunk = lane % kChunks;
+  const uint8_t *kbase = c.k_pool + chunk * 16, *vbase = c.v_pool + chunk * 16;
   Ring<C> ring{sh, k};
   int i = 0, end = 0;  // the next tile of the walk's segment
   ListTile seg{nullptr, 0, 0, -1, -1, false};
@@ -406,30 +413,31 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk w, uint32_t stages)
     const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
     if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
     const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
-    // byte offset of the (page, head), and the slot
-    const int64_t at0 = (static_cast<int64_t>(p0) * c.num_kv_heads + now.head) * kPageBytes;
-    const int64_t at1 = (static_cast<int64_t>(p1) * c.num_kv_heads + now.head) * kPageBytes;
-    const int64_t row0 = at0 + (now.s0 & (kPage - 1)) * C::kRow, row1 = at1 + (now.s1 & (kPage - 1)) * C::kRow;
+    // rows of the pool (of kRow bytes); -1: zeros instead
+    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s0 & (kPage - 1)) : -1;
+    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s1 & (kPage - 1)) : -1;
     if (ring.acquire()) {
       const int stage = ring.stage;
-      const uint32_t kdst = stages + stage * C::kStage, vdst = kdst + C::kMat;
+      const uint32_t kdst = stages + stage * C::kStage;
       if (lane == 0) {
         sh.mask[stage][0] = m0;
         sh.mask[stage][1] = m1;
       }
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll 8
-        for (int r = 0; r < 32; r += kRows) {
-          const int src = r + lane / kChunks;
-          const int64_t row = __shfl_sync(0xffffffffu, hh ? row1 : row0, src) + chunk * 16;
-          if ((((hh ? m1 : m0) >> src) & 1) == 0) continue;
-          const uint32_t to = tile_offset<C>(hh * 32 + src, chunk);
-          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(kdst + to), "l"(c.k_pool + row) : "memory");
-          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(vdst + to), "l"(c.v_pool + row) : "memory");
-        }
-        if (kFp8 && (((hh ? m1 : m0) >> lane) & 1)) {
-          const int64_t at = (hh ? at1 : at0) + kPage * D + ((hh ? now.s1 : now.s0) & (kPage - 1)) * 4;
+      for (int p = 0; p < kTile; p += kRows) {  // positions p .. p + kRows - 1
+        const int row = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, (p + lane / kChunks) & 31);
+        const int64_t at = static_cast<int64_t>(max(row, 0)) * C::kRow;
+        const uint32_t to = kdst + tile_offset<C>(p + lane / kChunks, chunk);
+        copy16(to, kbase + at, row >= 0);
+        copy16(to + C::kMat, vbase + at, row >= 0);
+      }
+      if (kFp8) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int row = hh ? row1 : row0;
+          if (row < 0) continue;
+          const int64_t page = row / kRowsPerPage;
+          const int64_t at = page * kPageBytes + kPage * D + (row - page * kRowsPerPage) * 4;
           const uint32_t to = stages + C::kStages * C::kStage + stage * 2 * C::kScale + (hh * 32 + lane) * 4;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(c.k_pool + at) : "memory");
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + C::kScale), "l"(c.v_pool + at) : "memory");
@@ -611,7 +619,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, floa
             }
           }
         }
-        if (!kFp8 && !all) {  // a position that does not count: its value must not reach a product with 0
+        if (!kFp8 && !all && a.pos == nullptr) {  // what follows a row's last position must not reach a product with 0
           for (int e = lane; e < 16 * MT * (C::kRow / 16); e += 32) {
             const int p = p0 + e / (C::kRow / 16);
             if ((mask >> p) & 1) continue;
