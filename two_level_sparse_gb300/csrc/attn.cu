@@ -12,10 +12,13 @@ using attn::Part;
 
 constexpr int kJoinWarps = 16;
 
-Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+// Whether the kernel of attn_wide.cu takes the call.
+bool is_wide(const CacheArgs& c) { return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > 16; }
+
+Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, bool wide) {
   const int group = num_q_heads / num_kv_heads;
-  const int heads = group <= 8 ? 8 : group <= 16 ? 16 : group <= 32 ? 32 : 64;
-  return Layout{device_sm_count() * (head_dim == 256 ? 1 : 2), heads, (group + heads - 1) / heads, group};
+  const int heads = wide ? 64 : group <= 8 ? 8 : group <= 16 ? 16 : group <= 32 ? 32 : 64;
+  return Layout{device_sm_count() * (wide || head_dim == 256 ? 1 : 2), heads, (group + heads - 1) / heads, group};
 }
 
 // With the parts' maxima m_i, sums l_i and unnormalised sums o_i:
@@ -127,13 +130,19 @@ cudaError_t launch_join(const Args& k, cudaStream_t stream) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int32_t, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-  const Layout l = layout_of(num_q_heads, num_kv_heads, head_dim);
-  return part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.heads * head_dim * 4;
+  int64_t most = 0;  // either kernel may take the call: the cache's format is not known here
+  for (const bool wide : {false, true}) {
+    const Layout l = layout_of(num_q_heads, num_kv_heads, head_dim, wide);
+    const int64_t n = part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.heads * head_dim * 4;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   const CacheArgs& c = a.c;
-  Args k{a, layout_of(c.num_q_heads, c.num_kv_heads, c.head_dim), nullptr, nullptr, nullptr};
+  const bool wide = is_wide(c);
+  Args k{a, layout_of(c.num_q_heads, c.num_kv_heads, c.head_dim, wide), nullptr, nullptr, nullptr};
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   k.part = reinterpret_cast<Part*>(ws);
   k.stat = reinterpret_cast<float*>(ws + part_bytes(k.l));
@@ -144,7 +153,8 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
   if (e == cudaSuccess)
     e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
-  if (e == cudaSuccess) e = c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
+  if (e == cudaSuccess)
+    e = wide ? attn::launch_wide(kmap, vmap, k, stream) : c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
   if (e != cudaSuccess) return e;
   return c.head_dim == 64    ? launch_join<64>(k, stream)
          : c.head_dim == 128 ? launch_join<128>(k, stream)

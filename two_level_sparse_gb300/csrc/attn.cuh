@@ -172,14 +172,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool re
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 
-// The tiles of row t (0: nothing to read).
+// The tiles (of kT positions) of row t (0: nothing to read).
+template <int kT>
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int t) {
   const int len = a.seq_len[t];
   if (len <= 0 || len > a.max_len) return 0;
-  return ((a.pos != nullptr ? a.npos : len) + kTile - 1) / kTile;
+  return static_cast<int>(((a.pos != nullptr ? a.npos : len) + static_cast<int64_t>(kT) - 1) / kT);
 }
 
 // A CTA's way through the list: segment by segment (tiles [i0, i1) of a unit).
+template <int kT>
 struct Walk {
   int64_t x, end, base;  // next tile, end of the range, first tile of the row
   int row, n, units;     // n: tiles of the row
@@ -188,7 +190,7 @@ struct Walk {
     if (x >= end) return false;
     while (x >= base + static_cast<int64_t>(n) * units) {
       base += static_cast<int64_t>(n) * units;
-      n = row_tiles(a, ++row);
+      n = row_tiles<kT>(a, ++row);
     }
     const int64_t off = x - base;
     unit = static_cast<int>(off / n);
@@ -204,11 +206,15 @@ struct Range {
   int32_t row, ctas;  // ctas: how many share the list (every one of them has a tile)
 };
 
+struct RangeShared {
+  Range range;
+  int64_t warp_sum[16];
+};
+
 struct Shared {
   uint64_t full[8], empty[8];
   uint32_t mask[8][2];  // per stage: which of the 64 positions count
-  Range range;
-  int64_t warp_sum[9];
+  RangeShared r;
   int32_t abort;
 };
 static_assert(sizeof(Shared) <= 1024, "");
@@ -216,8 +222,8 @@ static_assert(sizeof(Shared) <= 1024, "");
 // The CTA's range of the list and the row it starts in: every thread adds up
 // a run of rows, a scan over the threads gives the total, and the thread whose
 // run holds the range's first tile walks to its row.
-template <int kThreads>
-__device__ void find_range(const Args& k, Shared& sh, int units) {
+template <int kThreads, int kT>
+__device__ void find_range(const Args& k, RangeShared& sh, int units) {
   const AttnArgs& a = k.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.rows + kThreads - 1) / kThreads;
@@ -226,7 +232,7 @@ __device__ void find_range(const Args& k, Shared& sh, int units) {
   for (int r = r0; r < r1; ++r) {
     const int len = a.seq_len[r];
     if (blockIdx.x == 0 && (len < 0 || len > a.max_len)) report(a.c.dev_err, kDevErrLen);
-    mine += row_tiles(a, r);
+    mine += row_tiles<kT>(a, r);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -252,7 +258,7 @@ __device__ void find_range(const Args& k, Shared& sh, int units) {
   if (first < end && at <= first && first < at + mine * units) {
     int r = r0;
     for (;; ++r) {
-      const int64_t n = static_cast<int64_t>(row_tiles(a, r)) * units;
+      const int64_t n = static_cast<int64_t>(row_tiles<kT>(a, r)) * units;
       if (first < at + n) break;
       at += n;
     }
@@ -260,6 +266,19 @@ __device__ void find_range(const Args& k, Shared& sh, int units) {
     sh.range.base = at;
   }
   __syncthreads();
+}
+
+// Rows with nothing to read.
+template <int D, int kThreads>
+__device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
+  for (int t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    if (row_tiles<kTile>(a, t) != 0) continue;
+    for (int e = threadIdx.x; e < a.c.num_q_heads * (D / 8); e += kThreads)
+      *reinterpret_cast<uint4*>(a.out + t * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int h = threadIdx.x; h < a.c.num_q_heads; h += kThreads)
+        a.lse[static_cast<int64_t>(t) * a.c.num_q_heads + h] = -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------ producers
@@ -294,7 +313,7 @@ struct Ring {
 
 // Every position below the length: a tile is a page, fetched by TMA.
 template <class C, int D, bool kFp8>
-__device__ void produce_pages(const Args& k, Shared& sh, Walk w, const CUtensorMap* kmap, const CUtensorMap* vmap,
+__device__ void produce_pages(const Args& k, Shared& sh, Walk<kTile> w, const CUtensorMap* kmap, const CUtensorMap* vmap,
                               uint32_t stages) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
@@ -366,7 +385,7 @@ struct ListTile {
 };
 
 template <class C, int D, bool kFp8>
-__device__ void produce_list(const Args& k, Shared& sh, Walk w, uint32_t stages) {
+__device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stages) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   constexpr int64_t kPageBytes = cache_page_bytes<kFp8>(D);
@@ -456,14 +475,14 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk w, uint32_t stages)
 
 // ------------------------------------------------------------------ consumers
 template <class C, int D, bool kFp8, int NT, int WP, int WH>
-__device__ void consume(const Args& k, Shared& sh, Walk w, uint32_t stages, float* acc, float* stat) {
+__device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stages, float* acc, float* stat) {
   constexpr int kM = D / 16, kK = D / 16, MT = 4 / WP;
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int wp = warp % WP, wh = warp / WP, p0 = wp * 16 * MT;
   const int tid = threadIdx.x;
   const float factor = a.scale * kLog2e;
-  const Range range = sh.range;
+  const Range range = sh.r.range;
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;
@@ -796,19 +815,11 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     k.part[blockIdx.x].last = -1;
   }
   const int units = a.c.num_kv_heads * k.l.blocks;
-  find_range<C::kThreads>(k, sh, units);
-  // rows with nothing to read
-  for (int t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    if (row_tiles(a, t) != 0) continue;
-    for (int e = tid; e < a.c.num_q_heads * (D / 8); e += C::kThreads)
-      *reinterpret_cast<uint4*>(a.out + t * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr)
-      for (int h = tid; h < a.c.num_q_heads; h += C::kThreads)
-        a.lse[static_cast<int64_t>(t) * a.c.num_q_heads + h] = -INFINITY;
-  }
-  const Range r = sh.range;
+  find_range<C::kThreads, kTile>(k, sh.r, units);
+  write_empty_rows<D, C::kThreads>(a);
+  const Range r = sh.r.range;
   if (r.first < r.end) {
-    Walk w{r.first, r.end, r.base, r.row, row_tiles(a, r.row), units, 0, 0, 0};
+    Walk<kTile> w{r.first, r.end, r.base, r.row, row_tiles<kTile>(a, r.row), units, 0, 0, 0};
     if (warp != WP * WH)
       consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
     else if (a.pos != nullptr)
@@ -860,6 +871,7 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
 
 cudaError_t launch_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s);
 cudaError_t launch_fp8(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s);
+cudaError_t launch_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s);  // attn_wide.cu
 
 }  // namespace attn
 }  // namespace ci
