@@ -183,27 +183,32 @@ __device__ __forceinline__ int row_tiles(const AttnArgs& a, int t) {
 // A CTA's way through the list: segment by segment (tiles [i0, i1) of a unit).
 template <int kT>
 struct Walk {
-  int64_t x, end, base;  // next tile, end of the range, first tile of the row
-  int row, n, units;     // n: tiles of the row
-  int unit, i0, i1;
+  int64_t x, end;                    // next tile of the list, end of the CTA's range
+  int row, unit, tile, n, units;     // where that is; n: tiles of the row
+  int i0, i1;
   __device__ __forceinline__ bool next(const AttnArgs& a) {
     if (x >= end) return false;
-    while (x >= base + static_cast<int64_t>(n) * units) {
-      base += static_cast<int64_t>(n) * units;
-      n = row_tiles<kT>(a, ++row);
+    if (tile == n) {
+      tile = 0;
+      if (++unit == units) {
+        unit = 0;
+        do n = row_tiles<kT>(a, ++row);
+        while (n == 0);
+      }
     }
-    const int64_t off = x - base;
-    unit = static_cast<int>(off / n);
-    i0 = static_cast<int>(off - static_cast<int64_t>(unit) * n);
+    i0 = tile;
     i1 = static_cast<int>(min(static_cast<int64_t>(n), i0 + (end - x)));
     x += i1 - i0;
+    tile = i1;
     return true;
   }
+  // The list's index of the segment's unit's last tile.
+  __device__ __forceinline__ int64_t last() const { return x - i1 + n - 1; }
 };
 
 struct Range {
-  int64_t first, end, base, total;
-  int32_t row, ctas;  // ctas: how many share the list (every one of them has a tile)
+  int64_t first, end, total;
+  int32_t row, unit, tile, ctas;  // where the range starts; how many share the list (every one has a tile)
 };
 
 struct RangeShared {
@@ -262,10 +267,34 @@ __device__ void find_range(const Args& k, RangeShared& sh, int units) {
       if (first < at + n) break;
       at += n;
     }
+    const int n = row_tiles<kT>(a, r);
     sh.range.row = r;
-    sh.range.base = at;
+    sh.range.unit = static_cast<int>((first - at) / n);
+    sh.range.tile = static_cast<int>((first - at) % n);
   }
   __syncthreads();
+}
+template <int kT>
+__device__ __forceinline__ Walk<kT> walk_of(const AttnArgs& a, const Range& r, int units) {
+  return Walk<kT>{r.first, r.end, r.row, r.unit, r.tile, row_tiles<kT>(a, r.row), units, 0, 0};
+}
+// What a CTA leaves behind for the unit that goes on past its range.
+template <int kT>
+__device__ __forceinline__ Part part_of(const Walk<kT>& w, const Range& r) {
+  return Part{w.row, w.unit, static_cast<int32_t>(((w.last() + 1) * r.ctas - 1) / r.total), 0};
+}
+
+// A bounded wait of a whole warp for phase `parity`; false once it, or another
+// warp of the CTA, has given up (reported once).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* dev_err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!ok && *static_cast<volatile int32_t*>(abort) == 0 && globaltimer_ns() - t0 < 2000000000ull)
+    ok = mbar_try_wait_sleep(bar, parity);
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok && (threadIdx.x & 31) == 0 && atomicExch(abort, 1) == 0) report(dev_err, kDevErrTimeout);
+  return ok;
 }
 
 // Rows with nothing to read.
@@ -293,8 +322,7 @@ struct Ring {
   bool alive = true;
 
   __device__ __forceinline__ bool acquire() {
-    alive = alive && warp_wait_lane0(&sh.empty[stage], phase, &sh.abort);
-    if (!alive && (threadIdx.x & 31) == 0 && atomicExch(&sh.abort, 1) == 0) report(k.a.c.dev_err, kDevErrTimeout);
+    alive = alive && wait_warp(&sh.empty[stage], phase, &sh.abort, k.a.c.dev_err);
     return alive;
   }
   __device__ __forceinline__ void advance() {
@@ -420,13 +448,18 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t 
     p0 = x.s0 >= 0 && x.s0 < x.len ? x.table[x.s0 / kPage] : 0;
     p1 = x.s1 >= 0 && x.s1 < x.len ? x.table[x.s1 / kPage] : 0;
   };
-  ListTile now = fetch(), next = fetch();
-  int p0, p1;
-  look_up(now, p0, p1);
-  while (now.live) {
+  ListTile now = seg, next = seg;
+  int p0 = 0, p1 = 0;
+  while (true) {
     int n0, n1;
     look_up(next, n0, n1);
     const ListTile after = fetch();
+    if (!now.live) {  // the pipeline fills, or is empty
+      if (!next.live && !after.live) break;
+      now = next, next = after;
+      p0 = n0, p1 = n1;
+      continue;
+    }
     const bool in0 = now.s0 >= 0 && now.s0 < now.len, in1 = now.s1 >= 0 && now.s1 < now.len;
     if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
     const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
@@ -544,10 +577,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
       l[nt][0] = l[nt][1] = 0.f;
     }
     for (int i = w.i0; i < w.i1; ++i) {
-      alive = alive && warp_wait_fast(&sh.full[stage], phase, &sh.abort);
-      if (!alive && lane == 0) {
-        if (atomicExch(&sh.abort, 1) == 0) report(a.c.dev_err, kDevErrTimeout);
-      }
+      alive = alive && wait_warp(&sh.full[stage], phase, &sh.abort, a.c.dev_err);
       const uint32_t kbase = stages + stage * C::kStage, vbase = kbase + C::kMat;
       const uint32_t sbase = stages + C::kStages * C::kStage + stage * 2 * C::kScale;
       const uint64_t mask = static_cast<uint64_t>(sh.mask[stage][1]) << 32 | sh.mask[stage][0];
@@ -784,10 +814,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         *reinterpret_cast<float4*>(dst + h * D + d) = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d);
       }
       if (tid == 0 && w.i0 == 0) {
-        // the CTA that holds the unit's last tile
-        const int64_t end = w.base + static_cast<int64_t>(w.unit + 1) * w.n - 1;
-        const int64_t last = ((end + 1) * range.ctas - 1) / range.total;
-        k.part[blockIdx.x] = Part{w.row, w.unit, static_cast<int32_t>(last), 0};
+        k.part[blockIdx.x] = part_of(w, range);
       }
     }
   }
@@ -819,7 +846,7 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
   write_empty_rows<D, C::kThreads>(a);
   const Range r = sh.r.range;
   if (r.first < r.end) {
-    Walk<kTile> w{r.first, r.end, r.base, r.row, row_tiles<kTile>(a, r.row), units, 0, 0, 0};
+    const Walk<kTile> w = walk_of<kTile>(a, r, units);
     if (warp != WP * WH)
       consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
     else if (a.pos != nullptr)

@@ -19,10 +19,12 @@
 // segment's end), so that one group's exponentials run beside the other's
 // products.  K and V tiles share a ring of five 32 KB slots.
 //
-// The reference m of a head is not the running maximum but stays until a logit
-// passes it by 2^8: probabilities are then at most 256, whose sums are as exact
-// as those of probabilities below one, and the cross-lane maxima and the
-// rescaling of O are needed for a segment's first tile and rarely after it.
+// The reference m of a head is not the running maximum but the logit of the
+// segment's first position, kept until another one passes it by 2^40.  fp32 and
+// bf16 have the exponents for that: probabilities up to 2^40 are as exact as
+// those below one, the reference's own is 1, and maxima across the positions
+// (across lanes, here) and the rescaling of O happen only where a logit is
+// further off.
 #include "attn.cuh"
 
 namespace ci {
@@ -34,12 +36,12 @@ constexpr int kSlots = 5, kSlot = kPos * kD * 2;
 constexpr int kPBytes = kPos * kH * 2, kQBytes = kH * kD * 2;
 constexpr int kWideThreads = 512;
 constexpr int kTmem = 256, kColS = 0, kColO = 128;  // S and O of softmax group w at + 64 w
-constexpr float kLowest = -3.0e38f;                 // a reference that every logit passes
-constexpr float kSlack = 8.f;
+constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
+constexpr float kSlack = 40.f;
 
 struct WideShared {
   uint64_t full[kSlots], empty[kSlots], s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain;
-  uint32_t mask[4][4];  // of the last four tiles: which positions count
+  alignas(16) uint32_t mask[4][4];  // of the last four tiles: which positions count
   alignas(16) float ref[2][kH], alpha[2][kH];  // read four at a time
   RangeShared r;
   uint32_t tmem;
@@ -60,11 +62,23 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t next) {
 __host__ __device__ constexpr uint32_t idesc(bool mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 3u << 15 : 0u) | ((kH >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// Eight products along the reduced dimension, issued by one lane: step j reads
+// the operands at a + A_j, b + B_j (in 16 bytes), with A_j = A1 (j % 4) + A4 (j / 4).
+template <int A1, int A4, int B1, int B4>
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %12;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %13;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %14;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(A1), "n"(2 * A1), "n"(3 * A1), "n"(A4), "n"(A4 + A1), "n"(A4 + 2 * A1),
+      "n"(A4 + 3 * A1), "n"(B1), "n"(2 * B1), "n"(3 * B1), "n"(B4), "n"(B4 + B1), "n"(B4 + 2 * B1), "n"(B4 + 3 * B1)
       : "memory");
 }
 __device__ __forceinline__ float warp_max(float v) {
@@ -82,48 +96,56 @@ __device__ __forceinline__ bool group_any(int id, bool mine) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
 }
-
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 struct Buffers {
   uint32_t slots, p, q;  // shared-memory addresses
-  __device__ __forceinline__ uint32_t slot(int64_t item) const { return slots + static_cast<int>(item % kSlots) * kSlot; }
 };
 using WideWalk = Walk<kPos>;
 
-// One wait of a role: false once anything has given up (reported once); the
-// role then goes on through its loop without touching memory.
+// One role's waits: false once anything has given up; the role then goes on
+// through its loop without touching memory.
 struct Waiter {
   WideShared& sh;
   int32_t* dev_err;
   bool alive = true;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
-    alive = alive && warp_wait_fast(bar, parity, &sh.abort);
-    if (!alive && (threadIdx.x & 31) == 0 && atomicExch(&sh.abort, 1) == 0) report(dev_err, kDevErrTimeout);
+    alive = alive && wait_warp(bar, parity, &sh.abort, dev_err);
     return alive;
   }
 };
-// Item n of the ring: its slot's empty barrier has completed n / kSlots phases.
-__device__ __forceinline__ bool acquire(Waiter& wait, WideShared& sh, int64_t item) {
-  return wait(&sh.empty[item % kSlots], ((item / kSlots) + 1) & 1);
-}
+// A role's place in the ring of slots: K and V of the tiles, in turn.
+struct Place {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int by = 1) {
+    slot += by;
+    if (slot >= kSlots) slot -= kSlots, phase ^= 1;
+  }
+};
 
 // ------------------------------------------------------------------ producers
-__device__ void wide_pages(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, const CUtensorMap* kmap,
-                           const CUtensorMap* vmap) {
+__device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWalk w, const Buffers& b,
+                                           const CUtensorMap* kmap, const CUtensorMap* vmap) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, c.dev_err};
-  int64_t tile = 0;
+  Place at_slot;
+  int tile = 0;
   while (w.next(a)) {
     const int req = row_request(c, w.row), head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
@@ -140,45 +162,42 @@ __device__ void wide_pages(const Args& k, WideShared& sh, WideWalk w, const Buff
         if (lo >= c.num_pages) lo = -1;
         if (hi >= c.num_pages) hi = -1;
       }
-      const int page[2] = {__shfl_sync(0xffffffffu, lo, j), __shfl_sync(0xffffffffu, hi, j)};
-      uint32_t m[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int left = page[x / 2] >= 0 ? len - i * kPos - x * 32 : 0;
-        m[x] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
-      }
-      const int pages = (page[0] >= 0) + (page[1] >= 0);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {  // K, then V
-        const int64_t item = 2 * tile + v;
-        if (!acquire(wait, sh, item)) continue;
-        uint64_t* bar = &sh.full[item % kSlots];
+      const int page0 = __shfl_sync(0xffffffffu, lo, j), page1 = __shfl_sync(0xffffffffu, hi, j);
+      const int pages = (page0 >= 0) + (page1 >= 0);
+      const int mine = lane & 2 ? page1 : page0;  // lane 0..3: page lane / 2, dims 64 (lane % 2) ..
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v, at_slot.advance()) {  // K, then V
+        uint64_t* bar = &sh.full[at_slot.slot];
+        if (!wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) continue;
+        if (v == 0 && lane < 4) {
+          const int left = (lane & 2 ? page1 : page0) >= 0 ? len - i * kPos - lane * 32 : 0;
+          sh.mask[tile & 3][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+        }
+        __syncwarp();
         if (lane == 0) {
-          if (v == 0) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) sh.mask[tile & 3][x] = m[x];
-          }
           if (pages > 0)
             mbar_arrive_expect_tx(bar, pages * (kSlot / 2));
           else
             mbar_arrive(bar);
         }
         __syncwarp();
-        if (lane < 4 && page[lane >> 1] >= 0)  // page lane / 2, dims 64 (lane % 2) ..
-          tma_box(b.slot(item) + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4), v == 0 ? kmap : vmap,
-                  (lane & 1) * 128, (page[lane >> 1] * c.num_kv_heads + head) * kPage, smem_u32(bar));
+        if (lane < 4 && mine >= 0)
+          tma_box(b.slots + at_slot.slot * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4), v == 0 ? kmap : vmap,
+                  (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(bar));
       }
     }
   }
   if (!wait.alive)  // what is in flight lands before the CTA's memory goes
-    for (int64_t item = max(2 * tile - kSlots, static_cast<int64_t>(0)); item < 2 * tile; ++item)
-      mbar_wait(&sh.full[item % kSlots], (item / kSlots) & 1, nullptr, 1000000ull);
+    for (int s = 0; s < kSlots; ++s) {
+      const uint32_t last = s < at_slot.slot ? at_slot.phase : at_slot.phase ^ 1;  // parity of the slot's last fill
+      if (2 * tile > s) mbar_wait(&sh.full[s], last, nullptr, 1000000ull);
+    }
 }
 
 // Warp `part` of four copies positions 32 part .. 32 part + 31 of every tile.
 // The entries of the second next tile and the page ids of the next one are on
 // their way while a tile is copied.
-__device__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, int part) {
+__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, int part) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
@@ -209,25 +228,30 @@ __device__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffe
     return x;
   };
   auto look_up = [&](const Entry& x) { return x.s >= 0 && x.s < x.len ? x.table[x.s / kPage] : 0; };
-  Entry now = fetch(), next = fetch();
-  int page = look_up(now);
-  for (int64_t tile = 0; now.live; ++tile) {
+  Entry now = seg, next = seg;
+  int page = 0, tile = 0;
+  Place at_slot;
+  while (true) {
     const int page_next = look_up(next);
     const Entry after = fetch();
+    if (!now.live) {  // the pipeline fills, or is empty
+      if (!next.live && !after.live) break;
+      now = next, next = after, page = page_next;
+      continue;
+    }
     const bool in = now.s >= 0 && now.s < now.len;
     if (now.table != nullptr && !in && now.s != -1) report(c.dev_err, kDevErrPos);
     const bool ok = in && page >= 0 && page < c.num_pages;
     if (ok != in) report(c.dev_err, kDevErrPage);
     const int row = ok ? (page * c.num_kv_heads + now.head) * kPage + (now.s & (kPage - 1)) : -1;
     const uint32_t m = __ballot_sync(0xffffffffu, ok);
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int64_t item = 2 * tile + v;
-      if (!acquire(wait, sh, item)) continue;
-      uint64_t* bar = &sh.full[item % kSlots];
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v, at_slot.advance()) {  // K, then V
+      if (!wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) continue;
+      uint64_t* bar = &sh.full[at_slot.slot];
       if (v == 0 && lane == 0) sh.mask[tile & 3][part] = m;
       const uint8_t* base = v == 0 ? kbase : vbase;
-      const uint32_t dst = b.slot(item) + (chunk >> 3) * (kSlot / 2) + part * 32 * 128;
+      const uint32_t dst = b.slots + at_slot.slot * kSlot + (chunk >> 3) * (kSlot / 2) + part * 32 * 128;
 #pragma unroll
       for (int p = 0; p < 32; p += 2) {  // positions p and p + 1
         const int at = p + odd, r = __shfl_sync(0xffffffffu, row, at);
@@ -236,14 +260,13 @@ __device__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffe
       cp_async_arrive_noinc(bar);
       if (lane == 0) mbar_arrive(bar);  // the mask
     }
-    now = next;
-    next = after;
-    page = page_next;
+    ++tile;
+    now = next, next = after, page = page_next;
   }
   cp_async_wait<0>();
 }
 
-__device__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Buffers& b) {
+__device__ __forceinline__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Buffers& b) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
   Waiter wait{sh, a.c.dev_err};
@@ -263,74 +286,69 @@ __device__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Bu
 }
 
 // ------------------------------------------------------------------ products
-__device__ void wide_mma(const Args& k, WideShared& sh, const WideWalk& w0, const Buffers& b, uint32_t tmem) {
+__device__ __forceinline__ void wide_mma(const Args& k, WideShared& sh, const WideWalk& w0, const Buffers& b, uint32_t tmem) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, a.c.dev_err};
-  // two walks over the same tiles: the products with K run up to two tiles ahead
+  // two walks over the same tiles: the products with K run two tiles ahead
   WideWalk ws = w0, wp = w0;
-  int s_i = 0, s_end = 0, seg = -1, p_i = 0, p_end = 0;
-  int64_t ts = 0, tp = 0, first = 0;  // next tiles; the first tile of the segment that tp is in
-  auto scores = [&]() {
-    bool start = false;
-    if (s_i >= s_end) {
-      if (!ws.next(a)) return;
-      s_i = ws.i0, s_end = ws.i1, ++seg, start = true;
-    }
-    const int64_t item = 2 * ts;
-    if (start) wait(&sh.q_full[seg & 1], (seg >> 1) & 1);
-    if (wait(&sh.full[item % kSlots], (item / kSlots) & 1)) {
-      fence_proxy_async_smem();  // queries and listed rows are written through the generic proxy
-      tc_fence_after();
-      const uint32_t kb = b.slot(item), qb = b.q + (seg & 1) * kQBytes, d = tmem + kColS + kH * static_cast<uint32_t>(ts & 1);
-#pragma unroll
-      for (int j = 0; j < kD / 16; ++j)
-        mma_elect(d, desc128(kb + (j >> 2) * (kSlot / 2) + (j & 3) * 32, 16),
-                  desc128(qb + (j >> 2) * (kQBytes / 2) + (j & 3) * 32, 16), idesc(false), j > 0);
-      mma_commit_elect(&sh.empty[item % kSlots]);
-      mma_commit_elect(&sh.s_full[ts & 1]);
-      if (s_i + 1 == s_end) mma_commit_elect(&sh.q_empty[seg & 1]);
-    }
-    ++s_i, ++ts;
-  };
-  scores();
-  scores();
-  while (true) {
-    if (p_i >= p_end) {
-      if (!wp.next(a)) break;
-      p_i = wp.i0, p_end = wp.i1, first = tp;
-    }
-    const int g = static_cast<int>(tp & 1);
-    const int64_t item = 2 * tp + 1;
-    wait(&sh.p_full[g], (tp >> 1) & 1);
-    if (wait(&sh.full[item % kSlots], (item / kSlots) & 1)) {
-      const uint32_t vb = b.slot(item), pb = b.p + g * kPBytes;
-      uint32_t m[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) m[x] = sh.mask[tp & 3][x];
-      if (a.pos == nullptr && (m[0] & m[1] & m[2] & m[3]) != ~0u) {
-        // values that do not count must not reach a product with 0
-        for (int e = lane; e < kPos * 16; e += 32) {
-          const int p = e >> 4, c = e & 15;
-          if ((sh.mask[tp & 3][p >> 5] >> (p & 31)) & 1) continue;
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16),
-                       "r"(0)
-                       : "memory");
+  int s_i = 0, s_end = 0, seg = -1, p_i = 0, p_end = 0, first = 0;  // first: the first tile of wp's segment
+  Place ks, vs{1, 0};
+  bool more = true;
+  for (int t = 0;; ++t) {
+    const int tp = t - 2;
+    if (tp >= 0) {
+      if (p_i >= p_end) {
+        if (!wp.next(a)) break;
+        p_i = wp.i0, p_end = wp.i1, first = tp;
+      }
+      const int g = tp & 1;
+      wait(&sh.p_full[g], (tp >> 1) & 1);
+      if (wait(&sh.full[vs.slot], vs.phase)) {
+        const uint32_t vb = b.slots + vs.slot * kSlot, pb = b.p + g * kPBytes;
+        if (a.pos == nullptr && (sh.mask[tp & 3][0] & sh.mask[tp & 3][1] & sh.mask[tp & 3][2] & sh.mask[tp & 3][3]) != ~0u) {
+          // values that do not count must not reach a product with 0
+#pragma unroll 1
+          for (int e = lane; e < kPos * 16; e += 32) {
+            const int p = e >> 4, c = e & 15;
+            if ((sh.mask[tp & 3][p >> 5] >> (p & 31)) & 1) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
         fence_proxy_async_smem();
-        __syncwarp();
+        tc_fence_after();
+        mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), tp > first + 1);
+        mma_commit_elect(&sh.empty[vs.slot]);
+        mma_commit_elect(&sh.pv_done[g]);
       }
-      fence_proxy_async_smem();
-      tc_fence_after();
-      const uint32_t d = tmem + kColO + kH * g;
-#pragma unroll
-      for (int j = 0; j < kPos / 16; ++j)
-        mma_elect(d, desc128(vb + j * 2048, kSlot / 2), desc128(pb + j * 2048, 16), idesc(true), tp > first + 1 || j > 0);
-      mma_commit_elect(&sh.empty[item % kSlots]);
-      mma_commit_elect(&sh.pv_done[g]);
+      vs.advance(2);
+      ++p_i;
     }
-    ++p_i, ++tp;
-    scores();
+    if (more) {
+      bool start = false;
+      if (s_i >= s_end) {
+        more = ws.next(a);
+        s_i = ws.i0, s_end = ws.i1, ++seg, start = true;
+      }
+      if (more) {
+        if (start) wait(&sh.q_full[seg & 1], (seg >> 1) & 1);
+        if (wait(&sh.full[ks.slot], ks.phase)) {
+          fence_proxy_async_smem();  // queries and listed rows are written through the generic proxy
+          tc_fence_after();
+          mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * (t & 1), desc128(b.slots + ks.slot * kSlot, 16),
+                                                       desc128(b.q + (seg & 1) * kQBytes, 16), idesc(false), 0);
+          mma_commit_elect(&sh.empty[ks.slot]);
+          mma_commit_elect(&sh.s_full[t & 1]);
+          if (s_i + 1 == s_end) mma_commit_elect(&sh.q_empty[seg & 1]);
+        }
+        ks.advance(2);
+        ++s_i;
+      }
+    }
   }
   if (!wait.alive) {  // the products in flight end before the CTA's memory goes
     mma_commit_elect(&sh.drain);
@@ -339,7 +357,18 @@ __device__ void wide_mma(const Args& k, WideShared& sh, const WideWalk& w0, cons
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, uint8_t* pmem, uint32_t tmem,
+// Halves the heads that a lane keeps and adds the partner's share of them.
+template <int kHalf, int kBit>
+__device__ __forceinline__ void fold(float (&l)[kH], int lane) {
+  const bool up = (lane & kBit) != 0;
+#pragma unroll
+  for (int j = 0; j < kHalf; ++j) {
+    const float give = up ? l[j] : l[j + kHalf];
+    l[j] = (up ? l[j + kHalf] : l[j]) + __shfl_xor_sync(0xffffffffu, give, kBit);
+  }
+}
+
+__device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, uint8_t* pmem, uint32_t tmem,
                              int g) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
@@ -349,16 +378,16 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
   float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][kH], while no product reads the probabilities
   float *ref = sh.ref[g], *alpha = sh.alpha[g];
   Waiter wait{sh, a.c.dev_err};
-  int64_t tile = 0;
+  int tile = 0;
   uint32_t mine = 0;  // tiles of this group so far
   while (w.next(a)) {
     const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
-    const int64_t end = tile + (w.i1 - w.i0);
+    const int end = tile + (w.i1 - w.i0);
     const bool had[2] = {tile + (tile & 1) < end, tile + 1 - (tile & 1) < end};  // whether group 0, 1 has a tile
     float l[kH];
 #pragma unroll
     for (int h = 0; h < kH; ++h) l[h] = 0.f;
-    bool begun = false;
+    bool begun = false, set = false;  // this group has had a tile; its references are set
     for (; tile < end; ++tile) {
       if ((tile & 1) != g) continue;
       float s[kH];
@@ -371,7 +400,17 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
         tmem_ld32(tmem + lanes + kColS + kH * g + 32, hi);
         tmem_ld_wait();
       }
-      const bool valid = (sh.mask[tile & 3][quad] >> lane) & 1;
+      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[tile & 3]);
+      const bool valid = ((quad == 0 ? m.x : quad == 1 ? m.y : quad == 2 ? m.z : m.w) >> lane) & 1;
+      if (!set && (m.x | m.y | m.z | m.w) != 0) {  // the first position's logits
+        const int first = m.x ? __ffs(m.x) - 1 : m.y ? 31 + __ffs(m.y) : m.z ? 63 + __ffs(m.z) : 95 + __ffs(m.w);
+        if (row == first) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) ref[h] = fmaxf(fminf(s[h] * factor, kFar), -kFar);
+        }
+        named_sync(1 + g, 128);
+        set = true;
+      }
       float over = -INFINITY;
 #pragma unroll
       for (int h = 0; h < kH; h += 4) {
@@ -382,40 +421,39 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
       const bool raise = group_any(1 + g, valid && over > kSlack);
       if (mine > 0) wait(&sh.pv_done[g], (mine - 1) & 1);  // the probabilities' buffer is free, O is complete
       if (raise) {
-        float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < kH; h += 4) {  // (rare: short code rather than fast)
+          uint32_t x[4];
+          tmem_ld4(tmem + lanes + kColS + kH * g + h, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const float r = warp_max(valid ? s[h] * factor : -INFINITY);
-          if (lane == (h & 31)) most[h >> 5] = r;
+          for (int j = 0; j < 4; ++j) {
+            const float r = warp_max(valid ? __uint_as_float(x[j]) * factor : -INFINITY);
+            if (lane == 0) scratch[quad * kH + h + j] = r;
+          }
         }
-        scratch[quad * kH + lane] = most[0];
-        scratch[quad * kH + 32 + lane] = most[1];
         named_sync(1 + g, 128);
         if (row < kH) {
           const float old = ref[row];
-          float m = old;
+          float top = old;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) m = fmaxf(m, scratch[x * kH + row]);
-          alpha[row] = exp2_approx(old - m);
-          ref[row] = m;
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, scratch[x * kH + row]);
+          alpha[row] = exp2_approx(old - top);
+          ref[row] = top;
         }
         named_sync(1 + g, 128);
 #pragma unroll
-        for (int h = 0; h < kH; h += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(alpha + h);
-          l[h] *= f.x, l[h + 1] *= f.y, l[h + 2] *= f.z, l[h + 3] *= f.w;
-        }
+        for (int h = 0; h < kH; ++h) l[h] *= alpha[h];
         if (begun) {
           tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t o[32];
-            const uint32_t at = tmem + lanes + kColO + kH * g + 32 * x;
-            tmem_ld32(at, o);
+#pragma unroll 1
+          for (int h = 0; h < kH; h += 8) {
+            uint32_t o[8];
+            tmem_ld8(tmem + lanes + kColO + kH * g + h, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[32 * x + h]);
-            tmem_st32(at, o);
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[h + j]);
+            tmem_st8(tmem + lanes + kColO + kH * g + h, o);
           }
           tmem_st_wait();
         }
@@ -445,16 +483,11 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
     // ---- the segment's end: sums over the positions, the two groups joined
     if (begun) wait(&sh.pv_done[g], (mine - 1) & 1);
     tc_fence_after();
-    // each step halves the heads that a lane keeps and adds the partner's share
-#pragma unroll
-    for (int half = kH / 2, bit = 16; bit > 0; half >>= 1, bit >>= 1) {
-      const bool up = lane & bit;
-#pragma unroll
-      for (int j = 0; j < half; ++j) {
-        const float keep = up ? l[j + half] : l[j], give = up ? l[j] : l[j + half];
-        l[j] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
-      }
-    }
+    fold<32, 16>(l, lane);
+    fold<16, 8>(l, lane);
+    fold<8, 4>(l, lane);
+    fold<4, 2>(l, lane);
+    fold<2, 1>(l, lane);
     // lane bits 16, 8, 4, 2, 1 chose heads + 32, 16, 8, 4, 2
     *reinterpret_cast<float2*>(scratch + quad * kH + 2 * lane) = make_float2(l[0], l[1]);
     named_sync(3, 256);
@@ -467,7 +500,7 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
       for (int x = 0; x < 2; ++x) {
         const float* sc = reinterpret_cast<const float*>(pmem + x * kPBytes);
         sum[x] = had[x] ? (sc[h] + sc[kH + h]) + (sc[2 * kH + h] + sc[3 * kH + h]) : 0.f;
-        m[x] = had[x] ? sh.ref[x][h] : kLowest;
+        m[x] = sum[x] != 0.f ? sh.ref[x][h] : -kFar;
       }
       const float top = fmaxf(m[0], m[1]), f0 = exp2_approx(m[0] - top), f1 = exp2_approx(m[1] - top);
       const float total = sum[0] * f0 + sum[1] * f1;
@@ -487,36 +520,28 @@ __device__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Bu
     tc_fence_after();
     // group g writes heads 32 g .. 32 g + 31; a thread holds one dim
     {
-      float o[32];
-#pragma unroll
-      for (int h = 0; h < 32; ++h) o[h] = 0.f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!had[x]) continue;
-        uint32_t v[32];
-        tmem_ld32(tmem + lanes + kColO + kH * x + 32 * g, v);
+      uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD + row;
+      float* sum = k.sum + slot * kH * kD + row;
+#pragma unroll 1
+      for (int h = 32 * g; h < 32 * g + 32 && h < live; h += 8) {
+        uint32_t v[2][8];
+        tmem_ld8(tmem + lanes + kColO + h, v[0]);
+        tmem_ld8(tmem + lanes + kColO + kH + h, v[1]);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 32; ++h) o[h] = fmaf(__uint_as_float(v[h]), sh.alpha[x][32 * g + h], o[h]);
-      }
-      if (whole) {
-        uint16_t* dst = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0 + 32 * g) * kD + row;
-#pragma unroll
-        for (int h = 0; h < 32; ++h)
-          if (32 * g + h < live) dst[h * kD] = __bfloat16_as_ushort(__float2bfloat16_rn(o[h]));
-      } else {
-        float* dst = k.sum + (slot * kH + 32 * g) * kD + row;
-#pragma unroll
-        for (int h = 0; h < 32; ++h)
-          if (32 * g + h < live) dst[h * kD] = o[h];
+        for (int j = 0; j < 8; ++j) {
+          float o = 0.f;
+          if (had[0]) o = __uint_as_float(v[0][j]) * sh.alpha[0][h + j];
+          if (had[1]) o = fmaf(__uint_as_float(v[1][j]), sh.alpha[1][h + j], o);
+          if (h + j >= live) break;
+          if (whole)
+            out[(h + j) * kD] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+          else
+            sum[(h + j) * kD] = o;
+        }
       }
     }
-    if (g == 0 && row == 0 && !whole && w.i0 == 0) {
-      // the CTA that holds the unit's last tile
-      const int64_t last = w.base + static_cast<int64_t>(w.unit + 1) * w.n - 1;
-      k.part[blockIdx.x] = Part{w.row, w.unit, static_cast<int32_t>(((last + 1) * range.ctas - 1) / range.total), 0};
-    }
-    if (row < kH) ref[row] = kLowest;
+    if (g == 0 && row == 0 && !whole && w.i0 == 0) k.part[blockIdx.x] = part_of(w, range);
     tc_fence_before();
     named_sync(3, 256);  // O, the factors and the scratch have been read
   }
@@ -551,7 +576,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     sh.abort = 0;
     k.part[blockIdx.x].last = -1;
   }
-  if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = kLowest;
+  if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
   const int units = a.c.num_kv_heads * k.l.blocks;
   find_range<kWideThreads, kPos>(k, sh.r, units);
@@ -560,7 +585,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const Range r = sh.r.range;
   const uint32_t tmem = sh.tmem;
   if (r.first < r.end) {
-    const WideWalk w{r.first, r.end, r.base, r.row, row_tiles<kPos>(a, r.row), units, 0, 0, 0};
+    const WideWalk w = walk_of<kPos>(a, r, units);
     if (warp < 8) {
       regs_dec<64>();
       if (warp == 0 && a.pos == nullptr) wide_pages(k, sh, w, b, &kmap, &vmap);

@@ -7,9 +7,7 @@
 namespace ci {
 
 // The request of row t; -1 (reported) where the row starts name none.
-__device__ __forceinline__ int row_request(const CacheArgs& c, int t) {
-  if (c.layout == kLayoutDecode) return t;
-  if (c.layout == kLayoutPrefill) return 0;
+static __device__ __noinline__ int row_request_varlen(const CacheArgs& c, int t) {
   int lo = 0, hi = c.num_req;  // the last r with req_start[r] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -21,6 +19,9 @@ __device__ __forceinline__ int row_request(const CacheArgs& c, int t) {
   if (c.req_start[lo] <= t && t < c.req_start[lo + 1]) return lo;
   report(c.dev_err, kDevErrReq);
   return -1;
+}
+__device__ __forceinline__ int row_request(const CacheArgs& c, int t) {
+  return c.layout == kLayoutDecode ? t : c.layout == kLayoutPrefill ? 0 : row_request_varlen(c, t);
 }
 
 template <bool kFp8>
