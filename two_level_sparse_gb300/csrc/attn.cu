@@ -18,7 +18,7 @@ bool is_wide(const CacheArgs& c) { return !c.fp8 && c.head_dim == 128 && c.num_q
 Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, bool wide) {
   const int group = num_q_heads / num_kv_heads;
   const int heads = wide ? 64 : group <= 8 ? 8 : group <= 16 ? 16 : group <= 32 ? 32 : 64;
-  return Layout{device_sm_count() * (wide || head_dim == 256 ? 1 : 2), heads, (group + heads - 1) / heads, group};
+  return Layout{device_sm_count() * (head_dim == 256 ? 1 : 2), heads, (group + heads - 1) / heads, group};
 }
 
 // With the parts' maxima m_i, sums l_i and unnormalised sums o_i:
@@ -150,7 +150,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   const int row = c.fp8 ? c.head_dim : 2 * c.head_dim;
   const int per_page = static_cast<int>((c.fp8 ? cache_page_bytes<true>(c.head_dim) : cache_page_bytes<false>(c.head_dim)) / row);
   CUtensorMap kmap, vmap;
-  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
+  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, c.num_pages * c.num_kv_heads * per_page, row, a.pos != nullptr ? 1 : attn::kTile);
   if (e == cudaSuccess)
     e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
   if (e == cudaSuccess)

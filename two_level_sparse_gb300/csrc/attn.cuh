@@ -11,9 +11,8 @@
 // statistics in the workspace (two parts per CTA at most), and the join kernel
 // adds them in order.
 //
-// A tile.  One producer warp fetches K and V into a ring of stages, pages by TMA
-// (128-byte swizzled rows), or, for listed positions, by 16-byte asynchronous
-// copies of their rows.  WP x WH consumer warps compute, WP
+// A tile.  A producer warp fetches K and V into a ring of stages, pages by TMA
+// (128-byte swizzled rows); listed positions take two (produce_list).  WP x WH consumer warps compute, WP
 // along the positions and WH along the heads:
 //   S^T = K Q^T   A = K from shared memory (ldmatrix), B = Q in registers;
 //   online softmax per head, a column of S^T: its maximum over the warp's
@@ -49,7 +48,7 @@ struct Part {  // the unit that goes on past the end of a CTA's range; last < 0:
   int32_t row, unit, last, pad;
 };
 struct Layout {
-  int32_t ctas;      // CTAs that share the list of tiles
+  int32_t ctas;      // workers (CTAs, or halves of them) that share the list of tiles
   int32_t heads;     // query heads of a unit, padded (HB)
   int32_t blocks;    // head blocks per key-value head
   int32_t group;     // query heads per key-value head
@@ -83,7 +82,7 @@ struct Config {
   static_assert(kStages >= 2, "a ring needs two stages");
   static constexpr int kSmem = 1024 + kStages * (kStage + 2 * kScale) + kAcc + kStat + kMisc;
   static constexpr int kConsumers = 32 * WP * WH;
-  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kThreads = kConsumers + 64;  // and two producer warps
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -161,6 +160,16 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(map), "r"(x), "r"(row), "r"(bar)
       : "memory");
 }
+// Four rows (one box row each) to consecutive rows at dst; issued by one lane of a converged warp.
+__device__ __forceinline__ void gather4_elect(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                              uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -170,6 +179,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // 16 bytes to shared memory, asynchronously: from src, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool read) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async4_to(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // The tiles (of kT positions) of row t (0: nothing to read).
@@ -211,29 +224,31 @@ struct Range {
   int32_t row, unit, tile, ctas;  // where the range starts; how many share the list (every one has a tile)
 };
 
+template <int N>
 struct RangeShared {
-  Range range;
+  Range range[N];
   int64_t warp_sum[16];
 };
 
 struct Shared {
   uint64_t full[8], empty[8];
   uint32_t mask[8][2];  // per stage: which of the 64 positions count
-  RangeShared r;
+  RangeShared<1> r;
   int32_t abort;
 };
 static_assert(sizeof(Shared) <= 1024, "");
 
-// The CTA's range of the list and the row it starts in: every thread adds up
-// a run of rows, a scan over the threads gives the total, and the thread whose
-// run holds the range's first tile walks to its row.
-template <int kThreads, int kT>
-__device__ void find_range(const Args& k, RangeShared& sh, int units) {
+// The ranges of the list of workers blockIdx.x + i gridDim.x, i < N, and where
+// they start: every thread adds up a run of rows, a scan over the threads gives
+// the total, and the thread whose run holds a range's first tile walks to it.
+template <int kThreads, int kT, int N>
+__device__ __forceinline__ void find_ranges(const Args& k, RangeShared<N>& sh, int units) {
   const AttnArgs& a = k.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.rows + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
   int64_t mine = 0;
+#pragma unroll 4
   for (int r = r0; r < r1; ++r) {
     const int len = a.seq_len[r];
     if (blockIdx.x == 0 && (len < 0 || len > a.max_len)) report(a.c.dev_err, kDevErrLen);
@@ -254,29 +269,33 @@ __device__ void find_range(const Args& k, RangeShared& sh, int units) {
     total += sh.warp_sum[w];
   }
   total *= units;
-  const int64_t ctas = min(static_cast<int64_t>(k.l.ctas), total);
-  const int64_t first = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-  const int64_t end = blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
-  if (tid == 0)
-    sh.range.first = first, sh.range.end = end, sh.range.total = total, sh.range.ctas = static_cast<int32_t>(ctas);
-  int64_t at = before * units;
-  if (first < end && at <= first && first < at + mine * units) {
-    int r = r0;
-    for (;; ++r) {
-      const int64_t n = static_cast<int64_t>(row_tiles<kT>(a, r)) * units;
-      if (first < at + n) break;
-      at += n;
+  const int64_t workers = min(static_cast<int64_t>(k.l.ctas), total);
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
+    const int64_t worker = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+    const int64_t first = worker < workers ? worker * total / workers : total;
+    const int64_t end = worker < workers ? (worker + 1) * total / workers : total;
+    Range& range = sh.range[i];
+    if (tid == 0) range.first = first, range.end = end, range.total = total, range.ctas = static_cast<int32_t>(workers);
+    int64_t at = before * units;
+    if (first < end && at <= first && first < at + mine * units) {
+      int r = r0;
+      for (;; ++r) {
+        const int64_t n = static_cast<int64_t>(row_tiles<kT>(a, r)) * units;
+        if (first < at + n) break;
+        at += n;
+      }
+      const int n = row_tiles<kT>(a, r);
+      range.row = r;
+      range.unit = static_cast<int>((first - at) / n);
+      range.tile = static_cast<int>((first - at) % n);
     }
-    const int n = row_tiles<kT>(a, r);
-    sh.range.row = r;
-    sh.range.unit = static_cast<int>((first - at) / n);
-    sh.range.tile = static_cast<int>((first - at) % n);
   }
   __syncthreads();
 }
 template <int kT>
 __device__ __forceinline__ Walk<kT> walk_of(const AttnArgs& a, const Range& r, int units) {
-  return Walk<kT>{r.first, r.end, r.row, r.unit, r.tile, row_tiles<kT>(a, r.row), units, 0, 0};
+  return Walk<kT>{r.first, r.end, r.row, r.unit, r.tile, r.first < r.end ? row_tiles<kT>(a, r.row) : 0, units, 0, 0};
 }
 // What a CTA leaves behind for the unit that goes on past its range.
 template <int kT>
@@ -399,12 +418,14 @@ __device__ void produce_pages(const Args& k, Shared& sh, Walk<kTile> w, const CU
   ring.drain();
 }
 
-// Listed positions: every row is copied by 16-byte asynchronous copies, its
-// chunks put where the TMA swizzle would have put them (a TMA gather of four
-// rows took 55 cycles of the SM's copy engine, 1.9 us per tile of 64 positions
-// in bf16; these copies pass through the load path instead).  Two tiles of
-// look-ahead: the list entries of the second next tile and the page ids of the
-// next one are on their way while a tile is copied.
+// Listed positions, by two warps side by side: one gathers K, four rows per TMA
+// instruction; the other copies V by 16-byte asynchronous copies, its chunks put
+// where the TMA swizzle would have put them, and the FP8 scales.  (Alone, one
+// warp issues 18 and 22 bytes per ns and SM of 256-byte rows, and copies beyond
+// what the load path keeps in flight delay the consumers' shared-memory
+// accesses; the two ways do not share a path.)  Two tiles of look-ahead: the
+// list entries of the second next tile and the page ids of the next one are on
+// their way while a tile is copied.
 struct ListTile {
   const int32_t* table;  // null: the row has no request
   int head, len;
@@ -412,15 +433,14 @@ struct ListTile {
   bool live;
 };
 
-template <class C, int D, bool kFp8>
-__device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stages) {
+template <class C, int D, bool kFp8, bool kValues>
+__device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUtensorMap* kmap, uint32_t stages) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   constexpr int64_t kPageBytes = cache_page_bytes<kFp8>(D);
   constexpr int kChunks = C::kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows per warp and copy
   constexpr int kRowsPerPage = kPageBytes / C::kRow;
   const int lane = threadIdx.x & 31, chunk = lane % kChunks;
-  const uint8_t *kbase = c.k_pool + chunk * 16, *vbase = c.v_pool + chunk * 16;
   Ring<C> ring{sh, k};
   int i = 0, end = 0;  // the next tile of the walk's segment
   ListTile seg{nullptr, 0, 0, -1, -1, false};
@@ -443,67 +463,79 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t 
     ++i;
     return x;
   };
-  // page ids of a tile's entries (0 where an entry does not count)
-  auto look_up = [&](const ListTile& x, int& p0, int& p1) {
-    p0 = x.s0 >= 0 && x.s0 < x.len ? x.table[x.s0 / kPage] : 0;
-    p1 = x.s1 >= 0 && x.s1 < x.len ? x.table[x.s1 / kPage] : 0;
-  };
   ListTile now = seg, next = seg;
   int p0 = 0, p1 = 0;
   while (true) {
-    int n0, n1;
-    look_up(next, n0, n1);
+    // page ids of the next tile's entries (0 where an entry does not count)
+    const int n0 = next.s0 >= 0 && next.s0 < next.len ? next.table[next.s0 / kPage] : 0;
+    const int n1 = next.s1 >= 0 && next.s1 < next.len ? next.table[next.s1 / kPage] : 0;
     const ListTile after = fetch();
     if (!now.live) {  // the pipeline fills, or is empty
       if (!next.live && !after.live) break;
-      now = next, next = after;
-      p0 = n0, p1 = n1;
+      now = next, next = after, p0 = n0, p1 = n1;
       continue;
     }
     const bool in0 = now.s0 >= 0 && now.s0 < now.len, in1 = now.s1 >= 0 && now.s1 < now.len;
-    if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
     const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
-    if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
-    const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
-    // rows of the pool (of kRow bytes); -1: zeros instead
-    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s0 & (kPage - 1)) : -1;
-    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s1 & (kPage - 1)) : -1;
+    if (!kValues) {
+      if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
+      if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
+    }
+    // rows of the pool (of kRow bytes); an entry that does not count: row 0 of K, zeros of V
+    const int none = kValues ? -1 : 0;
+    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s0 & (kPage - 1)) : none;
+    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s1 & (kPage - 1)) : none;
     if (ring.acquire()) {
       const int stage = ring.stage;
       const uint32_t kdst = stages + stage * C::kStage;
-      if (lane == 0) {
-        sh.mask[stage][0] = m0;
-        sh.mask[stage][1] = m1;
-      }
-#pragma unroll
-      for (int p = 0; p < kTile; p += kRows) {  // positions p .. p + kRows - 1
-        const int row = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, (p + lane / kChunks) & 31);
-        const int64_t at = static_cast<int64_t>(max(row, 0)) * C::kRow;
-        const uint32_t to = kdst + tile_offset<C>(p + lane / kChunks, chunk);
-        copy16(to, kbase + at, row >= 0);
-        copy16(to + C::kMat, vbase + at, row >= 0);
-      }
-      if (kFp8) {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int row = hh ? row1 : row0;
-          if (row < 0) continue;
-          const int64_t page = row / kRowsPerPage;
-          const int64_t at = page * kPageBytes + kPage * D + (row - page * kRowsPerPage) * 4;
-          const uint32_t to = stages + C::kStages * C::kStage + stage * 2 * C::kScale + (hh * 32 + lane) * 4;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(c.k_pool + at) : "memory");
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + C::kScale), "l"(c.v_pool + at) : "memory");
+      if constexpr (!kValues) {
+        const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
+        if (lane == 0) {
+          sh.mask[stage][0] = m0;
+          sh.mask[stage][1] = m1;
+          mbar_arrive_expect_tx(&sh.full[stage], C::kMat);
         }
+        __syncwarp();
+        const uint32_t bar = smem_u32(&sh.full[stage]);
+#pragma unroll 2
+        for (int p = 0; p < kTile; p += 4) {
+          const int mine = p < 32 ? row0 : row1;
+          const int r0 = __shfl_sync(0xffffffffu, mine, p & 31), r1 = __shfl_sync(0xffffffffu, mine, (p & 31) + 1);
+          const int r2 = __shfl_sync(0xffffffffu, mine, (p & 31) + 2), r3 = __shfl_sync(0xffffffffu, mine, (p & 31) + 3);
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b)
+            gather4_elect(kdst + b * C::kSub + p * C::kBox, kmap, b * C::kBox, r0, r1, r2, r3, bar);
+        }
+      } else {
+        const uint8_t* vbase = c.v_pool + chunk * 16;
+#pragma unroll
+        for (int p = 0; p < kTile; p += kRows) {  // positions p .. p + kRows - 1
+          const int row = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, (p + lane / kChunks) & 31);
+          copy16(kdst + C::kMat + tile_offset<C>(p + lane / kChunks, chunk),
+                 vbase + static_cast<int64_t>(max(row, 0)) * C::kRow, row >= 0);
+        }
+        if (kFp8) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int row = hh ? row1 : row0;
+            if (row < 0) continue;
+            const int64_t page = row / kRowsPerPage;
+            const int64_t at = page * kPageBytes + kPage * D + (row - page * kRowsPerPage) * 4;
+            const uint32_t to = stages + C::kStages * C::kStage + stage * 2 * C::kScale + (hh * 32 + lane) * 4;
+            cp_async4_to(to, c.k_pool + at);
+            cp_async4_to(to + C::kScale, c.v_pool + at);
+          }
+        }
+        cp_async_arrive_noinc(&sh.full[stage]);
       }
-      cp_async_arrive_noinc(&sh.full[stage]);
-      if (lane == 0) mbar_arrive(&sh.full[stage]);  // the mask
     }
     ring.advance();
-    now = next;
-    next = after;
-    p0 = n0, p1 = n1;
+    now = next, next = after, p0 = n0, p1 = n1;
   }
-  ring.drain();
+  if (kValues)
+    cp_async_wait<0>();
+  else
+    ring.drain();
 }
 
 // ------------------------------------------------------------------ consumers
@@ -515,7 +547,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
   const int wp = warp % WP, wh = warp / WP, p0 = wp * 16 * MT;
   const int tid = threadIdx.x;
   const float factor = a.scale * kLog2e;
-  const Range range = sh.r.range;
+  const Range range = sh.r.range[0];
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;
@@ -842,16 +874,18 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     k.part[blockIdx.x].last = -1;
   }
   const int units = a.c.num_kv_heads * k.l.blocks;
-  find_range<C::kThreads, kTile>(k, sh.r, units);
+  find_ranges<C::kThreads, kTile, 1>(k, sh.r, units);
   write_empty_rows<D, C::kThreads>(a);
-  const Range r = sh.r.range;
+  const Range r = sh.r.range[0];
   if (r.first < r.end) {
     const Walk<kTile> w = walk_of<kTile>(a, r, units);
-    if (warp != WP * WH)
+    if (warp < WP * WH)
       consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
+    else if (a.pos != nullptr && warp == WP * WH)
+      produce_list<C, D, kFp8, false>(k, sh, w, &kmap, base);
     else if (a.pos != nullptr)
-      produce_list<C, D, kFp8>(k, sh, w, base);
-    else
+      produce_list<C, D, kFp8, true>(k, sh, w, &kmap, base);
+    else if (warp == WP * WH)
       produce_pages<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

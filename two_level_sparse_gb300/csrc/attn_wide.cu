@@ -13,11 +13,11 @@
 //   O^T [128 dims x 64 heads] += V^T P^T      A = V and B = P with the positions
 //                                             as the reduced rows (MN-major), O in tensor memory
 //
-// One CTA per SM, 16 warps: TMA producer, MMA issuer, query loader, four warps
-// that copy listed rows, and two groups of four softmax warps that take tiles
-// in turn, each with its own reference maxima, sums and O (joined at the
-// segment's end), so that one group's exponentials run beside the other's
-// products.  K and V tiles share a ring of five 32 KB slots.
+// One CTA per SM, two workers per CTA: each has its own range of the list, a
+// group of four softmax warps, references, sums and O, so that one's
+// exponentials and results run beside the other's products.  The workers' tiles
+// alternate in one ring of five 32 KB slots (K, V, K, V, ...) and before one
+// MMA-issuing warp.  Per worker one warp loads queries and two fetch K and V.
 //
 // The reference m of a head is not the running maximum but the logit of the
 // segment's first position, kept until another one passes it by 2^40.  fp32 and
@@ -35,15 +35,16 @@ constexpr int kD = 128, kH = 64, kPos = 128;
 constexpr int kSlots = 5, kSlot = kPos * kD * 2;
 constexpr int kPBytes = kPos * kH * 2, kQBytes = kH * kD * 2;
 constexpr int kWideThreads = 512;
-constexpr int kTmem = 256, kColS = 0, kColO = 128;  // S and O of softmax group w at + 64 w
+constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256;  // S, O and the sums of worker g at + 64 g
 constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
 constexpr float kSlack = 40.f;
 
 struct WideShared {
   uint64_t full[kSlots], empty[kSlots], s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain;
   alignas(16) uint32_t mask[4][4];  // of the last four tiles: which positions count
-  alignas(16) float ref[2][kH], alpha[2][kH];  // read four at a time
-  RangeShared r;
+  uint32_t ends[4];                 // bit 0: a segment's first tile, bit 1: its last one
+  alignas(16) float ref[2][kH], alpha[2][kH];
+  RangeShared<2> r;
   uint32_t tmem;
   int32_t abort;
 };
@@ -106,6 +107,23 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -127,38 +145,43 @@ struct Waiter {
     return alive;
   }
 };
-// A role's place in the ring of slots: K and V of the tiles, in turn.
+// A role's place in the ring: item 2 t is K of tile t, item 2 t + 1 its V; tile
+// t is worker (t % 2)'s tile t / 2.  (Where one worker has a tile more than the
+// other, the last tile's number has a gap before it; nothing follows that.)
 struct Place {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void advance(int by = 1) {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ explicit Place(int item) : slot(item), phase(0) {}
+  __device__ __forceinline__ void advance(int by) {
     slot += by;
     if (slot >= kSlots) slot -= kSlots, phase ^= 1;
   }
 };
 
 // ------------------------------------------------------------------ producers
+// Worker g's pages, by TMA: a tile is two pages.
 __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWalk w, const Buffers& b,
-                                           const CUtensorMap* kmap, const CUtensorMap* vmap) {
+                                           const CUtensorMap* kmap, const CUtensorMap* vmap, int g) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, c.dev_err};
-  Place at_slot;
-  int tile = 0;
+  Place at_slot(2 * g);
+  int tile = g;
   while (w.next(a)) {
     const int req = row_request(c, w.row), head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
     const int len = table != nullptr ? a.seq_len[w.row] : 0;
     int lo = -1, hi = -1;
-    for (int i = w.i0; i < w.i1; ++i, ++tile) {
+    for (int i = w.i0; i < w.i1; ++i, tile += 2) {
       const int j = (i - w.i0) & 31;
       if (j == 0) {  // the next 32 tiles' pages, two per lane
         const int64_t at = static_cast<int64_t>(i + lane) * kPos;
-        lo = at < len ? table[at / kPage] : -1;
-        hi = at + kPage < len ? table[at / kPage + 1] : -1;
-        const bool bad = (at < len && (lo < 0 || lo >= c.num_pages)) || (at + kPage < len && (hi < 0 || hi >= c.num_pages));
-        if (bad && i + lane < w.i1) report(c.dev_err, kDevErrPage);
+        const bool in = i + lane < w.i1;
+        lo = in && at < len ? table[at / kPage] : -1;
+        hi = in && at + kPage < len ? table[at / kPage + 1] : -1;
+        if (in && ((at < len && (lo < 0 || lo >= c.num_pages)) || (at + kPage < len && (hi < 0 || hi >= c.num_pages))))
+          report(c.dev_err, kDevErrPage);
         if (lo >= c.num_pages) lo = -1;
         if (hi >= c.num_pages) hi = -1;
       }
@@ -166,52 +189,62 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
       const int pages = (page0 >= 0) + (page1 >= 0);
       const int mine = lane & 2 ? page1 : page0;  // lane 0..3: page lane / 2, dims 64 (lane % 2) ..
 #pragma unroll 1
-      for (int v = 0; v < 2; ++v, at_slot.advance()) {  // K, then V
+      for (int v = 0; v < 2; ++v) {  // K, then V
         uint64_t* bar = &sh.full[at_slot.slot];
-        if (!wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) continue;
-        if (v == 0 && lane < 4) {
-          const int left = (lane & 2 ? page1 : page0) >= 0 ? len - i * kPos - lane * 32 : 0;
-          sh.mask[tile & 3][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+        if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
+          if (v == 0 && lane < 4) {
+            const int left = mine >= 0 ? len - i * kPos - lane * 32 : 0;
+            sh.mask[tile & 3][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+            if (lane == 0) sh.ends[tile & 3] = (i == w.i0) | (i + 1 == w.i1) << 1;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (pages > 0)
+              mbar_arrive_expect_tx(bar, pages * (kSlot / 2));
+            else
+              mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (lane < 4 && mine >= 0)
+            tma_box(b.slots + at_slot.slot * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4),
+                    v == 0 ? kmap : vmap, (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(bar));
         }
-        __syncwarp();
-        if (lane == 0) {
-          if (pages > 0)
-            mbar_arrive_expect_tx(bar, pages * (kSlot / 2));
-          else
-            mbar_arrive(bar);
-        }
-        __syncwarp();
-        if (lane < 4 && mine >= 0)
-          tma_box(b.slots + at_slot.slot * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4), v == 0 ? kmap : vmap,
-                  (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(bar));
+        at_slot.advance(v == 0 ? 1 : 3);
       }
     }
   }
-  if (!wait.alive)  // what is in flight lands before the CTA's memory goes
-    for (int s = 0; s < kSlots; ++s) {
-      const uint32_t last = s < at_slot.slot ? at_slot.phase : at_slot.phase ^ 1;  // parity of the slot's last fill
-      if (2 * tile > s) mbar_wait(&sh.full[s], last, nullptr, 1000000ull);
-    }
+  if (!wait.alive) {  // what is in flight lands before the CTA's memory goes: this worker's last two tiles
+    Place p(2 * g);
+    for (int x = g; x < tile; x += 2)
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        if (x + 4 >= tile) mbar_wait(&sh.full[p.slot], p.phase, nullptr, 1000000ull);
+        p.advance(v == 0 ? 1 : 3);
+      }
+  }
 }
 
-// Warp `part` of four copies positions 32 part .. 32 part + 31 of every tile.
+// Worker g's listed rows: warp `part` of two fetches positions 64 part .. 64 part
+// + 63 of every tile, K by TMA gathers and V by 16-byte asynchronous copies
+// (produce_list in attn.cuh says why).  Both warps take the ring's items in
+// order, so neither is ever a whole turn of the ring ahead of the consumers.
 // The entries of the second next tile and the page ids of the next one are on
 // their way while a tile is copied.
-__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, int part) {
+__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b,
+                                          const CUtensorMap* kmap, int g, int part) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
-  const uint8_t *kbase = c.k_pool + chunk * 16, *vbase = c.v_pool + chunk * 16;
   Waiter wait{sh, c.dev_err};
   struct Entry {
     const int32_t* table;  // null: the row has no request
-    int head, len, s;
+    int head, len, s0, s1, ends;
     bool live;
   };
   int i = 0, end = 0;
-  Entry seg{nullptr, 0, 0, -1, false};
+  Entry seg{nullptr, 0, 0, -1, -1, 0, false};
   auto fetch = [&]() {
-    Entry x{nullptr, 0, 0, -1, false};
+    Entry x{nullptr, 0, 0, -1, -1, 0, false};
     if (i >= end) {
       if (!w.next(a)) return x;
       i = w.i0, end = w.i1;
@@ -222,133 +255,165 @@ __device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWal
     }
     x = seg;
     x.live = true;
-    const int at = i * kPos + part * 32 + lane;
-    if (at < a.npos) x.s = a.pos[static_cast<int64_t>(w.row) * a.pos_stride + at];
+    x.ends = (i == w.i0) | (i + 1 == w.i1) << 1;
+    const int at = i * kPos + part * 64 + lane;
+    const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
+    if (at < a.npos) x.s0 = list[0];
+    if (at + 32 < a.npos) x.s1 = list[32];
     ++i;
     return x;
   };
-  auto look_up = [&](const Entry& x) { return x.s >= 0 && x.s < x.len ? x.table[x.s / kPage] : 0; };
   Entry now = seg, next = seg;
-  int page = 0, tile = 0;
-  Place at_slot;
+  int p0 = 0, p1 = 0, tile = g;
+  Place at_slot(2 * g);
   while (true) {
-    const int page_next = look_up(next);
+    const int n0 = next.s0 >= 0 && next.s0 < next.len ? next.table[next.s0 / kPage] : 0;
+    const int n1 = next.s1 >= 0 && next.s1 < next.len ? next.table[next.s1 / kPage] : 0;
     const Entry after = fetch();
     if (!now.live) {  // the pipeline fills, or is empty
       if (!next.live && !after.live) break;
-      now = next, next = after, page = page_next;
+      now = next, next = after, p0 = n0, p1 = n1;
       continue;
     }
-    const bool in = now.s >= 0 && now.s < now.len;
-    if (now.table != nullptr && !in && now.s != -1) report(c.dev_err, kDevErrPos);
-    const bool ok = in && page >= 0 && page < c.num_pages;
-    if (ok != in) report(c.dev_err, kDevErrPage);
-    const int row = ok ? (page * c.num_kv_heads + now.head) * kPage + (now.s & (kPage - 1)) : -1;
-    const uint32_t m = __ballot_sync(0xffffffffu, ok);
-#pragma unroll 1
-    for (int v = 0; v < 2; ++v, at_slot.advance()) {  // K, then V
-      if (!wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) continue;
+    const bool in0 = now.s0 >= 0 && now.s0 < now.len, in1 = now.s1 >= 0 && now.s1 < now.len;
+    if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
+    const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
+    if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
+    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kPage + (now.s0 & (kPage - 1)) : -1;
+    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kPage + (now.s1 & (kPage - 1)) : -1;
+    const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
+    // ---- K: an entry that does not count fetches row 0
+    if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
       uint64_t* bar = &sh.full[at_slot.slot];
-      if (v == 0 && lane == 0) sh.mask[tile & 3][part] = m;
-      const uint8_t* base = v == 0 ? kbase : vbase;
-      const uint32_t dst = b.slots + at_slot.slot * kSlot + (chunk >> 3) * (kSlot / 2) + part * 32 * 128;
-#pragma unroll
-      for (int p = 0; p < 32; p += 2) {  // positions p and p + 1
-        const int at = p + odd, r = __shfl_sync(0xffffffffu, row, at);
+      const uint32_t dst = b.slots + at_slot.slot * kSlot + part * 64 * 128;
+      if (lane == 0) {
+        sh.mask[tile & 3][2 * part] = m0;
+        sh.mask[tile & 3][2 * part + 1] = m1;
+        if (part == 0) sh.ends[tile & 3] = now.ends;
+        mbar_arrive_expect_tx(bar, kSlot / 2);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int p = 0; p < 64; p += 4) {
+        const int mine = max(p < 32 ? row0 : row1, 0);
+        const int r0 = __shfl_sync(0xffffffffu, mine, p & 31), r1 = __shfl_sync(0xffffffffu, mine, (p & 31) + 1);
+        const int r2 = __shfl_sync(0xffffffffu, mine, (p & 31) + 2), r3 = __shfl_sync(0xffffffffu, mine, (p & 31) + 3);
+        gather4_elect(dst + p * 128, kmap, 0, r0, r1, r2, r3, smem_u32(bar));
+        gather4_elect(dst + kSlot / 2 + p * 128, kmap, 128, r0, r1, r2, r3, smem_u32(bar));
+      }
+      mbar_arrive(bar);
+    }
+    at_slot.advance(1);
+    // ---- V: zeros for it
+    if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
+      uint64_t* bar = &sh.full[at_slot.slot];
+      const uint32_t dst = b.slots + at_slot.slot * kSlot + (chunk >> 3) * (kSlot / 2) + part * 64 * 128;
+      const uint8_t* base = c.v_pool + chunk * 16;
+#pragma unroll 4
+      for (int p = 0; p < 64; p += 2) {  // positions p and p + 1
+        const int at = p + odd, r = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, at & 31);
         copy16(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4), base + static_cast<int64_t>(max(r, 0)) * (kD * 2), r >= 0);
       }
       cp_async_arrive_noinc(bar);
-      if (lane == 0) mbar_arrive(bar);  // the mask
+      if (lane == 0) mbar_arrive(bar);
     }
-    ++tile;
-    now = next, next = after, page = page_next;
+    at_slot.advance(3);
+    tile += 2;
+    now = next, next = after, p0 = n0, p1 = n1;
   }
   cp_async_wait<0>();
+  if (!wait.alive) {  // what is in flight lands before the CTA's memory goes: the last two tiles' K
+    Place p(2 * g);
+    for (int x = g; x < tile; x += 2) {
+      if (x + 4 >= tile) mbar_wait(&sh.full[p.slot], p.phase, nullptr, 1000000ull);
+      p.advance(4);
+    }
+  }
 }
 
-__device__ __forceinline__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Buffers& b) {
+// Worker g's queries, one segment's after the last product with the one's before.
+__device__ __forceinline__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, int g) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
   Waiter wait{sh, a.c.dev_err};
-  for (int seg = 0; w.next(a); ++seg) {
+  const uint32_t dst = b.q + g * kQBytes + (chunk >> 3) * (kQBytes / 2);
+  for (uint32_t seg = 0; w.next(a); ++seg) {
     const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
     const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + w.row * a.q_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD) + chunk * 16;
-    if (!wait(&sh.q_empty[seg & 1], ((seg >> 1) + 1) & 1)) continue;
-    const uint32_t dst = b.q + (seg & 1) * kQBytes + (chunk >> 3) * (kQBytes / 2);
-#pragma unroll 8
+    if (!wait(&sh.q_empty[g], (seg + 1) & 1)) continue;
+#pragma unroll 4
     for (int p = 0; p < kH; p += 2) {
       const int h = p + odd;
       copy16(dst + h * 128 + (((chunk & 7) ^ (h & 7)) << 4), src + (h < live ? h : 0) * (kD * 2), h < live);
     }
-    cp_async_arrive_noinc(&sh.q_full[seg & 1]);
+    cp_async_arrive_noinc(&sh.q_full[g]);
   }
   cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ void wide_mma(const Args& k, WideShared& sh, const WideWalk& w0, const Buffers& b, uint32_t tmem) {
+// Step t: the product with V of tile t - 2, then the one with K of tile t.
+__device__ __forceinline__ void wide_mma(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, a.c.dev_err};
-  // two walks over the same tiles: the products with K run two tiles ahead
-  WideWalk ws = w0, wp = w0;
-  int s_i = 0, s_end = 0, seg = -1, p_i = 0, p_end = 0, first = 0;  // first: the first tile of wp's segment
-  Place ks, vs{1, 0};
-  bool more = true;
-  for (int t = 0;; ++t) {
-    const int tp = t - 2;
-    if (tp >= 0) {
-      if (p_i >= p_end) {
-        if (!wp.next(a)) break;
-        p_i = wp.i0, p_end = wp.i1, first = tp;
-      }
-      const int g = tp & 1;
-      wait(&sh.p_full[g], (tp >> 1) & 1);
-      if (wait(&sh.full[vs.slot], vs.phase)) {
-        const uint32_t vb = b.slots + vs.slot * kSlot, pb = b.p + g * kPBytes;
-        if (a.pos == nullptr && (sh.mask[tp & 3][0] & sh.mask[tp & 3][1] & sh.mask[tp & 3][2] & sh.mask[tp & 3][3]) != ~0u) {
-          // values that do not count must not reach a product with 0
+  const int n0 = static_cast<int>(sh.r.range[0].end - sh.r.range[0].first);
+  const int n1 = static_cast<int>(sh.r.range[1].end - sh.r.range[1].first);
+  const int steps = 2 * max(n0, n1) + 2;
+  Place ks(0), vs(1);
+  uint32_t seg[2] = {0, 0};  // segments begun
+  for (int t = 0; t < steps; ++t) {
+    const int g = t & 1;  // of both tiles
+    if (t >= 2) {
+      const int tp = t - 2;
+      if ((tp >> 1) < (g ? n1 : n0)) {
+        wait(&sh.p_full[g], (tp >> 1) & 1);
+        if (wait(&sh.full[vs.slot], vs.phase)) {
+          const uint32_t vb = b.slots + vs.slot * kSlot, pb = b.p + g * kPBytes;
+          const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[tp & 3]);
+          if (a.pos == nullptr && (m.x & m.y & m.z & m.w) != ~0u) {
+            // values that do not count must not reach a product with 0
 #pragma unroll 1
-          for (int e = lane; e < kPos * 16; e += 32) {
-            const int p = e >> 4, c = e & 15;
-            if ((sh.mask[tp & 3][p >> 5] >> (p & 31)) & 1) continue;
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16),
-                         "r"(0)
-                         : "memory");
+            for (int e = lane; e < kPos * 16; e += 32) {
+              const int p = e >> 4, c = e & 15;
+              if ((sh.mask[tp & 3][p >> 5] >> (p & 31)) & 1) continue;
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16),
+                           "r"(0)
+                           : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
+          const uint32_t more = (sh.ends[tp & 3] & 1) ^ 1;  // adds to the segment's earlier tiles
           fence_proxy_async_smem();
-          __syncwarp();
+          tc_fence_after();
+          mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), more);
+          mma_commit_elect(&sh.empty[vs.slot]);
+          mma_commit_elect(&sh.pv_done[g]);
         }
-        fence_proxy_async_smem();
-        tc_fence_after();
-        mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), tp > first + 1);
-        mma_commit_elect(&sh.empty[vs.slot]);
-        mma_commit_elect(&sh.pv_done[g]);
       }
       vs.advance(2);
-      ++p_i;
     }
-    if (more) {
-      bool start = false;
-      if (s_i >= s_end) {
-        more = ws.next(a);
-        s_i = ws.i0, s_end = ws.i1, ++seg, start = true;
-      }
-      if (more) {
-        if (start) wait(&sh.q_full[seg & 1], (seg >> 1) & 1);
-        if (wait(&sh.full[ks.slot], ks.phase)) {
+    if ((t >> 1) < (g ? n1 : n0)) {
+      if (wait(&sh.full[ks.slot], ks.phase)) {
+        const uint32_t ends = sh.ends[t & 3];
+        if (ends & 1) {
+          const uint32_t s = g ? seg[1] : seg[0];
+          wait(&sh.q_full[g], s & 1);
+          (g ? seg[1] : seg[0]) = s + 1;
+        }
+        if (wait.alive) {
           fence_proxy_async_smem();  // queries and listed rows are written through the generic proxy
           tc_fence_after();
-          mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * (t & 1), desc128(b.slots + ks.slot * kSlot, 16),
-                                                       desc128(b.q + (seg & 1) * kQBytes, 16), idesc(false), 0);
+          mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * g, desc128(b.slots + ks.slot * kSlot, 16),
+                                                       desc128(b.q + g * kQBytes, 16), idesc(false), 0);
           mma_commit_elect(&sh.empty[ks.slot]);
-          mma_commit_elect(&sh.s_full[t & 1]);
-          if (s_i + 1 == s_end) mma_commit_elect(&sh.q_empty[seg & 1]);
+          mma_commit_elect(&sh.s_full[g]);
+          if (ends & 2) mma_commit_elect(&sh.q_empty[g]);
         }
-        ks.advance(2);
-        ++s_i;
       }
     }
+    ks.advance(2);
   }
   if (!wait.alive) {  // the products in flight end before the CTA's memory goes
     mma_commit_elect(&sh.drain);
@@ -357,14 +422,19 @@ __device__ __forceinline__ void wide_mma(const Args& k, WideShared& sh, const Wi
 }
 
 // ------------------------------------------------------------------ softmax
+// S, the sums and O are read from tensor memory half of the heads at a time, in
+// loops that are not unrolled: with every role's code straight-line, the roles
+// together outgrew the instruction cache, and a row of 512 positions (four tiles)
+// took twice as long.
+//
 // Halves the heads that a lane keeps and adds the partner's share of them.
 template <int kHalf, int kBit>
-__device__ __forceinline__ void fold(float (&l)[kH], int lane) {
+__device__ __forceinline__ void fold(uint32_t (&l)[32], int lane) {
   const bool up = (lane & kBit) != 0;
 #pragma unroll
   for (int j = 0; j < kHalf; ++j) {
-    const float give = up ? l[j] : l[j + kHalf];
-    l[j] = (up ? l[j + kHalf] : l[j]) + __shfl_xor_sync(0xffffffffu, give, kBit);
+    const uint32_t give = up ? l[j] : l[j + kHalf], keep = up ? l[j + kHalf] : l[j];
+    l[j] = __float_as_uint(__uint_as_float(keep) + __uint_as_float(__shfl_xor_sync(0xffffffffu, give, kBit)));
   }
 }
 
@@ -372,63 +442,61 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
                              int g) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kH * g;  // this warp's, at the worker's columns
   const float factor = a.scale * kLog2e;
-  const Range range = sh.r.range;
+  const Range range = sh.r.range[g];
   float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][kH], while no product reads the probabilities
   float *ref = sh.ref[g], *alpha = sh.alpha[g];
+  const int worker = blockIdx.x + g * gridDim.x;
   Waiter wait{sh, a.c.dev_err};
-  int tile = 0;
-  uint32_t mine = 0;  // tiles of this group so far
+  uint32_t mine = 0;  // tiles so far: the CTA's tile 2 mine + g
   while (w.next(a)) {
     const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
-    const int end = tile + (w.i1 - w.i0);
-    const bool had[2] = {tile + (tile & 1) < end, tile + 1 - (tile & 1) < end};  // whether group 0, 1 has a tile
-    float l[kH];
-#pragma unroll
-    for (int h = 0; h < kH; ++h) l[h] = 0.f;
-    bool begun = false, set = false;  // this group has had a tile; its references are set
-    for (; tile < end; ++tile) {
-      if ((tile & 1) != g) continue;
-      float s[kH];
+    bool set = false;  // whether there are references
+    for (int i = w.i0; i < w.i1; ++i) {
       wait(&sh.s_full[g], mine & 1);
       tc_fence_after();
-      {
-        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
-        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
-        tmem_ld32(tmem + lanes + kColS + kH * g, lo);
-        tmem_ld32(tmem + lanes + kColS + kH * g + 32, hi);
-        tmem_ld_wait();
-      }
-      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[tile & 3]);
+      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[(2 * mine + g) & 3]);
       const bool valid = ((quad == 0 ? m.x : quad == 1 ? m.y : quad == 2 ? m.z : m.w) >> lane) & 1;
       if (!set && (m.x | m.y | m.z | m.w) != 0) {  // the first position's logits
         const int first = m.x ? __ffs(m.x) - 1 : m.y ? 31 + __ffs(m.y) : m.z ? 63 + __ffs(m.z) : 95 + __ffs(m.w);
-        if (row == first) {
+#pragma unroll 1
+        for (int h = 0; h < kH; h += 8) {
+          uint32_t s[8];
+          tmem_ld8(lanes + kColS + h, s);
+          tmem_ld_wait();
+          if (row == first) {
 #pragma unroll
-          for (int h = 0; h < kH; ++h) ref[h] = fmaxf(fminf(s[h] * factor, kFar), -kFar);
+            for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(__uint_as_float(s[j]) * factor, kFar), -kFar);
+          }
         }
         named_sync(1 + g, 128);
         set = true;
       }
       float over = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < kH; h += 32) {
+        uint32_t s[32];
+        tmem_ld32(lanes + kColS + h, s);
+        tmem_ld_wait();
 #pragma unroll
-      for (int h = 0; h < kH; h += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(ref + h);
-        over = fmaxf(over, fmaxf(fmaf(s[h], factor, -r.x), fmaf(s[h + 1], factor, -r.y)));
-        over = fmaxf(over, fmaxf(fmaf(s[h + 2], factor, -r.z), fmaf(s[h + 3], factor, -r.w)));
+        for (int j = 0; j < 32; j += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(ref + h + j);
+          over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j]), factor, -r.x), fmaf(__uint_as_float(s[j + 1]), factor, -r.y)));
+          over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j + 2]), factor, -r.z), fmaf(__uint_as_float(s[j + 3]), factor, -r.w)));
+        }
       }
       const bool raise = group_any(1 + g, valid && over > kSlack);
       if (mine > 0) wait(&sh.pv_done[g], (mine - 1) & 1);  // the probabilities' buffer is free, O is complete
       if (raise) {
 #pragma unroll 1
-        for (int h = 0; h < kH; h += 4) {  // (rare: short code rather than fast)
+        for (int h = 0; h < kH; h += 4) {
           uint32_t x[4];
-          tmem_ld4(tmem + lanes + kColS + kH * g + h, x);
+          tmem_ld4(lanes + kColS + h, x);
           tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 4; ++j) {
-            const float r = warp_max(valid ? __uint_as_float(x[j]) * factor : -INFINITY);
+            const float r = warp_max(valid ? __uint_as_float(j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3]) * factor : -INFINITY);
             if (lane == 0) scratch[quad * kH + h + j] = r;
           }
         }
@@ -442,108 +510,115 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
           ref[row] = top;
         }
         named_sync(1 + g, 128);
-#pragma unroll
-        for (int h = 0; h < kH; ++h) l[h] *= alpha[h];
-        if (begun) {
+        if (i > w.i0) {  // what the segment has so far
           tc_fence_after();
 #pragma unroll 1
-          for (int h = 0; h < kH; h += 8) {
+          for (int h = 0; h < 2 * kH; h += 8) {
             uint32_t o[8];
-            tmem_ld8(tmem + lanes + kColO + kH * g + h, o);
+            const uint32_t at = lanes + (h < kH ? kColO + h : kColL + h - kH);
+            tmem_ld8(at, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[h + j]);
-            tmem_st8(tmem + lanes + kColO + kH * g + h, o);
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[(h & (kH - 1)) + j]);
+            tmem_st8(at, o);
           }
           tmem_st_wait();
         }
       }
       uint8_t* prow = pmem + g * kPBytes + row * 128;
+#pragma unroll 1
+      for (int h = 0; h < kH; h += 32) {
+        uint32_t s[32], l[32];
+        tmem_ld32(lanes + kColS + h, s);
+        tmem_ld32(lanes + kColL + h, l);
+        tmem_ld_wait();
+        const bool fresh = i == w.i0;
 #pragma unroll
-      for (int h = 0; h < kH; h += 8) {
-        uint32_t v[4];
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t v[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 r = *reinterpret_cast<const float2*>(ref + h + 2 * x);
-          float p0 = exp2_approx(fmaf(s[h + 2 * x], factor, -r.x)), p1 = exp2_approx(fmaf(s[h + 2 * x + 1], factor, -r.y));
-          if (!valid) p0 = p1 = 0.f;
-          l[h + 2 * x] += p0;
-          l[h + 2 * x + 1] += p1;
-          v[x] = bf16x2(p0, p1);
+          for (int x = 0; x < 8; x += 2) {
+            const float2 r = *reinterpret_cast<const float2*>(ref + h + j + x);
+            float p0 = exp2_approx(fmaf(__uint_as_float(s[j + x]), factor, -r.x));
+            float p1 = exp2_approx(fmaf(__uint_as_float(s[j + x + 1]), factor, -r.y));
+            if (!valid) p0 = p1 = 0.f;
+            v[x / 2] = bf16x2(p0, p1);
+            l[j + x] = __float_as_uint(fresh ? p0 : __uint_as_float(l[j + x]) + p0);
+            l[j + x + 1] = __float_as_uint(fresh ? p1 : __uint_as_float(l[j + x + 1]) + p1);
+          }
+          *reinterpret_cast<uint4*>(prow + ((((h + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        *reinterpret_cast<uint4*>(prow + (((h >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        tmem_st32(lanes + kColL + h, l);
       }
+      tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[g]);
       ++mine;
-      begun = true;
     }
-    // ---- the segment's end: sums over the positions, the two groups joined
-    if (begun) wait(&sh.pv_done[g], (mine - 1) & 1);
-    tc_fence_after();
-    fold<32, 16>(l, lane);
-    fold<16, 8>(l, lane);
-    fold<8, 4>(l, lane);
-    fold<4, 2>(l, lane);
-    fold<2, 1>(l, lane);
-    // lane bits 16, 8, 4, 2, 1 chose heads + 32, 16, 8, 4, 2
-    *reinterpret_cast<float2*>(scratch + quad * kH + 2 * lane) = make_float2(l[0], l[1]);
-    named_sync(3, 256);
-    const bool whole = w.i0 == 0 && w.i1 == w.n;
-    const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
-    if (g == 0 && row < kH) {
-      const int h = row;
-      float sum[2], m[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float* sc = reinterpret_cast<const float*>(pmem + x * kPBytes);
-        sum[x] = had[x] ? (sc[h] + sc[kH + h]) + (sc[2 * kH + h] + sc[3 * kH + h]) : 0.f;
-        m[x] = sum[x] != 0.f ? sh.ref[x][h] : -kFar;
+    // ---- the segment's end: sums over the positions, the result
+#pragma unroll 1
+    for (int h = 0; h < kH; h += 32) {
+      uint32_t l[32];
+      tmem_ld32(lanes + kColL + h, l);
+      tmem_ld_wait();
+      fold<16, 16>(l, lane);
+      fold<8, 8>(l, lane);
+      fold<4, 4>(l, lane);
+      fold<2, 2>(l, lane);
+      fold<1, 1>(l, lane);
+      if (h == 0) {  // (the products that read the probabilities are done before the buffer is written)
+        wait(&sh.pv_done[g], (mine - 1) & 1);
+        tc_fence_after();
       }
-      const float top = fmaxf(m[0], m[1]), f0 = exp2_approx(m[0] - top), f1 = exp2_approx(m[1] - top);
-      const float total = sum[0] * f0 + sum[1] * f1;
-      const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
-      sh.alpha[0][h] = f0 * inv;
-      sh.alpha[1][h] = f1 * inv;
+      scratch[quad * kH + h + lane] = __uint_as_float(l[0]);  // lane bits 16 .. 1 chose heads + 16 .. + 1
+    }
+    named_sync(1 + g, 128);
+    const bool whole = w.i0 == 0 && w.i1 == w.n;
+    const int64_t slot = 2ll * worker + (w.i0 == 0 ? 1 : 0);
+    if (row < kH) {
+      const int h = row;
+      const float total = (scratch[h] + scratch[kH + h]) + (scratch[2 * kH + h] + scratch[3 * kH + h]);
+      const float top = total != 0.f ? ref[h] : -kFar;
+      alpha[h] = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
       if (!whole) {
-        float* st = k.stat + (slot * kH + h) * 2;
-        st[0] = top;
-        st[1] = total;
+        *reinterpret_cast<float2*>(k.stat + (slot * kH + h) * 2) = make_float2(top, total);
       } else if (a.lse != nullptr && h < live) {
         a.lse[static_cast<int64_t>(w.row) * a.c.num_q_heads + static_cast<int64_t>(head) * k.l.group + h0 + h] =
             total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
       }
     }
-    named_sync(3, 256);
-    tc_fence_after();
-    // group g writes heads 32 g .. 32 g + 31; a thread holds one dim
-    {
-      uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD + row;
-      float* sum = k.sum + slot * kH * kD + row;
+    named_sync(1 + g, 128);
+    // a thread holds one dim of all heads; whole results are turned in shared memory
+    uint16_t* turned = reinterpret_cast<uint16_t*>(pmem + g * kPBytes);  // [kH][kD]
+    float* sum = k.sum + slot * kH * kD + row;
 #pragma unroll 1
-      for (int h = 32 * g; h < 32 * g + 32 && h < live; h += 8) {
-        uint32_t v[2][8];
-        tmem_ld8(tmem + lanes + kColO + h, v[0]);
-        tmem_ld8(tmem + lanes + kColO + kH + h, v[1]);
-        tmem_ld_wait();
+    for (int h = 0; h < live; h += 16) {
+      uint32_t o[16];
+      tmem_ld16(lanes + kColO + h, o);
+      tmem_ld_wait();
+      if (whole) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float o = 0.f;
-          if (had[0]) o = __uint_as_float(v[0][j]) * sh.alpha[0][h + j];
-          if (had[1]) o = fmaf(__uint_as_float(v[1][j]), sh.alpha[1][h + j], o);
-          if (h + j >= live) break;
-          if (whole)
-            out[(h + j) * kD] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-          else
-            sum[(h + j) * kD] = o;
-        }
+        for (int j = 0; j < 16; ++j)
+          turned[(h + j) * kD + row] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[j]) * alpha[h + j]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (h + j < live) sum[(h + j) * kD] = __uint_as_float(o[j]);
       }
     }
-    if (g == 0 && row == 0 && !whole && w.i0 == 0) k.part[blockIdx.x] = part_of(w, range);
+    if (whole) {
+      named_sync(1 + g, 128);
+      uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD;
+#pragma unroll 4
+      for (int e = row; e < live * (kD / 8); e += 128)
+        *reinterpret_cast<uint4*>(out + e * 8) = *reinterpret_cast<const uint4*>(turned + e * 8);
+    } else if (row == 0 && w.i0 == 0) {
+      k.part[worker] = part_of(w, range);
+    }
     tc_fence_before();
-    named_sync(3, 256);  // O, the factors and the scratch have been read
+    named_sync(1 + g, 128);  // O, the factors and the shared buffer have been read
   }
 }
 
@@ -562,7 +637,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    const uint32_t fills = a.pos != nullptr ? 4 * 33 : 1;  // listed rows: every lane's copies, and one for the mask
+    const uint32_t fills = a.pos != nullptr ? 2 * 33 : 1;  // listed rows: every lane, and one for the mask or the bytes
     for (int s = 0; s < kSlots; ++s) mbar_init(&sh.full[s], fills), mbar_init(&sh.empty[s], 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sh.s_full[g], 1);
@@ -574,28 +649,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
     sh.abort = 0;
-    k.part[blockIdx.x].last = -1;
+    k.part[blockIdx.x].last = k.part[blockIdx.x + gridDim.x].last = -1;
   }
   if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
   const int units = a.c.num_kv_heads * k.l.blocks;
-  find_range<kWideThreads, kPos>(k, sh.r, units);
+  find_ranges<kWideThreads, kPos, 2>(k, sh.r, units);
   tc_fence_after();
   write_empty_rows<kD, kWideThreads>(a);
-  const Range r = sh.r.range;
   const uint32_t tmem = sh.tmem;
-  if (r.first < r.end) {
-    const WideWalk w = walk_of<kPos>(a, r, units);
-    if (warp < 8) {
-      regs_dec<64>();
-      if (warp == 0 && a.pos == nullptr) wide_pages(k, sh, w, b, &kmap, &vmap);
-      if (warp == 1) wide_mma(k, sh, w, b, tmem);
-      if (warp == 2) wide_queries(k, sh, w, b);
-      if (warp >= 4 && a.pos != nullptr) wide_list(k, sh, w, b, warp - 4);
-    } else {
-      regs_inc<192>();
-      wide_softmax(k, sh, w, b, pmem, tmem, (warp - 8) >> 2);
-    }
+  if (warp < 8) {
+    const int g = (warp >> 1) & 1;
+    const WideWalk w = walk_of<kPos>(a, sh.r.range[g], units);
+    if (warp == 1) wide_mma(k, sh, b, tmem);
+    if (warp == 0 || warp == 2) wide_queries(k, sh, w, b, g);
+    if (warp >= 4 && a.pos != nullptr) wide_list(k, sh, w, b, &kmap, g, warp & 1);
+    if ((warp == 4 || warp == 6) && a.pos == nullptr) wide_pages(k, sh, w, b, &kmap, &vmap, g);
+  } else {
+    const int g = (warp - 8) >> 2;
+    wide_softmax(k, sh, walk_of<kPos>(a, sh.r.range[g], units), b, pmem, tmem, g);
   }
   tc_fence_before();
   __syncthreads();
@@ -615,7 +687,7 @@ cudaError_t launch_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev] = true;
   }
-  attn_wide_kernel<<<k.l.ctas, kWideThreads, kWideSmem, stream>>>(kmap, vmap, k);
+  attn_wide_kernel<<<k.l.ctas / 2, kWideThreads, kWideSmem, stream>>>(kmap, vmap, k);
   return cudaGetLastError();
 }
 
