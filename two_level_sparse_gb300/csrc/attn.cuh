@@ -222,6 +222,7 @@ struct Walk {
 struct Range {
   int64_t first, end, total;
   int32_t row, unit, tile, ctas;  // where the range starts; how many share the list (every one has a tile)
+  int32_t worker, pad;
 };
 
 template <int N>
@@ -238,9 +239,9 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "");
 
-// The ranges of the list of workers blockIdx.x + i gridDim.x, i < N, and where
-// they start: every thread adds up a run of rows, a scan over the threads gives
-// the total, and the thread whose run holds a range's first tile walks to it.
+// The ranges of the list of this CTA's N workers, and where they start: every
+// thread adds up a run of rows, a scan over the threads gives the total, and the
+// thread whose run holds a range's first tile walks to it.
 template <int kThreads, int kT, int N>
 __device__ __forceinline__ void find_ranges(const Args& k, RangeShared<N>& sh, int units) {
   const AttnArgs& a = k.a;
@@ -272,11 +273,12 @@ __device__ __forceinline__ void find_ranges(const Args& k, RangeShared<N>& sh, i
   const int64_t workers = min(static_cast<int64_t>(k.l.ctas), total);
 #pragma unroll 1
   for (int i = 0; i < N; ++i) {
-    const int64_t worker = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+    const int worker = blockIdx.x + i * gridDim.x;
     const int64_t first = worker < workers ? worker * total / workers : total;
     const int64_t end = worker < workers ? (worker + 1) * total / workers : total;
     Range& range = sh.range[i];
-    if (tid == 0) range.first = first, range.end = end, range.total = total, range.ctas = static_cast<int32_t>(workers);
+    if (tid == 0)
+      range.first = first, range.end = end, range.total = total, range.ctas = static_cast<int32_t>(workers), range.worker = worker;
     int64_t at = before * units;
     if (first < end && at <= first && first < at + mine * units) {
       int r = r0;

@@ -15,9 +15,12 @@
 //
 // One CTA per SM, two workers per CTA: each has its own range of the list, a
 // group of four softmax warps, references, sums and O, so that one's
-// exponentials and results run beside the other's products.  The workers' tiles
-// alternate in one ring of five 32 KB slots (K, V, K, V, ...) and before one
-// MMA-issuing warp.  Per worker one warp loads queries and two fetch K and V.
+// exponentials and results run beside the other's products.  Tile t is worker
+// (t % 2)'s tile t / 2.  A K tile (32 KB) has the worker's own slot, V tiles
+// share three.  One warp issues the products with K, one those with V (a single
+// one took 2800 cycles for the two and their waits, as long as the HBM for the
+// tile); each worker has a warp per K and V that fetches pages, and listed rows
+// are fetched by four warps (K) and two (V) for both.
 //
 // The reference m of a head is not the running maximum but the logit of the
 // segment's first position, kept until another one passes it by 2^40.  fp32 and
@@ -32,7 +35,7 @@ namespace attn {
 namespace {
 
 constexpr int kD = 128, kH = 64, kPos = 128;
-constexpr int kSlots = 5, kSlot = kPos * kD * 2;
+constexpr int kVSlots = 3, kSlots = 2 + kVSlots, kSlot = kPos * kD * 2;  // a K slot per worker, then V's
 constexpr int kPBytes = kPos * kH * 2, kQBytes = kH * kD * 2;
 constexpr int kWideThreads = 512;
 constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256;  // S, O and the sums of worker g at + 64 g
@@ -40,9 +43,9 @@ constexpr float kFar = 1.0e30f;                     // references lie in [-kFar,
 constexpr float kSlack = 40.f;
 
 struct WideShared {
-  uint64_t full[kSlots], empty[kSlots], s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain;
-  alignas(16) uint32_t mask[4][4];  // of the last four tiles: which positions count
-  uint32_t ends[4];                 // bit 0: a segment's first tile, bit 1: its last one
+  uint64_t k_full[2], k_empty[2], v_full[kVSlots], v_empty[kVSlots], s_full[2], p_full[2], pv_done[2], drain[2];
+  alignas(16) uint32_t mask[8][4];  // of the last eight tiles: which positions count
+  uint32_t first[8];                // and whether they begin a segment
   alignas(16) float ref[2][kH], alpha[2][kH];
   RangeShared<2> r;
   uint32_t tmem;
@@ -145,42 +148,64 @@ struct Waiter {
     return alive;
   }
 };
-// A role's place in the ring: item 2 t is K of tile t, item 2 t + 1 its V; tile
-// t is worker (t % 2)'s tile t / 2.  (Where one worker has a tile more than the
-// other, the last tile's number has a gap before it; nothing follows that.)
-struct Place {
+// Tile t's V slot, t % 3, and the parity of its t / 3-th use.  (Where one worker
+// has a tile more than the other, the last tile's number has a gap before it;
+// nothing follows that, so the gap's slot is not used again.)
+struct VPlace {
   int slot;
   uint32_t phase;
-  __device__ __forceinline__ explicit Place(int item) : slot(item), phase(0) {}
-  __device__ __forceinline__ void advance(int by) {
-    slot += by;
-    if (slot >= kSlots) slot -= kSlots, phase ^= 1;
+  __device__ __forceinline__ explicit VPlace(int t) : slot(t), phase(0) {}
+  __device__ __forceinline__ void advance(int tiles) {
+    slot += tiles;
+    if (slot >= kVSlots) slot -= kVSlots, phase ^= 1;
   }
 };
 
 // ------------------------------------------------------------------ producers
-// Worker g's pages, by TMA: a tile is two pages.
+// The heads [p0, p0 + n) of a unit's queries; zeros past the last one.
+struct Queries {
+  const uint16_t* src;
+  int there;
+};
+__device__ __forceinline__ Queries queries_of(const Args& k, const WideWalk& w) {
+  const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH;
+  return {k.a.q + w.row * k.a.q_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD, min(kH, k.l.group - h0)};
+}
+__device__ __forceinline__ void copy_queries(const Queries& q, uint32_t dst, int p0, int n, int lane) {
+  const int chunk = lane & 15, odd = lane >> 4;
+#pragma unroll 2
+  for (int p = p0; p < p0 + n; p += 2) {
+    const int h = p + odd;
+    copy16(dst + (chunk >> 3) * (kQBytes / 2) + h * 128 + (((chunk & 7) ^ (h & 7)) << 4),
+           reinterpret_cast<const uint8_t*>(q.src) + (h < q.there ? h : 0) * (kD * 2) + chunk * 16, h < q.there);
+  }
+}
+
+// Worker g's pages, by TMA: a tile is two pages.  The K slot of a segment's first
+// tile is free once the last product with the segment before is done, and so is
+// the worker's query buffer: the queries are fetched with it.
+template <bool kValues>
 __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWalk w, const Buffers& b,
-                                           const CUtensorMap* kmap, const CUtensorMap* vmap, int g) {
+                                           const CUtensorMap* map, int g) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, c.dev_err};
-  Place at_slot(2 * g);
-  int tile = g;
+  VPlace vs(g);
+  uint32_t n = 0;  // tiles so far
   while (w.next(a)) {
     const int req = row_request(c, w.row), head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
     const int len = table != nullptr ? a.seq_len[w.row] : 0;
     int lo = -1, hi = -1;
-    for (int i = w.i0; i < w.i1; ++i, tile += 2) {
+    for (int i = w.i0; i < w.i1; ++i, ++n) {
       const int j = (i - w.i0) & 31;
       if (j == 0) {  // the next 32 tiles' pages, two per lane
         const int64_t at = static_cast<int64_t>(i + lane) * kPos;
         const bool in = i + lane < w.i1;
         lo = in && at < len ? table[at / kPage] : -1;
         hi = in && at + kPage < len ? table[at / kPage + 1] : -1;
-        if (in && ((at < len && (lo < 0 || lo >= c.num_pages)) || (at + kPage < len && (hi < 0 || hi >= c.num_pages))))
+        if (!kValues && in && ((at < len && (lo < 0 || lo >= c.num_pages)) || (at + kPage < len && (hi < 0 || hi >= c.num_pages))))
           report(c.dev_err, kDevErrPage);
         if (lo >= c.num_pages) lo = -1;
         if (hi >= c.num_pages) hi = -1;
@@ -188,236 +213,238 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
       const int page0 = __shfl_sync(0xffffffffu, lo, j), page1 = __shfl_sync(0xffffffffu, hi, j);
       const int pages = (page0 >= 0) + (page1 >= 0);
       const int mine = lane & 2 ? page1 : page0;  // lane 0..3: page lane / 2, dims 64 (lane % 2) ..
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {  // K, then V
-        uint64_t* bar = &sh.full[at_slot.slot];
-        if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
-          if (v == 0 && lane < 4) {
-            const int left = mine >= 0 ? len - i * kPos - lane * 32 : 0;
-            sh.mask[tile & 3][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
-            if (lane == 0) sh.ends[tile & 3] = (i == w.i0) | (i + 1 == w.i1) << 1;
-          }
-          __syncwarp();
-          if (lane == 0) {
-            if (pages > 0)
-              mbar_arrive_expect_tx(bar, pages * (kSlot / 2));
-            else
-              mbar_arrive(bar);
-          }
-          __syncwarp();
-          if (lane < 4 && mine >= 0)
-            tma_box(b.slots + at_slot.slot * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4),
-                    v == 0 ? kmap : vmap, (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(bar));
+      uint64_t* full = kValues ? &sh.v_full[vs.slot] : &sh.k_full[g];
+      if (kValues ? wait(&sh.v_empty[vs.slot], vs.phase ^ 1) : wait(&sh.k_empty[g], (n + 1) & 1)) {
+        if (!kValues && lane < 4) {
+          const int left = mine >= 0 ? len - i * kPos - lane * 32 : 0;
+          const int at = (2 * n + g) & 7;
+          sh.mask[at][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+          if (lane == 0) sh.first[at] = i == w.i0;
         }
-        at_slot.advance(v == 0 ? 1 : 3);
-      }
-    }
-  }
-  if (!wait.alive) {  // what is in flight lands before the CTA's memory goes: this worker's last two tiles
-    Place p(2 * g);
-    for (int x = g; x < tile; x += 2)
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        if (x + 4 >= tile) mbar_wait(&sh.full[p.slot], p.phase, nullptr, 1000000ull);
-        p.advance(v == 0 ? 1 : 3);
-      }
-  }
-}
-
-// Worker g's listed rows: warp `part` of two fetches positions 64 part .. 64 part
-// + 63 of every tile, K by TMA gathers and V by 16-byte asynchronous copies
-// (produce_list in attn.cuh says why).  Both warps take the ring's items in
-// order, so neither is ever a whole turn of the ring ahead of the consumers.
-// The entries of the second next tile and the page ids of the next one are on
-// their way while a tile is copied.
-__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b,
-                                          const CUtensorMap* kmap, int g, int part) {
-  const AttnArgs& a = k.a;
-  const CacheArgs& c = a.c;
-  const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
-  Waiter wait{sh, c.dev_err};
-  struct Entry {
-    const int32_t* table;  // null: the row has no request
-    int head, len, s0, s1, ends;
-    bool live;
-  };
-  int i = 0, end = 0;
-  Entry seg{nullptr, 0, 0, -1, -1, 0, false};
-  auto fetch = [&]() {
-    Entry x{nullptr, 0, 0, -1, -1, 0, false};
-    if (i >= end) {
-      if (!w.next(a)) return x;
-      i = w.i0, end = w.i1;
-      const int req = row_request(c, w.row);
-      seg.table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
-      seg.len = seg.table != nullptr ? a.seq_len[w.row] : 0;
-      seg.head = w.unit / k.l.blocks;
-    }
-    x = seg;
-    x.live = true;
-    x.ends = (i == w.i0) | (i + 1 == w.i1) << 1;
-    const int at = i * kPos + part * 64 + lane;
-    const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
-    if (at < a.npos) x.s0 = list[0];
-    if (at + 32 < a.npos) x.s1 = list[32];
-    ++i;
-    return x;
-  };
-  Entry now = seg, next = seg;
-  int p0 = 0, p1 = 0, tile = g;
-  Place at_slot(2 * g);
-  while (true) {
-    const int n0 = next.s0 >= 0 && next.s0 < next.len ? next.table[next.s0 / kPage] : 0;
-    const int n1 = next.s1 >= 0 && next.s1 < next.len ? next.table[next.s1 / kPage] : 0;
-    const Entry after = fetch();
-    if (!now.live) {  // the pipeline fills, or is empty
-      if (!next.live && !after.live) break;
-      now = next, next = after, p0 = n0, p1 = n1;
-      continue;
-    }
-    const bool in0 = now.s0 >= 0 && now.s0 < now.len, in1 = now.s1 >= 0 && now.s1 < now.len;
-    if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
-    const bool ok0 = in0 && p0 >= 0 && p0 < c.num_pages, ok1 = in1 && p1 >= 0 && p1 < c.num_pages;
-    if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
-    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kPage + (now.s0 & (kPage - 1)) : -1;
-    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kPage + (now.s1 & (kPage - 1)) : -1;
-    const uint32_t m0 = __ballot_sync(0xffffffffu, ok0), m1 = __ballot_sync(0xffffffffu, ok1);
-    // ---- K: an entry that does not count fetches row 0
-    if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
-      uint64_t* bar = &sh.full[at_slot.slot];
-      const uint32_t dst = b.slots + at_slot.slot * kSlot + part * 64 * 128;
-      if (lane == 0) {
-        sh.mask[tile & 3][2 * part] = m0;
-        sh.mask[tile & 3][2 * part + 1] = m1;
-        if (part == 0) sh.ends[tile & 3] = now.ends;
-        mbar_arrive_expect_tx(bar, kSlot / 2);
-      }
-      __syncwarp();
-#pragma unroll 1
-      for (int p = 0; p < 64; p += 4) {
-        const int mine = max(p < 32 ? row0 : row1, 0);
-        const int r0 = __shfl_sync(0xffffffffu, mine, p & 31), r1 = __shfl_sync(0xffffffffu, mine, (p & 31) + 1);
-        const int r2 = __shfl_sync(0xffffffffu, mine, (p & 31) + 2), r3 = __shfl_sync(0xffffffffu, mine, (p & 31) + 3);
-        gather4_elect(dst + p * 128, kmap, 0, r0, r1, r2, r3, smem_u32(bar));
-        gather4_elect(dst + kSlot / 2 + p * 128, kmap, 128, r0, r1, r2, r3, smem_u32(bar));
-      }
-      mbar_arrive(bar);
-    }
-    at_slot.advance(1);
-    // ---- V: zeros for it
-    if (wait(&sh.empty[at_slot.slot], at_slot.phase ^ 1)) {
-      uint64_t* bar = &sh.full[at_slot.slot];
-      const uint32_t dst = b.slots + at_slot.slot * kSlot + (chunk >> 3) * (kSlot / 2) + part * 64 * 128;
-      const uint8_t* base = c.v_pool + chunk * 16;
-#pragma unroll 4
-      for (int p = 0; p < 64; p += 2) {  // positions p and p + 1
-        const int at = p + odd, r = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, at & 31);
-        copy16(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4), base + static_cast<int64_t>(max(r, 0)) * (kD * 2), r >= 0);
-      }
-      cp_async_arrive_noinc(bar);
-      if (lane == 0) mbar_arrive(bar);
-    }
-    at_slot.advance(3);
-    tile += 2;
-    now = next, next = after, p0 = n0, p1 = n1;
-  }
-  cp_async_wait<0>();
-  if (!wait.alive) {  // what is in flight lands before the CTA's memory goes: the last two tiles' K
-    Place p(2 * g);
-    for (int x = g; x < tile; x += 2) {
-      if (x + 4 >= tile) mbar_wait(&sh.full[p.slot], p.phase, nullptr, 1000000ull);
-      p.advance(4);
-    }
-  }
-}
-
-// Worker g's queries, one segment's after the last product with the one's before.
-__device__ __forceinline__ void wide_queries(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, int g) {
-  const AttnArgs& a = k.a;
-  const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4;
-  Waiter wait{sh, a.c.dev_err};
-  const uint32_t dst = b.q + g * kQBytes + (chunk >> 3) * (kQBytes / 2);
-  for (uint32_t seg = 0; w.next(a); ++seg) {
-    const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + w.row * a.q_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD) + chunk * 16;
-    if (!wait(&sh.q_empty[g], (seg + 1) & 1)) continue;
-#pragma unroll 4
-    for (int p = 0; p < kH; p += 2) {
-      const int h = p + odd;
-      copy16(dst + h * 128 + (((chunk & 7) ^ (h & 7)) << 4), src + (h < live ? h : 0) * (kD * 2), h < live);
-    }
-    cp_async_arrive_noinc(&sh.q_full[g]);
-  }
-  cp_async_wait<0>();
-}
-
-// ------------------------------------------------------------------ products
-// Step t: the product with V of tile t - 2, then the one with K of tile t.
-__device__ __forceinline__ void wide_mma(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
-  const AttnArgs& a = k.a;
-  const int lane = threadIdx.x & 31;
-  Waiter wait{sh, a.c.dev_err};
-  const int n0 = static_cast<int>(sh.r.range[0].end - sh.r.range[0].first);
-  const int n1 = static_cast<int>(sh.r.range[1].end - sh.r.range[1].first);
-  const int steps = 2 * max(n0, n1) + 2;
-  Place ks(0), vs(1);
-  uint32_t seg[2] = {0, 0};  // segments begun
-  for (int t = 0; t < steps; ++t) {
-    const int g = t & 1;  // of both tiles
-    if (t >= 2) {
-      const int tp = t - 2;
-      if ((tp >> 1) < (g ? n1 : n0)) {
-        wait(&sh.p_full[g], (tp >> 1) & 1);
-        if (wait(&sh.full[vs.slot], vs.phase)) {
-          const uint32_t vb = b.slots + vs.slot * kSlot, pb = b.p + g * kPBytes;
-          const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[tp & 3]);
-          if (a.pos == nullptr && (m.x & m.y & m.z & m.w) != ~0u) {
-            // values that do not count must not reach a product with 0
-#pragma unroll 1
-            for (int e = lane; e < kPos * 16; e += 32) {
-              const int p = e >> 4, c = e & 15;
-              if ((sh.mask[tp & 3][p >> 5] >> (p & 31)) & 1) continue;
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16),
-                           "r"(0)
-                           : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+        __syncwarp();
+        if (lane == 0) {
+          if (pages > 0)
+            mbar_arrive_expect_tx(full, pages * (kSlot / 2));
+          else
+            mbar_arrive(full);
+        }
+        __syncwarp();
+        if (lane < 4 && mine >= 0)
+          tma_box(b.slots + (kValues ? 2 + vs.slot : g) * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4), map,
+                  (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(full));
+        if (!kValues) {
+          if (i == w.i0) {
+            copy_queries(queries_of(k, w), b.q + g * kQBytes, 0, kH, lane);
+            cp_async_arrive_noinc(full);
+          } else {
+            mbar_arrive(full);
           }
-          const uint32_t more = (sh.ends[tp & 3] & 1) ^ 1;  // adds to the segment's earlier tiles
-          fence_proxy_async_smem();
-          tc_fence_after();
-          mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), more);
-          mma_commit_elect(&sh.empty[vs.slot]);
-          mma_commit_elect(&sh.pv_done[g]);
         }
       }
       vs.advance(2);
     }
-    if ((t >> 1) < (g ? n1 : n0)) {
-      if (wait(&sh.full[ks.slot], ks.phase)) {
-        const uint32_t ends = sh.ends[t & 3];
-        if (ends & 1) {
-          const uint32_t s = g ? seg[1] : seg[0];
-          wait(&sh.q_full[g], s & 1);
-          (g ? seg[1] : seg[0]) = s + 1;
+  }
+  cp_async_wait<0>();
+}
+
+// Listed rows of both workers' tiles in turn: four warps gather K by TMA, 32
+// positions each, and two copy V by 16-byte asynchronous copies, 64 each
+// (produce_list in attn.cuh says why).  Of each worker, the list entries of the
+// second next tile and the page ids of the next one are on their way while a
+// tile is copied.
+template <int N>  // positions per warp: 32 N
+struct ListStream {
+  struct Entry {
+    const int32_t* table;  // null: the row has no request
+    int head, len, s[N];
+    bool live, first;
+    Queries q;
+  };
+  WideWalk w;
+  int i, end, page[N];
+  Entry seg, now, next;
+
+  __device__ __forceinline__ ListStream(const AttnArgs& a, const Range& r, int units)
+      : w(walk_of<kPos>(a, r, units)), i(0), end(0), seg{}, now{}, next{} {}
+  __device__ __forceinline__ Entry fetch(const Args& k, int first) {
+    const AttnArgs& a = k.a;
+    Entry x{};
+    if (i >= end) {
+      if (!w.next(a)) return x;
+      i = w.i0, end = w.i1;
+      const int req = row_request(a.c, w.row);
+      seg.table = req >= 0 ? a.c.page_table + static_cast<int64_t>(req) * a.c.max_pages : nullptr;
+      seg.len = seg.table != nullptr ? a.seq_len[w.row] : 0;
+      seg.head = w.unit / k.l.blocks;
+      if (N == 1) seg.q = queries_of(k, w);
+    }
+    x = seg;
+    x.live = true;
+    x.first = i == w.i0;
+    const int at = i * kPos + first;
+    const int32_t* list = a.pos + static_cast<int64_t>(w.row) * a.pos_stride + at;
+#pragma unroll
+    for (int j = 0; j < N; ++j) x.s[j] = at + 32 * j < a.npos ? list[32 * j] : -1;
+    ++i;
+    return x;
+  }
+  // The look-ahead moves on: the next tile becomes the current one.  first: the
+  // lane's first position in a tile.
+  __device__ __forceinline__ void step(const Args& k, int first) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) page[j] = next.live && next.s[j] >= 0 && next.s[j] < next.len ? next.table[next.s[j] / kPage] : 0;
+    const Entry after = fetch(k, first);
+    now = next, next = after;
+  }
+};
+
+template <bool kValues>
+__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, const Buffers& b, const CUtensorMap* kmap, int part,
+                                          int units) {
+  constexpr int N = kValues ? 2 : 1;
+  const AttnArgs& a = k.a;
+  const CacheArgs& c = a.c;
+  const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4, first = part * 32 * N + lane;
+  Waiter wait{sh, c.dev_err};
+  ListStream<N> cur(a, sh.r.range[0], units), other(a, sh.r.range[1], units);
+  VPlace vs(0);
+  // steps -4 .. -1 fill both streams' look-ahead
+  for (int t = -4; t < 0 || cur.now.live || other.now.live; ++t) {
+    const bool live = t >= 0 && cur.now.live;
+    int row[N];  // -1: an entry that does not count (row 0 of K, zeros of V)
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int s = cur.now.s[j];
+      const bool in = live && s >= 0 && s < cur.now.len, ok = in && cur.page[j] >= 0 && cur.page[j] < c.num_pages;
+      if (!kValues) {
+        if (live && cur.now.table != nullptr && !in && s != -1) report(c.dev_err, kDevErrPos);
+        if (ok != in) report(c.dev_err, kDevErrPage);
+        m = __ballot_sync(0xffffffffu, ok);
+      }
+      row[j] = ok ? (cur.page[j] * c.num_kv_heads + cur.now.head) * kPage + (s & (kPage - 1)) : -1;
+    }
+    const bool begins = cur.now.first;
+    const Queries q = cur.now.q;
+    cur.step(k, first);  // its loads land while the tile is copied
+    const int g = t & 1;
+    if (live && (kValues ? wait(&sh.v_empty[vs.slot], vs.phase ^ 1) : wait(&sh.k_empty[g], ((t >> 1) + 1) & 1))) {
+      if constexpr (!kValues) {
+        uint64_t* full = &sh.k_full[g];
+        const uint32_t dst = b.slots + g * kSlot + part * 32 * 128;
+        if (lane == 0) {
+          sh.mask[t & 7][part] = m;
+          if (part == 0) sh.first[t & 7] = begins;
+          mbar_arrive_expect_tx(full, kSlot / 4);
         }
-        if (wait.alive) {
-          fence_proxy_async_smem();  // queries and listed rows are written through the generic proxy
-          tc_fence_after();
-          mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * g, desc128(b.slots + ks.slot * kSlot, 16),
-                                                       desc128(b.q + g * kQBytes, 16), idesc(false), 0);
-          mma_commit_elect(&sh.empty[ks.slot]);
-          mma_commit_elect(&sh.s_full[g]);
-          if (ends & 2) mma_commit_elect(&sh.q_empty[g]);
+        __syncwarp();
+        const int mine = max(row[0], 0);
+#pragma unroll 2
+        for (int p = 0; p < 32; p += 4) {
+          const int r0 = __shfl_sync(0xffffffffu, mine, p), r1 = __shfl_sync(0xffffffffu, mine, p + 1);
+          const int r2 = __shfl_sync(0xffffffffu, mine, p + 2), r3 = __shfl_sync(0xffffffffu, mine, p + 3);
+          gather4_elect(dst + p * 128, kmap, 0, r0, r1, r2, r3, smem_u32(full));
+          gather4_elect(dst + kSlot / 2 + p * 128, kmap, 128, r0, r1, r2, r3, smem_u32(full));
         }
+        if (begins) {
+          copy_queries(q, b.q + g * kQBytes, part * (kH / 4), kH / 4, lane);
+          cp_async_arrive_noinc(full);
+        } else {
+          mbar_arrive(full);
+        }
+      } else {
+        uint64_t* full = &sh.v_full[vs.slot];
+        const uint32_t dst = b.slots + (2 + vs.slot) * kSlot + (chunk >> 3) * (kSlot / 2) + part * 64 * 128;
+        const uint8_t* base = c.v_pool + chunk * 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll 4
+          for (int p = 0; p < 32; p += 2) {  // positions p and p + 1
+            const int at = p + odd, r = __shfl_sync(0xffffffffu, row[j], at);
+            copy16(dst + (32 * j + at) * 128 + (((chunk & 7) ^ (at & 7)) << 4), base + static_cast<int64_t>(max(r, 0)) * (kD * 2),
+                   r >= 0);
+          }
+        cp_async_arrive_noinc(full);
       }
     }
-    ks.advance(2);
+    if (t >= 0) vs.advance(1);
+    const ListStream<N> turn = cur;
+    cur = other, other = turn;
+  }
+  cp_async_wait<0>();
+}
+
+// What the copies in flight write lands before the CTA's memory goes (after a
+// role has given up): both parities of a barrier, whichever is the last fill's.
+__device__ __forceinline__ void drain_copies(WideShared& sh) {
+#pragma unroll 1
+  for (int i = 0; i < 2 * (2 + kVSlots); ++i) {
+    const int s = i >> 1;
+    mbar_wait(s < 2 ? &sh.k_full[s] : &sh.v_full[s - 2], i & 1, nullptr, 1000000ull);
+  }
+}
+
+// ------------------------------------------------------------------ products
+__device__ __forceinline__ int tiles_of(const WideShared& sh, int g) {
+  return static_cast<int>(sh.r.range[g].end - sh.r.range[g].first);
+}
+
+__device__ __forceinline__ void wide_scores(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
+  Waiter wait{sh, k.a.c.dev_err};
+  const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
+  for (int t = 0; t < steps; ++t) {
+    const int g = t & 1, n = t >> 1;
+    if (n >= (g ? n1 : n0)) continue;
+    if (n > 0) wait(&sh.p_full[g], (n - 1) & 1);  // the last tile's scores have been read
+    if (!wait(&sh.k_full[g], n & 1)) continue;
+    fence_proxy_async_smem();  // queries are written through the generic proxy
+    tc_fence_after();
+    mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * g, desc128(b.slots + g * kSlot, 16),
+                                                 desc128(b.q + g * kQBytes, 16), idesc(false), 0);
+    mma_commit_elect(&sh.s_full[g]);
+    mma_commit_elect(&sh.k_empty[g]);
   }
   if (!wait.alive) {  // the products in flight end before the CTA's memory goes
-    mma_commit_elect(&sh.drain);
-    mbar_wait(&sh.drain, 0, nullptr, 1000000ull);
+    mma_commit_elect(&sh.drain[0]);
+    mbar_wait(&sh.drain[0], 0, nullptr, 1000000ull);
+  }
+}
+
+__device__ __forceinline__ void wide_values(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
+  const AttnArgs& a = k.a;
+  const int lane = threadIdx.x & 31;
+  Waiter wait{sh, a.c.dev_err};
+  const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
+  VPlace vs(0);
+  for (int t = 0; t < steps; ++t, vs.advance(1)) {
+    const int g = t & 1, n = t >> 1;
+    if (n >= (g ? n1 : n0)) continue;
+    wait(&sh.v_full[vs.slot], vs.phase);
+    if (!wait(&sh.p_full[g], n & 1)) continue;
+    const uint32_t vb = b.slots + (2 + vs.slot) * kSlot, pb = b.p + g * kPBytes;
+    const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[t & 7]);
+    const uint32_t more = sh.first[t & 7] ^ 1;  // adds to the segment's earlier tiles
+    if (a.pos == nullptr && (m.x & m.y & m.z & m.w) != ~0u) {
+      // values that do not count must not reach a product with 0
+#pragma unroll 1
+      for (int e = lane; e < kPos * 16; e += 32) {
+        const int p = e >> 4, c = e & 15;
+        if ((sh.mask[t & 7][p >> 5] >> (p & 31)) & 1) continue;
+        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16), "r"(0)
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    fence_proxy_async_smem();  // listed rows and probabilities are written through the generic proxy
+    tc_fence_after();
+    mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), more);
+    mma_commit_elect(&sh.pv_done[g]);
+    mma_commit_elect(&sh.v_empty[vs.slot]);
+  }
+  if (!wait.alive) {
+    mma_commit_elect(&sh.drain[1]);
+    mbar_wait(&sh.drain[1], 0, nullptr, 1000000ull);
   }
 }
 
@@ -447,7 +474,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
   const Range range = sh.r.range[g];
   float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][kH], while no product reads the probabilities
   float *ref = sh.ref[g], *alpha = sh.alpha[g];
-  const int worker = blockIdx.x + g * gridDim.x;
+  const int worker = range.worker;
   Waiter wait{sh, a.c.dev_err};
   uint32_t mine = 0;  // tiles so far: the CTA's tile 2 mine + g
   while (w.next(a)) {
@@ -456,7 +483,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
     for (int i = w.i0; i < w.i1; ++i) {
       wait(&sh.s_full[g], mine & 1);
       tc_fence_after();
-      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[(2 * mine + g) & 3]);
+      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[(2 * mine + g) & 7]);
       const bool valid = ((quad == 0 ? m.x : quad == 1 ? m.y : quad == 2 ? m.z : m.w) >> lane) & 1;
       if (!set && (m.x | m.y | m.z | m.w) != 0) {  // the first position's logits
         const int first = m.x ? __ffs(m.x) - 1 : m.y ? 31 + __ffs(m.y) : m.z ? 63 + __ffs(m.z) : 95 + __ffs(m.w);
@@ -637,19 +664,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    const uint32_t fills = a.pos != nullptr ? 2 * 33 : 1;  // listed rows: every lane, and one for the mask or the bytes
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sh.full[s], fills), mbar_init(&sh.empty[s], 1);
+    // K: per producer warp the bytes, and every lane (a segment's first tile: its copies of the queries); listed V: every lane
     for (int g = 0; g < 2; ++g) {
+      mbar_init(&sh.k_full[g], a.pos != nullptr ? 4 * 33 : 33);
+      mbar_init(&sh.k_empty[g], 1);
       mbar_init(&sh.s_full[g], 1);
       mbar_init(&sh.p_full[g], 4);
       mbar_init(&sh.pv_done[g], 1);
-      mbar_init(&sh.q_full[g], 32);
-      mbar_init(&sh.q_empty[g], 1);
+      mbar_init(&sh.drain[g], 1);
     }
-    mbar_init(&sh.drain, 1);
+    for (int s = 0; s < kVSlots; ++s) mbar_init(&sh.v_full[s], a.pos != nullptr ? 64 : 1), mbar_init(&sh.v_empty[s], 1);
     fence_mbar_init();
     sh.abort = 0;
-    k.part[blockIdx.x].last = k.part[blockIdx.x + gridDim.x].last = -1;
+    k.part[2 * blockIdx.x].last = k.part[2 * blockIdx.x + 1].last = -1;
   }
   if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
@@ -659,18 +686,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   write_empty_rows<kD, kWideThreads>(a);
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
-    const int g = (warp >> 1) & 1;
-    const WideWalk w = walk_of<kPos>(a, sh.r.range[g], units);
-    if (warp == 1) wide_mma(k, sh, b, tmem);
-    if (warp == 0 || warp == 2) wide_queries(k, sh, w, b, g);
-    if (warp >= 4 && a.pos != nullptr) wide_list(k, sh, w, b, &kmap, g, warp & 1);
-    if ((warp == 4 || warp == 6) && a.pos == nullptr) wide_pages(k, sh, w, b, &kmap, &vmap, g);
+    if (warp == 0) wide_scores(k, sh, b, tmem);
+    if (warp == 1) wide_values(k, sh, b, tmem);
+    if (a.pos != nullptr) {
+      if (warp == 2 || warp == 3) wide_list<true>(k, sh, b, &kmap, warp - 2, units);
+      if (warp >= 4) wide_list<false>(k, sh, b, &kmap, warp - 4, units);
+    } else if (warp >= 4) {
+      const int g = warp & 1;
+      const WideWalk w = walk_of<kPos>(a, sh.r.range[g], units);
+      if (warp < 6)
+        wide_pages<false>(k, sh, w, b, &kmap, g);
+      else
+        wide_pages<true>(k, sh, w, b, &vmap, g);
+    }
   } else {
     const int g = (warp - 8) >> 2;
     wide_softmax(k, sh, walk_of<kPos>(a, sh.r.range[g], units), b, pmem, tmem, g);
   }
   tc_fence_before();
   __syncthreads();
+  if (sh.abort != 0 && warp == 0) drain_copies(sh);
   if (warp == 1) tmem_dealloc(tmem, kTmem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
