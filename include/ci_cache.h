@@ -70,7 +70,9 @@ CI_API int64_t ci_cache_page_bytes(int32_t cache_format, int32_t head_dim);
  * q, out: bf16 [rows][num_q_heads][D] with row strides in elements (multiples
  * of 8); q and out 16-byte aligned.  lse: float [rows][num_q_heads] or NULL.
  * 1 <= num_q_heads / num_kv_heads <= 128, without remainder.
- * max_len <= 64 * max_pages.
+ * max_len <= 64 * max_pages.  With n = max_len, or npos for a list:
+ * rows * num_kv_heads * ceil(num_q_heads / num_kv_heads / 64) * (n / 64 + 1) <
+ * 2^31.
  * ws: at least ci_attn_workspace_bytes() bytes, 16-byte aligned, of any
  * content; one call's use of it ends with the call's work on the stream.
  */

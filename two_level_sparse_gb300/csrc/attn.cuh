@@ -190,45 +190,45 @@ template <int kT>
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int t) {
   const int len = a.seq_len[t];
   if (len <= 0 || len > a.max_len) return 0;
-  return static_cast<int>(((a.pos != nullptr ? a.npos : len) + static_cast<int64_t>(kT) - 1) / kT);
+  return static_cast<int>((static_cast<uint32_t>(a.pos != nullptr ? a.npos : len) + kT - 1) / kT);
 }
 
-// A CTA's way through the list: segment by segment (tiles [i0, i1) of a unit).
+// A worker's range of the list (the host has checked that its indices fit in 31
+// bits) and where it starts.
+struct Range {
+  int32_t first, end, total, workers;  // workers: how many share the list (every one has a tile)
+  int32_t row, unit, tile, worker;
+};
+
+// A worker's way through its range: segment by segment (tiles [i0, i1) of a unit).
 template <int kT>
 struct Walk {
-  int64_t x, end;                    // next tile of the list, end of the CTA's range
-  int row, unit, tile, n, units;     // where that is; n: tiles of the row
+  int left;                       // tiles of the range behind the segment
+  int row, unit, tile, n, units;  // where the next segment starts; n: tiles of the row
   int i0, i1;
   __device__ __forceinline__ bool next(const AttnArgs& a) {
-    if (x >= end) return false;
+    if (left == 0) return false;
     if (tile == n) {
       tile = 0;
       if (++unit == units) {
         unit = 0;
+#pragma unroll 1
         do n = row_tiles<kT>(a, ++row);
         while (n == 0);
       }
     }
     i0 = tile;
-    i1 = static_cast<int>(min(static_cast<int64_t>(n), i0 + (end - x)));
-    x += i1 - i0;
+    i1 = min(n, i0 + left);
+    left -= i1 - i0;
     tile = i1;
     return true;
   }
-  // The list's index of the segment's unit's last tile.
-  __device__ __forceinline__ int64_t last() const { return x - i1 + n - 1; }
-};
-
-struct Range {
-  int64_t first, end, total;
-  int32_t row, unit, tile, ctas;  // where the range starts; how many share the list (every one has a tile)
-  int32_t worker, pad;
 };
 
 template <int N>
 struct RangeShared {
   Range range[N];
-  int64_t warp_sum[16];
+  int32_t warp_sum[16];
 };
 
 struct Shared {
@@ -239,95 +239,111 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "");
 
-// The ranges of the list of this CTA's N workers, and where they start: every
-// thread adds up a run of rows, a scan over the threads gives the total, and the
-// thread whose run holds a range's first tile walks to it.
+// The list's first worker-th share: total / workers tiles each, the first total %
+// workers one more.
+__device__ __forceinline__ int share_start(int worker, int per, int rest) { return worker * per + min(worker, rest); }
+
+// The ranges of this CTA's N workers: every thread adds up a run of rows, a scan
+// over the threads gives the total, and the thread whose run holds a range's
+// first tile walks to it.  True where some row has nothing to read.
 template <int kThreads, int kT, int N>
-__device__ __forceinline__ void find_ranges(const Args& k, RangeShared<N>& sh, int units) {
+__device__ __forceinline__ bool find_ranges(const Args& k, RangeShared<N>& sh, int units) {
   const AttnArgs& a = k.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.rows + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
-  int64_t mine = 0;
+  const int per_thread = (a.rows + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per_thread, a.rows), r1 = min(r0 + per_thread, a.rows);
+  int mine = 0;
+  bool none = false, bad = false;
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
-    const int len = a.seq_len[r];
-    if (blockIdx.x == 0 && (len < 0 || len > a.max_len)) report(a.c.dev_err, kDevErrLen);
-    mine += row_tiles<kT>(a, r);
+    const int n = row_tiles<kT>(a, r), len = a.seq_len[r];
+    bad |= len < 0 || len > a.max_len;
+    none |= n == 0;
+    mine += n;
   }
-  int64_t incl = mine;
+  if (bad && blockIdx.x == 0) report(a.c.dev_err, kDevErrLen);
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) sh.warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-#pragma unroll
+  none = __syncthreads_or(none);
+  int before = incl - mine, total = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
   total *= units;
-  const int64_t workers = min(static_cast<int64_t>(k.l.ctas), total);
+  const int workers = min(k.l.ctas, total), per = workers > 0 ? total / workers : 0, rest = total - per * workers;
 #pragma unroll 1
   for (int i = 0; i < N; ++i) {
     const int worker = blockIdx.x + i * gridDim.x;
-    const int64_t first = worker < workers ? worker * total / workers : total;
-    const int64_t end = worker < workers ? (worker + 1) * total / workers : total;
+    const int first = share_start(min(worker, workers), per, rest), end = share_start(min(worker + 1, workers), per, rest);
     Range& range = sh.range[i];
-    if (tid == 0)
-      range.first = first, range.end = end, range.total = total, range.ctas = static_cast<int32_t>(workers), range.worker = worker;
-    int64_t at = before * units;
+    if (tid == 0) range.first = first, range.end = end, range.total = total, range.workers = workers, range.worker = worker;
+    int at = before * units;
     if (first < end && at <= first && first < at + mine * units) {
-      int r = r0;
-      for (;; ++r) {
-        const int64_t n = static_cast<int64_t>(row_tiles<kT>(a, r)) * units;
-        if (first < at + n) break;
-        at += n;
+      int r = r0, n = row_tiles<kT>(a, r);
+#pragma unroll 1
+      while (first >= at + n * units) {
+        at += n * units;
+        n = row_tiles<kT>(a, ++r);
       }
-      const int n = row_tiles<kT>(a, r);
       range.row = r;
-      range.unit = static_cast<int>((first - at) / n);
-      range.tile = static_cast<int>((first - at) % n);
+      range.unit = (first - at) / n;
+      range.tile = (first - at) - range.unit * n;
     }
   }
   __syncthreads();
+  return none;
 }
 template <int kT>
 __device__ __forceinline__ Walk<kT> walk_of(const AttnArgs& a, const Range& r, int units) {
-  return Walk<kT>{r.first, r.end, r.row, r.unit, r.tile, r.first < r.end ? row_tiles<kT>(a, r.row) : 0, units, 0, 0};
+  return Walk<kT>{r.end - r.first, r.row, r.unit, r.tile, r.first < r.end ? row_tiles<kT>(a, r.row) : 0, units, 0, 0};
 }
-// What a CTA leaves behind for the unit that goes on past its range.
+// What a worker leaves behind for the unit that goes on past its range: the
+// unit, and the worker that has its last tile.
 template <int kT>
 __device__ __forceinline__ Part part_of(const Walk<kT>& w, const Range& r) {
-  return Part{w.row, w.unit, static_cast<int32_t>(((w.last() + 1) * r.ctas - 1) / r.total), 0};
+  const int last = r.end - 1 + w.n - w.i1;  // (the segment ends where the range does)
+  const int per = r.total / r.workers, rest = r.total - per * r.workers, longer = rest * (per + 1);
+  return Part{w.row, w.unit, last < longer ? last / (per + 1) : rest + (last - longer) / per, 0};
 }
 
 // A bounded wait of a whole warp for phase `parity`; false once it, or another
 // warp of the CTA, has given up (reported once).
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* dev_err) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
+static __device__ __noinline__ bool wait_warp_slow(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* dev_err) {
   const uint64_t t0 = globaltimer_ns();
+  bool ok = false;
   while (!ok && *static_cast<volatile int32_t*>(abort) == 0 && globaltimer_ns() - t0 < 2000000000ull)
     ok = mbar_try_wait_sleep(bar, parity);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok && (threadIdx.x & 31) == 0 && atomicExch(abort, 1) == 0) report(dev_err, kDevErrTimeout);
   return ok;
 }
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* dev_err) {
+  // (the second probe sleeps in the barrier for a while)
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity))) return true;
+  return wait_warp_slow(bar, parity, abort, dev_err);
+}
 
 // Rows with nothing to read.
 template <int D, int kThreads>
 __device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
+#pragma unroll 1
   for (int t = blockIdx.x; t < a.rows; t += gridDim.x) {
     if (row_tiles<kTile>(a, t) != 0) continue;
+#pragma unroll 1
     for (int e = threadIdx.x; e < a.c.num_q_heads * (D / 8); e += kThreads)
       *reinterpret_cast<uint4*>(a.out + t * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr)
-      for (int h = threadIdx.x; h < a.c.num_q_heads; h += kThreads)
-        a.lse[static_cast<int64_t>(t) * a.c.num_q_heads + h] = -INFINITY;
+    if (a.lse == nullptr) continue;
+#pragma unroll 1
+    for (int h = threadIdx.x; h < a.c.num_q_heads; h += kThreads)
+      a.lse[static_cast<int64_t>(t) * a.c.num_q_heads + h] = -INFINITY;
   }
 }
 
@@ -369,12 +385,14 @@ __device__ void produce_pages(const Args& k, Shared& sh, Walk<kTile> w, const CU
   constexpr int kRowsPerPage = cache_page_bytes<kFp8>(D) / C::kRow;
   const int lane = threadIdx.x & 31;
   Ring<C> ring{sh, k};
+#pragma unroll 1
   while (w.next(a)) {
     const int req = row_request(c, w.row);
     const int head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
     const int len = table != nullptr ? a.seq_len[w.row] : 0;
     int ids = 0;
+#pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i) {
       const int j = (i - w.i0) & 31;
       if (j == 0) {  // the next 32 tiles' pages, one per lane
@@ -467,6 +485,7 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUt
   };
   ListTile now = seg, next = seg;
   int p0 = 0, p1 = 0;
+#pragma unroll 1
   while (true) {
     // page ids of the next tile's entries (0 where an entry does not count)
     const int n0 = next.s0 >= 0 && next.s0 < next.len ? next.table[next.s0 / kPage] : 0;
@@ -553,6 +572,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;
+#pragma unroll 1
   while (w.next(a)) {
     const int head = w.unit / k.l.blocks, hb = w.unit - head * k.l.blocks;
     const int h0 = hb * C::kHeadsU;                                // first head of the unit, within its group
@@ -610,6 +630,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
       top[nt][0] = top[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
+#pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i) {
       alive = alive && wait_warp(&sh.full[stage], phase, &sh.abort, a.c.dev_err);
       const uint32_t kbase = stages + stage * C::kStage, vbase = kbase + C::kMat;
@@ -703,6 +724,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
           }
         }
         if (!kFp8 && !all && a.pos == nullptr) {  // what follows a row's last position must not reach a product with 0
+#pragma unroll 1
           for (int e = lane; e < 16 * MT * (C::kRow / 16); e += 32) {
             const int p = p0 + e / (C::kRow / 16);
             if ((mask >> p) & 1) continue;
@@ -834,6 +856,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
     }
     if (whole) {
       uint16_t* dst = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * D;
+#pragma unroll 1
       for (int e = tid; e < live * (D / 8); e += C::kConsumers) {
         const int h = e / (D / 8), d = e % (D / 8) * 8;
         const float4 x = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d);
@@ -843,6 +866,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
     } else {
       const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
       float* dst = k.sum + slot * C::kHeadsU * D;
+#pragma unroll 1
       for (int e = tid; e < live * (D / 4); e += C::kConsumers) {
         const int h = e / (D / 4), d = e % (D / 4) * 4;
         *reinterpret_cast<float4*>(dst + h * D + d) = *reinterpret_cast<const float4*>(acc + h * C::kAccStride + d);
@@ -876,8 +900,7 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     k.part[blockIdx.x].last = -1;
   }
   const int units = a.c.num_kv_heads * k.l.blocks;
-  find_ranges<C::kThreads, kTile, 1>(k, sh.r, units);
-  write_empty_rows<D, C::kThreads>(a);
+  if (find_ranges<C::kThreads, kTile, 1>(k, sh.r, units)) write_empty_rows<D, C::kThreads>(a);
   const Range r = sh.r.range[0];
   if (r.first < r.end) {
     const Walk<kTile> w = walk_of<kTile>(a, r, units);

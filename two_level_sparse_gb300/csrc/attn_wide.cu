@@ -193,11 +193,13 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
   Waiter wait{sh, c.dev_err};
   VPlace vs(g);
   uint32_t n = 0;  // tiles so far
+#pragma unroll 1
   while (w.next(a)) {
     const int req = row_request(c, w.row), head = w.unit / k.l.blocks;
     const int32_t* table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
     const int len = table != nullptr ? a.seq_len[w.row] : 0;
     int lo = -1, hi = -1;
+#pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i, ++n) {
       const int j = (i - w.i0) & 31;
       if (j == 0) {  // the next 32 tiles' pages, two per lane
@@ -309,6 +311,7 @@ __device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, const B
   ListStream<N> cur(a, sh.r.range[0], units), other(a, sh.r.range[1], units);
   VPlace vs(0);
   // steps -4 .. -1 fill both streams' look-ahead
+#pragma unroll 1
   for (int t = -4; t < 0 || cur.now.live || other.now.live; ++t) {
     const bool live = t >= 0 && cur.now.live;
     int row[N];  // -1: an entry that does not count (row 0 of K, zeros of V)
@@ -386,12 +389,13 @@ __device__ __forceinline__ void drain_copies(WideShared& sh) {
 
 // ------------------------------------------------------------------ products
 __device__ __forceinline__ int tiles_of(const WideShared& sh, int g) {
-  return static_cast<int>(sh.r.range[g].end - sh.r.range[g].first);
+  return sh.r.range[g].end - sh.r.range[g].first;
 }
 
 __device__ __forceinline__ void wide_scores(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
   Waiter wait{sh, k.a.c.dev_err};
   const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
+#pragma unroll 1
   for (int t = 0; t < steps; ++t) {
     const int g = t & 1, n = t >> 1;
     if (n >= (g ? n1 : n0)) continue;
@@ -416,6 +420,7 @@ __device__ __forceinline__ void wide_values(const Args& k, WideShared& sh, const
   Waiter wait{sh, a.c.dev_err};
   const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
   VPlace vs(0);
+#pragma unroll 1
   for (int t = 0; t < steps; ++t, vs.advance(1)) {
     const int g = t & 1, n = t >> 1;
     if (n >= (g ? n1 : n0)) continue;
@@ -477,9 +482,11 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
   const int worker = range.worker;
   Waiter wait{sh, a.c.dev_err};
   uint32_t mine = 0;  // tiles so far: the CTA's tile 2 mine + g
+#pragma unroll 1
   while (w.next(a)) {
     const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
     bool set = false;  // whether there are references
+#pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i) {
       wait(&sh.s_full[g], mine & 1);
       tc_fence_after();
@@ -638,7 +645,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
     if (whole) {
       named_sync(1 + g, 128);
       uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD;
-#pragma unroll 4
+#pragma unroll 2
       for (int e = row; e < live * (kD / 8); e += 128)
         *reinterpret_cast<uint4*>(out + e * 8) = *reinterpret_cast<const uint4*>(turned + e * 8);
     } else if (row == 0 && w.i0 == 0) {
@@ -681,9 +688,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
   const int units = a.c.num_kv_heads * k.l.blocks;
-  find_ranges<kWideThreads, kPos, 2>(k, sh.r, units);
+  const bool none = find_ranges<kWideThreads, kPos, 2>(k, sh.r, units);
   tc_fence_after();
-  write_empty_rows<kD, kWideThreads>(a);
+  if (none) write_empty_rows<kD, kWideThreads>(a);
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
     if (warp == 0) wide_scores(k, sh, b, tmem);

@@ -93,6 +93,8 @@ int ci_attn_decode(const uint16_t* q, int64_t q_stride, int32_t rows, int32_t nu
   if (q_stride % 8 != 0 || out_stride % 8 != 0) return CI_ERR_ALIGN;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 16)) return CI_ERR_ALIGN;
   if (ws_bytes < ci::attn_workspace_bytes(rows, num_q_heads, num_kv_heads, head_dim)) return CI_ERR_SHAPE;
+  const int64_t tiles = (pos != nullptr ? npos : max_len) / CI_PAGE + 1, blocks = (num_q_heads / num_kv_heads + 63) / 64;
+  if (tiles * num_kv_heads * blocks > INT32_MAX / rows) return CI_ERR_RANGE;
   const ci::AttnArgs a{{const_cast<uint8_t*>(k_pool), const_cast<uint8_t*>(v_pool), num_pages,
                         cache_format == CI_CACHE_FP8, num_q_heads, num_kv_heads, head_dim, page_table, max_pages,
                         layout, req_row_start, num_req, dev_err},

@@ -9,6 +9,7 @@ namespace ci {
 // The request of row t; -1 (reported) where the row starts name none.
 static __device__ __noinline__ int row_request_varlen(const CacheArgs& c, int t) {
   int lo = 0, hi = c.num_req;  // the last r with req_start[r] <= t
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (c.req_start[mid] <= t)
