@@ -155,7 +155,8 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
     e = make_rows_tmap(&vmap, c.v_pool, c.num_pages * c.num_kv_heads * per_page, row, attn::kTile);
   if (e == cudaSuccess)
     e = wide ? attn::launch_wide(kmap, vmap, k, stream) : c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
-  if (e != cudaSuccess) return e;
+  // a unit of one tile has nothing to join
+  if (e != cudaSuccess || (a.pos != nullptr ? a.npos : a.max_len) <= (wide ? 2 : 1) * attn::kTile) return e;
   return c.head_dim == 64    ? launch_join<64>(k, stream)
          : c.head_dim == 128 ? launch_join<128>(k, stream)
                              : launch_join<256>(k, stream);

@@ -98,16 +98,17 @@ __device__ __forceinline__ Scan cluster_scan(cg::cluster_group& cl, int mine, in
 }
 
 // Exclusive prefix of need(i), i < n, into prefix[0 .. n]; returns prefix[n].
+// A thread takes as few neighbours as n allows: each is a chain of loads.
 template <class Need>
 __device__ int64_t demand_prefix(int n, int64_t* prefix, int64_t* wsum, Need need) {
-  constexpr int kPer = kMaxDemands / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t v[kPer], local = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    v[j] = i < n ? need(i) : 0;
-    local += v[j];
+  const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  int64_t local = 0;
+#pragma unroll 2
+  for (int i = i0; i < i1; ++i) {
+    const int64_t v = need(i);
+    prefix[i] = v;
+    local += v;
   }
   int64_t incl = local;
 #pragma unroll
@@ -117,18 +118,16 @@ __device__ int64_t demand_prefix(int n, int64_t* prefix, int64_t* wsum, Need nee
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
+  int64_t run = incl - local, total = 0;
+#pragma unroll 4
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += wsum[w];
+    if (w < warp) run += wsum[w];
     total += wsum[w];
   }
-  int64_t run = before + incl - local;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    if (i < n) prefix[i] = run;
-    run += v[j];
+  for (int i = i0; i < i1; ++i) {
+    const int64_t v = prefix[i];
+    prefix[i] = run;
+    run += v;
   }
   if (tid == 0) prefix[n] = total;
   __syncthreads();
