@@ -23,47 +23,69 @@ Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, bo
 
 // With the parts' maxima m_i, sums l_i and unnormalised sums o_i:
 //   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
-// CTA (x, y) takes the x-th split unit and 16 / ways of its heads; a head's
-// parts are dealt to `ways` warps, whose sums are added in order.  Bound by
-// the latency of its loads (the parts sit in L2), so few parts per warp.
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int ways) {
-  constexpr int kPer = D / 32;
+// CTA (x, y) takes a split unit and 16 / ways of its heads; a head's parts are
+// dealt to `ways` warps, whose sums are added in order.  x is a unit, or, where
+// units outnumber workers, the worker in whose range one starts and goes on.
+// Bound by latency (the parts sit in L2): which parts a unit has is worked out
+// before the wait for the main kernel, and sums and statistics are fetched
+// together.  (Joining in the main kernel, by the CTA that comes last, took 6 us
+// more: its code is cold there.)
+template <int D, int kT>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int ways, bool by_unit) {
+  constexpr int kPer = D / 32, kFetch = 4;
   __shared__ float sums[kJoinWarps][D];
-  __shared__ int counts[kJoinWarps], starts;
+  __shared__ int32_t warp_sum[2][kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) starts = -1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the CTA in whose range the x-th split unit starts
-  int seen = 0;
-  for (int c0 = 0; c0 < k.l.ctas; c0 += 32 * kJoinWarps) {
-    const bool one = c0 + tid < k.l.ctas && k.part[c0 + tid].last >= 0;
-    const uint32_t b = __ballot_sync(0xffffffffu, one);
-    if (lane == 0) counts[warp] = __popc(b);
+  const int units = k.a.c.num_kv_heads * k.l.blocks;
+  Part p{0, 0, -1, 0};
+  int first = blockIdx.x;
+  if (by_unit) {  // at most as many units as workers: at most one row per thread
+    p.row = blockIdx.x / units;
+    p.unit = blockIdx.x - p.row * units;
+    const int mine = tid < k.a.rows ? attn::row_tiles<kT>(k.a, tid) : 0;
+    const int all = __reduce_add_sync(0xffffffffu, mine), before = __reduce_add_sync(0xffffffffu, tid < p.row ? mine : 0);
+    if (lane == 0) warp_sum[0][warp] = all, warp_sum[1][warp] = before;
     __syncthreads();
-    int before = seen + __popc(b & lanemask_lt());
+    int total = 0, start = 0;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) before += counts[w];
-      seen += counts[w];
-    }
-    if (one && before == static_cast<int>(blockIdx.x)) starts = c0 + tid;
-    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) total += warp_sum[0][w], start += warp_sum[1][w];
+    const int n = attn::row_tiles<kT>(k.a, p.row);
+    if (n == 0) return;
+    attn::Range r{};
+    r.total = total * units;
+    r.workers = min(k.l.ctas, r.total);
+    start = start * units + p.unit * n;
+    first = attn::worker_of(start, r);
+    p.last = attn::worker_of(start + n - 1, r);
+    if (p.last == first) return;  // one worker had it all, and has written the result
   }
-  const int first = starts;
-  if (first < 0) return;
-  const Part p = k.part[first];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!by_unit) {
+    p = k.part[first];
+    if (p.last < 0) return;
+  }
   const int hw = warp / ways, way = warp - hw * ways;
   const int heads = k.l.heads, h = blockIdx.y * (kJoinWarps / ways) + hw;
   const int head = p.unit / k.l.blocks, hb = p.unit - head * k.l.blocks;
   const bool live = h < heads && hb * heads + h < k.l.group;
   const int n = p.last - first + 1;
-  auto slot = [&](int i) -> int64_t { return i == 0 ? 2ll * first + 1 : 2ll * (first + i); };
+  auto slot = [&](int i) { return attn::slot_of(first + i, i == 0); };
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) o[j] = 0.f;
   if (live) {
     const float2* stat = reinterpret_cast<const float2*>(k.stat) + h;
+    // the warp's first parts, under way before the statistics are needed
+    float x[kFetch][kPer], mx[kFetch];
+#pragma unroll
+    for (int f = 0; f < kFetch; ++f) {
+      const int i = way + f * ways;
+      mx[f] = -INFINITY;
+      if (i >= n) continue;
+      mx[f] = stat[slot(i) * heads].x;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[f][j] = k.sum[(slot(i) * heads + h) * D + lane + 32 * j];
+    }
     for (int i = lane; i < n; i += 32) {
       const float2 st = stat[slot(i) * heads];
       const float top = fmaxf(m, st.x), ref = top == -INFINITY ? 0.f : top;
@@ -78,27 +100,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int
     m = top;
 #pragma unroll
     for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+#pragma unroll
+    for (int f = 0; f < kFetch; ++f) {
+      if (way + f * ways >= n) continue;
+      const float g = attn::exp2_approx(mx[f] - ref);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[j] += g * x[f][j];
+    }
 #pragma unroll 4
-    for (int i = way; i < n; i += ways) {
+    for (int i = way + kFetch * ways; i < n; i += ways) {
       const float f = attn::exp2_approx(stat[slot(i) * heads].x - ref);
       const float* src = k.sum + (slot(i) * heads + h) * D + lane;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) o[j] += f * src[32 * j];
     }
   }
+  if (ways > 1) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) sums[warp][32 * j + lane] = o[j];
-  __syncthreads();
-  if (!live || way != 0) return;
+    for (int j = 0; j < kPer; ++j) sums[warp][32 * j + lane] = o[j];
+    __syncthreads();
+    if (!live || way != 0) return;
+#pragma unroll 1
+    for (int x = 1; x < ways; ++x)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[j] += sums[warp + x][32 * j + lane];
+  }
+  if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t qh = static_cast<int64_t>(head) * k.l.group + hb * heads + h;
   uint16_t* dst = k.a.out + p.row * k.a.out_stride + qh * D;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    float v = 0.f;
-    for (int x = 0; x < ways; ++x) v += sums[warp + x][32 * j + lane];
-    dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v * inv));
-  }
+  for (int j = 0; j < kPer; ++j) dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j] * inv));
   if (k.a.lse != nullptr && lane == 0)
     k.a.lse[static_cast<int64_t>(p.row) * k.a.c.num_q_heads + qh] =
         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -107,12 +139,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int
 int64_t part_bytes(const Layout& l) { return (static_cast<int64_t>(l.ctas) * sizeof(Part) + 15) / 16 * 16; }
 int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.heads * 2 * 4; }
 
-template <int D>
+template <int D, int kT>
 cudaError_t launch_join(const Args& k, cudaStream_t stream) {
-  // Units number rows * kv heads * blocks; at most one starts unfinished in a
-  // CTA's range.  The fewer units, the more parts each: 16, 4 or 1 warps a head.
+  // The fewer units, the more parts each: 16, 4 or 1 warps a head.
   const int64_t units = static_cast<int64_t>(k.a.rows) * k.a.c.num_kv_heads * k.l.blocks;
-  const int64_t split = units < k.l.ctas ? units : k.l.ctas, parts = k.l.ctas / split + 1;
+  const bool by_unit = units <= k.l.ctas && k.a.rows <= 32 * kJoinWarps;
+  const int64_t split = by_unit ? units : k.l.ctas, parts = k.l.ctas / (units < k.l.ctas ? units : k.l.ctas) + 1;
   const int ways = parts > 16 ? 16 : parts > 4 ? 4 : 1, per = kJoinWarps / ways;
   const int heads = k.l.heads < k.l.group ? k.l.heads : k.l.group;
   cudaLaunchConfig_t cfg{};
@@ -124,7 +156,7 @@ cudaError_t launch_join(const Args& k, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, k, ways);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, kT>, k, ways, by_unit);
 }
 
 }  // namespace
@@ -157,9 +189,10 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
     e = wide ? attn::launch_wide(kmap, vmap, k, stream) : c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
   // a unit of one tile has nothing to join
   if (e != cudaSuccess || (a.pos != nullptr ? a.npos : a.max_len) <= (wide ? 2 : 1) * attn::kTile) return e;
-  return c.head_dim == 64    ? launch_join<64>(k, stream)
-         : c.head_dim == 128 ? launch_join<128>(k, stream)
-                             : launch_join<256>(k, stream);
+  if (wide) return launch_join<128, 2 * attn::kTile>(k, stream);
+  return c.head_dim == 64    ? launch_join<64, attn::kTile>(k, stream)
+         : c.head_dim == 128 ? launch_join<128, attn::kTile>(k, stream)
+                             : launch_join<256, attn::kTile>(k, stream);
 }
 
 }  // namespace ci

@@ -304,14 +304,20 @@ template <int kT>
 __device__ __forceinline__ Walk<kT> walk_of(const AttnArgs& a, const Range& r, int units) {
   return Walk<kT>{r.end - r.first, r.row, r.unit, r.tile, r.first < r.end ? row_tiles<kT>(a, r.row) : 0, units, 0, 0};
 }
+// The worker that has tile x of the list.
+__device__ __forceinline__ int worker_of(int x, const Range& r) {
+  const int per = r.total / r.workers, rest = r.total - per * r.workers, longer = rest * (per + 1);
+  return x < longer ? x / (per + 1) : rest + (x - longer) / per;
+}
 // What a worker leaves behind for the unit that goes on past its range: the
 // unit, and the worker that has its last tile.
 template <int kT>
 __device__ __forceinline__ Part part_of(const Walk<kT>& w, const Range& r) {
-  const int last = r.end - 1 + w.n - w.i1;  // (the segment ends where the range does)
-  const int per = r.total / r.workers, rest = r.total - per * r.workers, longer = rest * (per + 1);
-  return Part{w.row, w.unit, last < longer ? last / (per + 1) : rest + (last - longer) / per, 0};
+  return Part{w.row, w.unit, worker_of(r.end - 1 + w.n - w.i1, r), 0};  // (the segment ends where the range does)
 }
+// Where a worker keeps its part of a unit: the unit's first part is the last
+// segment of its worker's range, every other one a first segment.
+__host__ __device__ __forceinline__ int64_t slot_of(int worker, bool begins) { return 2ll * worker + (begins ? 1 : 0); }
 
 // A bounded wait of a whole warp for phase `parity`; false once it, or another
 // warp of the CTA, has given up (reported once).
@@ -826,7 +832,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         if (whole) keep[nt][e] *= sum == 0.f ? 0.f : 1.f / sum;
         if (wp == 0 && g == 0) {
           if (!whole) {
-            const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
+            const int64_t slot = slot_of(blockIdx.x, w.i0 == 0);
             float* st = k.stat + (slot * C::kHeadsU + h) * 2;
             st[0] = m;
             st[1] = sum;
@@ -864,8 +870,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         *reinterpret_cast<uint4*>(dst + h * D + d) = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
       }
     } else {
-      const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
-      float* dst = k.sum + slot * C::kHeadsU * D;
+      float* dst = k.sum + slot_of(blockIdx.x, w.i0 == 0) * C::kHeadsU * D;
 #pragma unroll 1
       for (int e = tid; e < live * (D / 4); e += C::kConsumers) {
         const int h = e / (D / 4), d = e % (D / 4) * 4;
