@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) append_kernel(const A
   const int o0 = kNeox && turns ? 4 * m : 8 * m, o1 = kNeox && turns ? half + 4 * m : 8 * m + 4;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   int t = static_cast<int>(task / n.all), chunk = static_cast<int>(task - static_cast<int64_t>(t) * n.all);
+  wait_predecessor();
   if (t >= a.tokens) return;
   Loaded now;
   load_task<D>(a, n, t, chunk, o0, o1, sub, now);
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) append_kernel(const A
 }
 
 template <int D>
-void launch_d(const AppendArgs& a, cudaStream_t stream) {
+cudaError_t launch_d(const AppendArgs& a, cudaStream_t stream) {
   constexpr int kHeads = kBatch * (32 / (D / 8));  // of a task
   const int qc = (a.c.num_q_heads + kHeads - 1) / kHeads, kc = (a.c.num_kv_heads + kHeads - 1) / kHeads;
   const int all = qc + 2 * kc;
@@ -266,29 +267,19 @@ void launch_d(const AppendArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
   const int warps = static_cast<int>(grid) * kWarps;
   const Chunks n{qc, qc + kc, all, warps / all, warps % all};
-  if (a.c.fp8) {
-    if (a.neox)
-      append_kernel<D, true, true><<<grid, 32 * kWarps, 0, stream>>>(a, n);
-    else
-      append_kernel<D, true, false><<<grid, 32 * kWarps, 0, stream>>>(a, n);
-  } else {
-    if (a.neox)
-      append_kernel<D, false, true><<<grid, 32 * kWarps, 0, stream>>>(a, n);
-    else
-      append_kernel<D, false, false><<<grid, 32 * kWarps, 0, stream>>>(a, n);
-  }
+  const dim3 ctas3(grid);
+  constexpr int kThreads = 32 * kWarps;
+  if (a.c.fp8)
+    return a.neox ? launch_after(append_kernel<D, true, true>, ctas3, kThreads, 0, stream, a, n)
+                  : launch_after(append_kernel<D, true, false>, ctas3, kThreads, 0, stream, a, n);
+  return a.neox ? launch_after(append_kernel<D, false, true>, ctas3, kThreads, 0, stream, a, n)
+                : launch_after(append_kernel<D, false, false>, ctas3, kThreads, 0, stream, a, n);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
-  if (a.c.head_dim == 64)
-    launch_d<64>(a, stream);
-  else if (a.c.head_dim == 128)
-    launch_d<128>(a, stream);
-  else
-    launch_d<256>(a, stream);
-  return cudaGetLastError();
+  return a.c.head_dim == 64 ? launch_d<64>(a, stream) : a.c.head_dim == 128 ? launch_d<128>(a, stream) : launch_d<256>(a, stream);
 }
 
 }  // namespace ci

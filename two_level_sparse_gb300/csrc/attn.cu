@@ -50,20 +50,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k, int
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) total += warp_sum[0][w], start += warp_sum[1][w];
     const int n = attn::row_tiles<kT>(k.a, p.row);
-    if (n == 0) return;
-    attn::Range r{};
-    r.total = total * units;
-    r.workers = min(k.l.ctas, r.total);
-    start = start * units + p.unit * n;
-    first = attn::worker_of(start, r);
-    p.last = attn::worker_of(start + n - 1, r);
-    if (p.last == first) return;  // one worker had it all, and has written the result
+    if (n > 0) {
+      attn::Range r{};
+      r.total = total * units;
+      r.workers = min(k.l.ctas, r.total);
+      start = start * units + p.unit * n;
+      first = attn::worker_of(start, r);
+      p.last = attn::worker_of(start + n - 1, r);
+      if (p.last == first) p.last = -1;  // one worker had it all, and has written the result
+    }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!by_unit) {
-    p = k.part[first];
-    if (p.last < 0) return;
-  }
+  release_successor();
+  wait_predecessor();  // (every CTA: this kernel must not end before the main one)
+  if (!by_unit) p = k.part[first];
+  if (p.last < 0) return;
   const int hw = warp / ways, way = warp - hw * ways;
   const int heads = k.l.heads, h = blockIdx.y * (kJoinWarps / ways) + hw;
   const int head = p.unit / k.l.blocks, hb = p.unit - head * k.l.blocks;
@@ -145,18 +145,10 @@ cudaError_t launch_join(const Args& k, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(k.a.rows) * k.a.c.num_kv_heads * k.l.blocks;
   const bool by_unit = units <= k.l.ctas && k.a.rows <= 32 * kJoinWarps;
   const int64_t split = by_unit ? units : k.l.ctas, parts = k.l.ctas / (units < k.l.ctas ? units : k.l.ctas) + 1;
-  const int ways = parts > 16 ? 16 : parts > 4 ? 4 : 1, per = kJoinWarps / ways;
+  const int ways = parts > 32 ? 16 : parts > 4 ? 4 : 1, per = kJoinWarps / ways;
   const int heads = k.l.heads < k.l.group ? k.l.heads : k.l.group;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(split), (heads + per - 1) / per);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, kT>, k, ways, by_unit);
+  return launch_after(join_kernel<D, kT>, dim3(static_cast<unsigned>(split), (heads + per - 1) / per), 32 * kJoinWarps, 0,
+                      stream, k, ways, by_unit);
 }
 
 }  // namespace

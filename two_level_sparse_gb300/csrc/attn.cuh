@@ -902,8 +902,9 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     }
     fence_mbar_init();
     sh.abort = 0;
-    k.part[blockIdx.x].last = -1;
   }
+  wait_predecessor();
+  if (tid == 0) k.part[blockIdx.x].last = -1;
   const int units = a.c.num_kv_heads * k.l.blocks;
   if (find_ranges<C::kThreads, kTile, 1>(k, sh.r, units)) write_empty_rows<D, C::kThreads>(a);
   const Range r = sh.r.range[0];
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     else if (warp == WP * WH)
       produce_pages<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_successor();
 }
 
 template <int D, bool kFp8, int NT, int WP, int WH>
@@ -934,8 +935,7 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args&
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev] = true;
   }
-  fn<<<k.l.ctas, C::kThreads, C::kSmem, stream>>>(kmap, vmap, k);
-  return cudaGetLastError();
+  return launch_after(fn, dim3(k.l.ctas), C::kThreads, C::kSmem, stream, kmap, vmap, k);
 }
 
 // The instance for a head size and a padded number of heads per unit.

@@ -683,8 +683,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int s = 0; s < kVSlots; ++s) mbar_init(&sh.v_full[s], a.pos != nullptr ? 64 : 1), mbar_init(&sh.v_empty[s], 1);
     fence_mbar_init();
     sh.abort = 0;
-    k.part[2 * blockIdx.x].last = k.part[2 * blockIdx.x + 1].last = -1;
   }
+  wait_predecessor();
+  if (tid < 2) k.part[2 * blockIdx.x + tid].last = -1;
   if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
   const int units = a.c.num_kv_heads * k.l.blocks;
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __syncthreads();
   if (sh.abort != 0 && warp == 0) drain_copies(sh);
   if (warp == 1) tmem_dealloc(tmem, kTmem);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_successor();
 }
 
 }  // namespace
@@ -729,8 +730,7 @@ cudaError_t launch_wide(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev] = true;
   }
-  attn_wide_kernel<<<k.l.ctas / 2, kWideThreads, kWideSmem, stream>>>(kmap, vmap, k);
-  return cudaGetLastError();
+  return launch_after(attn_wide_kernel, dim3(k.l.ctas / 2), kWideThreads, kWideSmem, stream, kmap, vmap, k);
 }
 
 }  // namespace attn

@@ -6,6 +6,28 @@
 
 namespace ci {
 
+// Every kernel of the cache is launched to begin while its predecessor in the
+// stream ends (programmatic dependent launch), and waits here for that one's
+// results before it touches global memory.
+__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the successor's CTAs be scheduled; it still waits for this kernel's end.
+__device__ __forceinline__ void release_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // The request of row t; -1 (reported) where the row starts name none.
 static __device__ __noinline__ int row_request_varlen(const CacheArgs& c, int t) {
   int lo = 0, hi = c.num_req;  // the last r with req_start[r] <= t

@@ -196,6 +196,7 @@ __device__ __forceinline__ bool length_ok(const PagesArgs& p, int len) {
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     alloc_kernel(const PagesArgs p, const int32_t* old_len, const int32_t* new_len) {
+  wait_predecessor();
   __shared__ AllocShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int64_t wanted = demand_prefix(p.num_req, sh.prefix, sh.dsum, [&](int r) -> int64_t {
@@ -233,6 +234,7 @@ __device__ __forceinline__ int fork_tail(const ForkArgs& a, int i, bool tell) {
 // share the full pages (references only ever rise there, so a page that is
 // free to cluster 0 stays free: no order between the two is needed).
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
+  wait_predecessor();
   const PagesArgs& p = a.p;
   if (blockIdx.x < kCluster) {
     __shared__ AllocShared sh;
@@ -273,6 +275,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
 }
 
 __global__ void __launch_bounds__(kThreads) free_kernel(const PagesArgs p, const int32_t* req, int n) {
+  wait_predecessor();
   const int64_t entries = static_cast<int64_t>(n) * p.max_pages;
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < entries; e += threads) {
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PagesArgs p, const
 // With P(i) the number of live ids below i and n the live ids in all: the
 // free id i < n is hole i - P(i), the live id i >= n is mover P(i) - P(n).
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
+  wait_predecessor();
   __shared__ int wsum[kWarps], ctot, below;  // below: P(n), in the CTA whose range holds id n
   const PagesArgs& p = a.p;
   cg::cluster_group cl = cg::this_cluster();
@@ -357,6 +361,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
 // The second half of a compaction, over the whole card: the page table's
 // entries, and the -1 behind the pairs.
 __global__ void __launch_bounds__(kThreads) remap_kernel(const CompactArgs a) {
+  wait_predecessor();
   const PagesArgs& p = a.p;
   const int64_t entries = static_cast<int64_t>(p.num_req) * p.max_pages, moves = *a.count;
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
@@ -376,6 +381,7 @@ constexpr int64_t kCopyChunk = kCopyThreads * kCopyLoads * 16;  // bytes per CTA
 
 // One chunk of one page of one pool at a time.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a, int64_t chunks_per_pair) {
+  wait_predecessor();
   const int64_t n = a.count != nullptr ? min(a.n, *a.count) : a.n;
   for (int64_t c = blockIdx.x; c < n * chunks_per_pair; c += gridDim.x) {
     const int64_t i = c / chunks_per_pair;
@@ -416,36 +422,32 @@ unsigned grid_for(int64_t work, int per_cta, int ctas_per_sm) {
 }  // namespace
 
 cudaError_t launch_pages_alloc(const PagesArgs& p, const int32_t* old_len, const int32_t* new_len, cudaStream_t stream) {
-  alloc_kernel<<<kCluster, kThreads, 0, stream>>>(p, old_len, new_len);
-  return cudaGetLastError();
+  return launch_after(alloc_kernel, dim3(kCluster), kThreads, 0, stream, p, old_len, new_len);
 }
 
 cudaError_t launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
   const unsigned share = grid_for(static_cast<int64_t>(a.n) * a.p.max_pages, kThreads, 2);
   const unsigned clusters = 1 + (share + kCluster - 1) / kCluster;
-  fork_kernel<<<clusters * kCluster, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(fork_kernel, dim3(clusters * kCluster), kThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_free(const PagesArgs& p, const int32_t* req, int32_t n, cudaStream_t stream) {
-  free_kernel<<<grid_for(static_cast<int64_t>(n) * p.max_pages, kThreads, 2), kThreads, 0, stream>>>(p, req, n);
-  return cudaGetLastError();
+  return launch_after(free_kernel, dim3(grid_for(static_cast<int64_t>(n) * p.max_pages, kThreads, 2)), kThreads, 0, stream, p,
+                      req, n);
 }
 
 cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream) {
-  compact_kernel<<<kCluster, kThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(compact_kernel, dim3(kCluster), kThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   const int64_t entries = static_cast<int64_t>(a.p.num_req) * a.p.max_pages;
-  remap_kernel<<<grid_for(entries > a.p.num_pages ? entries : a.p.num_pages, kThreads, 2), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(remap_kernel, dim3(grid_for(entries > a.p.num_pages ? entries : a.p.num_pages, kThreads, 2)), kThreads, 0,
+                      stream, a);
 }
 
 cudaError_t launch_pages_copy(const CopyArgs& a, cudaStream_t stream) {
   int64_t per_pair = 0;
   for (int i = 0; i < a.num_pools; ++i) per_pair += (a.page_bytes[i] + kCopyChunk - 1) / kCopyChunk;
-  copy_kernel<<<grid_for(a.n * per_pair, 1, 8), kCopyThreads, 0, stream>>>(a, per_pair);
-  return cudaGetLastError();
+  return launch_after(copy_kernel, dim3(grid_for(a.n * per_pair, 1, 8)), kCopyThreads, 0, stream, a, per_pair);
 }
 
 }  // namespace ci
