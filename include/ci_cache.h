@@ -63,9 +63,11 @@ CI_API int64_t ci_cache_page_bytes(int32_t cache_format, int32_t head_dim);
  * outside [0, num_pages) drops its positions and sets CI_DEVERR_PAGE.
  *
  * Products are exact and accumulated in fp32; the softmax statistics are fp32;
- * the probabilities are rounded to bf16 for the product with the values (the
- * sum that divides them is not); out is rounded once.  Results do not depend
- * on the order in which blocks run.  FP8 scales: finite, |scale| <= 2^60.
+ * the probabilities are rounded to bf16 for the product with the values (FP8:
+ * with the value's scale in them) and divided by the sum of what they were
+ * rounded to, so that the error left is that of their ratios; lse has the sum
+ * of the unrounded ones; out is rounded once.  Results do not depend on the
+ * order in which blocks run.  FP8 scales: finite, |scale| <= 2^60.
  *
  * q, out: bf16 [rows][num_q_heads][D] with row strides in elements (multiples
  * of 8); q and out 16-byte aligned.  lse: float [rows][num_q_heads] or NULL.

@@ -19,6 +19,11 @@
 //                 positions is a reduction over registers and three shuffles;
 //   O^T += V^T P^T  A = V transposed by ldmatrix, B = P transposed in
 //                 registers (movmatrix).
+// P is rounded to bf16 for the second product, an error of its size of 2^-9 for
+// the positions that carry a row.  The sum that divides O is that of the rounded
+// P, so that it cancels for a position that carries the row alone; the one that
+// the row's statistics keep is of the unrounded P, and O is scaled from the one
+// to the other at a segment's end.
 // Positions sit on the 16-wide side of the MMA and heads on the 8-wide one, so
 // that a group of 8 query heads wastes nothing; a cache read at the HBM's rate
 // (64 positions x D = 128 in bf16 per 1400 cycles and SM) needs 128 x G / 8 of
@@ -112,6 +117,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -626,7 +636,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         }
       }
     }
-    float o[NT][kM][4], top[NT][2], l[NT][2];
+    float o[NT][kM][4], top[NT][2], l[NT][2], lr[NT][2];  // lr: the sums of P as it is rounded
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -634,7 +644,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.f;
       top[nt][0] = top[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = lr[nt][0] = lr[nt][1] = 0.f;
     }
 #pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i) {
@@ -721,6 +731,7 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
               keep[e] = now[nt][e] > top[nt][e] ? exp2_approx(top[nt][e] - now[nt][e]) : 1.f;
               top[nt][e] = now[nt][e];
               l[nt][e] *= keep[e];
+              lr[nt][e] *= keep[e];
             }
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
@@ -754,6 +765,8 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
               if (!((mask >> (p + g + 8)) & 1)) vb = 0.f;
             }
           }
+          // FP8: P is rounded with the value's scale in it
+          const float ia = !kFp8 || va == 0.f ? 0.f : rcp_approx(va), ib = !kFp8 || vb == 0.f ? 0.f : rcp_approx(vb);
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -766,9 +779,20 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
             v[3] = exp2_approx(v[3] - t1);
             l[nt][0] += v[0] + v[2];
             l[nt][1] += v[1] + v[3];
-            if (kFp8) v[0] *= va, v[1] *= va, v[2] *= vb, v[3] *= vb;
-            b0[nt] = transpose8x8(bf16x2(v[0], v[1]));
-            b1[nt] = transpose8x8(bf16x2(v[2], v[3]));
+            if (kFp8) {
+              const float w0 = v[0] * va, w1 = v[1] * va, w2 = v[2] * vb, w3 = v[3] * vb;
+              b0[nt] = bf16x2(w0, w1);
+              b1[nt] = bf16x2(w2, w3);
+              lr[nt][0] += fmaf(bf16_lo(b0[nt]) - w0, ia, v[0]) + fmaf(bf16_lo(b1[nt]) - w2, ib, v[2]);
+              lr[nt][1] += fmaf(bf16_hi(b0[nt]) - w1, ia, v[1]) + fmaf(bf16_hi(b1[nt]) - w3, ib, v[3]);
+            } else {
+              b0[nt] = bf16x2(v[0], v[1]);
+              b1[nt] = bf16x2(v[2], v[3]);
+              lr[nt][0] += bf16_lo(b0[nt]) + bf16_lo(b1[nt]);
+              lr[nt][1] += bf16_hi(b0[nt]) + bf16_hi(b1[nt]);
+            }
+            b0[nt] = transpose8x8(b0[nt]);
+            b1[nt] = transpose8x8(b1[nt]);
           }
           if (kFp8) {
 #pragma unroll
@@ -806,7 +830,10 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int b = 4; b < 32; b <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], b);
+        for (int b = 4; b < 32; b <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], b);
+          lr[nt][e] += __shfl_xor_sync(0xffffffffu, lr[nt][e], b);
+        }
         if (g == 0) {
           const int h = wh * 8 * NT + nt * 8 + 2 * q + e;
           stat[(wp * C::kHeadsU + h) * 2] = top[nt][e];
@@ -828,7 +855,8 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
 #pragma unroll
         for (int x = 0; x < WP; ++x)
           sum += stat[(x * C::kHeadsU + h) * 2 + 1] * exp2_approx(stat[(x * C::kHeadsU + h) * 2] - ref);
-        keep[nt][e] = exp2_approx(top[nt][e] - ref) * (kFp8 ? kTwo60 : 1.f);
+        // (lr is 0 only with l)
+        keep[nt][e] = exp2_approx(top[nt][e] - ref) * (kFp8 ? kTwo60 : 1.f) * (lr[nt][e] == 0.f ? 1.f : l[nt][e] / lr[nt][e]);
         if (whole) keep[nt][e] *= sum == 0.f ? 0.f : 1.f / sum;
         if (wp == 0 && g == 0) {
           if (!whole) {

@@ -38,7 +38,8 @@ constexpr int kD = 128, kH = 64, kPos = 128;
 constexpr int kVSlots = 3, kSlots = 2 + kVSlots, kSlot = kPos * kD * 2;  // a K slot per worker, then V's
 constexpr int kPBytes = kPos * kH * 2, kQBytes = kH * kD * 2;
 constexpr int kWideThreads = 512;
-constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256;  // S, O and the sums of worker g at + 64 g
+// of worker g, at + 64 g: S, O, the sums of P, those of P as it is rounded
+constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256, kColR = 384;
 constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
 constexpr float kSlack = 40.f;
 
@@ -117,14 +118,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -477,7 +475,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kH * g;  // this warp's, at the worker's columns
   const float factor = a.scale * kLog2e;
   const Range range = sh.r.range[g];
-  float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][kH], while no product reads the probabilities
+  float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][2 kH], while no product reads the probabilities
   float *ref = sh.ref[g], *alpha = sh.alpha[g];
   const int worker = range.worker;
   Waiter wait{sh, a.c.dev_err};
@@ -547,9 +545,9 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
         if (i > w.i0) {  // what the segment has so far
           tc_fence_after();
 #pragma unroll 1
-          for (int h = 0; h < 2 * kH; h += 8) {
+          for (int h = 0; h < 3 * kH; h += 8) {  // O and both sums: 2 kH columns apart
             uint32_t o[8];
-            const uint32_t at = lanes + (h < kH ? kColO + h : kColL + h - kH);
+            const uint32_t at = lanes + kColO + h + (h / kH) * kH;
             tmem_ld8(at, o);
             tmem_ld_wait();
 #pragma unroll
@@ -562,27 +560,37 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
       uint8_t* prow = pmem + g * kPBytes + row * 128;
 #pragma unroll 1
       for (int h = 0; h < kH; h += 32) {
-        uint32_t s[32], l[32];
+        uint32_t s[32];
         tmem_ld32(lanes + kColS + h, s);
-        tmem_ld32(lanes + kColL + h, l);
         tmem_ld_wait();
         const bool fresh = i == w.i0;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t v[4];
+        for (int j0 = 0; j0 < 32; j0 += 16) {
+          uint32_t l[16], lr[16];
+          tmem_ld16(lanes + kColL + h + j0, l);
+          tmem_ld16(lanes + kColR + h + j0, lr);
+          tmem_ld_wait();
 #pragma unroll
-          for (int x = 0; x < 8; x += 2) {
-            const float2 r = *reinterpret_cast<const float2*>(ref + h + j + x);
-            float p0 = exp2_approx(fmaf(__uint_as_float(s[j + x]), factor, -r.x));
-            float p1 = exp2_approx(fmaf(__uint_as_float(s[j + x + 1]), factor, -r.y));
-            if (!valid) p0 = p1 = 0.f;
-            v[x / 2] = bf16x2(p0, p1);
-            l[j + x] = __float_as_uint(fresh ? p0 : __uint_as_float(l[j + x]) + p0);
-            l[j + x + 1] = __float_as_uint(fresh ? p1 : __uint_as_float(l[j + x + 1]) + p1);
+          for (int j = 0; j < 16; j += 8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int x = 0; x < 8; x += 2) {
+              const float2 r = *reinterpret_cast<const float2*>(ref + h + j0 + j + x);
+              float p0 = exp2_approx(fmaf(__uint_as_float(s[j0 + j + x]), factor, -r.x));
+              float p1 = exp2_approx(fmaf(__uint_as_float(s[j0 + j + x + 1]), factor, -r.y));
+              if (!valid) p0 = p1 = 0.f;
+              v[x / 2] = bf16x2(p0, p1);
+              const float r0 = bf16_lo(v[x / 2]), r1 = bf16_hi(v[x / 2]);
+              l[j + x] = __float_as_uint(fresh ? p0 : __uint_as_float(l[j + x]) + p0);
+              l[j + x + 1] = __float_as_uint(fresh ? p1 : __uint_as_float(l[j + x + 1]) + p1);
+              lr[j + x] = __float_as_uint(fresh ? r0 : __uint_as_float(lr[j + x]) + r0);
+              lr[j + x + 1] = __float_as_uint(fresh ? r1 : __uint_as_float(lr[j + x + 1]) + r1);
+            }
+            *reinterpret_cast<uint4*>(prow + ((((h + j0 + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
-          *reinterpret_cast<uint4*>(prow + ((((h + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          tmem_st16(lanes + kColL + h + j0, l);
+          tmem_st16(lanes + kColR + h + j0, lr);
         }
-        tmem_st32(lanes + kColL + h, l);
       }
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -593,9 +601,9 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
     }
     // ---- the segment's end: sums over the positions, the result
 #pragma unroll 1
-    for (int h = 0; h < kH; h += 32) {
+    for (int h = 0; h < 2 * kH; h += 32) {  // the sums of P, then those of P as it is rounded
       uint32_t l[32];
-      tmem_ld32(lanes + kColL + h, l);
+      tmem_ld32(lanes + kColL + h + (h & kH), l);
       tmem_ld_wait();
       fold<16, 16>(l, lane);
       fold<8, 8>(l, lane);
@@ -606,16 +614,18 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
         wait(&sh.pv_done[g], (mine - 1) & 1);
         tc_fence_after();
       }
-      scratch[quad * kH + h + lane] = __uint_as_float(l[0]);  // lane bits 16 .. 1 chose heads + 16 .. + 1
+      scratch[quad * 2 * kH + h + lane] = __uint_as_float(l[0]);  // lane bits 16 .. 1 chose heads + 16 .. + 1
     }
     named_sync(1 + g, 128);
     const bool whole = w.i0 == 0 && w.i1 == w.n;
     const int64_t slot = 2ll * worker + (w.i0 == 0 ? 1 : 0);
     if (row < kH) {
       const int h = row;
-      const float total = (scratch[h] + scratch[kH + h]) + (scratch[2 * kH + h] + scratch[3 * kH + h]);
+      const float total = (scratch[h] + scratch[2 * kH + h]) + (scratch[4 * kH + h] + scratch[6 * kH + h]);
+      const float* sr = scratch + kH;
+      const float rounded = (sr[h] + sr[2 * kH + h]) + (sr[4 * kH + h] + sr[6 * kH + h]);  // 0 only with the other
       const float top = total != 0.f ? ref[h] : -kFar;
-      alpha[h] = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+      alpha[h] = rounded == 0.f ? 0.f : (whole ? 1.f : total) / rounded;  // (attn.cuh says why)
       if (!whole) {
         *reinterpret_cast<float2*>(k.stat + (slot * kH + h) * 2) = make_float2(top, total);
       } else if (a.lse != nullptr && h < live) {
@@ -639,7 +649,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
       } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (h + j < live) sum[(h + j) * kD] = __uint_as_float(o[j]);
+          if (h + j < live) sum[(h + j) * kD] = __uint_as_float(o[j]) * alpha[h + j];
       }
     }
     if (whole) {
