@@ -67,7 +67,8 @@ CI_API int64_t ci_cache_page_bytes(int32_t cache_format, int32_t head_dim);
  * with the value's scale in them) and divided by the sum of what they were
  * rounded to, so that the error left is that of their ratios; lse has the sum
  * of the unrounded ones; out is rounded once.  Results do not depend on the
- * order in which blocks run.  FP8 scales: finite, |scale| <= 2^60.
+ * order in which blocks run.  Values |v| <= 2^80; FP8 scales: finite, |scale|
+ * <= 2^60, and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *
  * q, out: bf16 [rows][num_q_heads][D] with row strides in elements (multiples
  * of 8); q and out 16-byte aligned.  lse: float [rows][num_q_heads] or NULL.
