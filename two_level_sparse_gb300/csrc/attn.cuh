@@ -238,7 +238,7 @@ struct Walk {
 template <int N>
 struct RangeShared {
   Range range[N];
-  int32_t warp_sum[16];
+  int32_t warp_sum[24];
 };
 
 struct Shared {

@@ -35,24 +35,27 @@ namespace attn {
 namespace {
 
 constexpr int kD = 128, kH = 64, kPos = 128;
-constexpr int kVSlots = 3, kSlots = 2 + kVSlots, kSlot = kPos * kD * 2;  // a K slot per worker, then V's
+constexpr int kKSlot = kPos * kD * 2, kVSlot = kKSlot / 2;  // K: a tile; V: half of one (a page)
+constexpr int kVSlots = 3;                                 // per worker
+constexpr int kSlotBytes = 2 * (kKSlot + kVSlots * kVSlot);  // the workers' K slots, then their V slots
 constexpr int kPBytes = kPos * kH * 2, kQBytes = kH * kD * 2;
-constexpr int kWideThreads = 512;
+constexpr int kSoftmaxWarps = 8;  // per worker: a quarter of a tile's positions and half of the heads each
+constexpr int kGroup = 32 * kSoftmaxWarps, kWideThreads = 256 + 2 * kGroup;
 // of worker g, at + 64 g: S, O, the sums of P, those of P as it is rounded
 constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256, kColR = 384;
 constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
 constexpr float kSlack = 40.f;
 
 struct WideShared {
-  uint64_t k_full[2], k_empty[2], v_full[kVSlots], v_empty[kVSlots], s_full[2], p_full[2], pv_done[2], drain[2];
-  alignas(16) uint32_t mask[8][4];  // of the last eight tiles: which positions count
-  uint32_t first[8];                // and whether they begin a segment
+  uint64_t k_full[2], k_empty[2], v_full[2][kVSlots], v_empty[2][kVSlots], s_full[2], p_full[2], pv_done[2], drain[2];
+  alignas(16) uint32_t mask[2][4][4];  // of each worker's last four tiles: which positions count
+  uint32_t first[2][4];                // and whether they begin a segment
   alignas(16) float ref[2][kH], alpha[2][kH];
   RangeShared<2> r;
   uint32_t tmem;
   int32_t abort;
 };
-constexpr int kWideSmem = 1024 + kSlots * kSlot + 2 * kPBytes + 2 * kQBytes + static_cast<int>(sizeof(WideShared));
+constexpr int kWideSmem = 1024 + kSlotBytes + 2 * kPBytes + 2 * kQBytes + static_cast<int>(sizeof(WideShared));
 static_assert(kWideSmem <= 227 * 1024, "");
 
 // 128-byte swizzled operand: K-major (rows of 64 elements of the reduced
@@ -86,18 +89,43 @@ __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_
       "n"(A4 + 3 * A1), "n"(B1), "n"(2 * B1), "n"(3 * B1), "n"(B4), "n"(B4 + B1), "n"(B4 + 2 * B1), "n"(B4 + 3 * B1)
       : "memory");
 }
+// Four of them, the operands `step` (in 16 bytes) apart.
+template <int kStep>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, o, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %5;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %7;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep)
+      : "memory");
+}
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// `bytes` (a multiple of 16) from shared memory to global memory; what was read
+// may be overwritten after the wait (of the same thread).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// Whether any of a softmax group's 128 threads says so (a barrier of the group).
+// Whether any of a softmax group's threads says so (a barrier of the group).
 __device__ __forceinline__ bool group_any(int id, bool mine) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(mine ? 1u : 0u), "r"(id)
+      : "r"(mine ? 1u : 0u), "r"(id), "n"(kGroup)
       : "memory");
   return r != 0;
 }
@@ -105,6 +133,16 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
+}
+// 16 rows x 32 columns as matrix fragments: per 8 columns, the lane's row lane / 4
+// (r[4 i], r[4 i + 1]) and the one 8 further (r[4 i + 2], r[4 i + 3]), at columns
+// 8 i + 2 (lane % 4) and the next.
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -117,13 +155,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -146,18 +177,18 @@ struct Waiter {
     return alive;
   }
 };
-// Tile t's V slot, t % 3, and the parity of its t / 3-th use.  (Where one worker
-// has a tile more than the other, the last tile's number has a gap before it;
-// nothing follows that, so the gap's slot is not used again.)
+// A worker's V slots in turn: the halves of its tiles, one after another.
 struct VPlace {
-  int slot;
-  uint32_t phase;
-  __device__ __forceinline__ explicit VPlace(int t) : slot(t), phase(0) {}
-  __device__ __forceinline__ void advance(int tiles) {
-    slot += tiles;
-    if (slot >= kVSlots) slot -= kVSlots, phase ^= 1;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == kVSlots) slot = 0, phase ^= 1;
   }
 };
+__device__ __forceinline__ uint32_t k_slot(const Buffers& b, int g) { return b.slots + g * kKSlot; }
+__device__ __forceinline__ uint32_t v_slot(const Buffers& b, int g, int slot) {
+  return b.slots + 2 * kKSlot + (g * kVSlots + slot) * kVSlot;
+}
 
 // ------------------------------------------------------------------ producers
 // The heads [p0, p0 + n) of a unit's queries; zeros past the last one.
@@ -189,7 +220,7 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 31;
   Waiter wait{sh, c.dev_err};
-  VPlace vs(g);
+  VPlace vs;
   uint32_t n = 0;  // tiles so far
 #pragma unroll 1
   while (w.next(a)) {
@@ -211,72 +242,84 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
         if (hi >= c.num_pages) hi = -1;
       }
       const int page0 = __shfl_sync(0xffffffffu, lo, j), page1 = __shfl_sync(0xffffffffu, hi, j);
-      const int pages = (page0 >= 0) + (page1 >= 0);
-      const int mine = lane & 2 ? page1 : page0;  // lane 0..3: page lane / 2, dims 64 (lane % 2) ..
-      uint64_t* full = kValues ? &sh.v_full[vs.slot] : &sh.k_full[g];
-      if (kValues ? wait(&sh.v_empty[vs.slot], vs.phase ^ 1) : wait(&sh.k_empty[g], (n + 1) & 1)) {
-        if (!kValues && lane < 4) {
+      if constexpr (kValues) {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x, vs.advance()) {
+          if (!wait(&sh.v_empty[g][vs.slot], vs.phase ^ 1)) continue;
+          const int page = x ? page1 : page0;
+          uint64_t* full = &sh.v_full[g][vs.slot];
+          if (lane == 0) {
+            if (page >= 0)
+              mbar_arrive_expect_tx(full, kVSlot);
+            else
+              mbar_arrive(full);
+          }
+          __syncwarp();
+          if (lane < 2 && page >= 0)
+            tma_box(v_slot(b, g, vs.slot) + lane * (kVSlot / 2), map, lane * 128, (page * c.num_kv_heads + head) * kPage, smem_u32(full));
+        }
+      } else if (wait(&sh.k_empty[g], (n + 1) & 1)) {
+        const int pages = (page0 >= 0) + (page1 >= 0);
+        const int mine = lane & 2 ? page1 : page0;  // lane 0..3: page lane / 2, dims 64 (lane % 2) ..
+        uint64_t* full = &sh.k_full[g];
+        if (lane < 4) {
           const int left = mine >= 0 ? len - i * kPos - lane * 32 : 0;
-          const int at = (2 * n + g) & 7;
-          sh.mask[at][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
-          if (lane == 0) sh.first[at] = i == w.i0;
+          sh.mask[g][n & 3][lane] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0;
+          if (lane == 0) sh.first[g][n & 3] = i == w.i0;
         }
         __syncwarp();
         if (lane == 0) {
           if (pages > 0)
-            mbar_arrive_expect_tx(full, pages * (kSlot / 2));
+            mbar_arrive_expect_tx(full, pages * (kKSlot / 2));
           else
             mbar_arrive(full);
         }
         __syncwarp();
         if (lane < 4 && mine >= 0)
-          tma_box(b.slots + (kValues ? 2 + vs.slot : g) * kSlot + (lane & 1) * (kSlot / 2) + (lane >> 1) * (kSlot / 4), map,
-                  (lane & 1) * 128, (mine * c.num_kv_heads + head) * kPage, smem_u32(full));
-        if (!kValues) {
-          if (i == w.i0) {
-            copy_queries(queries_of(k, w), b.q + g * kQBytes, 0, kH, lane);
-            cp_async_arrive_noinc(full);
-          } else {
-            mbar_arrive(full);
-          }
+          tma_box(k_slot(b, g) + (lane & 1) * (kKSlot / 2) + (lane >> 1) * (kKSlot / 4), map, (lane & 1) * 128,
+                  (mine * c.num_kv_heads + head) * kPage, smem_u32(full));
+        if (i == w.i0) {
+          copy_queries(queries_of(k, w), b.q + g * kQBytes, 0, kH, lane);
+          cp_async_arrive_noinc(full);
+        } else {
+          mbar_arrive(full);
         }
       }
-      vs.advance(2);
     }
   }
   cp_async_wait<0>();
 }
 
-// Listed rows of both workers' tiles in turn: four warps gather K by TMA, 32
-// positions each, and two copy V by 16-byte asynchronous copies, 64 each
-// (produce_list in attn.cuh says why).  Of each worker, the list entries of the
-// second next tile and the page ids of the next one are on their way while a
-// tile is copied.
-template <int N>  // positions per warp: 32 N
-struct ListStream {
+// Worker g's listed rows: two warps gather K by TMA, 64 positions each, and one
+// copies V by 16-byte asynchronous copies (produce_list in attn.cuh says why).
+// The list entries of the second next tile and the page ids of the next one are
+// on their way while a tile is copied.
+template <bool kValues>
+__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, const CUtensorMap* kmap,
+                                          int g, int part) {
+  constexpr int N = kValues ? 4 : 2;  // positions per lane
   struct Entry {
     const int32_t* table;  // null: the row has no request
     int head, len, s[N];
     bool live, first;
     Queries q;
   };
-  WideWalk w;
-  int i, end, page[N];
-  Entry seg, now, next;
-
-  __device__ __forceinline__ ListStream(const AttnArgs& a, const Range& r, int units)
-      : w(walk_of<kPos>(a, r, units)), i(0), end(0), seg{}, now{}, next{} {}
-  __device__ __forceinline__ Entry fetch(const Args& k, int first) {
-    const AttnArgs& a = k.a;
+  const AttnArgs& a = k.a;
+  const CacheArgs& c = a.c;
+  const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4, first = part * 32 * N + lane;
+  Waiter wait{sh, c.dev_err};
+  Entry seg{}, now{}, next{};
+  int i = 0, end = 0, page[N];
+  auto fetch = [&]() {
     Entry x{};
     if (i >= end) {
       if (!w.next(a)) return x;
       i = w.i0, end = w.i1;
-      const int req = row_request(a.c, w.row);
-      seg.table = req >= 0 ? a.c.page_table + static_cast<int64_t>(req) * a.c.max_pages : nullptr;
+      const int req = row_request(c, w.row);
+      seg.table = req >= 0 ? c.page_table + static_cast<int64_t>(req) * c.max_pages : nullptr;
       seg.len = seg.table != nullptr ? a.seq_len[w.row] : 0;
       seg.head = w.unit / k.l.blocks;
-      if (N == 1) seg.q = queries_of(k, w);
+      if (!kValues) seg.q = queries_of(k, w);
     }
     x = seg;
     x.live = true;
@@ -287,90 +330,78 @@ struct ListStream {
     for (int j = 0; j < N; ++j) x.s[j] = at + 32 * j < a.npos ? list[32 * j] : -1;
     ++i;
     return x;
-  }
-  // The look-ahead moves on: the next tile becomes the current one.  first: the
-  // lane's first position in a tile.
-  __device__ __forceinline__ void step(const Args& k, int first) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) page[j] = next.live && next.s[j] >= 0 && next.s[j] < next.len ? next.table[next.s[j] / kPage] : 0;
-    const Entry after = fetch(k, first);
-    now = next, next = after;
-  }
-};
-
-template <bool kValues>
-__device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, const Buffers& b, const CUtensorMap* kmap, int part,
-                                          int units) {
-  constexpr int N = kValues ? 2 : 1;
-  const AttnArgs& a = k.a;
-  const CacheArgs& c = a.c;
-  const int lane = threadIdx.x & 31, chunk = lane & 15, odd = lane >> 4, first = part * 32 * N + lane;
-  Waiter wait{sh, c.dev_err};
-  ListStream<N> cur(a, sh.r.range[0], units), other(a, sh.r.range[1], units);
-  VPlace vs(0);
-  // steps -4 .. -1 fill both streams' look-ahead
+  };
+  VPlace vs;
+  // steps -2 and -1 fill the look-ahead
 #pragma unroll 1
-  for (int t = -4; t < 0 || cur.now.live || other.now.live; ++t) {
-    const bool live = t >= 0 && cur.now.live;
+  for (int n = -2; n < 0 || now.live; ++n) {
+    const bool live = n >= 0 && now.live;
     int row[N];  // -1: an entry that does not count (row 0 of K, zeros of V)
-    uint32_t m = 0;
+    uint32_t m[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int s = cur.now.s[j];
-      const bool in = live && s >= 0 && s < cur.now.len, ok = in && cur.page[j] >= 0 && cur.page[j] < c.num_pages;
+      const int s = now.s[j];
+      const bool in = live && s >= 0 && s < now.len, ok = in && page[j] >= 0 && page[j] < c.num_pages;
       if (!kValues) {
-        if (live && cur.now.table != nullptr && !in && s != -1) report(c.dev_err, kDevErrPos);
+        if (live && now.table != nullptr && !in && s != -1) report(c.dev_err, kDevErrPos);
         if (ok != in) report(c.dev_err, kDevErrPage);
-        m = __ballot_sync(0xffffffffu, ok);
+        m[j] = __ballot_sync(0xffffffffu, ok);
       }
-      row[j] = ok ? (cur.page[j] * c.num_kv_heads + cur.now.head) * kPage + (s & (kPage - 1)) : -1;
+      row[j] = ok ? (page[j] * c.num_kv_heads + now.head) * kPage + (s & (kPage - 1)) : -1;
     }
-    const bool begins = cur.now.first;
-    const Queries q = cur.now.q;
-    cur.step(k, first);  // its loads land while the tile is copied
-    const int g = t & 1;
-    if (live && (kValues ? wait(&sh.v_empty[vs.slot], vs.phase ^ 1) : wait(&sh.k_empty[g], ((t >> 1) + 1) & 1))) {
-      if constexpr (!kValues) {
-        uint64_t* full = &sh.k_full[g];
-        const uint32_t dst = b.slots + g * kSlot + part * 32 * 128;
-        if (lane == 0) {
-          sh.mask[t & 7][part] = m;
-          if (part == 0) sh.first[t & 7] = begins;
-          mbar_arrive_expect_tx(full, kSlot / 4);
-        }
-        __syncwarp();
-        const int mine = max(row[0], 0);
+    const bool begins = now.first;
+    const Queries q = now.q;
+    // the look-ahead moves on: its loads land while the tile is copied
+#pragma unroll
+    for (int j = 0; j < N; ++j) page[j] = next.live && next.s[j] >= 0 && next.s[j] < next.len ? next.table[next.s[j] / kPage] : 0;
+    const Entry after = fetch();
+    now = next, next = after;
+    if constexpr (!kValues) {
+      if (!live || !wait(&sh.k_empty[g], (n + 1) & 1)) continue;
+      uint64_t* full = &sh.k_full[g];
+      const uint32_t dst = k_slot(b, g) + part * 64 * 128;
+      if (lane == 0) {
+        sh.mask[g][n & 3][2 * part] = m[0], sh.mask[g][n & 3][2 * part + 1] = m[1];
+        if (part == 0) sh.first[g][n & 3] = begins;
+        mbar_arrive_expect_tx(full, kKSlot / 2);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int mine = max(row[j], 0);
 #pragma unroll 2
         for (int p = 0; p < 32; p += 4) {
           const int r0 = __shfl_sync(0xffffffffu, mine, p), r1 = __shfl_sync(0xffffffffu, mine, p + 1);
           const int r2 = __shfl_sync(0xffffffffu, mine, p + 2), r3 = __shfl_sync(0xffffffffu, mine, p + 3);
-          gather4_elect(dst + p * 128, kmap, 0, r0, r1, r2, r3, smem_u32(full));
-          gather4_elect(dst + kSlot / 2 + p * 128, kmap, 128, r0, r1, r2, r3, smem_u32(full));
+          gather4_elect(dst + (32 * j + p) * 128, kmap, 0, r0, r1, r2, r3, smem_u32(full));
+          gather4_elect(dst + kKSlot / 2 + (32 * j + p) * 128, kmap, 128, r0, r1, r2, r3, smem_u32(full));
         }
-        if (begins) {
-          copy_queries(q, b.q + g * kQBytes, part * (kH / 4), kH / 4, lane);
-          cp_async_arrive_noinc(full);
-        } else {
-          mbar_arrive(full);
-        }
+      }
+      if (begins) {
+        copy_queries(q, b.q + g * kQBytes, part * (kH / 2), kH / 2, lane);
+        cp_async_arrive_noinc(full);
       } else {
-        uint64_t* full = &sh.v_full[vs.slot];
-        const uint32_t dst = b.slots + (2 + vs.slot) * kSlot + (chunk >> 3) * (kSlot / 2) + part * 64 * 128;
-        const uint8_t* base = c.v_pool + chunk * 16;
+        mbar_arrive(full);
+      }
+    } else if (live) {
+      const uint8_t* base = c.v_pool + chunk * 16;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x, vs.advance()) {
+        if (!wait(&sh.v_empty[g][vs.slot], vs.phase ^ 1)) continue;
+        const uint32_t dst = v_slot(b, g, vs.slot) + (chunk >> 3) * (kVSlot / 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
+          const int mine = x ? row[2 + j] : row[j];
 #pragma unroll 4
           for (int p = 0; p < 32; p += 2) {  // positions p and p + 1
-            const int at = p + odd, r = __shfl_sync(0xffffffffu, row[j], at);
+            const int at = p + odd, r = __shfl_sync(0xffffffffu, mine, at);
             copy16(dst + (32 * j + at) * 128 + (((chunk & 7) ^ (at & 7)) << 4), base + static_cast<int64_t>(max(r, 0)) * (kD * 2),
                    r >= 0);
           }
-        cp_async_arrive_noinc(full);
+        }
+        cp_async_arrive_noinc(&sh.v_full[g][vs.slot]);
       }
     }
-    if (t >= 0) vs.advance(1);
-    const ListStream<N> turn = cur;
-    cur = other, other = turn;
   }
   cp_async_wait<0>();
 }
@@ -379,121 +410,127 @@ __device__ __forceinline__ void wide_list(const Args& k, WideShared& sh, const B
 // role has given up): both parities of a barrier, whichever is the last fill's.
 __device__ __forceinline__ void drain_copies(WideShared& sh) {
 #pragma unroll 1
-  for (int i = 0; i < 2 * (2 + kVSlots); ++i) {
-    const int s = i >> 1;
-    mbar_wait(s < 2 ? &sh.k_full[s] : &sh.v_full[s - 2], i & 1, nullptr, 1000000ull);
+  for (int i = 0; i < 4 * (1 + kVSlots); ++i) {
+    const int g = (i >> 1) & 1, s = i >> 2;
+    mbar_wait(s == 0 ? &sh.k_full[g] : &sh.v_full[g][s - 1], i & 1, nullptr, 1000000ull);
   }
 }
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ int tiles_of(const WideShared& sh, int g) {
-  return sh.r.range[g].end - sh.r.range[g].first;
-}
-
-__device__ __forceinline__ void wide_scores(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
-  Waiter wait{sh, k.a.c.dev_err};
-  const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
+// Worker g's: the scores of a tile, as soon as those of the tile before have been
+// read, then the values of the tile before.
+__device__ __forceinline__ void wide_products(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem, int g) {
+  const AttnArgs& a = k.a;
+  const int lane = threadIdx.x & 31, tiles = sh.r.range[g].end - sh.r.range[g].first;
+  const uint32_t pb = b.p + g * kPBytes;
+  Waiter wait{sh, a.c.dev_err};
+  VPlace vs;
 #pragma unroll 1
-  for (int t = 0; t < steps; ++t) {
-    const int g = t & 1, n = t >> 1;
-    if (n >= (g ? n1 : n0)) continue;
-    if (n > 0) wait(&sh.p_full[g], (n - 1) & 1);  // the last tile's scores have been read
-    if (!wait(&sh.k_full[g], n & 1)) continue;
-    fence_proxy_async_smem();  // queries are written through the generic proxy
-    tc_fence_after();
-    mma8<2, kSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * g, desc128(b.slots + g * kSlot, 16),
-                                                 desc128(b.q + g * kQBytes, 16), idesc(false), 0);
-    mma_commit_elect(&sh.s_full[g]);
-    mma_commit_elect(&sh.k_empty[g]);
+  for (int n = 0; n <= tiles; ++n) {
+    if (n > 0) wait(&sh.p_full[g], (n - 1) & 1);
+    // the scores come first where their keys are there, so that the softmax goes on beside the values' product
+    const bool early = n < tiles && __all_sync(0xffffffffu, mbar_try_wait(&sh.k_full[g], n & 1));
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+      if (step != 1) {
+        if (n == tiles || early != (step == 0) || !wait(&sh.k_full[g], n & 1)) continue;
+        fence_proxy_async_smem();  // queries are written through the generic proxy
+        tc_fence_after();
+        mma8<2, kKSlot / 2 / 16, 2, kQBytes / 2 / 16>(tmem + kColS + kH * g, desc128(k_slot(b, g), 16),
+                                                      desc128(b.q + g * kQBytes, 16), idesc(false), 0);
+        mma_commit_elect(&sh.s_full[g]);
+        mma_commit_elect(&sh.k_empty[g]);
+        continue;
+      }
+      if (n == 0) continue;
+      const uint32_t* mask = sh.mask[g][(n - 1) & 3];
+      uint32_t more = sh.first[g][(n - 1) & 3] ^ 1;  // adds to the segment's earlier tiles
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x, vs.advance(), more = 1) {
+        if (!wait(&sh.v_full[g][vs.slot], vs.phase)) continue;
+        const uint32_t vb = v_slot(b, g, vs.slot);
+        if (a.pos == nullptr && (mask[2 * x] & mask[2 * x + 1]) != ~0u) {
+          // values that do not count must not reach a product with 0
+#pragma unroll 1
+          for (int e = lane; e < 64 * 16; e += 32) {
+            const int p = e >> 4, c = e & 15;
+            if ((mask[2 * x + (p >> 5)] >> (p & 31)) & 1) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kVSlot / 2) + p * 128 + (c & 7) * 16), "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        fence_proxy_async_smem();  // listed rows and probabilities are written through the generic proxy
+        tc_fence_after();
+        mma4<128>(tmem + kColO + kH * g, desc128(vb, kVSlot / 2), desc128(pb + x * 64 * 128, 16), idesc(true), more);
+        mma_commit_elect(&sh.v_empty[g][vs.slot]);
+      }
+      if (wait.alive) mma_commit_elect(&sh.pv_done[g]);
+    }
   }
   if (!wait.alive) {  // the products in flight end before the CTA's memory goes
-    mma_commit_elect(&sh.drain[0]);
-    mbar_wait(&sh.drain[0], 0, nullptr, 1000000ull);
-  }
-}
-
-__device__ __forceinline__ void wide_values(const Args& k, WideShared& sh, const Buffers& b, uint32_t tmem) {
-  const AttnArgs& a = k.a;
-  const int lane = threadIdx.x & 31;
-  Waiter wait{sh, a.c.dev_err};
-  const int n0 = tiles_of(sh, 0), n1 = tiles_of(sh, 1), steps = 2 * max(n0, n1);
-  VPlace vs(0);
-#pragma unroll 1
-  for (int t = 0; t < steps; ++t, vs.advance(1)) {
-    const int g = t & 1, n = t >> 1;
-    if (n >= (g ? n1 : n0)) continue;
-    wait(&sh.v_full[vs.slot], vs.phase);
-    if (!wait(&sh.p_full[g], n & 1)) continue;
-    const uint32_t vb = b.slots + (2 + vs.slot) * kSlot, pb = b.p + g * kPBytes;
-    const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[t & 7]);
-    const uint32_t more = sh.first[t & 7] ^ 1;  // adds to the segment's earlier tiles
-    if (a.pos == nullptr && (m.x & m.y & m.z & m.w) != ~0u) {
-      // values that do not count must not reach a product with 0
-#pragma unroll 1
-      for (int e = lane; e < kPos * 16; e += 32) {
-        const int p = e >> 4, c = e & 15;
-        if ((sh.mask[t & 7][p >> 5] >> (p & 31)) & 1) continue;
-        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + (c >> 3) * (kSlot / 2) + p * 128 + (c & 7) * 16), "r"(0)
-                     : "memory");
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    }
-    fence_proxy_async_smem();  // listed rows and probabilities are written through the generic proxy
-    tc_fence_after();
-    mma8<128, 512, 128, 512>(tmem + kColO + kH * g, desc128(vb, kSlot / 2), desc128(pb, 16), idesc(true), more);
-    mma_commit_elect(&sh.pv_done[g]);
-    mma_commit_elect(&sh.v_empty[vs.slot]);
-  }
-  if (!wait.alive) {
-    mma_commit_elect(&sh.drain[1]);
-    mbar_wait(&sh.drain[1], 0, nullptr, 1000000ull);
+    mma_commit_elect(&sh.drain[g]);
+    mbar_wait(&sh.drain[g], 0, nullptr, 1000000ull);
   }
 }
 
 // ------------------------------------------------------------------ softmax
-// S, the sums and O are read from tensor memory half of the heads at a time, in
-// loops that are not unrolled: with every role's code straight-line, the roles
-// together outgrew the instruction cache, and a row of 512 positions (four tiles)
-// took twice as long.
-//
-// Halves the heads that a lane keeps and adds the partner's share of them.
+// Halves the columns that a lane keeps and adds the partner's share of them.
 template <int kHalf, int kBit>
-__device__ __forceinline__ void fold(uint32_t (&l)[32], int lane) {
+__device__ __forceinline__ void fold(float (&l)[8], int lane) {
   const bool up = (lane & kBit) != 0;
 #pragma unroll
   for (int j = 0; j < kHalf; ++j) {
-    const uint32_t give = up ? l[j] : l[j + kHalf], keep = up ? l[j + kHalf] : l[j];
-    l[j] = __float_as_uint(__uint_as_float(keep) + __uint_as_float(__shfl_xor_sync(0xffffffffu, give, kBit)));
+    const float give = up ? l[j] : l[j + kHalf], keep = up ? l[j + kHalf] : l[j];
+    l[j] = keep + __shfl_xor_sync(0xffffffffu, give, kBit);
   }
+}
+// The sum over the warp's 32 rows of tensor memory of 32 columns; the lane gets
+// that of column sum_column(lane).  Read as matrix fragments (a lane has four
+// rows and eight columns), so that three exchanges are left.
+__device__ __forceinline__ int sum_column(int lane) { return 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1); }
+__device__ __forceinline__ float sum_rows(uint32_t taddr, int lane) {
+  uint32_t x[16], y[16];
+  tmem_ld_frag4(taddr, x);
+  tmem_ld_frag4(taddr + (16u << 16), y);
+  tmem_ld_wait();
+  float l[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // column block j / 2, column j % 2 of the lane's pair: rows r and r + 8
+    const int i = 4 * (j >> 1) + (j & 1);
+    l[j] = (__uint_as_float(x[i]) + __uint_as_float(x[i + 2])) + (__uint_as_float(y[i]) + __uint_as_float(y[i + 2]));
+  }
+  fold<4, 16>(l, lane);
+  fold<2, 8>(l, lane);
+  fold<1, 4>(l, lane);
+  return l[0];
 }
 
 __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, WideWalk w, const Buffers& b, uint8_t* pmem, uint32_t tmem,
                              int g) {
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kH * g;  // this warp's, at the worker's columns
-  const float factor = a.scale * kLog2e;
-  const Range range = sh.r.range[g];
-  float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [4][2 kH], while no product reads the probabilities
-  float *ref = sh.ref[g], *alpha = sh.alpha[g];
-  const int worker = range.worker;
+  const int in_group = threadIdx.x & (kGroup - 1), half = (in_group >> 7) * 32;  // the warp's heads: half .. half + 31
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kH * g + half;  // this warp's, at its columns
+  float* scratch = reinterpret_cast<float*>(pmem + g * kPBytes);  // [2][4][kH], while no product reads the probabilities
+  float *group_ref = sh.ref[g], *group_alpha = sh.alpha[g], *ref = group_ref + half, *alpha = group_alpha + half;
   Waiter wait{sh, a.c.dev_err};
-  uint32_t mine = 0;  // tiles so far: the CTA's tile 2 mine + g
+  uint32_t mine = 0;  // tiles so far
 #pragma unroll 1
   while (w.next(a)) {
-    const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
     bool set = false;  // whether there are references
 #pragma unroll 1
     for (int i = w.i0; i < w.i1; ++i) {
+      const float factor = a.scale * kLog2e;
       wait(&sh.s_full[g], mine & 1);
       tc_fence_after();
-      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[(2 * mine + g) & 7]);
+      const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[g][mine & 3]);
       const bool valid = ((quad == 0 ? m.x : quad == 1 ? m.y : quad == 2 ? m.z : m.w) >> lane) & 1;
       if (!set && (m.x | m.y | m.z | m.w) != 0) {  // the first position's logits
         const int first = m.x ? __ffs(m.x) - 1 : m.y ? 31 + __ffs(m.y) : m.z ? 63 + __ffs(m.z) : 95 + __ffs(m.w);
 #pragma unroll 1
-        for (int h = 0; h < kH; h += 8) {
+        for (int h = 0; h < 32; h += 8) {
           uint32_t s[8];
           tmem_ld8(lanes + kColS + h, s);
           tmem_ld_wait();
@@ -502,95 +539,88 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
             for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(__uint_as_float(s[j]) * factor, kFar), -kFar);
           }
         }
-        named_sync(1 + g, 128);
+        named_sync(1 + g, kGroup);
         set = true;
       }
       float over = -INFINITY;
+      {
+        uint32_t s[16];
 #pragma unroll 1
-      for (int h = 0; h < kH; h += 32) {
-        uint32_t s[32];
-        tmem_ld32(lanes + kColS + h, s);
+        for (int h = 0; h < 32; h += 16) {
+        tmem_ld16(lanes + kColS + h, s);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           const float4 r = *reinterpret_cast<const float4*>(ref + h + j);
           over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j]), factor, -r.x), fmaf(__uint_as_float(s[j + 1]), factor, -r.y)));
           over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j + 2]), factor, -r.z), fmaf(__uint_as_float(s[j + 3]), factor, -r.w)));
-        }
+        }}
       }
       const bool raise = group_any(1 + g, valid && over > kSlack);
       if (mine > 0) wait(&sh.pv_done[g], (mine - 1) & 1);  // the probabilities' buffer is free, O is complete
       if (raise) {
 #pragma unroll 1
-        for (int h = 0; h < kH; h += 4) {
+        for (int h = 0; h < 32; h += 4) {
           uint32_t x[4];
           tmem_ld4(lanes + kColS + h, x);
           tmem_ld_wait();
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {
             const float r = warp_max(valid ? __uint_as_float(j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3]) * factor : -INFINITY);
-            if (lane == 0) scratch[quad * kH + h + j] = r;
+            if (lane == 0) scratch[quad * kH + half + h + j] = r;
           }
         }
-        named_sync(1 + g, 128);
-        if (row < kH) {
-          const float old = ref[row];
+        named_sync(1 + g, kGroup);
+        if (in_group < kH) {
+          const float old = group_ref[in_group];
           float top = old;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top = fmaxf(top, scratch[x * kH + row]);
-          alpha[row] = exp2_approx(old - top);
-          ref[row] = top;
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, scratch[x * kH + in_group]);
+          group_alpha[in_group] = exp2_approx(old - top);
+          group_ref[in_group] = top;
         }
-        named_sync(1 + g, 128);
+        named_sync(1 + g, kGroup);
         if (i > w.i0) {  // what the segment has so far
           tc_fence_after();
 #pragma unroll 1
-          for (int h = 0; h < 3 * kH; h += 8) {  // O and both sums: 2 kH columns apart
+          for (int x = 0; x < 96; x += 8) {  // O and both sums: 2 kH columns apart
             uint32_t o[8];
-            const uint32_t at = lanes + kColO + h + (h / kH) * kH;
+            const int h = x & 31;
+            const uint32_t at = lanes + kColO + (x >> 5) * 2 * kH + h;
             tmem_ld8(at, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[(h & (kH - 1)) + j]);
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[h + j]);
             tmem_st8(at, o);
           }
           tmem_st_wait();
         }
       }
       uint8_t* prow = pmem + g * kPBytes + row * 128;
+      const bool fresh = i == w.i0;
 #pragma unroll 1
-      for (int h = 0; h < kH; h += 32) {
-        uint32_t s[32];
-        tmem_ld32(lanes + kColS + h, s);
+      for (int j0 = 0; j0 < 32; j0 += 8) {
+        uint32_t s[8], l[8], lr[8], v[4];
+        tmem_ld8(lanes + kColS + j0, s);
+        tmem_ld8(lanes + kColL + j0, l);
+        tmem_ld8(lanes + kColR + j0, lr);
         tmem_ld_wait();
-        const bool fresh = i == w.i0;
 #pragma unroll
-        for (int j0 = 0; j0 < 32; j0 += 16) {
-          uint32_t l[16], lr[16];
-          tmem_ld16(lanes + kColL + h + j0, l);
-          tmem_ld16(lanes + kColR + h + j0, lr);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; j += 8) {
-            uint32_t v[4];
-#pragma unroll
-            for (int x = 0; x < 8; x += 2) {
-              const float2 r = *reinterpret_cast<const float2*>(ref + h + j0 + j + x);
-              float p0 = exp2_approx(fmaf(__uint_as_float(s[j0 + j + x]), factor, -r.x));
-              float p1 = exp2_approx(fmaf(__uint_as_float(s[j0 + j + x + 1]), factor, -r.y));
-              if (!valid) p0 = p1 = 0.f;
-              v[x / 2] = bf16x2(p0, p1);
-              const float r0 = bf16_lo(v[x / 2]), r1 = bf16_hi(v[x / 2]);
-              l[j + x] = __float_as_uint(fresh ? p0 : __uint_as_float(l[j + x]) + p0);
-              l[j + x + 1] = __float_as_uint(fresh ? p1 : __uint_as_float(l[j + x + 1]) + p1);
-              lr[j + x] = __float_as_uint(fresh ? r0 : __uint_as_float(lr[j + x]) + r0);
-              lr[j + x + 1] = __float_as_uint(fresh ? r1 : __uint_as_float(lr[j + x + 1]) + r1);
-            }
-            *reinterpret_cast<uint4*>(prow + ((((h + j0 + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          tmem_st16(lanes + kColL + h + j0, l);
-          tmem_st16(lanes + kColR + h + j0, lr);
+        for (int x = 0; x < 8; x += 2) {
+          const float2 r = *reinterpret_cast<const float2*>(ref + j0 + x);
+          float p0 = exp2_approx(fmaf(__uint_as_float(s[x]), factor, -r.x));
+          float p1 = exp2_approx(fmaf(__uint_as_float(s[x + 1]), factor, -r.y));
+          if (!valid) p0 = p1 = 0.f;
+          v[x / 2] = bf16x2(p0, p1);
+          const float r0 = bf16_lo(v[x / 2]), r1 = bf16_hi(v[x / 2]);
+          l[x] = __float_as_uint(fresh ? p0 : __uint_as_float(l[x]) + p0);
+          l[x + 1] = __float_as_uint(fresh ? p1 : __uint_as_float(l[x + 1]) + p1);
+          lr[x] = __float_as_uint(fresh ? r0 : __uint_as_float(lr[x]) + r0);
+          lr[x + 1] = __float_as_uint(fresh ? r1 : __uint_as_float(lr[x + 1]) + r1);
         }
+        *reinterpret_cast<uint4*>(prow + ((((half + j0) >> 3) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        tmem_st8(lanes + kColL + j0, l);
+        tmem_st8(lanes + kColR + j0, lr);
       }
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -600,32 +630,22 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
       ++mine;
     }
     // ---- the segment's end: sums over the positions, the result
-#pragma unroll 1
-    for (int h = 0; h < 2 * kH; h += 32) {  // the sums of P, then those of P as it is rounded
-      uint32_t l[32];
-      tmem_ld32(lanes + kColL + h + (h & kH), l);
-      tmem_ld_wait();
-      fold<16, 16>(l, lane);
-      fold<8, 8>(l, lane);
-      fold<4, 4>(l, lane);
-      fold<2, 2>(l, lane);
-      fold<1, 1>(l, lane);
-      if (h == 0) {  // (the products that read the probabilities are done before the buffer is written)
-        wait(&sh.pv_done[g], (mine - 1) & 1);
-        tc_fence_after();
-      }
-      scratch[quad * 2 * kH + h + lane] = __uint_as_float(l[0]);  // lane bits 16 .. 1 chose heads + 16 .. + 1
-    }
-    named_sync(1 + g, 128);
+    const float sum_p = sum_rows(lanes + kColL, lane), sum_r = sum_rows(lanes + kColR, lane);
+    wait(&sh.pv_done[g], (mine - 1) & 1);  // the products that read the probabilities are done, O is complete
+    tc_fence_after();
+    scratch[quad * kH + half + sum_column(lane)] = sum_p;
+    scratch[(4 + quad) * kH + half + sum_column(lane)] = sum_r;
+    named_sync(1 + g, kGroup);
     const bool whole = w.i0 == 0 && w.i1 == w.n;
-    const int64_t slot = 2ll * worker + (w.i0 == 0 ? 1 : 0);
-    if (row < kH) {
-      const int h = row;
-      const float total = (scratch[h] + scratch[2 * kH + h]) + (scratch[4 * kH + h] + scratch[6 * kH + h]);
-      const float* sr = scratch + kH;
-      const float rounded = (sr[h] + sr[2 * kH + h]) + (sr[4 * kH + h] + sr[6 * kH + h]);  // 0 only with the other
-      const float top = total != 0.f ? ref[h] : -kFar;
-      alpha[h] = rounded == 0.f ? 0.f : (whole ? 1.f : total) / rounded;  // (attn.cuh says why)
+    const int64_t slot = slot_of(sh.r.range[g].worker, w.i0 == 0);
+    const int head = w.unit / k.l.blocks, h0 = (w.unit - head * k.l.blocks) * kH, live = min(kH, k.l.group - h0);
+    if (in_group < kH) {
+      const int h = in_group;
+      const float *sp = scratch + h, *sr = sp + 4 * kH;
+      const float total = (sp[0] + sp[kH]) + (sp[2 * kH] + sp[3 * kH]);
+      const float rounded = (sr[0] + sr[kH]) + (sr[2 * kH] + sr[3 * kH]);  // 0 only with the other
+      const float top = total != 0.f ? group_ref[h] : -kFar;
+      group_alpha[h] = rounded == 0.f ? 0.f : (whole ? 1.f : total) / rounded;  // (attn.cuh says why)
       if (!whole) {
         *reinterpret_cast<float2*>(k.stat + (slot * kH + h) * 2) = make_float2(top, total);
       } else if (a.lse != nullptr && h < live) {
@@ -633,36 +653,49 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
             total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
       }
     }
-    named_sync(1 + g, 128);
-    // a thread holds one dim of all heads; whole results are turned in shared memory
+    named_sync(1 + g, kGroup);
+    // O's fragments: the lane has dims quad * 32 + 16 d + lane / 4 (+ 8) of heads 8 x + 2 (lane % 4) (+ 1)
     uint16_t* turned = reinterpret_cast<uint16_t*>(pmem + g * kPBytes);  // [kH][kD]
-    float* sum = k.sum + slot * kH * kD + row;
+    const uint32_t row0 = smem_u32(turned) + (half + (lane & 7)) * (kD * 2) + (quad * 32 + (lane & 8)) * 2 + (lane >> 4) * 8 * (kD * 2);
 #pragma unroll 1
-    for (int h = 0; h < live; h += 16) {
+    for (int d = 0; d < 2; ++d) {
       uint32_t o[16];
-      tmem_ld16(lanes + kColO + h, o);
+      tmem_ld_frag4(lanes + kColO + (static_cast<uint32_t>(d * 16) << 16), o);
       tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = *reinterpret_cast<const float2*>(alpha + 8 * x + 2 * (lane & 3));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[4 * x + y] = __float_as_uint(__uint_as_float(o[4 * x + y]) * (y & 1 ? f.y : f.x));
+      }
       if (whole) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          turned[(h + j) * kD + row] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[j]) * alpha[h + j]));
+        for (int x = 0; x < 4; x += 2)  // heads 8 x .. 8 x + 15: matrices of 8 dims and 8 heads, turned
+          stmatrix4_trans(row0 + x * 8 * (kD * 2) + d * 32, bf16x2(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1])),
+                          bf16x2(__uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3])),
+                          bf16x2(__uint_as_float(o[4 * x + 4]), __uint_as_float(o[4 * x + 5])),
+                          bf16x2(__uint_as_float(o[4 * x + 6]), __uint_as_float(o[4 * x + 7])));
       } else {
+        float* sum = k.sum + (slot * kH + half + 2 * (lane & 3)) * kD + quad * 32 + d * 16 + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (h + j < live) sum[(h + j) * kD] = __uint_as_float(o[j]) * alpha[h + j];
+        for (int x = 0; x < 16; ++x)
+          if (half + 8 * (x >> 2) + 2 * (lane & 3) + (x & 1) < live)
+            sum[(8 * (x >> 2) + (x & 1)) * kD + (x & 2) * 4] = __uint_as_float(o[x]);
       }
     }
     if (whole) {
-      named_sync(1 + g, 128);
-      uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD;
-#pragma unroll 2
-      for (int e = row; e < live * (kD / 8); e += 128)
-        *reinterpret_cast<uint4*>(out + e * 8) = *reinterpret_cast<const uint4*>(turned + e * 8);
-    } else if (row == 0 && w.i0 == 0) {
-      k.part[worker] = part_of(w, range);
+      fence_proxy_async_smem();
+      named_sync(1 + g, kGroup);
+      if (in_group == 0) {
+        uint16_t* out = a.out + w.row * a.out_stride + (static_cast<int64_t>(head) * k.l.group + h0) * kD;
+        bulk_store(out, smem_u32(turned), live * kD * 2);
+        bulk_store_wait_read();
+      }
+    } else if (in_group == 0 && w.i0 == 0) {
+      k.part[sh.r.range[g].worker] = part_of(w, sh.r.range[g]);
     }
     tc_fence_before();
-    named_sync(1 + g, 128);  // O, the factors and the shared buffer have been read
+    // the next writes to references, factors and probabilities come behind a barrier of the group's next tile
   }
 }
 
@@ -671,9 +704,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;  // the swizzle is one of address bits
   uint8_t* mem = raw + (base - smem_u32(raw));
-  const Buffers b{base, base + kSlots * kSlot, base + kSlots * kSlot + 2 * kPBytes};
-  uint8_t* pmem = mem + kSlots * kSlot;
-  WideShared& sh = *reinterpret_cast<WideShared*>(mem + kSlots * kSlot + 2 * kPBytes + 2 * kQBytes);
+  const Buffers b{base, base + kSlotBytes, base + kSlotBytes + 2 * kPBytes};
+  uint8_t* pmem = mem + kSlotBytes;
+  WideShared& sh = *reinterpret_cast<WideShared*>(mem + kSlotBytes + 2 * kPBytes + 2 * kQBytes);
   const AttnArgs& a = k.a;
   const int tid = threadIdx.x, warp = tid >> 5;
   if (warp == 1) {
@@ -683,14 +716,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (tid == 0) {
     // K: per producer warp the bytes, and every lane (a segment's first tile: its copies of the queries); listed V: every lane
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&sh.k_full[g], a.pos != nullptr ? 4 * 33 : 33);
+      mbar_init(&sh.k_full[g], a.pos != nullptr ? 2 * 33 : 33);
       mbar_init(&sh.k_empty[g], 1);
       mbar_init(&sh.s_full[g], 1);
-      mbar_init(&sh.p_full[g], 4);
+      mbar_init(&sh.p_full[g], kSoftmaxWarps);
       mbar_init(&sh.pv_done[g], 1);
       mbar_init(&sh.drain[g], 1);
+      for (int s = 0; s < kVSlots; ++s) mbar_init(&sh.v_full[g][s], a.pos != nullptr ? 32 : 1), mbar_init(&sh.v_empty[g][s], 1);
     }
-    for (int s = 0; s < kVSlots; ++s) mbar_init(&sh.v_full[s], a.pos != nullptr ? 64 : 1), mbar_init(&sh.v_empty[s], 1);
     fence_mbar_init();
     sh.abort = 0;
   }
@@ -704,21 +737,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (none) write_empty_rows<kD, kWideThreads>(a);
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
-    if (warp == 0) wide_scores(k, sh, b, tmem);
-    if (warp == 1) wide_values(k, sh, b, tmem);
-    if (a.pos != nullptr) {
-      if (warp == 2 || warp == 3) wide_list<true>(k, sh, b, &kmap, warp - 2, units);
-      if (warp >= 4) wide_list<false>(k, sh, b, &kmap, warp - 4, units);
-    } else if (warp >= 4) {
-      const int g = warp & 1;
-      const WideWalk w = walk_of<kPos>(a, sh.r.range[g], units);
-      if (warp < 6)
-        wide_pages<false>(k, sh, w, b, &kmap, g);
+    const int g = warp & 1;
+    const WideWalk w = walk_of<kPos>(a, sh.r.range[g], units);
+    if (warp < 2) {
+      wide_products(k, sh, b, tmem, g);
+    } else if (warp < 4) {
+      if (a.pos != nullptr)
+        wide_list<true>(k, sh, w, b, &kmap, g, 0);
       else
         wide_pages<true>(k, sh, w, b, &vmap, g);
+    } else if (a.pos != nullptr) {
+      wide_list<false>(k, sh, w, b, &kmap, g, (warp >> 1) & 1);
+    } else if (warp < 6) {
+      wide_pages<false>(k, sh, w, b, &kmap, g);
     }
   } else {
-    const int g = (warp - 8) >> 2;
+    const int g = (warp - 8) >> 3;
     wide_softmax(k, sh, walk_of<kPos>(a, sh.r.range[g], units), b, pmem, tmem, g);
   }
   tc_fence_before();
