@@ -12,8 +12,14 @@ using attn::Part;
 
 constexpr int kJoinWarps = 16;
 
-// Whether the kernel of attn_wide.cu takes the call.
-bool is_wide(const CacheArgs& c) { return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > 16; }
+// Whether the kernel of attn_wide.cu takes the call.  Both measured, in us with
+// cold caches (the warp-level kernel, then the wide one), by heads per key-value head:
+//   17 rows of 0-100k, all positions   16: 95, 99    32: 97, 99    64: 124, 101
+//   4 rows of 1k-4k, all positions     16: 19, 20    32: 19, 21    64: 25, 25
+//   1024 rows over 512 listed          16: 68, 67    20: 76, 67    64: 109, 74
+bool is_wide(const CacheArgs& c, bool listed) {
+  return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > (listed ? 16 : 32);
+}
 
 Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, bool wide) {
   const int group = num_q_heads / num_kv_heads;
@@ -141,7 +147,9 @@ int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.heads * 2 * 4; }
 
 template <int D, int kT>
 cudaError_t launch_join(const Args& k, cudaStream_t stream) {
-  // The fewer units, the more parts each: 16, 4 or 1 warps a head.
+  // The fewer units, the more parts each: 16, 4 or 1 warps a head.  Both kernels with 1, 4 and 16 (us, cold caches):
+  // one row of 256k, 77 parts a unit: 116, 111, 107; 16 rows of 10k-20k, 5 parts: 101, 99, 103; 64 rows of 512
+  // listed, at most 2 parts: 46, 49, 58.
   const int64_t units = static_cast<int64_t>(k.a.rows) * k.a.c.num_kv_heads * k.l.blocks;
   const bool by_unit = units <= k.l.ctas && k.a.rows <= 32 * kJoinWarps;
   const int64_t split = by_unit ? units : k.l.ctas, parts = k.l.ctas / (units < k.l.ctas ? units : k.l.ctas) + 1;
@@ -165,7 +173,7 @@ int64_t attn_workspace_bytes(int32_t, int32_t num_q_heads, int32_t num_kv_heads,
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   const CacheArgs& c = a.c;
-  const bool wide = is_wide(c);
+  const bool wide = is_wide(c, a.pos != nullptr);
   Args k{a, layout_of(c.num_q_heads, c.num_kv_heads, c.head_dim, wide), nullptr, nullptr, nullptr};
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   k.part = reinterpret_cast<Part*>(ws);

@@ -12,8 +12,8 @@
 // adds them in order.
 //
 // A tile.  A producer warp fetches K and V into a ring of stages, pages by TMA
-// (128-byte swizzled rows); listed positions take two (produce_list).  WP x WH consumer warps compute, WP
-// along the positions and WH along the heads:
+// (128-byte swizzled rows); listed positions take two (produce_list).  WP x WH
+// consumer warps compute, WP along the positions and WH along the heads:
 //   S^T = K Q^T   A = K from shared memory (ldmatrix), B = Q in registers;
 //   online softmax per head, a column of S^T: its maximum over the warp's
 //                 positions is a reduction over registers and three shuffles;
@@ -25,9 +25,17 @@
 // the row's statistics keep is of the unrounded P, and O is scaled from the one
 // to the other at a segment's end.
 // Positions sit on the 16-wide side of the MMA and heads on the 8-wide one, so
-// that a group of 8 query heads wastes nothing; a cache read at the HBM's rate
-// (64 positions x D = 128 in bf16 per 1400 cycles and SM) needs 128 x G / 8 of
-// these instructions, which legacy tensor throughput covers up to G = 64.
+// that a group of 8 query heads wastes nothing.
+//
+// What bounds it: the HBM, where a row reads its whole cache.  64 rows of 16k-64k
+// in FP8, 64 heads over 8, D = 128: 5.54 GB in 817 us, 6.79 TB/s, a copy's rate;
+// one row of 256k in bf16, 28 heads over 4: 537 MB in 87 us with the join, 6.19
+// TB/s.  There the warps' arithmetic is half of what the SM issues, most of it the
+// softmax and FP8's conversions, tensor instructions a sixth; two CTAs per SM keep
+// the loads going while one reduces.  Short calls are bound by latency: 4 rows of
+// 1k-4k (42 MB) take 17 us, 6 of them at the HBM's rate, two launches and their
+// starts the rest.  64 rows of 512 listed positions over 8 heads (137 MB) take 34
+// us: 8 tiles a unit, whose rows (256 bytes) are fetched at 4 TB/s.
 //
 // FP8 pages.  K: e4m3 widens to f16 exactly, one conversion per pair; the
 // query becomes f16 exactly too once each head is scaled by a power of two to

@@ -3,24 +3,31 @@
 // list of tiles, its split over the CTAs and the join are those of attn.cuh).
 //
 // With G = 64 heads the products cost 64 flop per byte of cache: at the HBM's
-// rate 435 TFLOP/s, half of what the warp-level MMA instructions reached
-// (their kernel: 108 us for 436 MB, 47% of that pipe), so here the
-// fifth-generation tensor cores compute, a tile of 128 positions at a time:
+// rate 435 TFLOP/s, half of what the warp-level MMA instructions reach (attn.cu
+// has both kernels' times), so here the fifth-generation tensor cores compute, a
+// tile of 128 positions at a time:
 //
 //   S^T [128 positions x 64 heads] = K Q^T    A = K (rows of dims), B = Q, both
 //                                             from shared memory, S in tensor memory
-//   P = 2^(S c - m)                           one thread per position
+//   P = 2^(S c - m)                           a thread per position and half of the heads
 //   O^T [128 dims x 64 heads] += V^T P^T      A = V and B = P with the positions
 //                                             as the reduced rows (MN-major), O in tensor memory
 //
-// One CTA per SM, two workers per CTA: each has its own range of the list, a
-// group of four softmax warps, references, sums and O, so that one's
-// exponentials and results run beside the other's products.  Tile t is worker
-// (t % 2)'s tile t / 2.  A K tile (32 KB) has the worker's own slot, V tiles
-// share three.  One warp issues the products with K, one those with V (a single
-// one took 2800 cycles for the two and their waits, as long as the HBM for the
-// tile); each worker has a warp per K and V that fetches pages, and listed rows
-// are fetched by four warps (K) and two (V) for both.
+// One CTA per SM, two workers per CTA: each has its own range of the list, eight
+// softmax warps, references, sums and O, a warp that issues its products and warps
+// that fetch, so that one's exponentials and results run beside the other's
+// products.  A worker has one K slot (a tile, 32 KB), filled again while the tile's
+// probabilities are computed, and three V slots of half a tile.  Scores are issued
+// before the values of the tile before where their keys are there.
+//
+// What bounds it.  17 rows of 0-100k, one key-value head: 436 MB in 83 us with the
+// join, 5.3 TB/s of a copy's 6.8; the start (4 us until the first tile arrives) and
+// an uneven end are 10 us of it.  4096 rows over 512 listed positions each, of one
+// request: 1.07 GB of rows from L2 in 210 us, 5.1 TB/s; a worker's tile takes 5500
+// cycles, of which its keys' arrival is 3900 and the softmax 2700, and a row's end
+// 8000 every four tiles.  (Four softmax warps per worker instead of eight: 266 us.
+// Spilled registers cost more than they seem to: a reload that misses waits behind
+// the cache's own reads, 115 us instead of 85 for the 17 rows.)
 //
 // The reference m of a head is not the running maximum but the logit of the
 // segment's first position, kept until another one passes it by 2^40.  fp32 and
@@ -292,7 +299,7 @@ __device__ __forceinline__ void wide_pages(const Args& k, WideShared& sh, WideWa
 
 // 32 listed rows of 256 bytes of a pool, the lane's one (-1: zeros), by 16-byte
 // asynchronous copies to dst and behind it, 64 dims there and the others `other`
-// further.  (Gathers by TMA: 221 us for 4096 rows over 512 positions, these 207.)
+// further.  (Gathers by TMA: 221 us for 4096 rows over 512 positions, these 210.)
 __device__ __forceinline__ void copy_listed(uint32_t dst, uint32_t other, const uint8_t* pool, int row, int lane) {
   const int chunk = lane & 15, odd = lane >> 4;
   dst += (chunk >> 3) * other;
