@@ -181,12 +181,13 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   k.sum = reinterpret_cast<float*>(ws + part_bytes(k.l) + stat_bytes(k.l));
   const int row = c.fp8 ? c.head_dim : 2 * c.head_dim;
   const int per_page = static_cast<int>((c.fp8 ? cache_page_bytes<true>(c.head_dim) : cache_page_bytes<false>(c.head_dim)) / row);
-  // listed rows: the wide kernel uses no map, the other one that of K, a row at a time
-  CUtensorMap kmap{}, vmap{};
-  const int64_t rows = c.num_pages * c.num_kv_heads * per_page;
+  CUtensorMap kmap{}, vmap{};  // listed rows use none
   cudaError_t e = cudaSuccess;
-  if (a.pos == nullptr || !wide) e = make_rows_tmap(&kmap, c.k_pool, rows, row, a.pos != nullptr ? 1 : attn::kTile);
-  if (e == cudaSuccess && a.pos == nullptr) e = make_rows_tmap(&vmap, c.v_pool, rows, row, attn::kTile);
+  if (a.pos == nullptr) {
+    const int64_t rows = c.num_pages * c.num_kv_heads * per_page;
+    e = make_rows_tmap(&kmap, c.k_pool, rows, row, attn::kTile);
+    if (e == cudaSuccess) e = make_rows_tmap(&vmap, c.v_pool, rows, row, attn::kTile);
+  }
   if (e == cudaSuccess)
     e = wide ? attn::launch_wide(kmap, vmap, k, stream) : c.fp8 ? attn::launch_fp8(kmap, vmap, k, stream) : attn::launch_bf16(kmap, vmap, k, stream);
   // a unit of one tile has nothing to join

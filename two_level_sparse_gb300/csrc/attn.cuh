@@ -178,16 +178,6 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(map), "r"(x), "r"(row), "r"(bar)
       : "memory");
 }
-// Four rows (one box row each) to consecutive rows at dst; issued by one lane of a converged warp.
-__device__ __forceinline__ void gather4_elect(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
-                                              uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -462,12 +452,11 @@ __device__ void produce_pages(const Args& k, Shared& sh, Walk<kTile> w, const CU
   ring.drain();
 }
 
-// Listed positions, by two warps side by side: one gathers K, four rows per TMA
-// instruction; the other copies V by 16-byte asynchronous copies, its chunks put
-// where the TMA swizzle would have put them, and the FP8 scales.  (Alone, one
-// warp issues 18 and 22 bytes per ns and SM of 256-byte rows, and copies beyond
-// what the load path keeps in flight delay the consumers' shared-memory
-// accesses; the two ways do not share a path.)  Two tiles of look-ahead: the
+// Listed positions, by two warps side by side: one copies K, the other V and the
+// FP8 scales, by 16-byte asynchronous copies whose chunks are put where the TMA
+// swizzle would have put them.  (K gathered by TMA, four rows per instruction:
+// 300 rows over 512 positions of 4 heads of 64 in bf16 63 us, these 58; FP8 70, 66;
+// 64 rows of 8 heads of 128 45.7, 46.7; cold caches.)  Two tiles of look-ahead: the
 // list entries of the second next tile and the page ids of the next one are on
 // their way while a tile is copied.
 struct ListTile {
@@ -478,7 +467,7 @@ struct ListTile {
 };
 
 template <class C, int D, bool kFp8, bool kValues>
-__device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUtensorMap* kmap, uint32_t stages) {
+__device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stages) {
   const AttnArgs& a = k.a;
   const CacheArgs& c = a.c;
   constexpr int64_t kPageBytes = cache_page_bytes<kFp8>(D);
@@ -526,10 +515,9 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUt
       if (now.table != nullptr && ((!in0 && now.s0 != -1) || (!in1 && now.s1 != -1))) report(c.dev_err, kDevErrPos);
       if (ok0 != in0 || ok1 != in1) report(c.dev_err, kDevErrPage);
     }
-    // rows of the pool (of kRow bytes); an entry that does not count: row 0 of K, zeros of V
-    const int none = kValues ? -1 : 0;
-    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s0 & (kPage - 1)) : none;
-    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s1 & (kPage - 1)) : none;
+    // rows of the pool (of kRow bytes); -1: an entry that does not count, zeros
+    const int row0 = ok0 ? (p0 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s0 & (kPage - 1)) : -1;
+    const int row1 = ok1 ? (p1 * c.num_kv_heads + now.head) * kRowsPerPage + (now.s1 & (kPage - 1)) : -1;
     if (ring.acquire()) {
       const int stage = ring.stage;
       const uint32_t kdst = stages + stage * C::kStage;
@@ -538,19 +526,16 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUt
         if (lane == 0) {
           sh.mask[stage][0] = m0;
           sh.mask[stage][1] = m1;
-          mbar_arrive_expect_tx(&sh.full[stage], C::kMat);
+          mbar_arrive(&sh.full[stage]);
         }
         __syncwarp();
-        const uint32_t bar = smem_u32(&sh.full[stage]);
-#pragma unroll 2
-        for (int p = 0; p < kTile; p += 4) {
-          const int mine = p < 32 ? row0 : row1;
-          const int r0 = __shfl_sync(0xffffffffu, mine, p & 31), r1 = __shfl_sync(0xffffffffu, mine, (p & 31) + 1);
-          const int r2 = __shfl_sync(0xffffffffu, mine, (p & 31) + 2), r3 = __shfl_sync(0xffffffffu, mine, (p & 31) + 3);
+        const uint8_t* kbase = c.k_pool + chunk * 16;
 #pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b)
-            gather4_elect(kdst + b * C::kSub + p * C::kBox, kmap, b * C::kBox, r0, r1, r2, r3, bar);
+        for (int p = 0; p < kTile; p += kRows) {  // positions p .. p + kRows - 1
+          const int row = __shfl_sync(0xffffffffu, p < 32 ? row0 : row1, (p + lane / kChunks) & 31);
+          copy16(kdst + tile_offset<C>(p + lane / kChunks, chunk), kbase + static_cast<int64_t>(max(row, 0)) * C::kRow, row >= 0);
         }
+        cp_async_arrive_noinc(&sh.full[stage]);
       } else {
         const uint8_t* vbase = c.v_pool + chunk * 16;
 #pragma unroll
@@ -577,10 +562,7 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, const CUt
     ring.advance();
     now = next, next = after, p0 = n0, p1 = n1;
   }
-  if (kValues)
-    cp_async_wait<0>();
-  else
-    ring.drain();
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ consumers
@@ -933,7 +915,7 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh.full[s], a.pos != nullptr ? 33 : 1);
+      mbar_init(&sh.full[s], a.pos != nullptr ? 65 : 1);
       mbar_init(&sh.empty[s], WP * WH);
     }
     fence_mbar_init();
@@ -949,9 +931,9 @@ __global__ void __launch_bounds__(Config<D, kFp8, NT, WP, WH>::kThreads, Config<
     if (warp < WP * WH)
       consume<C, D, kFp8, NT, WP, WH>(k, sh, w, base, acc, stat);
     else if (a.pos != nullptr && warp == WP * WH)
-      produce_list<C, D, kFp8, false>(k, sh, w, &kmap, base);
+      produce_list<C, D, kFp8, false>(k, sh, w, base);
     else if (a.pos != nullptr)
-      produce_list<C, D, kFp8, true>(k, sh, w, &kmap, base);
+      produce_list<C, D, kFp8, true>(k, sh, w, base);
     else if (warp == WP * WH)
       produce_pages<C, D, kFp8>(k, sh, w, &kmap, &vmap, base);
   }
