@@ -34,8 +34,8 @@
 // softmax and FP8's conversions, tensor instructions a sixth; two CTAs per SM keep
 // the loads going while one reduces.  Short calls are bound by latency: 4 rows of
 // 1k-4k (42 MB) take 17 us, 6 of them at the HBM's rate, two launches and their
-// starts the rest.  64 rows of 512 listed positions over 8 heads (137 MB) take 34
-// us: 8 tiles a unit, whose rows (256 bytes) are fetched at 4 TB/s.
+// starts the rest.  64 rows of 512 listed positions over 8 heads (137 MB) take 35
+// us: 8 tiles a unit, whose rows (256 bytes) are fetched at 3.9 TB/s.
 //
 // FP8 pages.  K: e4m3 widens to f16 exactly, one conversion per pair; the
 // query becomes f16 exactly too once each head is scaled by a power of two to
