@@ -101,7 +101,8 @@ CI_API int ci_attn_decode(const uint16_t* q, int64_t q_stride, int32_t rows, int
  * rotated keys and the values as they are go to slot u % 64 of page
  * page_table[request of t][u / 64], u = cache_pos[t] (cache_pos == NULL: u =
  * p): rounded once to bf16, or (CI_CACHE_FP8) as e4m3(x / scale), nearest
- * even, with the position's own fp32 scale = max(amax, 1e-10) / 448 per head.
+ * even, with the position's own fp32 scale = max(amax, 1e-10) / 448 per head
+ * (NaN where a value is NaN, so that what reads the entry is NaN too).
  * A negative u writes no cache entry (padding).  p outside [0, max_pos) sets
  * CI_DEVERR_POS, the token's queries are 0 and its cache entry is not written;
  * so is an entry with u >= 64 * max_pages (CI_DEVERR_POS) or with a page id

@@ -246,3 +246,24 @@ def test_from_a_graph(cache, hq):
         torch.cuda.synchronize()
         assert torch.equal(got, out)
         check_rows(got, q, g["k"], g["v"], g["table"], lambda t: range(n[t]), 128, [(t, t) for t in range(3)])
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("hq", [8, 80])
+def test_nan_reaches_the_reader(cache, hq, what, fmt):
+    """A NaN in a new token's key or value shows in its heads' attention, whatever the format, and in no other's."""
+    d, n = 128, 3
+    x = torch.randn(n, hq + 4, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    x[1, hq + (0 if what == "k" else 2), 5] = math.nan
+    pools = [torch.zeros(1, 2, cache.page_bytes(fmt, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    q, out = (torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, at = i32([[0]]), i32([0, 1, 2])
+    cache.ci_qk_norm_rope_append(x[:, :hq], x[:, hq:hq + 2], x[:, hq + 2:], None, None, 1e-6, cos_sin(4, 0).cuda(), True,
+                                 at, q, *pools, table, PRE)
+    cache.ci_attn_decode(q, *pools, table, PRE, at + 1, 64, d ** -0.5, out)
+    assert out[0].isfinite().all() and out[1:, hq // 2:].isfinite().all()
+    if what == "k" or fmt == FP8:
+        assert out[1:, :hq // 2].isnan().all()
+    else:
+        assert out[1:, :hq // 2, 5].isnan().all()
