@@ -569,6 +569,10 @@ __device__ void produce_list(const Args& k, Shared& sh, Walk<kTile> w, uint32_t 
 template <class C, int D, bool kFp8, int NT, int WP, int WH>
 __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stages, float* acc, float* stat) {
   constexpr int kM = D / 16, kK = D / 16, MT = 4 / WP;
+  // How many of its 16-position tiles a warp has in registers at once: all, or half
+  // where that spills 192 bytes (FP8, D = 128, 64 heads: 17 rows of 0-100k 166 -> 156
+  // us, 1024 rows over 512 listed 161 -> 128; elsewhere all is as fast or faster).
+  constexpr int MS = kFp8 && D == 128 && MT == 4 ? 2 : MT;
   const AttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int wp = warp % WP, wh = warp / WP, p0 = wp * 16 * MT;
@@ -642,16 +646,19 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
       const uint32_t kbase = stages + stage * C::kStage, vbase = kbase + C::kMat;
       const uint32_t sbase = stages + C::kStages * C::kStage + stage * 2 * C::kScale;
       const uint64_t mask = static_cast<uint64_t>(sh.mask[stage][1]) << 32 | sh.mask[stage][0];
-      constexpr uint64_t kOnes = MT == 4 ? ~0ull : (1ull << (16 * MT & 63)) - 1;
-      const uint64_t here = (mask >> p0) & kOnes;  // the warp's positions
-      if (alive && here != 0) {
+      constexpr uint64_t kOnes = MS == 4 ? ~0ull : (1ull << (16 * MS & 63)) - 1;
+#pragma unroll 1
+      for (int part = 0; part < MT / MS; ++part) {
+        const int pp = p0 + part * 16 * MS;
+        const uint64_t here = (mask >> pp) & kOnes;  // these positions
+        if (!alive || here == 0) continue;
         // ---- S^T
-        float s[MT][NT][4];
+        float s[MS][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < MS; ++mt) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
-          const int p = p0 + mt * 16;
+          const int p = pp + mt * 16;
           if (kFp8) {
 #pragma unroll
             for (int kk = 0; kk < kK; kk += 2) {
@@ -683,8 +690,8 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) now[nt][0] = top[nt][0], now[nt][1] = top[nt][1];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int pa = p0 + mt * 16 + g;
+        for (int mt = 0; mt < MS; ++mt) {
+          const int pa = pp + mt * 16 + g;
           float fa = factor, fb = factor;
           if (kFp8) {
             fa *= lds_f32(sbase + pa * 4);
@@ -732,8 +739,8 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         }
         if (!kFp8 && !all && a.pos == nullptr) {  // what follows a row's last position must not reach a product with 0
 #pragma unroll 1
-          for (int e = lane; e < 16 * MT * (C::kRow / 16); e += 32) {
-            const int p = p0 + e / (C::kRow / 16);
+          for (int e = lane; e < 16 * MS * (C::kRow / 16); e += 32) {
+            const int p = pp + e / (C::kRow / 16);
             if ((mask >> p) & 1) continue;
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vbase + tile_offset<C>(p, e % (C::kRow / 16))),
                          "r"(0)
@@ -744,8 +751,8 @@ __device__ void consume(const Args& k, Shared& sh, Walk<kTile> w, uint32_t stage
         }
         // ---- probabilities; O^T += V^T P^T
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int p = p0 + mt * 16;
+        for (int mt = 0; mt < MS; ++mt) {
+          const int p = pp + mt * 16;
           float va = 1.f, vb = 1.f;
           if (kFp8) {
             va = kTwo60 * lds_f32(sbase + C::kScale + (p + g) * 4);
@@ -970,7 +977,8 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
     if (h == 8) return launch<128, kFp8, 1, 4, 1>(kmap, vmap, k, s);
     if (h == 16) return launch<128, kFp8, 2, 4, 1>(kmap, vmap, k, s);
     if (h == 32) return launch<128, kFp8, 2, 2, 2>(kmap, vmap, k, s);
-    return launch<128, kFp8, 2, 1, 4>(kmap, vmap, k, s);
+    if constexpr (kFp8) return launch<128, kFp8, 2, 1, 4>(kmap, vmap, k, s);
+    return cudaErrorInvalidValue;  // bf16: more than 32 heads are the wide kernel's
   }
   if (h == 8) return launch<256, kFp8, 1, 4, 1>(kmap, vmap, k, s);
   if (h == 16) return launch<256, kFp8, 1, 4, 2>(kmap, vmap, k, s);
