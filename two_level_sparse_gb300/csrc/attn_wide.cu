@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     sh.abort = 0;
   }
   wait_predecessor();
-  if (tid < 2) k.part[2 * blockIdx.x + tid].last = -1;
+  // each CTA its own workers' records: nothing orders it with the CTAs that write the others
+  if (tid < 2) k.part[blockIdx.x + tid * gridDim.x].last = -1;
   if (tid < 2 * kH) sh.ref[tid / kH][tid % kH] = 0.f;
   tc_fence_before();
   const int units = a.c.num_kv_heads * k.l.blocks;
