@@ -1,0 +1,91 @@
+"""The cache's binding without a GPU: what it hands to the library and which
+stream's memory it takes, with the library and the streams replaced."""
+import contextlib
+import ctypes
+import os
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+class Device(torch.Tensor):
+    """A host tensor that says it lives on the GPU."""
+
+    is_cuda = property(lambda self: True)
+
+
+def dev(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Device)
+
+
+@pytest.fixture
+def cache(monkeypatch):
+    from two_level_sparse_gb300 import build
+
+    if not os.path.exists(os.path.join(ROOT, "two_level_sparse_gb300", "libci.so")):
+        build.build()
+    from two_level_sparse_gb300 import cache as mod
+
+    calls = []
+
+    def entry(name):
+        return lambda *a: calls.append((name, a)) or 0
+
+    lib = SimpleNamespace(**{n: entry(n) for n in mod.SIGNATURES if n.startswith(("ci_attn_d", "ci_qk", "ci_pages"))},
+                          ci_attn_workspace_bytes=mod.lib.ci_attn_workspace_bytes,
+                          ci_cache_page_bytes=mod.lib.ci_cache_page_bytes)
+    monkeypatch.setattr(mod, "lib", lib)
+    monkeypatch.setattr(mod, "_current_stream", lambda device: 0)
+    return SimpleNamespace(mod=mod, calls=calls)
+
+
+@pytest.fixture
+def pools_asked(monkeypatch):
+    """(shape, stream) of every torch.empty: the stream whose memory it comes from, None for the current one."""
+    asked, on = [], [None]
+    empty = torch.empty
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(s)
+        yield
+        on.pop()
+
+    def recorded(*shape, **kw):
+        asked.append((tuple(shape[0]) if len(shape) == 1 and not isinstance(shape[0], int) else shape, on[-1]))
+        return empty(*shape, **kw).as_subclass(Device)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch, "empty", recorded)
+    return asked
+
+
+SIDE = SimpleNamespace(cuda_stream=77)
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+def test_workspace_comes_from_the_calls_stream(cache, pools_asked, stream):
+    q, pool = dev(2, 8, 64, dtype=torch.bfloat16), dev(4, 2, 8192, dtype=torch.uint8)
+    cache.mod.ci_attn_decode(q, pool, pool, dev(2, 2), 0, dev(2), 128, 1.0, q, stream=stream)
+    n = cache.mod.attn_workspace_bytes(2, 8, 2, 64)
+    assert pools_asked == [((n,), stream)]
+    assert cache.calls[-1][1][-1] == (77 if stream else 0)
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+def test_cache_results_come_from_the_calls_stream(cache, pools_asked, stream):
+    from two_level_sparse_gb300.paged import PagedCache
+
+    c = PagedCache(1, 2, 2, 4, 2, 64, device="cpu")
+    for t in ("k", "v", "page_table", "dev_err"):
+        setattr(c, t, getattr(c, t).as_subclass(Device))
+    q, kv = dev(2, 8, 64, dtype=torch.bfloat16), dev(2, 2, 64, dtype=torch.bfloat16)
+    pools_asked.clear()
+    c.append(0, q, kv, kv, None, None, 1e-6, dev(4, 0, dtype=torch.float32), True, dev(2), 0, stream=stream)
+    c.attend(0, q, 0, dev(2), stream=stream)
+    assert [name for name, _ in cache.calls] == ["ci_qk_norm_rope_append", "ci_attn_decode"]
+    assert len(pools_asked) == 3 and all(on is stream for _, on in pools_asked)

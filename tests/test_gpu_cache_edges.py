@@ -43,3 +43,29 @@ def test_attention_beside_other_work(cache, hq, listed):
     torch.cuda.synchronize()
     for o, z in res:
         assert torch.equal(o, out) and torch.equal(z, lse)
+
+
+@pytest.mark.parametrize("hq", [64, 8])
+def test_attention_on_another_stream(cache, hq):
+    """A call on a stream that is not the current one, with no workspace given, while the current stream
+    allocates and writes the same amounts of memory."""
+    from two_level_sparse_gb300.paged import PagedCache
+
+    p = Problem([20000, 1, 9000, 0], hq, 1, 128, BF16, seed=21)
+    out, lse = p.run(cache)
+    p.check(out, lse)
+    g = [getattr(p, n).cuda() for n in ("q", "k", "v", "table", "seq")]
+    c = PagedCache(1, 4, g[3].shape[1], g[1].shape[0], 1, 128)
+    c.k[0].copy_(g[1]), c.v[0].copy_(g[2]), c.page_table.copy_(g[3])
+    n, side = cache.attn_workspace_bytes(4, hq, 1, 128), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        o = torch.empty_like(out)
+        side.wait_stream(torch.cuda.current_stream())
+        cache.ci_attn_decode(*g[:4], 0, g[4], p.max_len, p.scale, o, stream=side)
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        got += [o, c.attend(0, g[0], 0, g[4], p.max_len, p.scale, stream=side)]
+        torch.empty(out.numel(), dtype=torch.bfloat16, device="cuda").fill_(7)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out) for o in got)

@@ -96,6 +96,16 @@ def _on(stream, like):
     return stream.cuda_stream if stream is not None else _current_stream(like.get_device())
 
 
+def empty_on(stream, shape, dtype, device):
+    """torch.empty of the memory of the stream that is to use it (None: the
+    current one): what another stream had there, or gets there once the tensor
+    is dropped, may not be ordered with the work on ``stream``."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(fn, status):
     if status != CI_OK:
         raise CIError(fn, status)
@@ -145,7 +155,8 @@ def ci_attn_decode(q, k_pool, v_pool, page_table, layout, seq_len, max_len, scal
                    workspace=None, dev_err=None, stream=None, req_start=None):
     """Attention of q [rows, q_heads, head_dim] over the cache, or over the
     positions ``pos`` [rows, n] of it (see include/ci_cache.h).  ``workspace``:
-    uint8, attn_workspace_bytes() of it; allocated here if None."""
+    uint8, attn_workspace_bytes() of it; allocated here, from the memory of the
+    call's stream, if None."""
     qp, q_stride, shape = _heads(q, "q")
     op, out_stride, out_shape = _heads(out, "out")
     if out_shape != shape:
@@ -162,7 +173,7 @@ def ci_attn_decode(q, k_pool, v_pool, page_table, layout, seq_len, max_len, scal
         # an empty tensor has a null pointer, which would mean "every position": any other one does, it is not read
         pp = _ints(pos, "pos") if pos_stride else qp
     if workspace is None:
-        workspace = torch.empty(attn_workspace_bytes(rows, hq, hkv, d), dtype=_U8, device=q.device)
+        workspace = empty_on(stream, (attn_workspace_bytes(rows, hq, hkv, d),), _U8, q.device)
     num_req, max_pages = page_table.shape
     starts = None
     if layout == LAYOUT_VARLEN:

@@ -30,7 +30,9 @@ class PagedCache:
     """``layers`` attention layers' keys and values for ``requests`` requests
     of up to ``64 * max_pages`` positions, in ``num_pages`` pages (every
     layer's pools use the same ids).  All lengths and ids that the methods take
-    are int32 tensors on the cache's device; nothing but ``check`` waits."""
+    are int32 tensors on the cache's device; nothing but ``check`` waits.
+    ``append`` and ``attend`` run on ``stream`` (None: the current one), whose
+    memory their results are."""
 
     def __init__(self, layers: int, requests: int, max_pages: int, num_pages: int, kv_heads: int, head_dim: int,
                  cache_format: int = ops.CACHE_BF16, companions=(), device="cuda"):
@@ -75,22 +77,23 @@ class PagedCache:
         ops.ci_pages_compact(self.page_table, self.ref_count, remap, src, dst, self._count, dev_err=self.dev_err)
         self._copy(src, dst, self._count)
 
-    def append(self, layer, q, k, v, q_norm, k_norm, eps, cos_sin, is_neox, positions, layout, q_out=None, **kw):
+    def append(self, layer, q, k, v, q_norm, k_norm, eps, cos_sin, is_neox, positions, layout, q_out=None, stream=None,
+               **kw):
         """The new tokens' keys and values into their pages; returns the normed and rotated queries."""
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        q_out = ops.empty_on(stream, q.shape, q.dtype, q.device) if q_out is None else q_out
         ops.ci_qk_norm_rope_append(q, k, v, q_norm, k_norm, eps, cos_sin, is_neox, positions, q_out, self.k[layer],
-                                   self.v[layer], self.page_table, layout, dev_err=self.dev_err, **kw)
+                                   self.v[layer], self.page_table, layout, dev_err=self.dev_err, stream=stream, **kw)
         return q_out
 
     def attend(self, layer, q, layout, seq_len, max_len=None, scale=None, pos=None, out=None, stream=None, **kw):
         """Attention of q [rows, heads, head_dim] over the cache or over ``pos``."""
         rows, heads, d = q.shape
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        out = ops.empty_on(stream, q.shape, q.dtype, q.device) if out is None else out
         on = stream if stream is not None else torch.cuda.current_stream(q.device)
         key = (rows, heads, on.cuda_stream)  # calls on two streams may overlap
         if key not in self._workspace:
             n = ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d)
-            self._workspace[key] = torch.empty(n, dtype=torch.uint8, device=q.device)
+            self._workspace[key] = ops.empty_on(stream, (n,), torch.uint8, q.device)
         max_len = ops.PAGE * self.page_table.shape[1] if max_len is None else max_len
         ops.ci_attn_decode(q, self.k[layer], self.v[layer], self.page_table, layout, seq_len, max_len,
                            d ** -0.5 if scale is None else scale, out, pos=pos, workspace=self._workspace[key],
