@@ -89,3 +89,28 @@ def test_cache_results_come_from_the_calls_stream(cache, pools_asked, stream):
     c.attend(0, q, 0, dev(2), stream=stream)
     assert [name for name, _ in cache.calls] == ["ci_qk_norm_rope_append", "ci_attn_decode"]
     assert len(pools_asked) == 3 and all(on is stream for _, on in pools_asked)
+
+
+def pool_args(call):
+    """Pointers, bytes per page and number of pages that ci_pages_copy was called with."""
+    ptrs, sizes, n, pages = call[1][:4]
+    return ((ctypes.c_uint64 * n).from_address(ptrs)[:], (ctypes.c_int64 * n).from_address(sizes)[:], pages)
+
+
+@pytest.mark.parametrize("view", ["whole", "every fourth of four", "one of two", "turned", "expanded", "wide pages"])
+def test_copy_takes_pages_as_they_are(cache, view, monkeypatch):
+    """A tensor of one pool is contiguous whatever its first stride says."""
+    x = {"whole": lambda: dev(4, 3, 64, dtype=torch.uint8),
+         "every fourth of four": lambda: dev(4, 3, 64, dtype=torch.uint8)[3::4],
+         "one of two": lambda: dev(2, 3, 64, dtype=torch.uint8)[::2],
+         "turned": lambda: dev(4, 1, 256, dtype=torch.uint8).transpose(0, 1),
+         "expanded": lambda: dev(3, 64, dtype=torch.uint8).as_strided((1, 3, 64), (0, 64, 1)),
+         "wide pages": lambda: dev(5, 3, 2, 32, dtype=torch.uint8)}[view]()
+    assert x.is_contiguous()
+    seen = []
+    monkeypatch.setattr(cache.mod.lib, "ci_pages_copy", lambda *a: seen.append(pool_args((None, a))) or 0)
+    cache.mod.ci_pages_copy(x, dev(2), dev(2))
+    a_pool = x[0].numel()
+    cache.mod.ci_pages_copy(list(x), dev(2), dev(2))
+    assert seen[0] == ([x.data_ptr() + i * a_pool for i in range(len(x))], [a_pool // x.shape[1]] * len(x), x.shape[1])
+    assert seen[1] == seen[0]

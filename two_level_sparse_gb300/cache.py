@@ -272,8 +272,8 @@ def ci_pages_copy(pools, copy_src, copy_dst, count=None, dev_err=None, stream=No
         raise ValueError(f"1 to {MAX_POOLS} pools per call")
     if isinstance(pools, torch.Tensor):
         base, num_pages = _dev(pools, _U8, "pools"), pools.shape[1]
-        step = pools.stride(0)
-        ptrs = array("Q", range(base, base + n * step, step)) if step else array("Q", [base] * n)
+        step = pools.numel() // n  # (the first stride of one pool may be anything)
+        ptrs = array("Q", [base + i * step for i in range(n)])
         sizes = array("q", [step // num_pages if num_pages else 0]) * n
     else:
         num_pages = pools[0].shape[0]
