@@ -69,3 +69,41 @@ def test_attention_on_another_stream(cache, hq):
         torch.empty(out.numel(), dtype=torch.bfloat16, device="cuda").fill_(7)
     torch.cuda.synchronize()
     assert all(torch.equal(o, out) for o in got)
+
+
+@pytest.mark.parametrize("hq", [64, 8])
+@pytest.mark.parametrize("logit", [11.0, 16.5, 27.0, 28.0])
+def test_attention_largest_values(cache, hq, logit):
+    """Values of 2^80, the most that is promised, under hundreds of equal logits far above the first one's."""
+    n = 700
+    p = Problem([n] * 700, hq, 1, 128, BF16, layout=PRE, seed=17)
+    p.scale = 1.0
+    p.q.zero_()
+    p.q[:, :, 0] = 1.0
+    k = p.k.view(torch.bfloat16).unflatten(-1, (64, 128))
+    k.zero_()
+    k[..., 0] = logit
+    k[p.table[0, 0], 0, 0, 0] = 0
+    p.v.view(torch.bfloat16).fill_(2.0 ** 80)
+    out, lse = p.run(cache)
+    assert ((out.double() / 2.0 ** 80 - 1).abs() <= 2.0 ** -8).all()
+    want = np.log(1 + (n - 1) * np.exp(logit))
+    assert ((lse.double() - want).abs() <= (n + 64) * 2.0 ** -23 + 2.0 ** -21 * (want + 1) + 136 * 2.0 ** -23 * logit).all()
+
+
+@pytest.mark.parametrize("hq", [64, 8])
+def test_attention_rising_logits(cache, hq):
+    """Logits that rise through a row in steps of every size: each passes what the ones before were kept against."""
+    rng = np.random.default_rng(18)
+    lens = [3000, 700, 129, 64]
+    for step in (0.01, 0.1, 1.0, 20.0):
+        p = Problem(lens, hq, 1, 128, BF16, seed=18)
+        p.scale = 1.0
+        k = p.k.view(torch.bfloat16).unflatten(-1, (64, 128))
+        p.q.normal_(generator=torch.Generator().manual_seed(2))
+        k.mul_(0.05)
+        p.q[:, :, 0] = torch.from_numpy(rng.choice([1.0, -1.0, 2.0], size=(4, hq))).to(torch.bfloat16)
+        for t, n in enumerate(lens):
+            s = torch.arange(n)
+            k[p.table[t, s // 64].long(), 0, s % 64, 0] = (step * s).bfloat16()
+        p.check(*p.run(cache))

@@ -29,12 +29,14 @@
 // Spilled registers cost more than they seem to: a reload that misses waits behind
 // the cache's own reads, 115 us instead of 85 for the 17 rows.)
 //
-// The reference m of a head is not the running maximum but the logit of the
-// segment's first position, kept until another one passes it by 2^40.  fp32 and
-// bf16 have the exponents for that: probabilities up to 2^40 are as exact as
-// those below one, the reference's own is 1, and maxima across the positions
-// (across lanes, here) and the rescaling of O happen only where a logit is
-// further off.
+// The reference m of a head is not the running maximum but 24 above the logit (in
+// base 2) of the segment's first position; once a tile has a logit 16 above a
+// reference, 24 above each head's largest of that tile, where that is more.  fp32 and
+// bf16 have the exponents for that: probabilities from 2^-24 to 2^16 are as exact as
+// those below one, and maxima across the positions (across lanes, here) and the
+// rescaling of O happen only where a logit lies 40 above the one that set the
+// reference.  Values of 2^80 under probabilities of 2^16 add up to less than 2^128
+// over 2^31 positions.
 #include "attn.cuh"
 
 namespace ci {
@@ -51,7 +53,7 @@ constexpr int kGroup = 32 * kSoftmaxWarps, kWideThreads = 256 + 2 * kGroup;
 // of worker g, at + 64 g: S, O, the sums of P, those of P as it is rounded
 constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256, kColR = 384;
 constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
-constexpr float kSlack = 40.f;
+constexpr float kLead = 24.f, kSlack = 16.f;       // a reference over its logit; a logit over its reference
 
 struct WideShared {
   uint64_t k_full[2], k_empty[2], v_full[2][kVSlots], v_empty[2][kVSlots], s_full[2], p_full[2], pv_done[2], drain[2];
@@ -532,7 +534,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
           tmem_ld_wait();
           if (row == first) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(__uint_as_float(s[j]) * factor, kFar), -kFar);
+            for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(__uint_as_float(s[j]) * factor + kLead, kFar), -kFar);
           }
         }
         named_sync(1 + g, kGroup);
@@ -571,7 +573,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
           const float old = group_ref[in_group];
           float top = old;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top = fmaxf(top, scratch[x * kH + in_group]);
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, scratch[x * kH + in_group] + kLead);
           group_alpha[in_group] = exp2_approx(old - top);
           group_ref[in_group] = top;
         }
