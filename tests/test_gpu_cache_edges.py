@@ -107,3 +107,34 @@ def test_attention_rising_logits(cache, hq):
             s = torch.arange(n)
             k[p.table[t, s // 64].long(), 0, s % 64, 0] = (step * s).bfloat16()
         p.check(*p.run(cache))
+
+
+@pytest.mark.parametrize("hq", [64, 8])
+@pytest.mark.parametrize("power", [40, 60, 80, 100, 110])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_huge_logits(cache, hq, power, sign):
+    """Logits of whole numbers times 2^power, both signs, one position ahead of all others: the result is its
+    value, to the bit, and lse its logit."""
+    d, lens, group = 128, [1, 64, 700, 3000, 129], hq
+    p = Problem(lens, hq, 1, d, BF16, seed=16)
+    p.scale = 0.75
+    p.q.zero_()
+    p.q[:, :, 0] = 2.0 ** (power // 2)
+    k = p.k.view(torch.bfloat16).unflatten(-1, (64, d))
+    v = p.v.view(torch.bfloat16).unflatten(-1, (64, d))
+    k.zero_()
+    rng = np.random.default_rng(power)
+    best = []
+    for t, n in enumerate(lens):
+        best.append(int(rng.integers(0, n)))
+        s = np.arange(n)
+        size = torch.from_numpy(rng.integers(2, 100, n).astype(np.float32))
+        size[best[t]] = 1 if sign < 0 else 101
+        k[p.table[t, s // 64].long(), 0, torch.from_numpy(s % 64), 0] = (sign * size * 2.0 ** (power - power // 2)).bfloat16()
+    out, lse = p.run(cache)
+    out, lse = out.cpu(), lse.double().cpu()
+    for t, s in enumerate(best):
+        want = v[p.table[t, s // 64], 0, s % 64]
+        z = p.scale * sign * (1 if sign < 0 else 101) * 2.0 ** power
+        assert torch.equal(out[t], want.expand(group, d)), (t, s)
+        assert ((lse[t] - z).abs() <= 2.0 ** -20 * abs(z)).all()

@@ -52,7 +52,7 @@ constexpr int kSoftmaxWarps = 8;  // per worker: a quarter of a tile's positions
 constexpr int kGroup = 32 * kSoftmaxWarps, kWideThreads = 256 + 2 * kGroup;
 // of worker g, at + 64 g: S, O, the sums of P, those of P as it is rounded
 constexpr int kTmem = 512, kColS = 0, kColO = 128, kColL = 256, kColR = 384;
-constexpr float kFar = 1.0e30f;                     // references lie in [-kFar, kFar]
+constexpr float kFar = 3.0e38f;                     // a first logit's reference lies in [-kFar, kFar]
 constexpr float kLead = 24.f, kSlack = 16.f;       // a reference over its logit; a logit over its reference
 
 struct WideShared {
@@ -169,6 +169,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+// A score's logit in base 2, rounded by itself: the reference is made of rounded
+// logits, and the distance to it would otherwise be off by half of their last place,
+// more than any slack from logits of 2^30 on.
+__device__ __forceinline__ float logit_of(uint32_t score, float factor) { return __fmul_rn(__uint_as_float(score), factor); }
+// Two logits less their references.  (Packed products are fused with the packed
+// differences, so these are scalar.)
+__device__ __forceinline__ float2 over_ref(uint32_t s0, uint32_t s1, float factor, float r0, float r1) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\tsub.rn.f32x2 x, x, r;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(logit_of(s0, factor)), "f"(logit_of(s1, factor)), "f"(r0), "f"(r1));
+  return d;
 }
 struct Buffers {
   uint32_t slots, p, q;  // shared-memory addresses
@@ -534,7 +548,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
           tmem_ld_wait();
           if (row == first) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(__uint_as_float(s[j]) * factor + kLead, kFar), -kFar);
+            for (int j = 0; j < 8; ++j) ref[h + j] = fmaxf(fminf(logit_of(s[j], factor) + kLead, kFar), -kFar);
           }
         }
         named_sync(1 + g, kGroup);
@@ -550,8 +564,9 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 r = *reinterpret_cast<const float4*>(ref + h + j);
-          over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j]), factor, -r.x), fmaf(__uint_as_float(s[j + 1]), factor, -r.y)));
-          over = fmaxf(over, fmaxf(fmaf(__uint_as_float(s[j + 2]), factor, -r.z), fmaf(__uint_as_float(s[j + 3]), factor, -r.w)));
+          const float2 a = over_ref(s[j], s[j + 1], factor, r.x, r.y), b = over_ref(s[j + 2], s[j + 3], factor, r.z, r.w);
+          over = fmaxf(over, fmaxf(a.x, a.y));
+          over = fmaxf(over, fmaxf(b.x, b.y));
         }}
       }
       const bool raise = group_any(1 + g, valid && over > kSlack);
@@ -564,7 +579,7 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
           tmem_ld_wait();
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {
-            const float r = warp_max(valid ? __uint_as_float(j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3]) * factor : -INFINITY);
+            const float r = warp_max(valid ? logit_of(j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3], factor) : -INFINITY);
             if (lane == 0) scratch[quad * kH + half + h + j] = r;
           }
         }
@@ -606,8 +621,8 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
 #pragma unroll
         for (int x = 0; x < 8; x += 2) {
           const float2 r = *reinterpret_cast<const float2*>(ref + j0 + x);
-          float p0 = exp2_approx(fmaf(__uint_as_float(s[x]), factor, -r.x));
-          float p1 = exp2_approx(fmaf(__uint_as_float(s[x + 1]), factor, -r.y));
+          const float2 d = over_ref(s[x], s[x + 1], factor, r.x, r.y);
+          float p0 = exp2_approx(d.x), p1 = exp2_approx(d.y);
           if (!valid) p0 = p1 = 0.f;
           v[x / 2] = bf16x2(p0, p1);
           const float r0 = bf16_lo(v[x / 2]), r1 = bf16_hi(v[x / 2]);
