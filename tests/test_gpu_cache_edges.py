@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import BF16, PRE, Problem, picks
+from test_gpu_cache import BF16, FP8, PRE, Problem, cos_sin, picks
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
@@ -138,3 +138,60 @@ def test_attention_huge_logits(cache, hq, power, sign):
         z = p.scale * sign * (1 if sign < 0 else 101) * 2.0 ** power
         assert torch.equal(out[t], want.expand(group, d)), (t, s)
         assert ((lse[t] - z).abs() <= 2.0 ** -20 * abs(z)).all()
+
+
+def codes_of(x):
+    """e4m3 codes and scales of bf16 heads [..., d], by fp32 division."""
+    x = x.float().numpy()
+    scale = np.maximum(np.abs(x).max(-1), np.float32(1e-10)) / np.float32(448)
+    with np.errstate(invalid="ignore"):
+        y = torch.from_numpy(x / scale[..., None])
+    return y.to(torch.float8_e4m3fn).view(torch.uint8).numpy(), scale
+
+
+def append_raw(cache, x, d):
+    """Keys and values x [tokens, 2, d] as they are into FP8 pages: the codes and scales of both."""
+    n = x.shape[0]
+    pools = [torch.zeros(-(-n // 64), 1, cache.page_bytes(FP8, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    g, table = x.cuda(), torch.arange(-(-n // 64), dtype=torch.int32, device="cuda")[None]
+    cache.ci_qk_norm_rope_append(g[:, :1], g[:, :1], g[:, 1:], None, None, 1e-6, cos_sin(n, 0).cuda(), True,
+                                 torch.arange(n, dtype=torch.int32, device="cuda"), torch.empty_like(g[:, :1]), *pools,
+                                 table, PRE)
+    body = [p[:, 0, :64 * d].reshape(-1, d)[:n].cpu().numpy() for p in pools]
+    scale = [p[:, 0, 64 * d:].contiguous().view(torch.float32).reshape(-1)[:n].cpu().numpy() for p in pools]
+    return body, scale
+
+
+def test_append_codes_are_a_divisions(cache):
+    """The codes that a reciprocal and its correction give are those of an IEEE division, over all sizes of heads."""
+    gen = torch.Generator().manual_seed(19)
+    x = torch.randn(20000, 2, 128, generator=gen)
+    x *= 2.0 ** (torch.rand(20000, 2, 1, generator=gen) * 200 - 90)
+    x[:300] = torch.randint(-448, 449, (300, 2, 128), generator=gen).float()  # many exact ties
+    x = x.bfloat16()
+    body, scale = append_raw(cache, x, 128)
+    for i in range(2):
+        want, z = codes_of(x[:, i])
+        assert np.array_equal(scale[i], z)
+        assert np.array_equal(body[i], want)
+
+
+def test_append_infinite_heads(cache):
+    """FP8: x / scale with an infinite scale is 0 where x is finite, NaN where it is not."""
+    x = torch.randn(6, 2, 64, generator=torch.Generator().manual_seed(20)).bfloat16()
+    x[1, 0, 5] = x[2, 1, 9] = x[3, :, 0] = float("inf")
+    x[4, :, 63] = -float("inf")
+    x[4, :, 7] = float("nan")
+    body, scale = append_raw(cache, x, 64)
+    for i in range(2):
+        for t in range(6):
+            head = x[t, i].float()
+            codes = body[i][t] & 0x7F
+            if head.isnan().any():
+                assert np.isnan(scale[i][t])
+            elif head.isinf().any():
+                assert np.isposinf(scale[i][t])
+                assert np.array_equal(codes == 0x7F, head.isinf().numpy()) and (codes[head.isfinite().numpy()] == 0).all()
+            else:
+                want, z = codes_of(x[t, i])
+                assert np.array_equal(body[i][t], want) and scale[i][t] == z

@@ -176,7 +176,9 @@ __device__ __forceinline__ void store_entry(uint8_t* at, int slot, int o0, int o
 #pragma unroll
   for (int o = 1; o < D / 8; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float scale = __fdiv_rn(max_nan(amax, 1e-10f), 448.f), inv = __frcp_rn(scale);
-  const float2 inv2 = make_float2(inv, inv), minus = make_float2(-scale, -scale);
+  // (an infinite scale has an exact reciprocal, 0, and nothing to correct)
+  const float back = scale == INFINITY ? 0.f : -scale;
+  const float2 inv2 = make_float2(inv, inv), minus = make_float2(back, back);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {  // x / scale: a product with the reciprocal, and Markstein's correction of it
     const float2 y = mul2(x[j], inv2);
