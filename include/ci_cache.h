@@ -76,8 +76,9 @@ CI_API int64_t ci_cache_page_bytes(int32_t cache_format, int32_t head_dim);
  * max_len <= 64 * max_pages.  With n = max_len, or npos for a list:
  * rows * num_kv_heads * ceil(num_q_heads / num_kv_heads / 64) * (n / 64 + 1) <
  * 2^31.
- * ws: at least ci_attn_workspace_bytes() bytes, 16-byte aligned, of any
- * content; one call's use of it ends with the call's work on the stream.
+ * ws: at least ci_attn_workspace_bytes() bytes (the same for any `rows`),
+ * 16-byte aligned, of any content; one call's use of it ends with the call's
+ * work on the stream.
  */
 CI_API int64_t ci_attn_workspace_bytes(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 CI_API int ci_attn_decode(const uint16_t* q, int64_t q_stride, int32_t rows, int32_t num_q_heads,

@@ -76,13 +76,19 @@ def test_workspace_comes_from_the_calls_stream(cache, pools_asked, stream):
     assert cache.calls[-1][1][-1] == (77 if stream else 0)
 
 
-@pytest.mark.parametrize("stream", [None, SIDE])
-def test_cache_results_come_from_the_calls_stream(cache, pools_asked, stream):
+def host_cache(*args):
+    """A PagedCache of host tensors that say they live on the GPU."""
     from two_level_sparse_gb300.paged import PagedCache
 
-    c = PagedCache(1, 2, 2, 4, 2, 64, device="cpu")
-    for t in ("k", "v", "page_table", "dev_err"):
+    c = PagedCache(*args, device="cpu")
+    for t in ("k", "v", "page_table", "ref_count", "dev_err"):
         setattr(c, t, getattr(c, t).as_subclass(Device))
+    return c
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+def test_cache_results_come_from_the_calls_stream(cache, pools_asked, stream):
+    c = host_cache(1, 2, 2, 4, 2, 64)
     q, kv = dev(2, 8, 64, dtype=torch.bfloat16), dev(2, 2, 64, dtype=torch.bfloat16)
     pools_asked.clear()
     c.append(0, q, kv, kv, None, None, 1e-6, dev(4, 0, dtype=torch.float32), True, dev(2), 0, stream=stream)
@@ -114,3 +120,21 @@ def test_copy_takes_pages_as_they_are(cache, view, monkeypatch):
     cache.mod.ci_pages_copy(list(x), dev(2), dev(2))
     assert seen[0] == ([x.data_ptr() + i * a_pool for i in range(len(x))], [a_pool // x.shape[1]] * len(x), x.shape[1])
     assert seen[1] == seen[0]
+
+
+def test_workspaces_do_not_grow_with_the_calls(cache, pools_asked):
+    """One workspace per stream and number of heads, whatever the rows."""
+    c = host_cache(1, 2, 2, 4, 2, 64)
+
+    def taken(rows, heads, stream=None):
+        q = dev(rows, heads, 64, dtype=torch.bfloat16)
+        pools_asked.clear()
+        c.attend(0, q, 1, dev(rows), out=q, stream=stream)
+        return len(pools_asked)
+
+    assert taken(2, 8) == 1
+    assert [taken(n, 8) for n in (1, 3, 1000, 2)] == [0] * 4
+    assert taken(5, 16) == 1 and taken(6, 16) == 0
+    assert taken(5, 8, SIDE) == 1 and taken(7, 8, SIDE) == 0
+    n = cache.mod.attn_workspace_bytes
+    assert all(n(rows, 8, 2, 64) == n(1, 8, 2, 64) for rows in (0, 2, 77, 10 ** 6))

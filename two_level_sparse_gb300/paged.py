@@ -90,7 +90,7 @@ class PagedCache:
         rows, heads, d = q.shape
         out = ops.empty_on(stream, q.shape, q.dtype, q.device) if out is None else out
         on = stream if stream is not None else torch.cuda.current_stream(q.device)
-        key = (rows, heads, on.cuda_stream)  # calls on two streams may overlap
+        key = (heads, on.cuda_stream)  # calls on two streams may overlap; the rows do not change the size
         if key not in self._workspace:
             n = ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d)
             self._workspace[key] = ops.empty_on(stream, (n,), torch.uint8, q.device)
