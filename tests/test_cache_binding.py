@@ -138,3 +138,17 @@ def test_workspaces_do_not_grow_with_the_calls(cache, pools_asked):
     assert taken(5, 8, SIDE) == 1 and taken(7, 8, SIDE) == 0
     n = cache.mod.attn_workspace_bytes
     assert all(n(rows, 8, 2, 64) == n(1, 8, 2, 64) for rows in (0, 2, 77, 10 ** 6))
+
+
+@pytest.mark.parametrize("hkv", [1, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_workspace_goes_by_the_heads(cache, d, hkv):
+    """A worker keeps sums and statistics of a unit's heads, padded to 8, 16, 32 or 64, twice: no call needs more."""
+    n = {group: cache.mod.attn_workspace_bytes(3, group * hkv, hkv, d) for group in (1, 8, 9, 16, 17, 32, 33, 64, 65, 128)}
+    part = 2 * (1 if d == 256 else 2) * (d + 2) * 4  # bytes per SM and head
+    sms = n[128] // (64 * part)
+    for group, got in n.items():
+        heads = next((h for h in (8, 16, 32) if group <= h), 64)
+        if d == 128 and 16 < group <= 32:
+            heads = 64  # lists of positions take the kernel of many heads
+        assert 0 <= got - heads * part * sms <= 32 * sms + 16, group

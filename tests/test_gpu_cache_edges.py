@@ -195,3 +195,18 @@ def test_append_infinite_heads(cache):
             else:
                 want, z = codes_of(x[t, i])
                 assert np.array_equal(body[i][t], want) and scale[i][t] == z
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (12, 1, 64), (17, 1, 128), (64, 2, 128), (40, 1, 128), (128, 1, 128),
+                                      (8, 1, 256), (60, 2, 256), (33, 1, 64)])
+def test_attention_keeps_to_its_workspace(cache, hq, hkv, d, fmt):
+    """The bytes that are asked for, between bytes that stay as they are."""
+    rng = np.random.default_rng(22)
+    lens = [int(n) for n in rng.integers(1, 700, 40)]
+    n, guard = cache.attn_workspace_bytes(40, hq, hkv, d), 64 << 20
+    ws = torch.full((n + 2 * guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    for pos in (None, picks(rng, lens, 200)):
+        p = Problem(lens, hq, hkv, d, fmt, seed=22, pos=pos)
+        p.check(*p.run(cache, workspace=ws[guard:guard + n]))
+    assert (ws[:guard] == 0x5A).all() and (ws[guard + n:] == 0x5A).all()

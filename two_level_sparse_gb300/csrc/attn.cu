@@ -17,8 +17,9 @@ constexpr int kJoinWarps = 16;
 //   17 rows of 0-100k, all positions   16: 95, 99    32: 97, 99    64: 124, 101
 //   4 rows of 1k-4k, all positions     16: 19, 20    32: 19, 21    64: 25, 25
 //   1024 rows over 512 listed          16: 68, 67    20: 76, 67    64: 109, 74
+constexpr int kWideListed = 16, kWideAll = 32;
 bool is_wide(const CacheArgs& c, bool listed) {
-  return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > (listed ? 16 : 32);
+  return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > (listed ? kWideListed : kWideAll);
 }
 
 Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, bool wide) {
@@ -162,8 +163,12 @@ cudaError_t launch_join(const Args& k, cudaStream_t stream) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int32_t, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-  int64_t most = 0;  // either kernel may take the call: the cache's format is not known here
+  // Where the wide kernel takes calls of so many heads, either may take this one: neither the cache's format nor
+  // whether positions are listed is known here.
+  const bool may_be_wide = head_dim == 128 && num_q_heads / num_kv_heads > kWideListed;
+  int64_t most = 0;
   for (const bool wide : {false, true}) {
+    if (wide && !may_be_wide) continue;
     const Layout l = layout_of(num_q_heads, num_kv_heads, head_dim, wide);
     const int64_t n = part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.heads * head_dim * 4;
     most = n > most ? n : most;
