@@ -43,7 +43,9 @@ class PagedCache:
         self.companions = list(companions)
         self.page_table = torch.full((requests, max_pages), -1, dtype=_I32, device=device)
         self.ref_count = torch.zeros(num_pages, dtype=_I32, device=device)
-        self.length = torch.zeros(requests, dtype=_I32, device=device)
+        # one entry more than there are requests, for what is said of others
+        self._length = torch.zeros(requests + 1, dtype=_I32, device=device)
+        self.length = self._length[:requests]
         self.dev_err = torch.zeros(1, dtype=_I32, device=device)
         self._pairs = torch.empty(3, num_pages, dtype=_I32, device=device)  # remap, copy_src, copy_dst
         self._count = torch.empty(1, dtype=_I32, device=device)
@@ -59,17 +61,30 @@ class PagedCache:
         ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, new_len, dev_err=self.dev_err)
         self.length.copy_(new_len)
 
+    def _known(self, req):
+        return (req >= 0) & (req < self.length.shape[0])
+
+    def _at(self, req, known):
+        """Where ``_length`` has the requests; its last entry where they are not known."""
+        return torch.where(known, req, self.length.shape[0]).long()
+
     def fork(self, parent, child, length):
-        """``child[i]`` becomes the first ``length[i]`` positions of ``parent[i]``; what it held is released."""
-        self.free(child)
+        """``child[i]`` becomes the first ``length[i]`` positions of ``parent[i]``; what it held is released.
+        A fork that the call refuses (its bits are in ``dev_err``) leaves both as they are."""
+        done = self._known(parent) & self._known(child) & (parent != child)
+        done &= (length >= 0) & (length <= ops.PAGE * self.page_table.shape[1])
+        child_done = torch.where(done, child, -1)
+        bits = torch.zeros_like(self.dev_err)
+        ops.ci_pages_free(self.page_table, self.ref_count, child_done, dev_err=bits)
+        self.dev_err |= bits & ~ops.DEVERR_REQ  # (the fork itself says which requests are bad)
         src, dst = torch.empty_like(parent), torch.empty_like(parent)
         ops.ci_pages_fork(self.page_table, self.ref_count, parent, child, length, src, dst, dev_err=self.dev_err)
         self._copy(src, dst)
-        self.length.index_copy_(0, child.long(), length)
+        self._length.index_copy_(0, self._at(child, done), length)
 
     def free(self, req):
         ops.ci_pages_free(self.page_table, self.ref_count, req, dev_err=self.dev_err)
-        self.length.index_fill_(0, req.long(), 0)
+        self._length.index_fill_(0, self._at(req, self._known(req)), 0)
 
     def compact(self):
         """Every live page into the lowest ids."""
