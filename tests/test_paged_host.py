@@ -121,3 +121,71 @@ def test_fork_that_is_refused_changes_nothing(make, parent, child, length, err):
     else:  # the forks beside it are carried out
         assert c.length.tolist() == [100, 130, 70, 130] and c.page_table[1, :2].tolist() == table[3, :2].tolist()
     consistent(c)
+
+
+def test_growth_that_runs_out_goes_as_far_as_the_pages(make):
+    from two_level_sparse_gb300 import cache as ops
+
+    c = make(num_pages=5)
+    c.grow(i32(100, 70, 200, 1))
+    assert c.length.tolist() == [100, 70, 64, 0] and c.short.tolist() == [0, 0, 1, 1]
+    assert int(c.dev_err) == ops.DEVERR_PAGE
+    consistent(c)
+    c.free(i32(0))
+    c.grow(i32(0, 70, 200, 1))  # what was short is asked for again
+    assert c.length.tolist() == [0, 70, 192, 0] and c.short.tolist() == [0, 0, 1, 1]
+    consistent(c)
+    c.free(i32(1))
+    assert c.short.tolist() == [0, 0, 1, 1]
+    c.free(i32(2, 3))
+    assert c.short.tolist() == [0] * 4 and c.length.tolist() == [0] * 4
+    c.grow(i32(0, 128, 0, 192))
+    assert c.length.tolist() == [0, 128, 0, 192] and c.short.tolist() == [0] * 4
+    consistent(c)
+
+
+def test_growth_that_is_refused_changes_nothing(make):
+    from two_level_sparse_gb300 import cache as ops
+
+    c = make()
+    c.grow(i32(100, 64, 5, 0))
+    c.grow(i32(99, 257, -1, 130))
+    assert c.length.tolist() == [100, 64, 5, 130] and c.short.tolist() == [1, 1, 1, 0]
+    assert int(c.dev_err) == ops.DEVERR_LEN
+    consistent(c)
+    c.grow(i32(101, 65, 5, 130))
+    assert c.length.tolist() == [101, 65, 5, 130] and c.short.tolist() == [0] * 4
+    consistent(c)
+
+
+def test_fork_without_a_page_for_its_end(make):
+    from two_level_sparse_gb300 import cache as ops
+
+    c = make(num_pages=5)
+    c.grow(i32(100, 0, 65, 0))
+    c.fork(i32(0, 2), i32(1, 3), i32(100, 65))
+    assert c.length.tolist() == [100, 100, 65, 64] and c.short.tolist() == [0, 0, 0, 1]
+    assert int(c.dev_err) == ops.DEVERR_PAGE
+    consistent(c)
+    c.fork(i32(2), i32(1), i32(65))  # the page that the child before it had
+    assert c.length.tolist() == [100, 65, 65, 64] and c.short.tolist() == [0, 0, 0, 1]
+    consistent(c)
+
+
+def test_a_step_writes_no_token_that_has_no_place(make, monkeypatch):
+    """Where a request's growth was cut, its last position is an older token's: it stays as it is."""
+    from types import SimpleNamespace
+
+    from two_level_sparse_gb300 import paged
+
+    c = make(num_pages=3)
+    c.grow(i32(64, 63, 0, 64))
+    c.grow(i32(65, 64, 0, 65))
+    assert c.length.tolist() == [64, 64, 0, 64] and c.short.tolist() == [1, 0, 0, 1]
+    seen = []
+    monkeypatch.setattr(paged.ops, "ci_qk_norm_rope_append",
+                        lambda *a, cache_pos, **k: seen.append((a[8].tolist(), cache_pos.tolist())))
+    monkeypatch.setattr(paged.PagedCache, "attend", lambda self, j, q, *a, **k: q)
+    step = SimpleNamespace(run=lambda: None, max_len=256, pos=[None])
+    paged.sparse_decode_step(c, step, [torch.zeros(4, 6, 64)], None, None, 1e-6, None)
+    assert seen == [([63, 63, 0, 63], [-1, 63, -1, -1])]

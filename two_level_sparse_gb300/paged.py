@@ -31,6 +31,8 @@ class PagedCache:
     of up to ``64 * max_pages`` positions, in ``num_pages`` pages (every
     layer's pools use the same ids).  All lengths and ids that the methods take
     are int32 tensors on the cache's device; nothing but ``check`` waits.
+    ``length`` [requests] is what every request holds; ``short`` is 1 where its
+    last growth or fork got less than it asked for.
     ``append`` and ``attend`` run on ``stream`` (None: the current one), whose
     memory their results are."""
 
@@ -43,9 +45,10 @@ class PagedCache:
         self.companions = list(companions)
         self.page_table = torch.full((requests, max_pages), -1, dtype=_I32, device=device)
         self.ref_count = torch.zeros(num_pages, dtype=_I32, device=device)
-        # one entry more than there are requests, for what is said of others
-        self._length = torch.zeros(requests + 1, dtype=_I32, device=device)
-        self.length = self._length[:requests]
+        # one column more than there are requests, for what is said of others
+        self._state = torch.zeros(2, requests + 1, dtype=_I32, device=device)
+        self.length, self.short = self._state[:, :requests]
+        self._column = torch.arange(max_pages, dtype=_I32, device=device)
         self.dev_err = torch.zeros(1, dtype=_I32, device=device)
         self._pairs = torch.empty(3, num_pages, dtype=_I32, device=device)  # remap, copy_src, copy_dst
         self._count = torch.empty(1, dtype=_I32, device=device)
@@ -56,23 +59,35 @@ class PagedCache:
         for at in range(0, len(pools), ops.MAX_POOLS):
             ops.ci_pages_copy(pools[at:at + ops.MAX_POOLS], src, dst, count=count, dev_err=self.dev_err)
 
+    def _limit(self):
+        return ops.PAGE * self.page_table.shape[1]
+
+    def _room(self, rows):
+        """The positions for which rows of the page table have pages, from the first on."""
+        return ops.PAGE * torch.where(rows < 0, self._column, self._column.shape[0]).amin(1)
+
     def grow(self, new_len):
-        """Pages up to ``new_len`` [requests] positions; a request that is not to grow has its present length."""
+        """Pages up to ``new_len`` [requests] positions; a request that is not to grow has its present length.
+        Where the pages run out the length goes as far as they do, where the call refuses (fewer positions than
+        there are, or more than a row has) it stays; either is ``short`` then, and in ``dev_err``."""
         ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, new_len, dev_err=self.dev_err)
-        self.length.copy_(new_len)
+        asked = torch.where(new_len <= self._limit(), new_len, 0)
+        torch.maximum(self.length, torch.minimum(asked, self._room(self.page_table)), out=self.length)
+        self.short.copy_(self.length != new_len)
 
     def _known(self, req):
         return (req >= 0) & (req < self.length.shape[0])
 
     def _at(self, req, known):
-        """Where ``_length`` has the requests; its last entry where they are not known."""
+        """Where ``_state`` has the requests; its last column where they are not known."""
         return torch.where(known, req, self.length.shape[0]).long()
 
     def fork(self, parent, child, length):
         """``child[i]`` becomes the first ``length[i]`` positions of ``parent[i]``; what it held is released.
-        A fork that the call refuses (its bits are in ``dev_err``) leaves both as they are."""
+        A fork that the call refuses (its bits are in ``dev_err``) leaves both as they are; a child without a page
+        for its end is ``short`` of it."""
         done = self._known(parent) & self._known(child) & (parent != child)
-        done &= (length >= 0) & (length <= ops.PAGE * self.page_table.shape[1])
+        done &= (length >= 0) & (length <= self._limit())
         child_done = torch.where(done, child, -1)
         bits = torch.zeros_like(self.dev_err)
         ops.ci_pages_free(self.page_table, self.ref_count, child_done, dev_err=bits)
@@ -80,11 +95,13 @@ class PagedCache:
         src, dst = torch.empty_like(parent), torch.empty_like(parent)
         ops.ci_pages_fork(self.page_table, self.ref_count, parent, child, length, src, dst, dev_err=self.dev_err)
         self._copy(src, dst)
-        self._length.index_copy_(0, self._at(child, done), length)
+        at = self._at(child, done)
+        got = torch.minimum(length, self._room(self.page_table[at.clamp(max=self.length.shape[0] - 1)]))
+        self._state.index_copy_(1, at, torch.stack([got, (got != length).to(_I32)]))
 
     def free(self, req):
         ops.ci_pages_free(self.page_table, self.ref_count, req, dev_err=self.dev_err)
-        self._length.index_fill_(0, self._at(req, self._known(req)), 0)
+        self._state.index_fill_(1, self._at(req, self._known(req)), 0)
 
     def compact(self):
         """Every live page into the lowest ids."""
@@ -126,11 +143,14 @@ def sparse_decode_step(cache: PagedCache, step, qkv, q_norm, k_norm, eps, cos_si
     """One decode step of every layer of ``step`` (an IndexerStep over
     ``cache.page_table``): one new token per request, at its last position.
     ``qkv[layer]``: bf16 [requests, q_heads + 2 kv_heads, head_dim].  Returns
-    the layers' attention outputs; a request of length 0 gets zeros."""
+    the layers' attention outputs; a request of length 0 gets zeros.  Where a
+    request is ``short`` its last position is an older token's and nothing is
+    stored: its output does not count."""
     hkv = cache.k.shape[2]
     hq = qkv[0].shape[1] - 2 * hkv
     last = cache.length - 1
     where = last.clamp(min=0)  # a request of length 0: any row of cos_sin, and nothing is stored (-1)
+    last = torch.where(cache.short != 0, -1, last)
     queries = [cache.append(j, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], q_norm, k_norm, eps, cos_sin, is_neox,
                             where, ops.LAYOUT_DECODE, cache_pos=last) for j, x in enumerate(qkv)]
     step.run()
