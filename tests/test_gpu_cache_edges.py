@@ -210,3 +210,58 @@ def test_attention_keeps_to_its_workspace(cache, hq, hkv, d, fmt):
         p = Problem(lens, hq, hkv, d, fmt, seed=22, pos=pos)
         p.check(*p.run(cache, workspace=ws[guard:guard + n]))
     assert (ws[:guard] == 0x5A).all() and (ws[guard + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("hq", [64, 8])
+def test_attention_on_two_streams_at_once(cache, hq):
+    """Calls that overlap, from two threads, each with its own workspace: the bits of calls one after another."""
+    import threading
+
+    problems = [Problem([30000 + n, 1, 5000], hq, 1, 128, BF16, seed=23 + n) for n in (0, 1)]
+    want = [p.run(cache) for p in problems]
+    got, sides = [[], []], [torch.cuda.Stream() for _ in problems]
+    args = [[getattr(p, n).cuda() for n in ("q", "k", "v", "table", "seq")] for p in problems]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(sides[i]):
+            for _ in range(30):
+                o, z = torch.empty_like(want[i][0]), torch.empty_like(want[i][1])
+                cache.ci_attn_decode(*args[i][:4], 0, args[i][4], problems[i].max_len, problems[i].scale, o, lse=z)
+                got[i].append((o, z))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert len(got[i]) == 30
+        assert all(torch.equal(o, want[i][0]) and torch.equal(z, want[i][1]) for o, z in got[i])
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8])
+def test_views_of_larger_tensors(cache, fmt):
+    """Pools, tables and lists that are slices of larger tensors, as layers of one allocation are."""
+    rng = np.random.default_rng(24)
+    lens = [700, 3, 129]
+    p = Problem(lens, 8, 2, 128, fmt, seed=24, pos=picks(rng, lens, 100))
+    want = p.run(cache)
+
+    def inside(t):
+        x = torch.full((3, *t.shape), 0x55, dtype=t.dtype, device="cuda")
+        x[1] = t.cuda()
+        return x[1]
+
+    out = torch.empty_like(want[0])
+    cache.ci_attn_decode(inside(p.q), inside(p.k), inside(p.v), inside(p.table), 0, inside(p.seq), p.max_len, p.scale, out,
+                         pos=inside(p.pos))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0])
+    pools = torch.randint(0, 256, (4, 5, 64), dtype=torch.uint8, device="cuda")
+    before = pools.clone()
+    one = lambda v: torch.tensor([v], dtype=torch.int32, device="cuda")  # noqa: E731
+    cache.ci_pages_copy(pools[1::4], one(0), one(4))
+    before[1, 4] = before[1, 0]
+    assert torch.equal(pools, before)
