@@ -7,8 +7,8 @@
 // Memory-bound: every head is read once and written once: 16384 tokens of 64 + 16
 // heads of 128 into FP8 pages move 647 MB in 110 us, 5.9 TB/s of a copy's 6.8 (IEEE
 // divisions by the FP8 scale took it to 248 us; the scale's reciprocal and one
-// correction give the same codes).  A call with few tokens is as long as its host
-// side: 18 us for 8 tokens.
+// correction give the same codes, as a test compares).  A call with few tokens is as
+// long as its host side: 18-19 us for 8 tokens.
 //
 // D / 8 lanes hold a head, eight dims each, as two runs of four that are chosen so
 // that both elements of every rotated pair sit in one lane (half layout: dims 4m..

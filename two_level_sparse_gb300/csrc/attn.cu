@@ -12,11 +12,11 @@ using attn::Part;
 
 constexpr int kJoinWarps = 16;
 
-// Whether the kernel of attn_wide.cu takes the call.  Both measured, in us with
-// cold caches (the warp-level kernel, then the wide one), by heads per key-value head:
-//   17 rows of 0-100k, all positions   16: 95, 99    32: 97, 99    64: 124, 101
-//   4 rows of 1k-4k, all positions     16: 19, 20    32: 19, 21    64: 25, 25
-//   1024 rows over 512 listed          16: 68, 67    20: 76, 67    64: 109, 74
+// Whether the kernel of attn_wide.cu takes the call.  Both measured, in us of calls one
+// after another (the warp-level kernel, then the wide one), by heads per key-value head:
+//   17 rows of 0-100k, all positions   16: 76.8, 79.3   20: 79.8, 78.6   32: 80.7, 79.8   64: 116.9, 83.3
+//   4 rows of 1k-4k, all positions     16: 12.0, 13.4   20: 12.5, 14.2   32: 13.1, 14.5   64: 18.8, 18.3
+//   1024 rows over 512 listed          16: 57.9, 60.5   20: 65.5, 61.6   32: 68.3, 62.5   64: 101.8, 66.5
 constexpr int kWideListed = 16, kWideAll = 32;
 bool is_wide(const CacheArgs& c, bool listed) {
   return !c.fp8 && c.head_dim == 128 && c.num_q_heads / c.num_kv_heads > (listed ? kWideListed : kWideAll);
@@ -148,9 +148,9 @@ int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.heads * 2 * 4; }
 
 template <int D, int kT>
 cudaError_t launch_join(const Args& k, cudaStream_t stream) {
-  // The fewer units, the more parts each: 16, 4 or 1 warps a head.  Both kernels with 1, 4 and 16 (us, cold caches):
-  // one row of 256k, 77 parts a unit: 116, 111, 107; 16 rows of 10k-20k, 5 parts: 101, 99, 103; 64 rows of 512
-  // listed, at most 2 parts: 46, 49, 58.
+  // The fewer units, the more parts each: 16, 4 or 1 warps a head.  Both kernels with 1, 4 and 16 (us of calls one
+  // after another): one row of 256k, 77 parts a unit: 95.2, 90.1, 87.8; 16 rows of 10k-20k, 5 parts: 81.5, 80.5, 83.9;
+  // 64 rows of 512 listed, at most 2 parts: 33.8, 36.1, 46.6.
   const int64_t units = static_cast<int64_t>(k.a.rows) * k.a.c.num_kv_heads * k.l.blocks;
   const bool by_unit = units <= k.l.ctas && k.a.rows <= 32 * kJoinWarps;
   const int64_t split = by_unit ? units : k.l.ctas, parts = k.l.ctas / (units < k.l.ctas ? units : k.l.ctas) + 1;

@@ -28,8 +28,8 @@
 // that a group of 8 query heads wastes nothing.
 //
 // What bounds it: the HBM, where a row reads its whole cache.  64 rows of 16k-64k
-// in FP8, 64 heads over 8, D = 128: 5.54 GB in 817 us, 6.79 TB/s, a copy's rate;
-// one row of 256k in bf16, 28 heads over 4: 537 MB in 87 us with the join, 6.19
+// in FP8, 64 heads over 8, D = 128: 5.54 GB in 820 us, 6.75 TB/s, a copy's rate;
+// one row of 256k in bf16, 28 heads over 4: 537 MB in 87 us with the join, 6.15
 // TB/s.  There the warps' arithmetic is half of what the SM issues, most of it the
 // softmax and FP8's conversions, tensor instructions a sixth; two CTAs per SM keep
 // the loads going while one reduces.  Short calls are bound by latency: 4 rows of
@@ -122,6 +122,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// 2^x and 1 / x to within about 2^-22 of their values, results below 2^-126 as 0: as
+// good as the fp32 sums that they go into.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -963,7 +965,15 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args&
   return launch_after(fn, dim3(k.l.ctas), C::kThreads, C::kSmem, stream, kmap, vmap, k);
 }
 
-// The instance for a head size and a padded number of heads per unit.
+// The instance for a head size and a padded number of heads per unit.  A thread
+// keeps NT D / 4 sums of O, which registers bound to 64: NT = 2 heads of eight, or 1
+// for D = 256.  The positions go to the warps that the heads leave of four (of eight
+// for D = 256, one CTA per SM).  More heads cost more, as each of WH warps reads the
+// whole tile from shared memory (and widens it, in FP8): 17 rows of 0-100k, one
+// key-value head, 8, 16, 32 and 64 query heads, us (floor: the bytes):
+//   D =  64  bf16  43.6,  46.5,  49.0,  69.9 (32)    FP8  36.4,  42.7,  59.2,  92.7 (17)
+//   D = 128  bf16  73.0,  77.0,  80.7, wide  (64)    FP8  47.7,  58.9,  92.7, 151.8 (33)
+//   D = 256  bf16 135.8, 139.1, 157.0, 263.5 (128)   FP8  84.3, 126.1, 210.1, 363.8 (65)
 template <bool kFp8>
 cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t s) {
   const int d = k.a.c.head_dim, h = k.l.heads;

@@ -1,6 +1,7 @@
-// Attention over a paged bf16 cache where many query heads (more than 16)
-// share a key-value head of 128 dims (contract in include/ci_cache.h; the
-// list of tiles, its split over the CTAs and the join are those of attn.cuh).
+// Attention over a paged bf16 cache where many query heads (more than 32, or more
+// than 16 where positions are listed) share a key-value head of 128 dims (contract
+// in include/ci_cache.h; the list of tiles, its split over the CTAs and the join are
+// those of attn.cuh).
 //
 // With G = 64 heads the products cost 64 flop per byte of cache: at the HBM's
 // rate 435 TFLOP/s, half of what the warp-level MMA instructions reach (attn.cu
@@ -21,9 +22,9 @@
 // before the values of the tile before where their keys are there.
 //
 // What bounds it.  17 rows of 0-100k, one key-value head: 436 MB in 83 us with the
-// join, 5.3 TB/s of a copy's 6.8; the start (4 us until the first tile arrives) and
+// join, 5.2 TB/s of a copy's 6.8; the start (4 us until the first tile arrives) and
 // an uneven end are 10 us of it.  4096 rows over 512 listed positions each, of one
-// request: 1.07 GB of rows from L2 in 210 us, 5.1 TB/s; a worker's tile takes 5500
+// request: 1.07 GB of rows from L2 in 215 us, 5.0 TB/s; a worker's tile takes 5500
 // cycles, of which its keys' arrival is 3900 and the softmax 2700, and a row's end
 // 8000 every four tiles.  (Four softmax warps per worker instead of eight: 266 us.
 // Spilled registers cost more than they seem to: a reload that misses waits behind

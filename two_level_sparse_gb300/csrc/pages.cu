@@ -13,9 +13,12 @@
 //
 // Page tables are rewritten by plain grids.  Copies move `page_bytes` per pair
 // and pool, read once and written once: a compaction of 6000 pages that moves 1394
-// of 8 x 128 KB, 2.92 GB, takes 488 us, 452 of them the copy at 6.5 TB/s.  A fork of
-// 64 requests of 16k-64k into 256 (81 MB of partly filled pages) takes 28 us, 12 at
-// the HBM's rate: two launches, each a chain of loads before the first byte moves.
+// of 8 x 128 KB, 2.92 GB, takes 475-487 us, 452 of them the copy at 6.5 TB/s.  A fork
+// of 64 requests of 16k-64k into 256 (81 MB of partly filled pages) takes 28 us with
+// the release before it, 12 at the HBM's rate: three launches (release, fork, copy),
+// each a chain of loads before the first byte moves.  An allocation of one page for
+// each of 64 requests, 2^16 pages of which 64000 are taken: 11 us; for each of 4096: 27
+// us; where none needs one: 9 and 13 us (single calls between events).
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"

@@ -142,6 +142,10 @@ class PagedCache:
 def sparse_decode_step(cache: PagedCache, step, qkv, q_norm, k_norm, eps, cos_sin, is_neox=True):
     """One decode step of every layer of ``step`` (an IndexerStep over
     ``cache.page_table``): one new token per request, at its last position.
+    It puts the calls together where every layer's inputs are at hand, as
+    ``step`` has every layer's index queries, under one pair of norms; a model
+    whose layers follow from one another makes the same two calls, ``append``
+    and ``attend``, layer by layer.
     ``qkv[layer]``: bf16 [requests, q_heads + 2 kv_heads, head_dim].  Returns
     the layers' attention outputs; a request of length 0 gets zeros.  Where a
     request is ``short`` its last position is an older token's and nothing is
