@@ -540,7 +540,8 @@ __device__ __forceinline__ void wide_softmax(const Args& k, WideShared& sh, Wide
       tc_fence_after();
       const uint4 m = *reinterpret_cast<const uint4*>(sh.mask[g][mine & 3]);
       const bool valid = ((quad == 0 ? m.x : quad == 1 ? m.y : quad == 2 ? m.z : m.w) >> lane) & 1;
-      if (!set && (m.x | m.y | m.z | m.w) != 0) {  // the first position's logits
+      // (asked of the group: after a role has given up, its warps may see different masks, and must still meet)
+      if (!set && group_any(1 + g, (m.x | m.y | m.z | m.w) != 0)) {  // the first position's logits
         const int first = m.x ? __ffs(m.x) - 1 : m.y ? 31 + __ffs(m.y) : m.z ? 63 + __ffs(m.z) : 95 + __ffs(m.w);
 #pragma unroll 1
         for (int h = 0; h < 32; h += 8) {
