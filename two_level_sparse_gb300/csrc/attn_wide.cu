@@ -24,7 +24,7 @@
 // What bounds it.  17 rows of 0-100k, one key-value head: 436 MB in 83 us with the
 // join, 5.2 TB/s of a copy's 6.8; the start (4 us until the first tile arrives) and
 // an uneven end are 10 us of it.  4096 rows over 512 listed positions each, of one
-// request: 1.07 GB of rows from L2 in 215 us, 5.0 TB/s; a worker's tile takes 5500
+// request: 1.07 GB of rows from L2 in 214 us, 5.0 TB/s; a worker's tile takes 5500
 // cycles, of which its keys' arrival is 3900 and the softmax 2700, and a row's end
 // 8000 every four tiles.  (Four softmax warps per worker instead of eight: 266 us.
 // Spilled registers cost more than they seem to: a reload that misses waits behind
