@@ -20,7 +20,8 @@ OUT = os.path.join(HERE, "libci.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["ci_api.cu", "dense_tc.cu", "publish.cu", "publish_rows.cu", "sparse_tc.cu", "tail.cu", "qprod.cu", "dcp.cu", "cache_api.cu",
            "attn.cu", "attn_bf16.cu", "attn_fp8.cu", "attn_wide.cu",
-           "append.cu", "pages.cu", "draft_api.cu", "draft.cu", "attn_draft.cu"]
+           "append.cu", "pages.cu", "draft_api.cu", "draft.cu", "attn_draft.cu", "attn_draft_bf16.cu",
+           "attn_draft_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

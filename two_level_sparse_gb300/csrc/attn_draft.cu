@@ -1,109 +1,127 @@
-// Attention of drafted rows over the paged cache (contract in
-// include/ci_draft.h).
-//
-// A warp per row and query head, 32 positions at a time: a lane computes the
-// logit of its position, then the lanes share the dims of the sum.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "cache_common.cuh"
-#include "draft_internal.h"
+// Attention of drafted rows over the paged cache: dispatch, the workspace's
+// layout, and the join of units that several teams worked on (contract in
+// include/ci_draft.h; the main kernel is in attn_draft.cuh).
+#include "attn_draft.cuh"
 
 namespace ci {
 namespace {
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(128) draft_kernel(const DraftArgs a) {
-  const int lane = threadIdx.x & 31;
-  const CacheArgs& c = a.c;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  wait_predecessor();
-  if (unit >= static_cast<int64_t>(a.rows) * c.num_q_heads) return;
-  const int t = static_cast<int>(unit / c.num_q_heads), h = static_cast<int>(unit % c.num_q_heads);
-  const int head = h / (c.num_q_heads / c.num_kv_heads);
-  int r = -1;
-  for (int x = lane; x < c.num_req; x += 32)
-    if (c.req_start[x] < 0 || c.req_start[x] > c.req_start[x + 1] || c.req_start[x + 1] > a.rows)
-      report(c.dev_err, kDevErrReq);
-    else if (c.req_start[x] <= t && t < c.req_start[x + 1])
-      r = x;
-  r = __reduce_max_sync(0xffffffffu, r);
-  if (r < 0) return;
-  const int first = c.req_start[r], n = c.req_start[r + 1] - first;
-  int len = a.length[r], all = 0;
-  if (len < 0 || n > a.max_rows || static_cast<int64_t>(len) + n > a.max_len) {
-    if (lane == 0) report(c.dev_err, kDevErrLen);
-  } else {
-    all = len + n;
-  }
-  float m = -INFINITY, l = 0.f, o[D / 32];
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
-  const uint16_t* q = a.q + t * a.q_stride + static_cast<int64_t>(h) * D;
-  constexpr int64_t kHead = cache_page_bytes<kFp8>(D);
-  auto value = [&](const uint8_t* at, int slot, int dim) {
-    if (kFp8) {
-      const uint8_t x = at[slot * D + dim];
-      const float v = (x & 127) == 127 ? 480.f : __half2float(__half(__nv_cvt_fp8_to_halfraw(x & 127, __NV_E4M3)));
-      return (x & 128 ? -v : v) * reinterpret_cast<const float*>(at + kPage * D)[slot];
-    }
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(at)[slot * D + dim]);
-  };
-  for (int s0 = 0; s0 < all; s0 += 32) {
-    const int s = s0 + lane, j = s - len;
-    bool ok = s < all;
-    if (ok && j >= 0) ok = a.mask != nullptr ? j < 32 * a.mask_words && (a.mask[static_cast<int64_t>(t) * a.mask_words + j / 32] >> (j % 32)) & 1 : j <= t - first;
-    int page = ok ? c.page_table[static_cast<int64_t>(r) * c.max_pages + s / kPage] : 0;
-    if (page < 0 || page >= c.num_pages) {
-      report(c.dev_err, kDevErrPage);
-      ok = false, page = 0;
-    }
-    const int64_t at = (static_cast<int64_t>(page) * c.num_kv_heads + head) * kHead;
-    float x = -INFINITY;
-    if (ok) {
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) dot += bf16_lo(q[d]) * value(c.k_pool + at, s % kPage, d);
-      x = dot * a.scale;
-    }
-    float top = m;
-    top = fmaxf(top, x);
-    for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
-    const float ref = top == -INFINITY ? 0.f : top, f = expf(m - ref), p = ok ? expf(x - ref) : 0.f;
-    m = top;
-    l = l * f + p;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] *= f;
-    const uint32_t seen = __ballot_sync(0xffffffffu, ok);
-    for (int i = 0; i < 32; ++i) {
-      if (!((seen >> i) & 1)) continue;
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      const int64_t ai = __shfl_sync(0xffffffffu, at, i);
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[k] += pi * value(c.v_pool + ai, (s0 + i) % kPage, lane + 32 * k);
-    }
-  }
-  for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k)
-    a.out[t * a.out_stride + static_cast<int64_t>(h) * D + lane + 32 * k] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k] * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(t) * c.num_q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+using draft::Args;
+using draft::Layout;
+using draft::Part;
+
+constexpr int kJoinWarps = 16, kJoinRows = 8;
+
+int block_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
+
+Layout layout_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const int group = num_q_heads / num_kv_heads, rows = block_rows(head_dim);
+  const int64_t blocks = (static_cast<int64_t>(max_rows) * group + rows - 1) / rows;
+  return Layout{device_sm_count(), static_cast<int>(blocks < 2 ? blocks : 2), group, rows};
 }
 
+// With the parts' references m_i, sums l_i and unnormalised sums o_i:
+//   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
+// CTA (x, y) takes the unit that begins in CTA x and goes on, and every
+// gridDim.y-th group of its rows; a row's parts are dealt to `ways` warps, whose
+// sums are added in order.
 template <int D>
-cudaError_t launch_d(const DraftArgs& a, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(a.rows) * a.c.num_q_heads;
-  const dim3 grid(static_cast<unsigned>((units + 3) / 4));
-  return a.c.fp8 ? launch_after(draft_kernel<D, true>, grid, 128, 0, stream, a)
-                 : launch_after(draft_kernel<D, false>, grid, 128, 0, stream, a);
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k) {
+  constexpr int kPer = D / 32;
+  __shared__ float sums[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  release_successor();
+  wait_predecessor();
+  const Part p = k.part[blockIdx.x];
+  if (p.last < 0) return;
+  const int team = static_cast<int>(blockIdx.x) / k.l.team, member = static_cast<int>(blockIdx.x) % k.l.team;
+  const int n = p.last - team + 1, ways = n > 32 ? 16 : n > 4 ? 4 : 1, per = kJoinWarps / ways;
+  const int hw = warp / ways, way = warp % ways;
+  const int first = k.a.c.req_start[p.req], row0 = p.block * k.l.block_rows;
+  const int rows = min(k.l.block_rows, (k.a.c.req_start[p.req + 1] - first) * k.l.group - row0);
+  auto slot = [&](int i) { return 2ll * ((team + i) * k.l.team + member) + (i == 0 ? 1 : 0); };
+#pragma unroll 1
+  for (int base = blockIdx.y * per; base < rows; base += gridDim.y * per) {
+    const int m = base + hw;
+    const bool live = m < rows;
+    float top = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] = 0.f;
+    if (live) {
+      auto stat = [&](int i) { return reinterpret_cast<const float2*>(k.stat)[slot(i) * k.l.block_rows + m]; };
+      for (int i = lane; i < n; i += 32) {
+        const float2 st = stat(i);
+        const float up = fmaxf(top, st.x);
+        l = l * draft::exp2_approx(top - up) + st.y * draft::exp2_approx(st.x - up);  // (references are finite)
+        top = up;
+      }
+      float up = top;
+#pragma unroll
+      for (int b = 16; b > 0; b >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, b));
+      l *= draft::exp2_approx(top - up);
+      top = up;
+#pragma unroll
+      for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+#pragma unroll 4
+      for (int i = way; i < n; i += ways) {
+        const float f = draft::exp2_approx(stat(i).x - top);
+        const float* src = k.sum + (slot(i) * k.l.block_rows + m) * D + lane;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] += f * src[32 * j];
+      }
+    }
+    if (ways > 1) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) sums[warp][32 * j + lane] = o[j];
+      __syncthreads();
+      if (way == 0)
+#pragma unroll 1
+        for (int x = 1; x < ways; ++x)
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) o[j] += sums[warp + x][32 * j + lane];
+      __syncthreads();
+    }
+    if (!live || way != 0) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int x = row0 + m, node = x / k.l.group;
+    const int64_t t = first + node, qh = static_cast<int64_t>(p.head) * k.l.group + x - node * k.l.group;
+    uint16_t* dst = k.a.out + t * k.a.out_stride + qh * D;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o[j] * inv));
+    if (k.a.lse != nullptr && lane == 0)
+      k.a.lse[t * k.a.c.num_q_heads + qh] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+  }
 }
+
+int64_t part_bytes(const Layout& l) { return (static_cast<int64_t>(l.ctas) * sizeof(Part) + 15) / 16 * 16; }
+int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.block_rows * 2 * 4; }
 
 }  // namespace
 
-int64_t attn_draft_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 16; }
+int64_t attn_draft_workspace_bytes(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const Layout l = layout_of(max_rows, num_q_heads, num_kv_heads, head_dim);
+  return part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.block_rows * head_dim * 4;
+}
 
 cudaError_t launch_attn_draft(const DraftArgs& a, cudaStream_t stream) {
-  return a.c.head_dim == 64 ? launch_d<64>(a, stream) : a.c.head_dim == 128 ? launch_d<128>(a, stream) : launch_d<256>(a, stream);
+  const CacheArgs& c = a.c;
+  Args k{a, layout_of(a.max_rows, c.num_q_heads, c.num_kv_heads, c.head_dim), nullptr, nullptr, nullptr};
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  k.part = reinterpret_cast<Part*>(ws);
+  k.stat = reinterpret_cast<float*>(ws + part_bytes(k.l));
+  k.sum = reinterpret_cast<float*>(ws + part_bytes(k.l) + stat_bytes(k.l));
+  const int row = c.fp8 ? c.head_dim : 2 * c.head_dim;
+  const int64_t page = c.fp8 ? cache_page_bytes<true>(c.head_dim) : cache_page_bytes<false>(c.head_dim);
+  CUtensorMap kmap{}, vmap{};
+  const int64_t rows = c.num_pages * c.num_kv_heads * (page / row);
+  cudaError_t e = make_rows_tmap(&kmap, c.k_pool, rows, row, kPage);
+  if (e == cudaSuccess) e = make_rows_tmap(&vmap, c.v_pool, rows, row, kPage);
+  if (e == cudaSuccess) e = c.fp8 ? draft::launch_fp8(kmap, vmap, k, stream) : draft::launch_bf16(kmap, vmap, k, stream);
+  if (e != cudaSuccess || a.max_len <= draft::kKeys) return e;  // a unit of one tile has nothing to join
+  const dim3 grid(k.l.ctas, kJoinRows);
+  return c.head_dim == 64    ? launch_after(join_kernel<64>, grid, 32 * kJoinWarps, 0, stream, k)
+         : c.head_dim == 128 ? launch_after(join_kernel<128>, grid, 32 * kJoinWarps, 0, stream, k)
+                             : launch_after(join_kernel<256>, grid, 32 * kJoinWarps, 0, stream, k);
 }
 
 }  // namespace ci

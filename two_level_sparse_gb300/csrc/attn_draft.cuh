@@ -1,0 +1,1092 @@
+// Attention of drafted rows over the paged cache (contract in
+// include/ci_draft.h): the main kernel; instances per cache format in
+// attn_draft_bf16.cu and attn_draft_fp8.cu, dispatch and the join in
+// attn_draft.cu.
+//
+// Work.  The rows of a request that share a key-value head, n nodes times G
+// query heads, are one matrix Q of n G rows (row m is node m / G, head m % G).
+// A unit is (request, key-value head, block of 128 or 256 of those rows); it
+// reads the request's positions in tiles of 128.  The units' tiles, in order,
+// are one list, split evenly over teams of CTAs (one CTA per SM); the CTAs of
+// a team take neighbouring blocks of the same rows and read the same tiles at
+// the same time, once from HBM.  A unit that several teams worked on is joined
+// in a second launch, in order.
+//
+// A tile, on the fifth-generation tensor cores:
+//   S [128 rows x 128 positions] = Q K^T   both from shared memory, S in tensor memory
+//   P = 2^(S c - m), a thread per row      over S, as bf16
+//   O [128 rows x D] += P V                A = P from tensor memory, V positions-major
+// Two streams of such steps run in turn, so that one's exponentials are beside
+// the other's products: the two halves of a block of 256 rows over the same
+// tiles, or, where the block has no more than 128 rows, even and odd tiles with
+// sums of their own that are put together at the end.  With D = 256 tensor
+// memory holds one O: one stream with two score buffers.
+//
+// The reference m of a row is the largest logit of its first tile, raised where
+// a later one passes it by 8 (in base 2): probabilities are at most 2^8, and O
+// is rescaled only then.
+//
+// Masks.  Only tiles that reach past the positions that all rows of a block see
+// have any: there a row's 128 bits come from its mask words, shifted to the
+// tile.  Values that some rows do not see must not meet their zeros as NaN or
+// infinities: in those tiles everything that is not finite becomes 0 in shared
+// memory before the product, and at the end the rows that do see it add it.
+//
+// FP8 pages.  K widens to f16 and V to bf16 (x 2^-120) on the way from a ring of
+// raw tiles to the operands; the query becomes f16 after each row is scaled by a
+// power of two to a largest magnitude in [2^14, 2^15) (what it loses lies 2^-39
+// below that).  A position's scales join its logit and its probability.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "attn.cuh"
+#include "draft_internal.h"
+
+namespace ci {
+namespace draft {
+
+using attn::bf16x2;
+using attn::exp2_approx;
+
+constexpr int kKeys = 128;               // positions of a tile
+constexpr float kFar = 3.0e38f;          // references lie in [-kFar, kFar]
+constexpr float kSlack = 8.f;            // a logit over its reference
+constexpr int kTmem = 512, kColO = 256;  // score buffers at columns 0 and 128, then O
+constexpr float kTwo52 = 4503599627370496.f, kTwo68 = 295147905179352825856.f;
+
+struct Part {  // the unit that goes on past the end of a CTA's range; last < 0: none
+  int32_t req, head, block, last;
+};
+struct Layout {
+  int32_t ctas, team;  // CTAs, and how many make a team
+  int32_t group;       // query heads per key-value head
+  int32_t block_rows;  // rows of a block: 128 or 256
+};
+struct Args {
+  DraftArgs a;
+  Layout l;
+  Part* part;   // [ctas]
+  float* stat;  // [2 ctas][block_rows][2]: reference (base 2) and sum
+  float* sum;   // [2 ctas][block_rows][D]
+};
+
+template <int D_, bool kFp8_>
+struct Config {
+  static constexpr int D = D_;
+  static constexpr bool kFp8 = kFp8_, kTwo = D < 256;     // kTwo: two streams
+  static constexpr int kTiles = kTwo ? 2 : 1;             // of 128 rows in a block
+  static constexpr int kBlockRows = 128 * kTiles;
+  static constexpr int kParts = D == 256 ? 2 : 1;         // slots of a tile's K or V
+  static constexpr int kSlotKeys = kKeys / kParts;
+  static constexpr int kOperand = kSlotKeys * D * 2;      // bytes of a slot
+  static constexpr int kQ = 128 * D * 2;                  // of a tile of Q
+  static constexpr int kRow = kFp8 ? D : 2 * D;           // of a cached position
+  static constexpr int kBox = kRow < 128 ? kRow : 128;
+  static constexpr int kBoxes = kRow / kBox;
+  static constexpr int kScales = kFp8 ? 2 * kSlotKeys * 4 : 0;  // with K: those of K and of V
+  static constexpr int kRaw = kSlotKeys * kRow;           // of a loaded slot, without its scales
+  // bf16: the loaded slots are the operands; FP8: loaded slots, and operands
+  static constexpr int kLoads = kFp8 ? (D == 64 ? 8 : 3) : (D == 64 ? 10 : 5);
+  static constexpr int kOps = kFp8 ? (D == 64 ? 4 : 3) : 0;
+  static constexpr int kPageBytes = kFp8 ? 64 * D + 256 : 128 * D;
+};
+
+constexpr int kMaxSlots = 10;
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];      // loaded slots
+  uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // what the products read: values looked over (bf16), operands (FP8)
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
+  float stat[3][128];                // a stream's reference and sums, when two are put together
+  uint32_t pages[16];                // of the last sixteen tiles: which of the two pages are there
+  int32_t odd[4];                    // of the last four segments: the one where a value was not finite
+  int64_t warp_sum[16];
+  int32_t first, end, total, teams;  // the team's range of the list
+  int32_t req, head, block, tile;    // where it starts
+  uint32_t tmem;
+  int32_t abort;
+};
+struct Scales {  // FP8
+  alignas(16) float k[4][kKeys], v[4][kKeys];  // of the last four tiles
+  float factor[2][2][128];                     // of the last two segments: what the rows of Q were divided by
+};
+
+template <class C>
+constexpr int smem_bytes() {
+  return C::kTiles * C::kQ + C::kLoads * (C::kRaw + C::kScales) + C::kOps * C::kOperand +
+         (C::kFp8 ? static_cast<int>(sizeof(Scales)) : 0) + static_cast<int>(sizeof(Shared));
+}
+
+// ------------------------------------------------------------------ the list
+struct Request {
+  int first, n, len;  // rows first .. first + n - 1
+  int limit;          // positions that there are: len + n, or 0
+  int blocks;
+};
+enum { kGood = 0, kBadLen = 1, kBadReq = 2 };
+__device__ __forceinline__ Request request_of(const Args& k, int r, int& bad) {
+  const DraftArgs& a = k.a;
+  Request q;
+  q.first = a.c.req_start[r];
+  const int end = a.c.req_start[r + 1];
+  q.len = a.length[r];
+  bad = kGood;
+  if (q.first < 0 || end < q.first || end > a.rows) {
+    bad = kBadReq;
+    q.n = 0;
+  } else {
+    q.n = end - q.first;
+  }
+  q.limit = q.len + q.n;
+  if (q.n > 0 && (q.len < 0 || q.n > a.max_rows || q.n > a.max_len - q.len)) {
+    bad = kBadLen;
+    q.len = q.limit = 0;
+  }
+  q.blocks = static_cast<int>((static_cast<int64_t>(q.n) * k.l.group + k.l.block_rows - 1) / k.l.block_rows);
+  return q;
+}
+// The last node of a team's blocks b, b + 1, ...
+__device__ __forceinline__ int last_node(const Args& k, const Request& q, int b) {
+  return static_cast<int>(min(static_cast<int64_t>(q.n), (static_cast<int64_t>(b + k.l.team) * k.l.block_rows - 1) / k.l.group + 1)) - 1;
+}
+// Tiles of the team's blocks from b on.
+__device__ __forceinline__ int block_tiles(const Args& k, const Request& q, int b) {
+  const int keys = q.limit == 0 ? 1 : k.a.mask != nullptr ? q.limit : q.len + last_node(k, q, b) + 1;
+  return (keys - 1) / kKeys + 1;
+}
+// Tiles of one key-value head.
+__device__ __forceinline__ int head_tiles(const Args& k, const Request& q) {
+  if (k.a.mask != nullptr || q.limit == 0) return q.n == 0 ? 0 : (q.blocks + k.l.team - 1) / k.l.team * block_tiles(k, q, 0);
+  int n = 0;
+#pragma unroll 1
+  for (int b = 0; b < q.blocks; b += k.l.team) n += block_tiles(k, q, b);
+  return n;
+}
+
+// A CTA's way through its team's range: tiles [i0, i1) of a unit at a time.
+struct Walk {
+  int left;                         // tiles of the range behind the segment
+  int r, head, block, tile, tiles;  // where the next segment starts; block: the team's first
+  Request q;
+  int i0, i1;
+  __device__ __forceinline__ bool next(const Args& k) {
+    if (left == 0) return false;
+    if (tile == tiles) {
+      tile = 0;
+      block += k.l.team;
+      if (block >= q.blocks) {
+        block = 0;
+        if (++head == k.a.c.num_kv_heads) {
+          head = 0;
+          int bad;
+#pragma unroll 1
+          do q = request_of(k, ++r, bad);
+          while (q.n == 0);
+        }
+      }
+      tiles = block_tiles(k, q, block);
+    }
+    i0 = tile;
+    i1 = min(tiles, i0 + left);
+    left -= i1 - i0;
+    tile = i1;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int share_start(int team, int per, int rest) { return team * per + min(team, rest); }
+// The team that has tile x of the list.
+__device__ __forceinline__ int team_of(int x, int total, int teams) {
+  const int per = total / teams, rest = total - per * teams, longer = rest * (per + 1);
+  return x < longer ? x / (per + 1) : rest + (x - longer) / per;
+}
+
+// The range of this CTA's team: every thread adds up a run of requests, a scan
+// over the threads gives the total, and the thread whose run holds the range's
+// first tile walks to it.
+template <int kThreads>
+__device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = k.a.c.num_kv_heads;
+  const int per_thread = (k.a.c.num_req + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per_thread, k.a.c.num_req), r1 = min(r0 + per_thread, k.a.c.num_req);
+  int64_t mine = 0;
+  int bits = 0;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    int bad;
+    const Request q = request_of(k, r, bad);
+    bits |= bad;
+    mine += static_cast<int64_t>(head_tiles(k, q)) * heads;
+  }
+  if (bits != 0 && blockIdx.x == 0)
+    report(k.a.c.dev_err, (bits & kBadLen ? kDevErrLen : 0) | (bits & kBadReq ? kDevErrReq : 0));
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, sum = 0;
+#pragma unroll 1
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    sum += sh.warp_sum[w];
+  }
+  if (sum > INT32_MAX) {  // starts that descend: requests with the same rows
+    if (blockIdx.x == 0 && tid == 0) report(k.a.c.dev_err, kDevErrReq);
+    sum = 0;
+  }
+  const int total = static_cast<int>(sum);
+  const int teams = min(k.l.ctas / k.l.team, total), per = teams > 0 ? total / teams : 0, rest = total - per * teams;
+  const int team = static_cast<int>(blockIdx.x) / k.l.team;
+  const int first = share_start(min(team, teams), per, rest), end = share_start(min(team + 1, teams), per, rest);
+  if (tid == 0) sh.first = first, sh.end = end, sh.total = total, sh.teams = teams;
+  if (first < end && before <= first && first < before + mine) {
+    int at = static_cast<int>(first - before), r = r0, bad;
+    Request q = request_of(k, r, bad);
+    int n = head_tiles(k, q);
+#pragma unroll 1
+    while (at >= static_cast<int64_t>(n) * heads) {
+      at -= n * heads;
+      q = request_of(k, ++r, bad);
+      n = head_tiles(k, q);
+    }
+    const int head = at / n;
+    at -= head * n;
+    int b = 0;
+    if (k.a.mask != nullptr || q.limit == 0) {
+      const int t = block_tiles(k, q, 0);
+      b = at / t * k.l.team;
+      at -= at / t * t;
+    } else {
+#pragma unroll 1
+      for (int t; at >= (t = block_tiles(k, q, b)); b += k.l.team) at -= t;
+    }
+    sh.req = r, sh.head = head, sh.block = b, sh.tile = at;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ Walk walk_of(const Args& k, const Shared& sh) {
+  Walk w{};
+  w.left = sh.end - sh.first;
+  if (w.left == 0) return w;
+  int bad;
+  w.r = sh.req, w.head = sh.head, w.block = sh.block, w.tile = sh.tile;
+  w.q = request_of(k, w.r, bad);
+  w.tiles = block_tiles(k, w.q, w.block);
+  return w;
+}
+
+// A segment as one CTA of the team has it.
+struct Segment {
+  int block, rows;  // its block, and how many rows that has (0: nothing to do)
+  int row0;         // its first row of the request's matrix
+  bool two;         // two tiles of rows, over the same positions
+  int tiles, steps;
+  int seen;         // positions that every row of the block sees
+};
+template <class C>
+__device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
+  Segment s;
+  s.block = w.block + static_cast<int>(blockIdx.x) % k.l.team;
+  s.row0 = s.block * C::kBlockRows;
+  s.rows = s.block < w.q.blocks ? min(C::kBlockRows, w.q.n * k.l.group - s.row0) : 0;
+  s.two = C::kTwo && s.rows > 128;
+  s.tiles = w.i1 - w.i0;
+  s.steps = s.two ? 2 * s.tiles : s.tiles;
+  s.seen = w.q.limit == 0 ? 0 : w.q.len + (k.a.mask != nullptr ? 0 : s.row0 / k.l.group + 1);
+  return s;
+}
+
+// ------------------------------------------------------------------ small things
+// One role's waits: false once anything has given up; the role then goes on
+// through its loop without touching memory.
+struct Waiter {
+  Shared& sh;
+  int32_t* dev_err;
+  bool alive = true;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
+    alive = alive && attn::wait_warp(bar, parity, &sh.abort, dev_err);
+    return alive;
+  }
+};
+template <int N>
+struct Place {  // a ring's slot
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
+// 128-byte swizzled operands: K-major (rows of 64 elements of the reduced
+// dimension), or MN-major (rows of 64 elements of the other dimension, one per
+// element of the reduced one; the next 64 elements `next` bytes further).
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t next) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((next >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+// Instruction descriptor: M = 128, fp32 sums; bf16 or f16 operands, B MN-major or not.
+__host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Chunk `chunk` of 16 bytes of row p of an operand with `rows` rows.
+__device__ __forceinline__ uint32_t operand_offset(int rows, int p, int chunk) {
+  return (chunk >> 3) * (rows * 128) + p * 128 + (((chunk & 7) ^ (p & 7)) << 4);
+}
+
+struct Buffers {
+  uint32_t q, load, op, scales;  // shared-memory addresses; scales: of the loaded slots
+  Scales* sc;                    // FP8
+};
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+
+// ------------------------------------------------------------------ loads
+// K and V of the tiles, in the order in which the products take them: with two
+// tiles of rows K and V of a tile, else V a tile behind K.
+template <class C>
+__device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, const Buffers& b, const CUtensorMap* kmap,
+                                           const CUtensorMap* vmap) {
+  const CacheArgs& c = k.a.c;
+  const int lane = threadIdx.x & 31;
+  constexpr int kPages = C::kSlotKeys / kPage, kPerPage = C::kPageBytes / C::kRow;
+  Waiter wait{sh, c.dev_err};
+  Place<C::kLoads> at;
+  uint32_t base = 0;  // tiles so far
+#pragma unroll 1
+  while (w.next(k)) {
+    const Segment s = segment_of<C>(k, w);
+    if (s.rows == 0) continue;
+    const int32_t* table = c.page_table + static_cast<int64_t>(w.r) * c.max_pages;
+    const int lag = s.two ? 0 : 1;
+    // the pages of 32 tiles, two per lane; those of the 32 before, for V
+    int lo = -1, hi = -1, lo0 = -1, hi0 = -1;
+#pragma unroll 1
+    for (int j = 0; j < s.tiles + lag; ++j) {
+      if ((j & 31) == 0) {
+        const int64_t pos = static_cast<int64_t>(w.i0 + j + lane) * kKeys;
+        const bool in = j + lane < s.tiles, in0 = in && pos < w.q.limit, in1 = in && pos + kPage < w.q.limit;
+        lo0 = lo, hi0 = hi;
+        lo = in0 ? table[pos / kPage] : -1;
+        hi = in1 ? table[pos / kPage + 1] : -1;
+        const bool out0 = lo < 0 || lo >= c.num_pages, out1 = hi < 0 || hi >= c.num_pages;
+        if ((in0 && out0) || (in1 && out1)) report(c.dev_err, kDevErrPage);
+        if (out0) lo = -1;
+        if (out1) hi = -1;
+      }
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const int t = v ? j - lag : j;
+        if (t < 0 || t >= s.tiles) continue;
+        const bool old = (t >> 5) != (j >> 5);
+        const int page0 = __shfl_sync(0xffffffffu, old ? lo0 : lo, t & 31), page1 = __shfl_sync(0xffffffffu, old ? hi0 : hi, t & 31);
+        if (v == 0 && lane == 0) sh.pages[(base + t) & 15] = (page0 >= 0 ? 1u : 0u) | (page1 >= 0 ? 2u : 0u);
+#pragma unroll 1
+        for (int x = 0; x < C::kParts; ++x, at.advance()) {
+          if (!wait(&sh.empty[at.slot], at.phase ^ 1)) continue;
+          uint64_t* full = &sh.full[at.slot];
+          // a lane per box: page lane / boxes of the slot, box lane % boxes; a lane per page's scales
+          const int which = lane / C::kBoxes, box = lane % C::kBoxes;
+          const int page = (kPages == 1 ? x : which) ? page1 : page0;
+          const int there = kPages == 1 ? page >= 0 : (page0 >= 0) + (page1 >= 0);
+          __syncwarp();
+          if (lane == 0) {
+            if (there > 0)
+              mbar_arrive_expect_tx(full, there * (kPage * C::kRow + (C::kFp8 && v == 0 ? 512 : 0)));
+            else
+              mbar_arrive(full);
+          }
+          __syncwarp();
+          const uint32_t dst = b.load + at.slot * C::kRaw, scales = b.scales + at.slot * C::kScales;
+          if (which < kPages && page >= 0) {
+            const int row = page * c.num_kv_heads + w.head;
+            attn::tma_box(dst + box * (C::kSlotKeys * C::kBox) + which * (kPage * C::kBox), v ? vmap : kmap, box * 128,
+                          row * kPerPage, smem_u32(full));
+            if (C::kFp8 && v == 0 && box == 0) {
+              const int64_t from = static_cast<int64_t>(row) * C::kPageBytes + kPage * C::D;
+              attn::bulk_load(scales + which * 256, c.k_pool + from, 256, smem_u32(full));
+              attn::bulk_load(scales + C::kSlotKeys * 4 + which * 256, c.v_pool + from, 256, smem_u32(full));
+            }
+          }
+        }
+      }
+    }
+    base += s.tiles;
+  }
+}
+
+// ------------------------------------------------------------------ preparation
+constexpr int kPrepWarps = 4;
+
+// A tile of the rows of Q: row m of the request's matrix is node m / G.  FP8: in
+// f16, each row scaled by a power of two, 1 / factor.
+template <class C>
+__device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const Segment& s, const Buffers& b,
+                                             float (*factor)[128], int tid) {
+  constexpr int kChunks = C::D / 8, kRowsAtOnce = 32 * kPrepWarps / kChunks;
+  const int chunk = tid % kChunks;
+  const int rows = s.two ? 256 : 128;
+#pragma unroll 4
+  for (int m = tid / kChunks; m < rows; m += kRowsAtOnce) {
+    const int x = s.row0 + m, node = x / k.l.group;
+    const bool there = m < s.rows;
+    const uint16_t* src = k.a.q + (w.q.first + (there ? node : 0)) * k.a.q_stride +
+                          (static_cast<int64_t>(w.head) * k.l.group + (there ? x - node * k.l.group : 0)) * C::D + chunk * 8;
+    const uint32_t dst = b.q + (m >> 7) * C::kQ + operand_offset(128, m & 127, chunk);
+    if (!C::kFp8) {
+      attn::copy16(dst, reinterpret_cast<const uint8_t*>(src), there);
+      continue;
+    }
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (there) v = *reinterpret_cast<const uint4*>(src);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int o = 1; o < kChunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = static_cast<int>(top >> 7);  // biased; 255: not finite
+    const int up = e == 255 || top == 0 ? 0 : min(14 - (e - 127), 126);
+    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -113 <= up <= 126
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = attn::f16x2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
+    sts128(dst, make_uint4(h[0], h[1], h[2], h[3]));
+    if (chunk == 0) factor[m >> 7][m & 127] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+  }
+  if (!C::kFp8) wait_copies();
+  fence_proxy_async_smem();
+}
+
+// Values of a slot that not every row of the block sees (positions from s.seen
+// on): zeros where there are none or where they are not finite, which is noted.
+template <class C>
+__device__ __forceinline__ void prep_values(Shared& sh, const Walk& w, const Segment& s, uint32_t slot, int64_t pos0,
+                                            uint32_t pages, int x, int warp, int lane, int segment) {
+  constexpr int kChunks = C::D / 8, kPer = C::kSlotKeys / kPrepWarps;
+  bool odd = false;
+#pragma unroll 2
+  for (int e = lane; e < kPer * kChunks; e += 32) {
+    const int p = warp * kPer + e / kChunks;
+    const int64_t pos = pos0 + p;
+    const bool page = (pages >> (C::kParts == 1 ? p / kPage : x)) & 1;
+    if (page && pos < s.seen) continue;
+    const uint32_t at = slot + operand_offset(C::kSlotKeys, p, e % kChunks);
+    if (!page || pos >= w.q.limit) {
+      sts128(at, make_uint4(0, 0, 0, 0));
+      continue;
+    }
+    const uint4 v = lds128(at);
+    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    bool here = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((u[i] & 0x7F80u) == 0x7F80u) u[i] &= 0xFFFF0000u, here = true;
+      if ((u[i] & 0x7F800000u) == 0x7F800000u) u[i] &= 0xFFFFu, here = true;
+    }
+    if (here) sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+    odd |= here;
+  }
+  if (odd) sh.odd[segment & 3] = segment;
+  fence_proxy_async_smem();
+}
+
+// Bytes 0 .. 3 of r (e4m3) as two bf16 pairs of the value x 2^-120, in order.
+__device__ __forceinline__ uint2 widen_bf16(uint32_t r) {
+  const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);  // bytes to the upper half of each 16 bits
+  return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
+}
+// e4m3's NaN codes as the largest code's successor, 480, which f16 has.
+__device__ __forceinline__ uint2 widen_f16(uint32_t r) {
+  const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);
+  // the exponent and mantissa moved into an f16's are the value x 2^-8
+  const __half2 up = __float2half2_rn(256.f);
+  const uint32_t x = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u), y = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
+  const __half2 hx = __hmul2(*reinterpret_cast<const __half2*>(&x), up), hy = __hmul2(*reinterpret_cast<const __half2*>(&y), up);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&hx), *reinterpret_cast<const uint32_t*>(&hy));
+}
+// A raw slot into an operand: f16 of K, bf16 x 2^-120 of V.
+template <class C, bool kValues>
+__device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int tid) {
+  constexpr int kUnits = C::D / 16;  // of 16 codes
+#pragma unroll 4
+  for (int e = tid; e < C::kSlotKeys * kUnits; e += 32 * kPrepWarps) {
+    const int p = e / kUnits, u = e % kUnits;
+    const uint32_t from = C::kBox == 128 ? (u >> 3) * (C::kSlotKeys * 128) + p * 128 + (((u & 7) ^ (p & 7)) << 4)
+                                         : p * 64 + ((u ^ ((p >> 1) & 3)) << 4);
+    const uint4 v = lds128(raw + from);
+    uint2 r[4];
+    const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = kValues ? widen_bf16(c[i]) : widen_f16(c[i]);
+    const uint4 first = make_uint4(r[0].x, r[0].y, r[1].x, r[1].y), second = make_uint4(r[2].x, r[2].y, r[3].x, r[3].y);
+    // (lanes of the later half write the second chunk first: no two on the same banks)
+    const bool swap = (u & 4) != 0;
+    sts128(op + operand_offset(C::kSlotKeys, p, 2 * u + swap), swap ? second : first);
+    sts128(op + operand_offset(C::kSlotKeys, p, 2 * u + !swap), swap ? first : second);
+  }
+}
+
+template <class C>
+__device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const Buffers& b) {
+  const int tid = threadIdx.x & (32 * kPrepWarps - 1), lane = tid & 31, warp = tid >> 5;
+  Waiter wait{sh, k.a.c.dev_err};
+  Place<C::kLoads> at;
+  Place<C::kFp8 ? C::kOps : 1> op;
+  uint32_t segments = 0, base = 0;
+#pragma unroll 1
+  while (w.next(k)) {
+    const Segment s = segment_of<C>(k, w);
+    if (s.rows == 0) continue;
+    if (wait(&sh.q_empty, (segments & 1) ^ 1)) {
+      prep_queries<C>(k, w, s, b, C::kFp8 ? b.sc->factor[(segments + 1) & 1] : nullptr, tid);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+    }
+    ++segments;
+    const int lag = s.two ? 0 : 1;
+#pragma unroll 1
+    for (int j = 0; j < s.tiles + lag; ++j) {
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const int t = v ? j - lag : j;
+        if (t < 0 || t >= s.tiles) continue;
+#pragma unroll 1
+        for (int x = 0; x < C::kParts; ++x, at.advance()) {
+          const uint32_t raw = b.load + at.slot * C::kRaw;
+          const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys + x * C::kSlotKeys;
+          if (!C::kFp8) {
+            if (v == 0 || !wait(&sh.full[at.slot], at.phase)) continue;
+            const uint32_t pages = sh.pages[(base + t) & 15];
+            if (pages != 3 || pos0 + C::kSlotKeys > s.seen)
+              prep_values<C>(sh, w, s, raw, pos0, pages, x, warp, lane, static_cast<int>(segments));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.ready[at.slot]);
+            continue;
+          }
+          if (wait(&sh.full[at.slot], at.phase) && wait(&sh.op_empty[op.slot], op.phase ^ 1)) {
+            if (v == 0 && tid < C::kSlotKeys) {
+              const uint32_t from = b.scales + at.slot * C::kScales + tid * 4;
+              b.sc->k[(base + t) & 3][x * C::kSlotKeys + tid] = lds_f32(from);
+              b.sc->v[(base + t) & 3][x * C::kSlotKeys + tid] = lds_f32(from + C::kSlotKeys * 4) * kTwo52;
+            }
+            const uint32_t dst = b.op + op.slot * C::kOperand;
+            if (v)
+              widen<C, true>(raw, dst, tid);
+            else
+              widen<C, false>(raw, dst, tid);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sh.ready[op.slot]);
+              mbar_arrive(&sh.empty[at.slot]);
+            }
+          }
+          op.advance();
+        }
+      }
+    }
+    base += s.tiles;
+  }
+}
+
+// ------------------------------------------------------------------ products
+template <class C>
+__device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, const Buffers& b, uint32_t tmem) {
+  constexpr int kRing = C::kFp8 ? C::kOps : C::kLoads;
+  constexpr uint32_t kIdQ = idesc(C::kSlotKeys, !C::kFp8, false), kIdP = idesc(C::D, true, true);
+  Waiter wait{sh, k.a.c.dev_err};
+  const uint32_t ring = C::kFp8 ? b.op : b.load;
+  uint64_t* release = C::kFp8 ? sh.op_empty : sh.empty;
+  Place<kRing> at;                  // of the next item
+  int k_slot = 0, v_slot = 0;       // of the present tiles' first parts
+  uint32_t v_turn = 0;              // bf16: parities of the slots' values
+  uint32_t p_turn[2] = {0, 0};
+  uint32_t segments = 0;
+  // Waits for the next item; false after giving up.
+  auto arrived = [&](bool values) {
+    bool ok = wait(C::kFp8 ? &sh.ready[at.slot] : &sh.full[at.slot], at.phase);
+    if (!C::kFp8 && values) {
+      ok = ok && wait(&sh.ready[at.slot], (v_turn >> at.slot) & 1);
+      v_turn ^= 1u << at.slot;
+    }
+    return ok;
+  };
+#pragma unroll 1
+  while (w.next(k)) {
+    const Segment s = segment_of<C>(k, w);
+    if (s.rows == 0) continue;
+    wait(&sh.q_full, segments & 1);
+    ++segments;
+#pragma unroll 1
+    for (int i = 0; i <= s.steps; ++i) {
+      if (i < s.steps) {
+        const bool fresh = !s.two || (i & 1) == 0, last = !s.two || (i & 1) == 1;
+        const uint32_t q = b.q + (s.two ? (i & 1) * C::kQ : 0);
+        if (fresh) k_slot = at.slot;
+        int slot = k_slot;
+#pragma unroll 1
+        for (int x = 0; x < C::kParts; ++x) {
+          if (fresh) arrived(false);
+          if (wait.alive) {
+            tc_fence_after();
+            const uint64_t da = desc128(q, 16), db = desc128(ring + slot * C::kOperand, 16);
+#pragma unroll
+            for (int e = 0; e < C::D / 16; ++e)
+              mma_ss(tmem + 128 * (i & 1) + x * C::kSlotKeys, da + (e >> 2) * (128 * 128 / 16) + (e & 3) * 2,
+                     db + (e >> 2) * (C::kSlotKeys * 128 / 16) + (e & 3) * 2, kIdQ, e > 0);
+            if (last) mma_commit_elect(&release[slot]);
+          }
+          if (fresh) at.advance();
+          if (++slot == kRing) slot = 0;
+        }
+        if (wait.alive) {
+          mma_commit_elect(&sh.s_full[i & 1]);
+          if (i == s.steps - 1) mma_commit_elect(&sh.q_empty);
+        }
+      }
+      if (i == 0) continue;
+      const int p = i - 1, o = C::kTwo ? p & 1 : 0;
+      const bool fresh = !s.two || (p & 1) == 0, last = !s.two || (p & 1) == 1;
+      wait(&sh.p_full[p & 1], p_turn[p & 1]);
+      p_turn[p & 1] ^= 1;
+      if (fresh) v_slot = at.slot;
+      int slot = v_slot;
+#pragma unroll 1
+      for (int x = 0; x < C::kParts; ++x) {
+        if (fresh) arrived(true);
+        if (wait.alive) {
+          tc_fence_after();
+          const uint64_t db = desc128(ring + slot * C::kOperand, C::kSlotKeys * 128);
+#pragma unroll
+          for (int e = 0; e < C::kSlotKeys / 16; ++e)
+            mma_ts(tmem + kColO + o * C::D, tmem + 128 * (p & 1) + x * (C::kSlotKeys / 2) + e * 8, db + e * 128, kIdP,
+                   x > 0 || e > 0 || p >= (C::kTwo ? 2 : 1));
+          if (last) mma_commit_elect(&release[slot]);
+        }
+        if (fresh) at.advance();
+        if (++slot == kRing) slot = 0;
+      }
+      if (wait.alive) mma_commit_elect(&sh.pv_done[o]);
+    }
+  }
+  if (!wait.alive) {  // the products in flight end before the CTA's memory goes
+    mma_commit_elect(&sh.drain);
+    mbar_wait(&sh.drain, 0, nullptr, 1000000ull);
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// Which of the 32 positions from pos on a row sees.
+struct RowMask {
+  const uint32_t* words;  // null: a chain
+  int node, n, len, limit, count;
+};
+__device__ __forceinline__ uint32_t mask_word(const RowMask& m, int i) {
+  if (i >= m.count || 32 * i >= m.n) return 0;
+  const uint32_t v = m.words[i];
+  return 32 * i + 32 > m.n ? v & ((1u << (m.n - 32 * i)) - 1) : v;
+}
+__device__ __forceinline__ uint32_t seen_of(const RowMask& m, int64_t pos) {
+  if (m.limit == 0) return 0;
+  const int64_t rel = pos - m.len;
+  if (m.words == nullptr) {
+    const int64_t c = m.node + 1 - rel;
+    return c >= 32 ? ~0u : c <= 0 ? 0 : (1u << c) - 1;
+  }
+  if (rel <= -32) return ~0u;
+  if (rel < 0) return (mask_word(m, 0) << -rel) | ((1u << -rel) - 1);
+  if (rel >= m.n) return 0;
+  const int i = static_cast<int>(rel) >> 5;
+  return __funnelshift_r(mask_word(m, i), mask_word(m, i + 1), static_cast<int>(rel) & 31);
+}
+
+// What a row sees that is not finite, of 32 dims from d0 on: added as it is.
+template <class C>
+__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int d0, uint32_t (&o)[32]) {
+  const CacheArgs& c = k.a.c;
+  const int64_t first = max(static_cast<int64_t>(w.i0) * kKeys, static_cast<int64_t>(w.q.len)), end = min(static_cast<int64_t>(w.i1) * kKeys, static_cast<int64_t>(w.q.limit));
+#pragma unroll 1
+  for (int64_t pos = first; pos < end; ++pos) {
+    if ((seen_of(m, pos) & 1) == 0) continue;
+    const int page = c.page_table[static_cast<int64_t>(w.r) * c.max_pages + pos / kPage];
+    if (page < 0 || page >= c.num_pages) continue;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                            c.v_pool + (static_cast<int64_t>(page) * c.num_kv_heads + w.head) * C::kPageBytes) +
+                        (pos & (kPage - 1)) * C::D + d0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if ((v[i] & 0x7F80) == 0x7F80) o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_lo(v[i]));
+  }
+}
+
+// Two logits in base 2, rounded by themselves: the reference is one of them.
+template <class C>
+__device__ __forceinline__ float2 logits_of(uint32_t s0, uint32_t s1, float factor, float k0, float k1) {
+  float2 x = make_float2(__uint_as_float(s0), __uint_as_float(s1));
+  if (C::kFp8) x = mul2(x, make_float2(k0, k1));
+  return make_float2(__fmul_rn(x.x, factor), __fmul_rn(x.y, factor));
+}
+
+template <class C>
+__device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const Scales* sc, uint32_t tmem, int g) {
+  const DraftArgs& a = k.a;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), own = lanes + kColO + (C::kTwo ? g * C::D : 0);
+  constexpr int kStride = C::kTwo ? 2 : 1;
+  Waiter wait{sh, a.c.dev_err};
+  uint32_t turn[2] = {0, 0}, done = 0, base = 0, segment = 0;  // done: products with this stream's probabilities
+#pragma unroll 1
+  while (w.next(k)) {
+    const Segment s = segment_of<C>(k, w);
+    if (s.rows == 0) continue;
+    ++segment;
+    const int m0 = (s.two ? g * 128 : 0) + row;  // this thread's row of the block
+    const bool live = m0 < s.rows;
+    const int x0 = s.row0 + (live ? m0 : 0), node = x0 / k.l.group;
+    const RowMask mask{a.mask != nullptr ? a.mask + static_cast<int64_t>(w.q.first + node) * a.mask_words : nullptr,
+                       node, w.q.n, w.q.len, w.q.limit, a.mask_words};
+    const int seen = C::kTwo && s.two && g == 1 && a.mask == nullptr && w.q.limit > 0
+                         ? w.q.len + (s.row0 + 128) / k.l.group + 1 : s.seen;
+    float factor = a.scale * attn::kLog2e, ref = -kFar;
+    float2 l = make_float2(0.f, 0.f), lr = l;
+#pragma unroll 1
+    for (int i = C::kTwo ? g : 0; i < s.steps; i += kStride) {
+      const int buf = i & 1, t = s.two ? i >> 1 : i;
+      const bool first = i < kStride;
+      wait(&sh.s_full[buf], turn[buf]);
+      turn[buf] ^= 1;
+      tc_fence_after();
+      if (C::kFp8 && first) factor = a.scale * attn::kLog2e * sc->factor[segment & 1][s.two ? g : 0][row];
+      const uint32_t at = lanes + 128 * buf;
+      const uint32_t pages = sh.pages[(base + t) & 15];
+      const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys;
+      const float *ks = C::kFp8 ? sc->k[(base + t) & 3] : nullptr, *vs = C::kFp8 ? sc->v[(base + t) & 3] : nullptr;
+      const bool masked = pages != 3 || pos0 + kKeys > seen;
+      uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) bits[c] = (pages >> (c >> 1)) & 1 ? seen_of(mask, pos0 + 32 * c) : 0;
+      }
+      // ---- the tile's largest logit
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_ld32(at + 32 * c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+          if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
+          float2 y = logits_of<C>(x[j], x[j + 1], factor, f.x, f.y), z = logits_of<C>(x[j + 2], x[j + 3], factor, f.z, f.w);
+          if (masked) {
+            if (!((bits[c] >> j) & 1)) y.x = -INFINITY;
+            if (!((bits[c] >> (j + 1)) & 1)) y.y = -INFINITY;
+            if (!((bits[c] >> (j + 2)) & 1)) z.x = -INFINITY;
+            if (!((bits[c] >> (j + 3)) & 1)) z.y = -INFINITY;
+          }
+          top = fmaxf(top, fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
+        }
+      }
+      if (first) {
+        ref = fmaxf(fminf(top, kFar), -kFar);
+      } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+        const float up = fmaxf(ref, fminf(top, kFar)), by = exp2_approx(ref - up);
+        ref = up;
+        l = mul2(l, make_float2(by, by)), lr = mul2(lr, make_float2(by, by));
+        if (wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < C::D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(own + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+            tmem_st32(own + c, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      // ---- probabilities, over the scores
+      const float2 less = make_float2(-ref, -ref);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], p[16];
+        tmem_ld32(at + 32 * c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
+          if (C::kFp8) {
+            f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
+            h = *reinterpret_cast<const float4*>(vs + 32 * c + j);
+          }
+          float2 y = add2(logits_of<C>(x[j], x[j + 1], factor, f.x, f.y), less);
+          float2 z = add2(logits_of<C>(x[j + 2], x[j + 3], factor, f.z, f.w), less);
+          y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+          if (masked) {
+            if (!((bits[c] >> j) & 1)) y.x = 0.f;
+            if (!((bits[c] >> (j + 1)) & 1)) y.y = 0.f;
+            if (!((bits[c] >> (j + 2)) & 1)) z.x = 0.f;
+            if (!((bits[c] >> (j + 3)) & 1)) z.y = 0.f;
+          }
+          l = add2(l, y), l = add2(l, z);
+          if (C::kFp8) {
+            y = mul2(y, make_float2(h.x, h.y)), z = mul2(z, make_float2(h.z, h.w));
+            if (masked) {  // (a scale that is not finite must not meet a 0)
+              if (!((bits[c] >> j) & 1)) y.x = 0.f;
+              if (!((bits[c] >> (j + 1)) & 1)) y.y = 0.f;
+              if (!((bits[c] >> (j + 2)) & 1)) z.x = 0.f;
+              if (!((bits[c] >> (j + 3)) & 1)) z.y = 0.f;
+            }
+          }
+          const uint32_t r0 = bf16x2(y.x, y.y), r1 = bf16x2(z.x, z.y);
+          if (!C::kFp8) {
+            lr = add2(lr, make_float2(bf16_lo(r0), bf16_hi(r0)));
+            lr = add2(lr, make_float2(bf16_lo(r1), bf16_hi(r1)));
+          }
+          p[j / 2] = r0, p[j / 2 + 1] = r1;
+        }
+        tmem_st16(at + 16 * c, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+      ++done;
+    }
+    base += s.tiles;
+    // ---- the segment's end
+    const int mine = s.two ? s.tiles : C::kTwo ? (s.steps + 1 - g) / 2 : s.steps;  // steps of this stream
+    if (mine > 0) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
+    tc_fence_after();
+    float total = l.x + l.y, rounded = C::kFp8 ? total : lr.x + lr.y;
+    const bool joined = C::kTwo && !s.two;
+    float fa = 1.f, fb = 0.f;
+    int c0 = 0, c1 = C::D;
+    if (joined) {  // both streams have the same rows: a half of the dims each
+      float* stat = &sh.stat[0][row];
+      auto leave = [&]() { stat[0] = ref, stat[128] = total, stat[256] = rounded; };
+      float3 x = make_float3(ref, total, rounded);
+      if (g == 1) leave();
+      tc_fence_before();
+      named_sync(1, 256);
+      tc_fence_after();
+      if (g == 0) x = make_float3(stat[0], stat[128], stat[256]), leave();
+      named_sync(1, 256);
+      if (g == 1) x = make_float3(stat[0], stat[128], stat[256]);
+      const bool both = s.steps > 1;  // else the second one has nothing
+      const float top = both ? fmaxf(ref, x.x) : g == 0 ? ref : x.x;
+      const float f = both || g == 0 ? exp2_approx(ref - top) : 0.f, fx = both || g == 1 ? exp2_approx(x.x - top) : 0.f;
+      total = total * f + x.y * fx, rounded = rounded * f + x.z * fx;
+      fa = g == 0 ? f : fx, fb = g == 0 ? fx : f;
+      ref = top;
+      c0 = g * (C::D / 2), c1 = c0 + C::D / 2;
+    }
+    const bool whole = w.i0 == 0 && w.i1 == w.tiles;
+    // whole: O / rounded; else O total / rounded, which the join divides by the sum of the totals
+    const float by = rounded == 0.f ? 0.f : (whole ? 1.f : total) / rounded * (C::kFp8 ? kTwo68 : 1.f);
+    const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0), qh = static_cast<int64_t>(w.head) * k.l.group + x0 - node * k.l.group;
+    const int64_t t = w.q.first + node;
+    const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
+    const uint32_t from = C::kTwo && !joined ? own : lanes + kColO;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(from + c, o);
+      tmem_ld_wait();
+      if (joined && s.steps > 1) {
+        uint32_t y[32];
+        tmem_ld32(from + C::D + c, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fa + __uint_as_float(y[j]) * fb);
+      }
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = rounded == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * by);
+        if (odd) {
+          uint32_t y[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = o[j];
+          add_odd<C>(k, w, mask, c, y);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = y[j];
+        }
+        if (whole) {
+          uint16_t* dst = a.out + t * a.out_stride + qh * C::D + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            *reinterpret_cast<uint4*>(dst + j) = make_uint4(
+                bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
+                bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])), bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
+        } else {
+          float* dst = k.sum + (slot * C::kBlockRows + m0) * C::D + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    if (live && c0 == 0) {
+      if (!whole)
+        *reinterpret_cast<float2*>(k.stat + (slot * C::kBlockRows + m0) * 2) = make_float2(ref, total);
+      else if (a.lse != nullptr)
+        a.lse[t * a.c.num_q_heads + qh] = total == 0.f ? -INFINITY : (ref + log2f(total)) * 0.6931471805599453f;
+    }
+    if (!whole && w.i0 == 0 && g == 0 && row == 0)  // (the segment ends where the range does)
+      k.part[blockIdx.x] = Part{w.r, w.head, s.block, team_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.teams)};
+    if (joined) named_sync(1, 256);  // both have read both sums
+  }
+}
+
+// What the copies in flight write lands before the CTA's memory goes (after a
+// role has given up): both parities of a barrier, whichever is the last fill's.
+template <class C>
+__device__ __forceinline__ void drain_copies(Shared& sh) {
+#pragma unroll 1
+  for (int i = 0; i < 2 * C::kLoads; ++i) mbar_wait(&sh.full[i >> 1], i & 1, nullptr, 1000000ull);
+}
+
+constexpr int kThreads = 512;
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    draft_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args k) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t mem = smem_u32(raw);  // (checked below: the swizzle is one of address bits)
+  constexpr int kOpAt = C::kTiles * C::kQ, kLoadAt = kOpAt + C::kOps * C::kOperand, kScaleAt = kLoadAt + C::kLoads * C::kRaw,
+                kEnd = kScaleAt + C::kLoads * C::kScales, kSharedAt = kEnd + (C::kFp8 ? static_cast<int>(sizeof(Scales)) : 0);
+  const Buffers b{mem, mem + kLoadAt, mem + kOpAt, mem + kScaleAt, C::kFp8 ? reinterpret_cast<Scales*>(raw + kEnd) : nullptr};
+  Shared& sh = *reinterpret_cast<Shared*>(raw + kSharedAt);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == 12) {
+    tmem_alloc(&sh.tmem, kTmem);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::kLoads; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], C::kFp8 ? kPrepWarps : 1);
+      mbar_init(&sh.ready[i], kPrepWarps);
+    }
+    for (int i = 0; i < C::kOps; ++i) {
+      if (i >= C::kLoads) mbar_init(&sh.ready[i], kPrepWarps);
+      mbar_init(&sh.op_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4), mbar_init(&sh.pv_done[i], 1);
+    mbar_init(&sh.q_full, kPrepWarps);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.drain, 1);
+    fence_mbar_init();
+    sh.abort = 0;
+    for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+  }
+  wait_predecessor();
+  if (tid == 0) k.part[blockIdx.x].last = -1;
+  tc_fence_before();
+  find_range<kThreads>(k, sh);
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  if ((mem & 1023u) != 0) {  // not by the launch's rules: nothing is read
+    if (tid == 0) report(k.a.c.dev_err, kDevErrTimeout);
+  } else if (warp < 4) {
+    softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, 0);
+  } else if (warp < 8) {
+    if (C::kTwo) softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, 1);
+  } else if (warp < 12) {
+    prepare<C>(k, sh, walk_of(k, sh), b);
+  } else if (warp == 12) {
+    products<C>(k, sh, walk_of(k, sh), b, tmem);
+  } else if (warp == 13) {
+    load_tiles<C>(k, sh, walk_of(k, sh), b, &kmap, &vmap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (sh.abort != 0 && warp == 0) drain_copies<C>(sh);
+  if (warp == 12) tmem_dealloc(tmem, kTmem);
+  release_successor();
+}
+
+template <class C>
+cudaError_t launch_config(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t stream) {
+  static_assert(smem_bytes<C>() <= 227 * 1024, "");
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set[dev]) {
+    e = cudaFuncSetAttribute(draft_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<C>());
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev] = true;
+  }
+  return launch_after(draft_kernel<C>, dim3(k.l.ctas), kThreads, smem_bytes<C>(), stream, kmap, vmap, k);
+}
+
+cudaError_t launch_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t stream);
+cudaError_t launch_fp8(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& k, cudaStream_t stream);
+
+}  // namespace draft
+}  // namespace ci

@@ -75,6 +75,7 @@ int ci_attn_draft(const uint16_t* q, int64_t q_stride, int32_t rows, int32_t num
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16))
     return CI_ERR_ALIGN;
   const int64_t group = num_q_heads / num_kv_heads;
+  if (rows * group > INT32_MAX) return CI_ERR_RANGE;
   const int64_t each = (max_rows * group + 127) / 128 * num_req, all = (rows * group + 127) / 128 + num_req;
   if (num_kv_heads * (each < all ? each : all) > INT32_MAX / (static_cast<int64_t>(max_len) / 128 + 1)) return CI_ERR_RANGE;
   if (ws_bytes < ci::attn_draft_workspace_bytes(max_rows, num_q_heads, num_kv_heads, head_dim)) return CI_ERR_SHAPE;
