@@ -129,6 +129,30 @@ def test_attention_lengths(draft, lens, nodes, kind, fmt):
 
 
 @pytest.mark.parametrize("fmt", [BF16, FP8])
+@pytest.mark.parametrize("nodes", [3, 40])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 1), (128, 8, 1), (256, 7, 1)])
+def test_attention_many_tiles_per_cta(draft, d, hq, hkv, nodes, fmt):
+    """Long units and many of them: whole and split, with logits that grow along the cache; the same bits again."""
+    lens = [2000 + 37 * i for i in range(150)]
+    p = Drafted(lens, [nodes] * 150, hq, hkv, d, fmt, seed=d + nodes)
+    for r in (10, 20):  # keys that outgrow the reference again and again
+        for j in range(0, lens[r], 100):
+            page, slot = int(p.table[r, j // 64]), j % 64
+            t = int(p.starts[r])
+            if fmt == BF16:
+                k = p.k.view(torch.bfloat16).view(len(p.k), hkv, 64, d)
+                k[page, 0, slot] = (p.q[t, 0].float() * (0.3 + j / lens[r])).bfloat16()
+            else:
+                p.k[..., 64 * d:].view(torch.float32)[page, 0, slot] = 0.1 + 4 * j / lens[r]
+    out, lse = p.run(draft)
+    rows = {int(p.starts[r]) + i for r in (0, 1, 10, 20, 77, 120, 149) for i in {0, nodes - 1, nodes // 2}}
+    p.check(out, lse, rows=rows)
+    for _ in range(5):
+        again = p.run(draft)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8])
 @pytest.mark.parametrize("d,hq,hkv", [(128, 16, 2), (64, 6, 2), (256, 4, 1)])
 def test_attention_long_chain(draft, d, hq, hkv, fmt):
     """A prompt's chunk behind its prefix, and a prompt with none: sampled rows."""

@@ -93,7 +93,9 @@ struct Config {
 
 constexpr int kMaxSlots = 10;
 struct Shared {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];      // loaded slots
+  // Loaded slots.  bf16: those with values have barriers of their own: a role that waited for some phases of a barrier
+  // only, or that is not waited for by those that free the slot, would take one phase for another.
+  uint64_t full[kMaxSlots], v_full[kMaxSlots], empty[kMaxSlots];
   uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // what the products read: values looked over (bf16), operands (FP8)
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
   float stat[3][128];                // a stream's reference and sums, when two are put together
@@ -442,7 +444,7 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 #pragma unroll 1
         for (int x = 0; x < C::kParts; ++x, at.advance()) {
           if (!wait(&sh.empty[at.slot], at.phase ^ 1)) continue;
-          uint64_t* full = &sh.full[at.slot];
+          uint64_t* full = !C::kFp8 && v ? &sh.v_full[at.slot] : &sh.full[at.slot];
           // a lane per box: page lane / boxes of the slot, box lane % boxes; a lane per page's scales
           const int which = lane / C::kBoxes, box = lane % C::kBoxes;
           const int page = (kPages == 1 ? x : which) ? page1 : page0;
@@ -591,7 +593,7 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
   Waiter wait{sh, k.a.c.dev_err};
   Place<C::kLoads> at;
   Place<C::kFp8 ? C::kOps : 1> op;
-  uint32_t segments = 0, base = 0;
+  uint32_t segments = 0, base = 0, v_turn = 0;  // v_turn: parities of the slots' values
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
@@ -614,7 +616,10 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
           const uint32_t raw = b.load + at.slot * C::kRaw;
           const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys + x * C::kSlotKeys;
           if (!C::kFp8) {
-            if (v == 0 || !wait(&sh.full[at.slot], at.phase)) continue;
+            if (v == 0) continue;
+            const uint32_t turn = (v_turn >> at.slot) & 1;
+            v_turn ^= 1u << at.slot;
+            if (!wait(&sh.v_full[at.slot], turn)) continue;
             const uint32_t pages = sh.pages[(base + t) & 15];
             if (pages != 3 || pos0 + C::kSlotKeys > s.seen)
               prep_values<C>(sh, w, s, raw, pos0, pages, x, warp, lane, static_cast<int>(segments));
@@ -658,17 +663,21 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
   uint64_t* release = C::kFp8 ? sh.op_empty : sh.empty;
   Place<kRing> at;                  // of the next item
   int k_slot = 0, v_slot = 0;       // of the present tiles' first parts
-  uint32_t v_turn = 0;              // bf16: parities of the slots' values
+  uint32_t k_turn = 0, v_turn = 0;  // bf16: parities of the slots' keys and values
   uint32_t p_turn[2] = {0, 0};
   uint32_t segments = 0;
-  // Waits for the next item; false after giving up.
+  // Waits for the next item.
   auto arrived = [&](bool values) {
-    bool ok = wait(C::kFp8 ? &sh.ready[at.slot] : &sh.full[at.slot], at.phase);
-    if (!C::kFp8 && values) {
-      ok = ok && wait(&sh.ready[at.slot], (v_turn >> at.slot) & 1);
+    if (C::kFp8) {
+      wait(&sh.ready[at.slot], at.phase);
+    } else if (values) {
+      const uint32_t turn = (v_turn >> at.slot) & 1;
+      if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
       v_turn ^= 1u << at.slot;
+    } else {
+      wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
+      k_turn ^= 1u << at.slot;
     }
-    return ok;
   };
 #pragma unroll 1
   while (w.next(k)) {
@@ -911,6 +920,8 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
         tmem_st16(at + 16 * c, p);
       }
       tmem_st_wait();
+      // every phase is waited for in turn, as a wait tells only the present one from the one before
+      if (!first) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[buf]);
@@ -1007,7 +1018,8 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
 template <class C>
 __device__ __forceinline__ void drain_copies(Shared& sh) {
 #pragma unroll 1
-  for (int i = 0; i < 2 * C::kLoads; ++i) mbar_wait(&sh.full[i >> 1], i & 1, nullptr, 1000000ull);
+  for (int i = 0; i < 4 * C::kLoads; ++i)
+    mbar_wait(i & 1 ? &sh.v_full[i >> 2] : &sh.full[i >> 2], (i >> 1) & 1, nullptr, 1000000ull);
 }
 
 constexpr int kThreads = 512;
@@ -1029,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kLoads; ++i) {
       mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.empty[i], C::kFp8 ? kPrepWarps : 1);
       mbar_init(&sh.ready[i], kPrepWarps);
     }
