@@ -89,13 +89,11 @@ CI_API int ci_draft_plan(const int32_t* length, const int32_t* count, const int3
  * positions and sets CI_DEVERR_PAGE.
  *
  * Products are exact and accumulated in fp32; the softmax statistics are fp32;
- * the probabilities are rounded to bf16 for the product with the values and
- * divided by the sum of what they were rounded to (FP8: rounded with the
- * value's scale in them, divided by the sum of the unrounded ones); lse has the
- * sum of the unrounded ones; out is rounded once.  Results do not depend on the
- * order in which blocks run.  Any finite logits; values |v| <= 2^80; FP8:
- * scales finite, |scale| <= 2^60, and a NaN code (0x7F, 0xFF) reads as
- * +-480 * scale.
+ * the probabilities are rounded to bf16 for the product with the values (FP8:
+ * with the value's scale in them) and divided by the sum of the unrounded ones;
+ * out is rounded once.  Results do not depend on the order in which blocks run.
+ * Any finite logits; values |v| <= 2^80; FP8: scales finite, |scale| <= 2^60,
+ * and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *
  * max_len <= 64 * max_pages; max_rows >= 1: no request has more rows;
  * mask_words >= 1 (ignored for NULL).  rows * G < 2^31, and with B = min(num_req * ceil(max_rows *

@@ -98,7 +98,7 @@ struct Shared {
   uint64_t full[kMaxSlots], v_full[kMaxSlots], empty[kMaxSlots];
   uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // what the products read: values looked over (bf16), operands (FP8)
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
-  float stat[3][128];                // a stream's reference and sums, when two are put together
+  float stat[2][128];                // a stream's reference and sums, when two are put together
   uint32_t pages[16];                // of the last sixteen tiles: which of the two pages are there
   int32_t odd[4];                    // of the last four segments: the one where a value was not finite
   int64_t warp_sum[16];
@@ -389,6 +389,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 // Chunk `chunk` of 16 bytes of row p of an operand with `rows` rows.
 __device__ __forceinline__ uint32_t operand_offset(int rows, int p, int chunk) {
   return (chunk >> 3) * (rows * 128) + p * 128 + (((chunk & 7) ^ (p & 7)) << 4);
@@ -556,15 +564,6 @@ __device__ __forceinline__ uint2 widen_bf16(uint32_t r) {
   const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);  // bytes to the upper half of each 16 bits
   return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
 }
-// e4m3's NaN codes as the largest code's successor, 480, which f16 has.
-__device__ __forceinline__ uint2 widen_f16(uint32_t r) {
-  const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);
-  // the exponent and mantissa moved into an f16's are the value x 2^-8
-  const __half2 up = __float2half2_rn(256.f);
-  const uint32_t x = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u), y = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
-  const __half2 hx = __hmul2(*reinterpret_cast<const __half2*>(&x), up), hy = __hmul2(*reinterpret_cast<const __half2*>(&y), up);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&hx), *reinterpret_cast<const uint32_t*>(&hy));
-}
 // A raw slot into an operand: f16 of K, bf16 x 2^-120 of V.
 template <class C, bool kValues>
 __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int tid) {
@@ -578,7 +577,12 @@ __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int tid) {
     uint2 r[4];
     const uint32_t c[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = kValues ? widen_bf16(c[i]) : widen_f16(c[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (kValues)
+        r[i] = widen_bf16(c[i]);
+      else
+        attn::e4m3_to_f16(c[i], r[i].x, r[i].y);
+    }
     const uint4 first = make_uint4(r[0].x, r[0].y, r[1].x, r[1].y), second = make_uint4(r[2].x, r[2].y, r[3].x, r[3].y);
     // (lanes of the later half write the second chunk first: no two on the same banks)
     const bool swap = (u & 4) != 0;
@@ -664,7 +668,7 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
   Place<kRing> at;                  // of the next item
   int k_slot = 0, v_slot = 0;       // of the present tiles' first parts
   uint32_t k_turn = 0, v_turn = 0;  // bf16: parities of the slots' keys and values
-  uint32_t p_turn[2] = {0, 0};
+  uint32_t p_turn = 0;
   uint32_t segments = 0;
   // Waits for the next item.
   auto arrived = [&](bool values) {
@@ -715,8 +719,8 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
       if (i == 0) continue;
       const int p = i - 1, o = C::kTwo ? p & 1 : 0;
       const bool fresh = !s.two || (p & 1) == 0, last = !s.two || (p & 1) == 1;
-      wait(&sh.p_full[p & 1], p_turn[p & 1]);
-      p_turn[p & 1] ^= 1;
+      wait(&sh.p_full[p & 1], (p_turn >> (p & 1)) & 1);
+      p_turn ^= 1u << (p & 1);
       if (fresh) v_slot = at.slot;
       int slot = v_slot;
 #pragma unroll 1
@@ -787,12 +791,97 @@ __device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask
   }
 }
 
-// Two logits in base 2, rounded by themselves: the reference is one of them.
+// A row's 128 scores, 32 columns at a time, the next ones on their way.
+template <class F>
+__device__ __forceinline__ void over_scores(uint32_t at, F f) {
+  uint32_t x[2][32];
+  tmem_ld32(at, x[0]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld_wait();
+    if (c < 3) tmem_ld32(at + 32 * (c + 1), x[(c + 1) & 1]);
+    f(c, x[c & 1]);
+  }
+}
+// Two scores, times their keys' scales.
 template <class C>
-__device__ __forceinline__ float2 logits_of(uint32_t s0, uint32_t s1, float factor, float k0, float k1) {
-  float2 x = make_float2(__uint_as_float(s0), __uint_as_float(s1));
-  if (C::kFp8) x = mul2(x, make_float2(k0, k1));
-  return make_float2(__fmul_rn(x.x, factor), __fmul_rn(x.y, factor));
+__device__ __forceinline__ float2 scores_of(uint32_t s0, uint32_t s1, float k0, float k1) {
+  const float2 x = make_float2(__uint_as_float(s0), __uint_as_float(s1));
+  return C::kFp8 ? mul2(x, make_float2(k0, k1)) : x;
+}
+__device__ __forceinline__ bool bit(uint32_t bits, int j) { return (bits >> j) & 1; }
+
+// The row's largest logit (base 2) of a tile: of the scores, as rounding keeps their order.
+template <class C, bool kMasked>
+__device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[4], const float* ks, float factor) {
+  const bool down = factor < 0.f;
+  float top = down ? INFINITY : -INFINITY, other = top;
+  over_scores(at, [&](int c, const uint32_t (&x)[32]) {
+    const float none = down ? INFINITY : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
+      float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
+      if (kMasked) {
+        y.x = bit(bits[c], j) ? y.x : none, y.y = bit(bits[c], j + 1) ? y.y : none;
+        z.x = bit(bits[c], j + 2) ? z.x : none, z.y = bit(bits[c], j + 3) ? z.y : none;
+      }
+      if (down) {
+        top = fminf(top, fminf(y.x, y.y)), other = fminf(other, fminf(z.x, z.y));
+      } else {
+        top = fmaxf(top, fmaxf(y.x, y.y)), other = fmaxf(other, fmaxf(z.x, z.y));
+      }
+    }
+  });
+  top = down ? fminf(top, other) : fmaxf(top, other);
+  return kMasked && (top == INFINITY || top == -INFINITY) && factor == 0.f ? -INFINITY : top * factor;
+}
+
+// The row's probabilities of a tile, over its scores, and their sum.  kCareful:
+// masked, or logits that are rounded by themselves, as the reference is (a
+// product and a difference in one step are off by half of the reference's last
+// place, which only counts where logits pass 2^22).
+template <class C, bool kCareful>
+__device__ __forceinline__ void tile_probabilities(uint32_t at, const uint32_t (&bits)[4], const float* ks, const float* vs,
+                                                   float factor, float ref, float2& sum) {
+  const float2 less = make_float2(-ref, -ref), by = make_float2(factor, factor);
+  float2 other = make_float2(0.f, 0.f);
+  over_scores(at, [&](int c, const uint32_t (&x)[32]) {
+    uint32_t p[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
+      if (C::kFp8) {
+        f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
+        h = *reinterpret_cast<const float4*>(vs + 32 * c + j);
+      }
+      float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
+      if (kCareful) {
+        y = add2(make_float2(__fmul_rn(y.x, factor), __fmul_rn(y.y, factor)), less);
+        z = add2(make_float2(__fmul_rn(z.x, factor), __fmul_rn(z.y, factor)), less);
+      } else {
+        y = fma2(y, by, less), z = fma2(z, by, less);
+      }
+      y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+      z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+      if (kCareful) {
+        y.x = bit(bits[c], j) ? y.x : 0.f, y.y = bit(bits[c], j + 1) ? y.y : 0.f;
+        z.x = bit(bits[c], j + 2) ? z.x : 0.f, z.y = bit(bits[c], j + 3) ? z.y : 0.f;
+      }
+      sum = add2(sum, y), other = add2(other, z);
+      if (C::kFp8) {
+        y = mul2(y, make_float2(h.x, h.y)), z = mul2(z, make_float2(h.z, h.w));
+        if (kCareful) {  // (a scale that is not finite must not meet a 0)
+          y.x = bit(bits[c], j) ? y.x : 0.f, y.y = bit(bits[c], j + 1) ? y.y : 0.f;
+          z.x = bit(bits[c], j + 2) ? z.x : 0.f, z.y = bit(bits[c], j + 3) ? z.y : 0.f;
+        }
+      }
+      p[j / 2] = bf16x2(y.x, y.y), p[j / 2 + 1] = bf16x2(z.x, z.y);
+    }
+    tmem_st16(at + 16 * c, p);
+  });
+  sum = add2(sum, other);
 }
 
 template <class C>
@@ -802,7 +891,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), own = lanes + kColO + (C::kTwo ? g * C::D : 0);
   constexpr int kStride = C::kTwo ? 2 : 1;
   Waiter wait{sh, a.c.dev_err};
-  uint32_t turn[2] = {0, 0}, done = 0, base = 0, segment = 0;  // done: products with this stream's probabilities
+  uint32_t turn = 0, done = 0, base = 0, segment = 0;  // done: products with this stream's probabilities
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
@@ -816,13 +905,14 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     const int seen = C::kTwo && s.two && g == 1 && a.mask == nullptr && w.q.limit > 0
                          ? w.q.len + (s.row0 + 128) / k.l.group + 1 : s.seen;
     float factor = a.scale * attn::kLog2e, ref = -kFar;
-    float2 l = make_float2(0.f, 0.f), lr = l;
+    float2 l = make_float2(0.f, 0.f);
+    const bool busy = (s.two ? g * 128 : 0) + quad * 32 < s.rows;  // whether the warp has rows
 #pragma unroll 1
     for (int i = C::kTwo ? g : 0; i < s.steps; i += kStride) {
       const int buf = i & 1, t = s.two ? i >> 1 : i;
       const bool first = i < kStride;
-      wait(&sh.s_full[buf], turn[buf]);
-      turn[buf] ^= 1;
+      wait(&sh.s_full[buf], (turn >> buf) & 1);
+      turn ^= 1u << buf;
       tc_fence_after();
       if (C::kFp8 && first) factor = a.scale * attn::kLog2e * sc->factor[segment & 1][s.two ? g : 0][row];
       const uint32_t at = lanes + 128 * buf;
@@ -835,33 +925,14 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
 #pragma unroll
         for (int c = 0; c < 4; ++c) bits[c] = (pages >> (c >> 1)) & 1 ? seen_of(mask, pos0 + 32 * c) : 0;
       }
-      // ---- the tile's largest logit
       float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tmem_ld32(at + 32 * c, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-          if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
-          float2 y = logits_of<C>(x[j], x[j + 1], factor, f.x, f.y), z = logits_of<C>(x[j + 2], x[j + 3], factor, f.z, f.w);
-          if (masked) {
-            if (!((bits[c] >> j) & 1)) y.x = -INFINITY;
-            if (!((bits[c] >> (j + 1)) & 1)) y.y = -INFINITY;
-            if (!((bits[c] >> (j + 2)) & 1)) z.x = -INFINITY;
-            if (!((bits[c] >> (j + 3)) & 1)) z.y = -INFINITY;
-          }
-          top = fmaxf(top, fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
-        }
-      }
+      if (busy) top = masked ? tile_top<C, true>(at, bits, ks, factor) : tile_top<C, false>(at, bits, ks, factor);
       if (first) {
         ref = fmaxf(fminf(top, kFar), -kFar);
       } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
         const float up = fmaxf(ref, fminf(top, kFar)), by = exp2_approx(ref - up);
         ref = up;
-        l = mul2(l, make_float2(by, by)), lr = mul2(lr, make_float2(by, by));
+        l = mul2(l, make_float2(by, by));
         if (wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1)) {
           tc_fence_after();
 #pragma unroll 1
@@ -876,50 +947,13 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
           tmem_st_wait();
         }
       }
-      // ---- probabilities, over the scores
-      const float2 less = make_float2(-ref, -ref);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], p[16];
-        tmem_ld32(at + 32 * c, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
-          if (C::kFp8) {
-            f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
-            h = *reinterpret_cast<const float4*>(vs + 32 * c + j);
-          }
-          float2 y = add2(logits_of<C>(x[j], x[j + 1], factor, f.x, f.y), less);
-          float2 z = add2(logits_of<C>(x[j + 2], x[j + 3], factor, f.z, f.w), less);
-          y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-          if (masked) {
-            if (!((bits[c] >> j) & 1)) y.x = 0.f;
-            if (!((bits[c] >> (j + 1)) & 1)) y.y = 0.f;
-            if (!((bits[c] >> (j + 2)) & 1)) z.x = 0.f;
-            if (!((bits[c] >> (j + 3)) & 1)) z.y = 0.f;
-          }
-          l = add2(l, y), l = add2(l, z);
-          if (C::kFp8) {
-            y = mul2(y, make_float2(h.x, h.y)), z = mul2(z, make_float2(h.z, h.w));
-            if (masked) {  // (a scale that is not finite must not meet a 0)
-              if (!((bits[c] >> j) & 1)) y.x = 0.f;
-              if (!((bits[c] >> (j + 1)) & 1)) y.y = 0.f;
-              if (!((bits[c] >> (j + 2)) & 1)) z.x = 0.f;
-              if (!((bits[c] >> (j + 3)) & 1)) z.y = 0.f;
-            }
-          }
-          const uint32_t r0 = bf16x2(y.x, y.y), r1 = bf16x2(z.x, z.y);
-          if (!C::kFp8) {
-            lr = add2(lr, make_float2(bf16_lo(r0), bf16_hi(r0)));
-            lr = add2(lr, make_float2(bf16_lo(r1), bf16_hi(r1)));
-          }
-          p[j / 2] = r0, p[j / 2 + 1] = r1;
-        }
-        tmem_st16(at + 16 * c, p);
+      if (busy) {
+        if (masked || __any_sync(0xffffffffu, fabsf(ref) >= 4194304.f))
+          tile_probabilities<C, true>(at, bits, ks, vs, factor, ref, l);
+        else
+          tile_probabilities<C, false>(at, bits, ks, vs, factor, ref, l);
+        tmem_st_wait();
       }
-      tmem_st_wait();
       // every phase is waited for in turn, as a wait tells only the present one from the one before
       if (!first) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
       tc_fence_before();
@@ -932,38 +966,37 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     const int mine = s.two ? s.tiles : C::kTwo ? (s.steps + 1 - g) / 2 : s.steps;  // steps of this stream
     if (mine > 0) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
     tc_fence_after();
-    float total = l.x + l.y, rounded = C::kFp8 ? total : lr.x + lr.y;
+    float total = l.x + l.y;
     const bool joined = C::kTwo && !s.two;
     float fa = 1.f, fb = 0.f;
     int c0 = 0, c1 = C::D;
     if (joined) {  // both streams have the same rows: a half of the dims each
       float* stat = &sh.stat[0][row];
-      auto leave = [&]() { stat[0] = ref, stat[128] = total, stat[256] = rounded; };
-      float3 x = make_float3(ref, total, rounded);
+      auto leave = [&]() { stat[0] = ref, stat[128] = total; };
+      float2 x = make_float2(ref, total);
       if (g == 1) leave();
       tc_fence_before();
       named_sync(1, 256);
       tc_fence_after();
-      if (g == 0) x = make_float3(stat[0], stat[128], stat[256]), leave();
+      if (g == 0) x = make_float2(stat[0], stat[128]), leave();
       named_sync(1, 256);
-      if (g == 1) x = make_float3(stat[0], stat[128], stat[256]);
+      if (g == 1) x = make_float2(stat[0], stat[128]);
       const bool both = s.steps > 1;  // else the second one has nothing
       const float top = both ? fmaxf(ref, x.x) : g == 0 ? ref : x.x;
       const float f = both || g == 0 ? exp2_approx(ref - top) : 0.f, fx = both || g == 1 ? exp2_approx(x.x - top) : 0.f;
-      total = total * f + x.y * fx, rounded = rounded * f + x.z * fx;
+      total = total * f + x.y * fx;
       fa = g == 0 ? f : fx, fb = g == 0 ? fx : f;
       ref = top;
       c0 = g * (C::D / 2), c1 = c0 + C::D / 2;
     }
     const bool whole = w.i0 == 0 && w.i1 == w.tiles;
-    // whole: O / rounded; else O total / rounded, which the join divides by the sum of the totals
-    const float by = rounded == 0.f ? 0.f : (whole ? 1.f : total) / rounded * (C::kFp8 ? kTwo68 : 1.f);
+    const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (C::kFp8 ? kTwo68 : 1.f);  // O is 0 where the sum is
     const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0), qh = static_cast<int64_t>(w.head) * k.l.group + x0 - node * k.l.group;
     const int64_t t = w.q.first + node;
     const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
     const uint32_t from = C::kTwo && !joined ? own : lanes + kColO;
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
+    for (int c = busy ? c0 : c1; c < c1; c += 32) {
       uint32_t o[32];
       tmem_ld32(from + c, o);
       tmem_ld_wait();
@@ -976,7 +1009,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       }
       if (live) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = rounded == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * by);
+        for (int j = 0; j < 32; ++j) o[j] = total == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * by);
         if (odd) {
           uint32_t y[32];
 #pragma unroll
@@ -1063,12 +1096,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_range<kThreads>(k, sh);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // 512 x 128 registers at launch: 256 x 168 and 256 x 88
+  if (warp < 8)
+    regs_inc<160>();
+  else
+    regs_dec<96>();
   if ((mem & 1023u) != 0) {  // not by the launch's rules: nothing is read
     if (tid == 0) report(k.a.c.dev_err, kDevErrTimeout);
-  } else if (warp < 4) {
-    softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, 0);
   } else if (warp < 8) {
-    if (C::kTwo) softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, 1);
+    if (C::kTwo || warp < 4) softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, warp >> 2);
   } else if (warp < 12) {
     prepare<C>(k, sh, walk_of(k, sh), b);
   } else if (warp == 12) {
