@@ -210,6 +210,18 @@ def test_attention_ignores_what_is_not_seen(draft, d, kind, fmt):
         p.v = v
 
 
+@pytest.mark.parametrize("d,nodes", [(128, 2), (128, 7), (128, 16), (128, 40), (64, 3), (256, 3), (256, 20)])
+def test_attention_infinite_values_that_all_see(draft, d, nodes):
+    """An infinity in the cache gives that dim an infinity in every row, however many there are, and no NaN elsewhere."""
+    p = Drafted([700], [nodes], 8, 1, d, BF16, seed=nodes)
+    clean, lse = p.run(draft)
+    p.v.view(torch.bfloat16).view(len(p.v), 1, 64, d)[int(p.table[0, 4]), 0, 33, 7] = math.inf
+    out, again = p.run(draft)
+    rest = [x for x in range(d) if x != 7]
+    assert torch.isposinf(out[:, :, 7]).all() and torch.equal(out[:, :, rest], clean[:, :, rest])
+    assert torch.equal(lse, again)
+
+
 def test_attention_keys_that_are_not_finite(draft):
     """A NaN in a node's key reaches the rows that see it, and no other."""
     p = Drafted([100], [12], 4, 2, 128, BF16, "tree", seed=1)

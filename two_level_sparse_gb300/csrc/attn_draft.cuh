@@ -86,8 +86,9 @@ struct Config {
   static constexpr int kScales = kFp8 ? 2 * kSlotKeys * 4 : 0;  // with K: those of K and of V
   static constexpr int kRaw = kSlotKeys * kRow;           // of a loaded slot, without its scales
   // bf16: the loaded slots are the operands; FP8: loaded slots, and operands
-  static constexpr int kLoads = kFp8 ? (D == 64 ? 8 : 3) : (D == 64 ? 10 : 5);
+  static constexpr int kLoads = kFp8 ? (D == 64 ? 8 : 3) : (D == 64 ? 8 : 4);
   static constexpr int kOps = kFp8 ? (D == 64 ? 4 : 3) : 0;
+  static constexpr int kStreamThreads = kTwo ? 256 : 128;  // of the softmax
   static constexpr int kPageBytes = kFp8 ? 64 * D + 256 : 128 * D;
 };
 
@@ -98,7 +99,8 @@ struct Shared {
   uint64_t full[kMaxSlots], v_full[kMaxSlots], empty[kMaxSlots];
   uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // what the products read: values looked over (bf16), operands (FP8)
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
-  float stat[2][128];                // a stream's reference and sums, when two are put together
+  float ref[2][128], sums[2][128];  // the streams' references and sums, when they are put together
+  float fold[2][8][96];              // and eight dims of the copies of rows
   uint32_t pages[16];                // of the last sixteen tiles: which of the two pages are there
   int32_t odd[4];                    // of the last four segments: the one where a value was not finite
   int64_t warp_sum[16];
@@ -285,6 +287,7 @@ struct Segment {
   int block, rows;  // its block, and how many rows that has (0: nothing to do)
   int row0;         // its first row of the request's matrix
   bool two;         // two tiles of rows, over the same positions
+  int span;         // else rows are there 128 / span times, each copy for its own span positions of a tile
   int tiles, steps;
   int seen;         // positions that every row of the block sees
 };
@@ -295,6 +298,7 @@ __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
   s.row0 = s.block * C::kBlockRows;
   s.rows = s.block < w.q.blocks ? min(C::kBlockRows, w.q.n * k.l.group - s.row0) : 0;
   s.two = C::kTwo && s.rows > 128;
+  s.span = s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
   s.tiles = w.i1 - w.i0;
   s.steps = s.two ? 2 * s.tiles : s.tiles;
   s.seen = w.q.limit == 0 ? 0 : w.q.len + (k.a.mask != nullptr ? 0 : s.row0 / k.l.group + 1);
@@ -496,8 +500,8 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
   const int rows = s.two ? 256 : 128;
 #pragma unroll 4
   for (int m = tid / kChunks; m < rows; m += kRowsAtOnce) {
-    const int x = s.row0 + m, node = x / k.l.group;
-    const bool there = m < s.rows;
+    const int of = s.two ? m : m & (s.span - 1), x = s.row0 + of, node = x / k.l.group;
+    const bool there = of < s.rows;
     const uint16_t* src = k.a.q + (w.q.first + (there ? node : 0)) * k.a.q_stride +
                           (static_cast<int64_t>(w.head) * k.l.group + (there ? x - node * k.l.group : 0)) * C::D + chunk * 8;
     const uint32_t dst = b.q + (m >> 7) * C::kQ + operand_offset(128, m & 127, chunk);
@@ -527,33 +531,38 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
 }
 
 // Values of a slot that not every row of the block sees (positions from s.seen
-// on): zeros where there are none or where they are not finite, which is noted.
+// on; any, where rows are there more than once, as each copy has zeros for the
+// others' positions): zeros where there are none or where they are not finite,
+// which is noted.
 template <class C>
 __device__ __forceinline__ void prep_values(Shared& sh, const Walk& w, const Segment& s, uint32_t slot, int64_t pos0,
                                             uint32_t pages, int x, int warp, int lane, int segment) {
   constexpr int kChunks = C::D / 8, kPer = C::kSlotKeys / kPrepWarps;
+  const bool copies = !s.two && s.span < 128;
   bool odd = false;
-#pragma unroll 2
+#pragma unroll 4
   for (int e = lane; e < kPer * kChunks; e += 32) {
     const int p = warp * kPer + e / kChunks;
     const int64_t pos = pos0 + p;
     const bool page = (pages >> (C::kParts == 1 ? p / kPage : x)) & 1;
-    if (page && pos < s.seen) continue;
+    if (page && pos < s.seen && !copies) continue;
     const uint32_t at = slot + operand_offset(C::kSlotKeys, p, e % kChunks);
     if (!page || pos >= w.q.limit) {
       sts128(at, make_uint4(0, 0, 0, 0));
       continue;
     }
     const uint4 v = lds128(at);
-    uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    bool here = false;
+    uint32_t u[4] = {v.x, v.y, v.z, v.w}, any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) any |= ((u[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;  // an exponent of ones carries
+    if (any == 0) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if ((u[i] & 0x7F80u) == 0x7F80u) u[i] &= 0xFFFF0000u, here = true;
-      if ((u[i] & 0x7F800000u) == 0x7F800000u) u[i] &= 0xFFFFu, here = true;
+      if ((u[i] & 0x7F80u) == 0x7F80u) u[i] &= 0xFFFF0000u;
+      if ((u[i] & 0x7F800000u) == 0x7F800000u) u[i] &= 0xFFFFu;
     }
-    if (here) sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
-    odd |= here;
+    sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+    odd = true;
   }
   if (odd) sh.odd[segment & 3] = segment;
   fence_proxy_async_smem();
@@ -564,30 +573,39 @@ __device__ __forceinline__ uint2 widen_bf16(uint32_t r) {
   const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);  // bytes to the upper half of each 16 bits
   return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
 }
-// A raw slot into an operand: f16 of K, bf16 x 2^-120 of V.
+// A raw slot into an operand: f16 of K, bf16 x 2^-120 of V.  A warp takes 8
+// positions of 64 dims at a time, 16 codes per lane: eight neighbouring lanes have
+// positions q and q ^ 5, which the swizzles of both layouts put on different banks.
 template <class C, bool kValues>
-__device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int tid) {
-  constexpr int kUnits = C::D / 16;  // of 16 codes
-#pragma unroll 4
-  for (int e = tid; e < C::kSlotKeys * kUnits; e += 32 * kPrepWarps) {
-    const int p = e / kUnits, u = e % kUnits;
-    const uint32_t from = C::kBox == 128 ? (u >> 3) * (C::kSlotKeys * 128) + p * 128 + (((u & 7) ^ (p & 7)) << 4)
-                                         : p * 64 + ((u ^ ((p >> 1) & 3)) << 4);
-    const uint4 v = lds128(raw + from);
-    uint2 r[4];
-    const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int lane) {
+  constexpr int kBlocks = C::D / 64, kCount = C::kSlotKeys / 8 * kBlocks / kPrepWarps;
+  static_assert(kPrepWarps % kBlocks == 0, "");
+  const int u = lane & 3, p = (lane >> 3) ^ ((lane & 4) ? 5 : 0), block = warp % kBlocks;
+  raw += C::kBox == 128 ? (block >> 1) * (C::kSlotKeys * 128) + p * 128 + (((4 * (block & 1) + u) ^ p) << 4)
+                        : p * 64 + ((u ^ ((p >> 1) & 3)) << 4);
+  const uint32_t row = op + block * (C::kSlotKeys * 128) + p * 128;
+  const uint32_t op0 = row + (((2 * u) ^ p) << 4), op1 = row + (((2 * u + 1) ^ p) << 4);
+  const int first = warp / kBlocks;
+#pragma unroll
+  for (int j = 0; j < kCount; j += 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lds128(raw + (first + (j + i) * (kPrepWarps / kBlocks)) * (8 * C::kBox));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (kValues)
-        r[i] = widen_bf16(c[i]);
-      else
-        attn::e4m3_to_f16(c[i], r[i].x, r[i].y);
+      const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint2 r[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (kValues)
+          r[x] = widen_bf16(c[x]);
+        else
+          attn::e4m3_to_f16(c[x], r[x].x, r[x].y);
+      }
+      const uint32_t at = (first + (j + i) * (kPrepWarps / kBlocks)) * 1024;
+      sts128(op0 + at, make_uint4(r[0].x, r[0].y, r[1].x, r[1].y));
+      sts128(op1 + at, make_uint4(r[2].x, r[2].y, r[3].x, r[3].y));
     }
-    const uint4 first = make_uint4(r[0].x, r[0].y, r[1].x, r[1].y), second = make_uint4(r[2].x, r[2].y, r[3].x, r[3].y);
-    // (lanes of the later half write the second chunk first: no two on the same banks)
-    const bool swap = (u & 4) != 0;
-    sts128(op + operand_offset(C::kSlotKeys, p, 2 * u + swap), swap ? second : first);
-    sts128(op + operand_offset(C::kSlotKeys, p, 2 * u + !swap), swap ? first : second);
   }
 }
 
@@ -625,7 +643,7 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
             v_turn ^= 1u << at.slot;
             if (!wait(&sh.v_full[at.slot], turn)) continue;
             const uint32_t pages = sh.pages[(base + t) & 15];
-            if (pages != 3 || pos0 + C::kSlotKeys > s.seen)
+            if (pages != 3 || pos0 + C::kSlotKeys > s.seen || (!s.two && s.span < 128))
               prep_values<C>(sh, w, s, raw, pos0, pages, x, warp, lane, static_cast<int>(segments));
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.ready[at.slot]);
@@ -639,9 +657,9 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
             }
             const uint32_t dst = b.op + op.slot * C::kOperand;
             if (v)
-              widen<C, true>(raw, dst, tid);
+              widen<C, true>(raw, dst, warp, lane);
             else
-              widen<C, false>(raw, dst, tid);
+              widen<C, false>(raw, dst, warp, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -772,34 +790,42 @@ __device__ __forceinline__ uint32_t seen_of(const RowMask& m, int64_t pos) {
   return __funnelshift_r(mask_word(m, i), mask_word(m, i + 1), static_cast<int>(rel) & 31);
 }
 
-// What a row sees that is not finite, of 32 dims from d0 on: added as it is.
+// What a row sees that is not finite, of 32 dims from d0 on and positions from
+// `first` on: added as it is.
 template <class C>
-__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int d0, uint32_t (&o)[32]) {
+__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int64_t first, int d0, uint32_t (&o)[32]) {
   const CacheArgs& c = k.a.c;
-  const int64_t first = max(static_cast<int64_t>(w.i0) * kKeys, static_cast<int64_t>(w.q.len)), end = min(static_cast<int64_t>(w.i1) * kKeys, static_cast<int64_t>(w.q.limit));
+  const int64_t end = min(static_cast<int64_t>(w.i1) * kKeys, static_cast<int64_t>(w.q.limit));
 #pragma unroll 1
-  for (int64_t pos = first; pos < end; ++pos) {
+  for (int64_t pos = max(first, static_cast<int64_t>(w.i0) * kKeys); pos < end; ++pos) {
     if ((seen_of(m, pos) & 1) == 0) continue;
     const int page = c.page_table[static_cast<int64_t>(w.r) * c.max_pages + pos / kPage];
     if (page < 0 || page >= c.num_pages) continue;
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(
-                            c.v_pool + (static_cast<int64_t>(page) * c.num_kv_heads + w.head) * C::kPageBytes) +
-                        (pos & (kPage - 1)) * C::D + d0;
+    const uint4* v = reinterpret_cast<const uint4*>(
+        c.v_pool + (static_cast<int64_t>(page) * c.num_kv_heads + w.head) * C::kPageBytes + ((pos & (kPage - 1)) * C::D + d0) * 2);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if ((v[i] & 0x7F80) == 0x7F80) o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_lo(v[i]));
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = v[i];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t &lo = o[8 * i + 2 * j], &hi = o[8 * i + 2 * j + 1];
+        if ((u[j] & 0x7F80u) == 0x7F80u) lo = __float_as_uint(__uint_as_float(lo) + bf16_lo(u[j]));
+        if ((u[j] & 0x7F800000u) == 0x7F800000u) hi = __float_as_uint(__uint_as_float(hi) + bf16_hi(u[j]));
+      }
+    }
   }
 }
 
-// A row's 128 scores, 32 columns at a time, the next ones on their way.
-template <class F>
+// 32 N of a row's scores, 32 columns at a time, the next ones on their way.
+template <int N, class F>
 __device__ __forceinline__ void over_scores(uint32_t at, F f) {
   uint32_t x[2][32];
   tmem_ld32(at, x[0]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < N; ++c) {
     tmem_ld_wait();
-    if (c < 3) tmem_ld32(at + 32 * (c + 1), x[(c + 1) & 1]);
+    if (c < N - 1) tmem_ld32(at + 32 * (c + 1), x[(c + 1) & 1]);
     f(c, x[c & 1]);
   }
 }
@@ -812,11 +838,11 @@ __device__ __forceinline__ float2 scores_of(uint32_t s0, uint32_t s1, float k0, 
 __device__ __forceinline__ bool bit(uint32_t bits, int j) { return (bits >> j) & 1; }
 
 // The row's largest logit (base 2) of a tile: of the scores, as rounding keeps their order.
-template <class C, bool kMasked>
-__device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[4], const float* ks, float factor) {
+template <class C, bool kMasked, int N>
+__device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[N], const float* ks, float factor) {
   const bool down = factor < 0.f;
   float top = down ? INFINITY : -INFINITY, other = top;
-  over_scores(at, [&](int c, const uint32_t (&x)[32]) {
+  over_scores<N>(at, [&](int c, const uint32_t (&x)[32]) {
     const float none = down ? INFINITY : -INFINITY;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -842,12 +868,12 @@ __device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[4]
 // masked, or logits that are rounded by themselves, as the reference is (a
 // product and a difference in one step are off by half of the reference's last
 // place, which only counts where logits pass 2^22).
-template <class C, bool kCareful>
-__device__ __forceinline__ void tile_probabilities(uint32_t at, const uint32_t (&bits)[4], const float* ks, const float* vs,
+template <class C, bool kCareful, int N>
+__device__ __forceinline__ void tile_probabilities(uint32_t at, uint32_t to, const uint32_t (&bits)[N], const float* ks, const float* vs,
                                                    float factor, float ref, float2& sum) {
   const float2 less = make_float2(-ref, -ref), by = make_float2(factor, factor);
   float2 other = make_float2(0.f, 0.f);
-  over_scores(at, [&](int c, const uint32_t (&x)[32]) {
+  over_scores<N>(at, [&](int c, const uint32_t (&x)[32]) {
     uint32_t p[16];
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -879,9 +905,64 @@ __device__ __forceinline__ void tile_probabilities(uint32_t at, const uint32_t (
       }
       p[j / 2] = bf16x2(y.x, y.y), p[j / 2 + 1] = bf16x2(z.x, z.y);
     }
-    tmem_st16(at + 16 * c, p);
+    tmem_st16(to + 16 * c, p);
   });
   sum = add2(sum, other);
+}
+
+// A step of the softmax for a warp that has the 32 N columns of the buffer `at` from
+// 32 c0 on: reference, rescaling of O, probabilities; zeros in the other columns.
+struct Row {
+  float factor, ref;
+  float2 sum;
+};
+template <class C, int N>
+__device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const RowMask& mask, int64_t pos0, uint32_t pages,
+                                             int seen, const float* ks, const float* vs, uint32_t at, uint32_t own, int c0,
+                                             bool first, int g, uint32_t done, Row& r) {
+  const bool masked = pages != 3 || pos0 + kKeys > seen;
+  uint32_t bits[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) bits[c] = ~0u;
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) bits[c] = (pages >> ((c0 + c) >> 1)) & 1 ? seen_of(mask, pos0 + 32 * (c0 + c)) : 0;
+  }
+  const uint32_t scores = at + 32 * c0, to = at + 16 * c0;
+  if (C::kFp8) ks += 32 * c0, vs += 32 * c0;
+  const float top = masked ? tile_top<C, true, N>(scores, bits, ks, r.factor) : tile_top<C, false, N>(scores, bits, ks, r.factor);
+  if (first) {
+    r.ref = fmaxf(fminf(top, kFar), -kFar);
+  } else if (__any_sync(0xffffffffu, top > r.ref + kSlack)) {
+    const float up = fmaxf(r.ref, fminf(top, kFar)), by = exp2_approx(r.ref - up);
+    r.ref = up;
+    r.sum = mul2(r.sum, make_float2(by, by));
+    if (wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1)) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < C::D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(own + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+        tmem_st32(own + c, o);
+      }
+      tmem_st_wait();
+    }
+  }
+  if (masked || __any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f))
+    tile_probabilities<C, true, N>(scores, to, bits, ks, vs, r.factor, r.ref, r.sum);
+  else
+    tile_probabilities<C, false, N>(scores, to, bits, ks, vs, r.factor, r.ref, r.sum);
+  if (N < 4) {
+    uint32_t none[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) none[j] = 0;
+#pragma unroll
+    for (int c = N; c < 4; ++c) tmem_st16(at + 16 * ((c0 + c) & 3), none);
+  }
+  tmem_st_wait();
 }
 
 template <class C>
@@ -897,16 +978,17 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     const Segment s = segment_of<C>(k, w);
     if (s.rows == 0) continue;
     ++segment;
-    const int m0 = (s.two ? g * 128 : 0) + row;  // this thread's row of the block
-    const bool live = m0 < s.rows;
-    const int x0 = s.row0 + (live ? m0 : 0), node = x0 / k.l.group;
+    // this thread's row of the block, and its copy's first 32 columns of a tile
+    const int m0 = s.two ? g * 128 + row : row & (s.span - 1), c0 = s.two ? 0 : (row & ~(s.span - 1)) >> 5;
+    const bool live = m0 < s.rows && c0 == 0;
+    const int x0 = s.row0 + (m0 < s.rows ? m0 : 0), node = x0 / k.l.group;
     const RowMask mask{a.mask != nullptr ? a.mask + static_cast<int64_t>(w.q.first + node) * a.mask_words : nullptr,
                        node, w.q.n, w.q.len, w.q.limit, a.mask_words};
     const int seen = C::kTwo && s.two && g == 1 && a.mask == nullptr && w.q.limit > 0
                          ? w.q.len + (s.row0 + 128) / k.l.group + 1 : s.seen;
-    float factor = a.scale * attn::kLog2e, ref = -kFar;
-    float2 l = make_float2(0.f, 0.f);
-    const bool busy = (s.two ? g * 128 : 0) + quad * 32 < s.rows;  // whether the warp has rows
+    Row r{a.scale * attn::kLog2e, -kFar, make_float2(0.f, 0.f)};
+    const int span = s.two ? 128 : s.span;
+    const bool busy = (m0 & ~31) < s.rows;  // whether the warp has rows
 #pragma unroll 1
     for (int i = C::kTwo ? g : 0; i < s.steps; i += kStride) {
       const int buf = i & 1, t = s.two ? i >> 1 : i;
@@ -914,45 +996,18 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       wait(&sh.s_full[buf], (turn >> buf) & 1);
       turn ^= 1u << buf;
       tc_fence_after();
-      if (C::kFp8 && first) factor = a.scale * attn::kLog2e * sc->factor[segment & 1][s.two ? g : 0][row];
+      if (C::kFp8 && first) r.factor = a.scale * attn::kLog2e * sc->factor[segment & 1][s.two ? g : 0][row];
       const uint32_t at = lanes + 128 * buf;
       const uint32_t pages = sh.pages[(base + t) & 15];
       const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys;
       const float *ks = C::kFp8 ? sc->k[(base + t) & 3] : nullptr, *vs = C::kFp8 ? sc->v[(base + t) & 3] : nullptr;
-      const bool masked = pages != 3 || pos0 + kKeys > seen;
-      uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) bits[c] = (pages >> (c >> 1)) & 1 ? seen_of(mask, pos0 + 32 * c) : 0;
-      }
-      float top = -INFINITY;
-      if (busy) top = masked ? tile_top<C, true>(at, bits, ks, factor) : tile_top<C, false>(at, bits, ks, factor);
-      if (first) {
-        ref = fmaxf(fminf(top, kFar), -kFar);
-      } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-        const float up = fmaxf(ref, fminf(top, kFar)), by = exp2_approx(ref - up);
-        ref = up;
-        l = mul2(l, make_float2(by, by));
-        if (wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1)) {
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < C::D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(own + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-            tmem_st32(own + c, o);
-          }
-          tmem_st_wait();
-        }
-      }
-      if (busy) {
-        if (masked || __any_sync(0xffffffffu, fabsf(ref) >= 4194304.f))
-          tile_probabilities<C, true>(at, bits, ks, vs, factor, ref, l);
-        else
-          tile_probabilities<C, false>(at, bits, ks, vs, factor, ref, l);
-        tmem_st_wait();
+      if (!busy) {
+      } else if (span == 128) {
+        softmax_step<C, 4>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, 0, first, g, done, r);
+      } else if (span == 64) {
+        softmax_step<C, 2>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, first, g, done, r);
+      } else {
+        softmax_step<C, 1>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, first, g, done, r);
       }
       // every phase is waited for in turn, as a wait tells only the present one from the one before
       if (!first) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
@@ -966,46 +1021,65 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     const int mine = s.two ? s.tiles : C::kTwo ? (s.steps + 1 - g) / 2 : s.steps;  // steps of this stream
     if (mine > 0) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
     tc_fence_after();
-    float total = l.x + l.y;
-    const bool joined = C::kTwo && !s.two;
+    float ref = r.ref, total = r.sum.x + r.sum.y;
+    const bool both = C::kTwo && !s.two;  // both streams have the same rows
+    const bool joined = both || span < 128;
     float fa = 1.f, fb = 0.f;
-    int c0 = 0, c1 = C::D;
-    if (joined) {  // both streams have the same rows: a half of the dims each
-      float* stat = &sh.stat[0][row];
-      auto leave = [&]() { stat[0] = ref, stat[128] = total; };
-      float2 x = make_float2(ref, total);
-      if (g == 1) leave();
+    int d0 = 0, d1 = C::D;
+    if (joined) {
+      sh.ref[g][row] = ref, sh.sums[g][row] = total;
       tc_fence_before();
-      named_sync(1, 256);
+      named_sync(1, C::kStreamThreads);
       tc_fence_after();
-      if (g == 0) x = make_float2(stat[0], stat[128]), leave();
-      named_sync(1, 256);
-      if (g == 1) x = make_float2(stat[0], stat[128]);
-      const bool both = s.steps > 1;  // else the second one has nothing
-      const float top = both ? fmaxf(ref, x.x) : g == 0 ? ref : x.x;
-      const float f = both || g == 0 ? exp2_approx(ref - top) : 0.f, fx = both || g == 1 ? exp2_approx(x.x - top) : 0.f;
-      total = total * f + x.y * fx;
-      fa = g == 0 ? f : fx, fb = g == 0 ? fx : f;
+      const int streams = both && s.steps > 1 ? 2 : 1;  // (of one step the second stream has nothing)
+      float top = -kFar;
+      for (int x = 0; x < streams; ++x)
+        for (int y = row & (span - 1); y < 128; y += span) top = fmaxf(top, sh.ref[x][y]);
+      total = 0.f;
+      for (int x = 0; x < streams; ++x)
+        for (int y = row & (span - 1); y < 128; y += span) total += sh.sums[x][y] * exp2_approx(sh.ref[x][y] - top);
+      fa = exp2_approx(sh.ref[0][row] - top), fb = streams > 1 ? exp2_approx(sh.ref[1][row] - top) : 0.f;
       ref = top;
-      c0 = g * (C::D / 2), c1 = c0 + C::D / 2;
+      if (both) d0 = g * (C::D / 2), d1 = d0 + C::D / 2;  // a half of the dims each
     }
     const bool whole = w.i0 == 0 && w.i1 == w.tiles;
     const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (C::kFp8 ? kTwo68 : 1.f);  // O is 0 where the sum is
     const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0), qh = static_cast<int64_t>(w.head) * k.l.group + x0 - node * k.l.group;
     const int64_t t = w.q.first + node;
     const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
-    const uint32_t from = C::kTwo && !joined ? own : lanes + kColO;
+    const uint32_t from = both ? lanes + kColO : own;
 #pragma unroll 1
-    for (int c = busy ? c0 : c1; c < c1; c += 32) {
+    for (int c = busy ? d0 : d1; c < d1; c += 32) {
       uint32_t o[32];
       tmem_ld32(from + c, o);
       tmem_ld_wait();
-      if (joined && s.steps > 1) {
+      if (joined) {
         uint32_t y[32];
-        tmem_ld32(from + C::D + c, y);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = 0;
+        if (both && s.steps > 1) tmem_ld32(from + C::D + c, y);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fa + __uint_as_float(y[j]) * fb);
+      }
+      if (span < 128) {  // the copies' sums, eight dims at a time (all of the stream's warps are busy)
+#pragma unroll
+        for (int j0 = 0; j0 < 32; j0 += 8) {
+          if (c0 != 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sh.fold[g][j][row - span] = __uint_as_float(o[j0 + j]);
+          }
+          named_sync(2 + g, 128);
+          if (c0 == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float v = __uint_as_float(o[j0 + j]);
+              for (int y = row; y < 128 - span; y += span) v += sh.fold[g][j][y];
+              o[j0 + j] = __float_as_uint(v);
+            }
+          }
+          named_sync(2 + g, 128);
+        }
       }
       if (live) {
 #pragma unroll
@@ -1014,7 +1088,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
           uint32_t y[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) y[j] = o[j];
-          add_odd<C>(k, w, mask, c, y);
+          add_odd<C>(k, w, mask, span < 128 ? 0 : w.q.len, c, y);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = y[j];
         }
@@ -1034,7 +1108,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       __syncwarp();
     }
     tc_fence_before();
-    if (live && c0 == 0) {
+    if (live && d0 == 0) {
       if (!whole)
         *reinterpret_cast<float2*>(k.stat + (slot * C::kBlockRows + m0) * 2) = make_float2(ref, total);
       else if (a.lse != nullptr)
@@ -1042,7 +1116,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     }
     if (!whole && w.i0 == 0 && g == 0 && row == 0)  // (the segment ends where the range does)
       k.part[blockIdx.x] = Part{w.r, w.head, s.block, team_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.teams)};
-    if (joined) named_sync(1, 256);  // both have read both sums
+    if (joined) named_sync(1, C::kStreamThreads);  // all have read the sums
   }
 }
 
