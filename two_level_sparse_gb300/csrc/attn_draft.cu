@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o[j] * inv));
     if (k.a.lse != nullptr && lane == 0)
-      k.a.lse[t * k.a.c.num_q_heads + qh] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+      k.a.lse[t * k.a.c.num_q_heads + qh] = l == 0.f ? -INFINITY : (top - (k.a.c.fp8 ? draft::kLift : 0.f) + log2f(l)) * 0.6931471805599453f;
   }
 }
 

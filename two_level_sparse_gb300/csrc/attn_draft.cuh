@@ -32,12 +32,15 @@
 // infinities: in those tiles everything that is not finite becomes 0 in shared
 // memory before the product, and at the end the rows that do see it add it.
 //
-// FP8 pages.  K widens to f16 and V to bf16 (x 2^-120) on the way from a ring of
-// raw tiles to the operands; the query becomes f16 after each row is scaled by a
-// power of two to a largest magnitude in [2^14, 2^15) (what it loses lies 2^-39
-// below that).  A position's scales join its logit and its probability.
+// FP8 pages.  Keys are multiplied as they are: the query, each row scaled by a
+// power of two to a largest magnitude in [2^7, 2^8), is the sum of two e4m3
+// numbers, exactly where an element is no smaller than 2^-10 of the row's largest,
+// else to 2^-18 of it.  Values widen to bf16 (x 2^-120) on the way from a ring of
+// raw tiles to the operands.  A position's scales join its logit and its
+// probability.
 #pragma once
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "attn.cuh"
 #include "draft_internal.h"
@@ -52,7 +55,8 @@ constexpr int kKeys = 128;               // positions of a tile
 constexpr float kFar = 3.0e38f;          // references lie in [-kFar, kFar]
 constexpr float kSlack = 8.f;            // a logit over its reference
 constexpr int kTmem = 512, kColO = 256;  // score buffers at columns 0 and 128, then O
-constexpr float kTwo52 = 4503599627370496.f, kTwo68 = 295147905179352825856.f;
+// FP8: probabilities carry 2^52, so that with values of 2^-120 O is no smaller than the values by more than 2^-68
+constexpr float kLift = 52.f, kTwo120 = 1329227995784915872903807060280344576.f;
 
 struct Part {  // the unit that goes on past the end of a CTA's range; last < 0: none
   int32_t req, head, block, last;
@@ -83,21 +87,20 @@ struct Config {
   static constexpr int kRow = kFp8 ? D : 2 * D;           // of a cached position
   static constexpr int kBox = kRow < 128 ? kRow : 128;
   static constexpr int kBoxes = kRow / kBox;
-  static constexpr int kScales = kFp8 ? 2 * kSlotKeys * 4 : 0;  // with K: those of K and of V
-  static constexpr int kRaw = kSlotKeys * kRow;           // of a loaded slot, without its scales
-  // bf16: the loaded slots are the operands; FP8: loaded slots, and operands
-  static constexpr int kLoads = kFp8 ? (D == 64 ? 8 : 3) : (D == 64 ? 8 : 4);
-  static constexpr int kOps = kFp8 ? (D == 64 ? 4 : 3) : 0;
+  static constexpr int kRaw = kSlotKeys * kRow;           // of a loaded slot
+  // K is read from the loaded slots, and so is V in bf16; FP8: V from operand slots
+  static constexpr int kLoads = kFp8 ? (D == 64 ? 10 : 5) : (D == 64 ? 8 : 4);
+  static constexpr int kOps = kFp8 ? (D == 64 ? 4 : 2) : 0;
   static constexpr int kStreamThreads = kTwo ? 256 : 128;  // of the softmax
   static constexpr int kPageBytes = kFp8 ? 64 * D + 256 : 128 * D;
 };
 
 constexpr int kMaxSlots = 10;
 struct Shared {
-  // Loaded slots.  bf16: those with values have barriers of their own: a role that waited for some phases of a barrier
-  // only, or that is not waited for by those that free the slot, would take one phase for another.
+  // Loaded slots, with barriers of their own for keys and values: a role that waited for some phases of a barrier only,
+  // or that is not waited for by those that free the slot, would take one phase for another.
   uint64_t full[kMaxSlots], v_full[kMaxSlots], empty[kMaxSlots];
-  uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // what the products read: values looked over (bf16), operands (FP8)
+  uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // values looked over (bf16), operands (FP8)
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
   float ref[2][128], sums[2][128];  // the streams' references and sums, when they are put together
   float fold[2][8][96];              // and eight dims of the copies of rows
@@ -110,13 +113,13 @@ struct Shared {
   int32_t abort;
 };
 struct Scales {  // FP8
-  alignas(16) float k[4][kKeys], v[4][kKeys];  // of the last four tiles
+  alignas(16) float k[8][kKeys], v[8][kKeys];  // of the last eight tiles
   float factor[2][2][128];                     // of the last two segments: what the rows of Q were divided by
 };
 
 template <class C>
 constexpr int smem_bytes() {
-  return C::kTiles * C::kQ + C::kLoads * (C::kRaw + C::kScales) + C::kOps * C::kOperand +
+  return C::kTiles * C::kQ + C::kLoads * C::kRaw + C::kOps * C::kOperand +
          (C::kFp8 ? static_cast<int>(sizeof(Scales)) : 0) + static_cast<int>(sizeof(Shared));
 }
 
@@ -333,7 +336,11 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t next) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((next >> 4) & 0x3FFFu) << 16 |
          static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
 }
-// Instruction descriptor: M = 128, fp32 sums; bf16 or f16 operands, B MN-major or not.
+// Rows of 64 bytes (64 e4m3 dims), 64-byte swizzle; K-major.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr, int row_bytes) {
+  return row_bytes == 64 ? sdesc_k64_sw64(addr) : desc128(addr, 16);
+}
+// Instruction descriptor: M = 128, fp32 sums; bf16 or e4m3 operands, B MN-major or not.
 __host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          ((128u >> 4) << 24);
@@ -342,6 +349,13 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
   asm volatile(
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(accumulate)
       : "memory");
 }
@@ -401,14 +415,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 // Chunk `chunk` of 16 bytes of row p of an operand with `rows` rows.
 __device__ __forceinline__ uint32_t operand_offset(int rows, int p, int chunk) {
   return (chunk >> 3) * (rows * 128) + p * 128 + (((chunk & 7) ^ (p & 7)) << 4);
 }
 
 struct Buffers {
-  uint32_t q, load, op, scales;  // shared-memory addresses; scales: of the loaded slots
-  Scales* sc;                    // FP8
+  uint32_t q, load, op;  // shared-memory addresses
+  Scales* sc;            // FP8
 };
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -456,7 +473,7 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 #pragma unroll 1
         for (int x = 0; x < C::kParts; ++x, at.advance()) {
           if (!wait(&sh.empty[at.slot], at.phase ^ 1)) continue;
-          uint64_t* full = !C::kFp8 && v ? &sh.v_full[at.slot] : &sh.full[at.slot];
+          uint64_t* full = v ? &sh.v_full[at.slot] : &sh.full[at.slot];
           // a lane per box: page lane / boxes of the slot, box lane % boxes; a lane per page's scales
           const int which = lane / C::kBoxes, box = lane % C::kBoxes;
           const int page = (kPages == 1 ? x : which) ? page1 : page0;
@@ -469,15 +486,17 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
               mbar_arrive(full);
           }
           __syncwarp();
-          const uint32_t dst = b.load + at.slot * C::kRaw, scales = b.scales + at.slot * C::kScales;
+          const uint32_t dst = b.load + at.slot * C::kRaw;
           if (which < kPages && page >= 0) {
             const int row = page * c.num_kv_heads + w.head;
             attn::tma_box(dst + box * (C::kSlotKeys * C::kBox) + which * (kPage * C::kBox), v ? vmap : kmap, box * 128,
                           row * kPerPage, smem_u32(full));
             if (C::kFp8 && v == 0 && box == 0) {
+              // (the tile's eighth predecessor has been read: its slots have been filled again since)
               const int64_t from = static_cast<int64_t>(row) * C::kPageBytes + kPage * C::D;
-              attn::bulk_load(scales + which * 256, c.k_pool + from, 256, smem_u32(full));
-              attn::bulk_load(scales + C::kSlotKeys * 4 + which * 256, c.v_pool + from, 256, smem_u32(full));
+              const int first = x * C::kSlotKeys + which * kPage;
+              attn::bulk_load(smem_u32(&b.sc->k[(base + t) & 7][first]), c.k_pool + from, 256, smem_u32(full));
+              attn::bulk_load(smem_u32(&b.sc->v[(base + t) & 7][first]), c.v_pool + from, 256, smem_u32(full));
             }
           }
         }
@@ -490,8 +509,9 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 // ------------------------------------------------------------------ preparation
 constexpr int kPrepWarps = 4;
 
-// A tile of the rows of Q: row m of the request's matrix is node m / G.  FP8: in
-// f16, each row scaled by a power of two, 1 / factor.
+// The rows of Q: row m of the request's matrix is node m / G.  FP8: each row
+// scaled by a power of two, 1 / factor, and split into two e4m3 numbers per
+// element, one tile of each.
 template <class C>
 __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const Segment& s, const Buffers& b,
                                              float (*factor)[128], int tid) {
@@ -504,9 +524,10 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
     const bool there = of < s.rows;
     const uint16_t* src = k.a.q + (w.q.first + (there ? node : 0)) * k.a.q_stride +
                           (static_cast<int64_t>(w.head) * k.l.group + (there ? x - node * k.l.group : 0)) * C::D + chunk * 8;
-    const uint32_t dst = b.q + (m >> 7) * C::kQ + operand_offset(128, m & 127, chunk);
+    const int row = m & 127;
+    const uint32_t tile = b.q + (m >> 7) * C::kQ;
     if (!C::kFp8) {
-      attn::copy16(dst, reinterpret_cast<const uint8_t*>(src), there);
+      attn::copy16(tile + operand_offset(128, row, chunk), reinterpret_cast<const uint8_t*>(src), there);
       continue;
     }
     uint4 v = make_uint4(0, 0, 0, 0);
@@ -518,13 +539,25 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
 #pragma unroll
     for (int o = 1; o < kChunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = static_cast<int>(top >> 7);  // biased; 255: not finite
-    const int up = e == 255 || top == 0 ? 0 : min(14 - (e - 127), 126);
-    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -113 <= up <= 126
-    uint32_t h[4];
+    const int up = e == 255 || top == 0 ? 0 : min(7 - (e - 127), 126);
+    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -120 <= up <= 126
+    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = attn::f16x2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
-    sts128(dst, make_uint4(h[0], h[1], h[2], h[3]));
-    if (chunk == 0) factor[m >> 7][m & 127] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = make_float2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
+      uint32_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+      const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3)));
+      const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E4M3);
+      if (e == 255) h = 0x7F7F;  // a row that is not finite: NaN
+      hi[i >> 1] |= h << (16 * (i & 1)), lo[i >> 1] |= l << (16 * (i & 1));
+    }
+    const int c16 = chunk >> 1;
+    const uint32_t at = tile + (chunk & 1) * 8 +
+                        (C::D == 64 ? row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4)
+                                    : (c16 >> 3) * (128 * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+    sts64(at, hi[0], hi[1]);
+    sts64(at + 128 * C::D, lo[0], lo[1]);
+    if (chunk == 0) factor[m >> 7][row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
   }
   if (!C::kFp8) wait_copies();
   fence_proxy_async_smem();
@@ -573,10 +606,10 @@ __device__ __forceinline__ uint2 widen_bf16(uint32_t r) {
   const uint32_t a = __byte_perm(r, 0, 0x1404), b = __byte_perm(r, 0, 0x3424);  // bytes to the upper half of each 16 bits
   return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
 }
-// A raw slot into an operand: f16 of K, bf16 x 2^-120 of V.  A warp takes 8
+// A raw slot of V into an operand, bf16 x 2^-120.  A warp takes 8
 // positions of 64 dims at a time, 16 codes per lane: eight neighbouring lanes have
 // positions q and q ^ 5, which the swizzles of both layouts put on different banks.
-template <class C, bool kValues>
+template <class C>
 __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int lane) {
   constexpr int kBlocks = C::D / 64, kCount = C::kSlotKeys / 8 * kBlocks / kPrepWarps;
   static_assert(kPrepWarps % kBlocks == 0, "");
@@ -596,12 +629,7 @@ __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int l
       const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       uint2 r[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (kValues)
-          r[x] = widen_bf16(c[x]);
-        else
-          attn::e4m3_to_f16(c[x], r[x].x, r[x].y);
-      }
+      for (int x = 0; x < 4; ++x) r[x] = widen_bf16(c[x]);
       const uint32_t at = (first + (j + i) * (kPrepWarps / kBlocks)) * 1024;
       sts128(op0 + at, make_uint4(r[0].x, r[0].y, r[1].x, r[1].y));
       sts128(op1 + at, make_uint4(r[2].x, r[2].y, r[3].x, r[3].y));
@@ -637,10 +665,10 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
         for (int x = 0; x < C::kParts; ++x, at.advance()) {
           const uint32_t raw = b.load + at.slot * C::kRaw;
           const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys + x * C::kSlotKeys;
+          if (v == 0) continue;
+          const uint32_t turn = (v_turn >> at.slot) & 1;
+          v_turn ^= 1u << at.slot;
           if (!C::kFp8) {
-            if (v == 0) continue;
-            const uint32_t turn = (v_turn >> at.slot) & 1;
-            v_turn ^= 1u << at.slot;
             if (!wait(&sh.v_full[at.slot], turn)) continue;
             const uint32_t pages = sh.pages[(base + t) & 15];
             if (pages != 3 || pos0 + C::kSlotKeys > s.seen || (!s.two && s.span < 128))
@@ -649,17 +677,8 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
             if (lane == 0) mbar_arrive(&sh.ready[at.slot]);
             continue;
           }
-          if (wait(&sh.full[at.slot], at.phase) && wait(&sh.op_empty[op.slot], op.phase ^ 1)) {
-            if (v == 0 && tid < C::kSlotKeys) {
-              const uint32_t from = b.scales + at.slot * C::kScales + tid * 4;
-              b.sc->k[(base + t) & 3][x * C::kSlotKeys + tid] = lds_f32(from);
-              b.sc->v[(base + t) & 3][x * C::kSlotKeys + tid] = lds_f32(from + C::kSlotKeys * 4) * kTwo52;
-            }
-            const uint32_t dst = b.op + op.slot * C::kOperand;
-            if (v)
-              widen<C, true>(raw, dst, warp, lane);
-            else
-              widen<C, false>(raw, dst, warp, lane);
+          if (wait(&sh.v_full[at.slot], turn) && wait(&sh.op_empty[op.slot], op.phase ^ 1)) {
+            widen<C>(raw, b.op + op.slot * C::kOperand, warp, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -678,29 +697,13 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
 // ------------------------------------------------------------------ products
 template <class C>
 __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, const Buffers& b, uint32_t tmem) {
-  constexpr int kRing = C::kFp8 ? C::kOps : C::kLoads;
   constexpr uint32_t kIdQ = idesc(C::kSlotKeys, !C::kFp8, false), kIdP = idesc(C::D, true, true);
   Waiter wait{sh, k.a.c.dev_err};
-  const uint32_t ring = C::kFp8 ? b.op : b.load;
-  uint64_t* release = C::kFp8 ? sh.op_empty : sh.empty;
-  Place<kRing> at;                  // of the next item
+  Place<C::kLoads> at;              // of the next item
+  Place<C::kFp8 ? C::kOps : 1> op;  // FP8: of the next values
   int k_slot = 0, v_slot = 0;       // of the present tiles' first parts
-  uint32_t k_turn = 0, v_turn = 0;  // bf16: parities of the slots' keys and values
-  uint32_t p_turn = 0;
-  uint32_t segments = 0;
-  // Waits for the next item.
-  auto arrived = [&](bool values) {
-    if (C::kFp8) {
-      wait(&sh.ready[at.slot], at.phase);
-    } else if (values) {
-      const uint32_t turn = (v_turn >> at.slot) & 1;
-      if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
-      v_turn ^= 1u << at.slot;
-    } else {
-      wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
-      k_turn ^= 1u << at.slot;
-    }
-  };
+  uint32_t k_turn = 0, v_turn = 0;  // parities of the slots' keys and values
+  uint32_t p_turn = 0, segments = 0;
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
@@ -716,18 +719,30 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
         int slot = k_slot;
 #pragma unroll 1
         for (int x = 0; x < C::kParts; ++x) {
-          if (fresh) arrived(false);
+          if (fresh) {
+            wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
+            k_turn ^= 1u << at.slot;
+          }
           if (wait.alive) {
             tc_fence_after();
-            const uint64_t da = desc128(q, 16), db = desc128(ring + slot * C::kOperand, 16);
+            constexpr int kBytes = C::kRow < 128 ? C::kRow : 128;  // of an operand's rows; 32 of them per product
+            const uint64_t da = desc_rows(q, kBytes), db = desc_rows(b.load + slot * C::kRaw, kBytes);
+            const uint32_t d = tmem + 128 * (i & 1) + x * C::kSlotKeys;
 #pragma unroll
-            for (int e = 0; e < C::D / 16; ++e)
-              mma_ss(tmem + 128 * (i & 1) + x * C::kSlotKeys, da + (e >> 2) * (128 * 128 / 16) + (e & 3) * 2,
-                     db + (e >> 2) * (C::kSlotKeys * 128 / 16) + (e & 3) * 2, kIdQ, e > 0);
-            if (last) mma_commit_elect(&release[slot]);
+            for (int e = 0; e < C::kRow / 32; ++e) {
+              const uint64_t ea = da + (e >> 2) * (128 * 128 / 16) + (e & 3) * 2, eb = db + (e >> 2) * (C::kSlotKeys * 128 / 16) + (e & 3) * 2;
+              if (C::kFp8) {
+                mma_f8(d, ea, eb, kIdQ, e > 0);
+                mma_f8(d, ea + 128 * C::D / 16, eb, kIdQ, 1);
+              } else {
+                mma_ss(d, ea, eb, kIdQ, e > 0);
+              }
+            }
+            if (last)
+              for (int y = 0; y < (C::kFp8 ? kPrepWarps : 1); ++y) mma_commit_elect(&sh.empty[slot]);
           }
           if (fresh) at.advance();
-          if (++slot == kRing) slot = 0;
+          if (++slot == C::kLoads) slot = 0;
         }
         if (wait.alive) {
           mma_commit_elect(&sh.s_full[i & 1]);
@@ -739,22 +754,28 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
       const bool fresh = !s.two || (p & 1) == 0, last = !s.two || (p & 1) == 1;
       wait(&sh.p_full[p & 1], (p_turn >> (p & 1)) & 1);
       p_turn ^= 1u << (p & 1);
-      if (fresh) v_slot = at.slot;
+      if (fresh) v_slot = C::kFp8 ? op.slot : at.slot;
       int slot = v_slot;
 #pragma unroll 1
       for (int x = 0; x < C::kParts; ++x) {
-        if (fresh) arrived(true);
+        if (fresh && C::kFp8) {
+          wait(&sh.ready[op.slot], op.phase);
+        } else if (fresh) {
+          const uint32_t turn = (v_turn >> at.slot) & 1;
+          if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
+          v_turn ^= 1u << at.slot;
+        }
         if (wait.alive) {
           tc_fence_after();
-          const uint64_t db = desc128(ring + slot * C::kOperand, C::kSlotKeys * 128);
+          const uint64_t db = desc128(C::kFp8 ? b.op + slot * C::kOperand : b.load + slot * C::kRaw, C::kSlotKeys * 128);
 #pragma unroll
           for (int e = 0; e < C::kSlotKeys / 16; ++e)
             mma_ts(tmem + kColO + o * C::D, tmem + 128 * (p & 1) + x * (C::kSlotKeys / 2) + e * 8, db + e * 128, kIdP,
                    x > 0 || e > 0 || p >= (C::kTwo ? 2 : 1));
-          if (last) mma_commit_elect(&release[slot]);
+          if (last) mma_commit_elect(C::kFp8 ? &sh.op_empty[slot] : &sh.empty[slot]);
         }
-        if (fresh) at.advance();
-        if (++slot == kRing) slot = 0;
+        if (fresh) at.advance(), op.advance();
+        if (++slot == (C::kFp8 ? C::kOps : C::kLoads)) slot = 0;
       }
       if (wait.alive) mma_commit_elect(&sh.pv_done[o]);
     }
@@ -871,7 +892,8 @@ __device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[N]
 template <class C, bool kCareful, int N>
 __device__ __forceinline__ void tile_probabilities(uint32_t at, uint32_t to, const uint32_t (&bits)[N], const float* ks, const float* vs,
                                                    float factor, float ref, float2& sum) {
-  const float2 less = make_float2(-ref, -ref), by = make_float2(factor, factor);
+  const float up = C::kFp8 ? kLift - ref : -ref;
+  const float2 less = make_float2(up, up), by = make_float2(factor, factor);
   float2 other = make_float2(0.f, 0.f);
   over_scores<N>(at, [&](int c, const uint32_t (&x)[32]) {
     uint32_t p[16];
@@ -884,8 +906,9 @@ __device__ __forceinline__ void tile_probabilities(uint32_t at, uint32_t to, con
       }
       float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
       if (kCareful) {
-        y = add2(make_float2(__fmul_rn(y.x, factor), __fmul_rn(y.y, factor)), less);
-        z = add2(make_float2(__fmul_rn(z.x, factor), __fmul_rn(z.y, factor)), less);
+        y = add2(make_float2(__fmul_rn(y.x, factor), __fmul_rn(y.y, factor)), make_float2(-ref, -ref));
+        z = add2(make_float2(__fmul_rn(z.x, factor), __fmul_rn(z.y, factor)), make_float2(-ref, -ref));
+        if (C::kFp8) y = add2(y, make_float2(kLift, kLift)), z = add2(z, make_float2(kLift, kLift));
       } else {
         y = fma2(y, by, less), z = fma2(z, by, less);
       }
@@ -930,7 +953,8 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
   }
   const uint32_t scores = at + 32 * c0, to = at + 16 * c0;
   if (C::kFp8) ks += 32 * c0, vs += 32 * c0;
-  const float top = masked ? tile_top<C, true, N>(scores, bits, ks, r.factor) : tile_top<C, false, N>(scores, bits, ks, r.factor);
+  float top = masked ? tile_top<C, true, N>(scores, bits, ks, r.factor) : tile_top<C, false, N>(scores, bits, ks, r.factor);
+  if (C::kFp8) top = ceilf(top);  // so that kLift less a reference is exact
   if (first) {
     r.ref = fmaxf(fminf(top, kFar), -kFar);
   } else if (__any_sync(0xffffffffu, top > r.ref + kSlack)) {
@@ -1000,7 +1024,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       const uint32_t at = lanes + 128 * buf;
       const uint32_t pages = sh.pages[(base + t) & 15];
       const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys;
-      const float *ks = C::kFp8 ? sc->k[(base + t) & 3] : nullptr, *vs = C::kFp8 ? sc->v[(base + t) & 3] : nullptr;
+      const float *ks = C::kFp8 ? sc->k[(base + t) & 7] : nullptr, *vs = C::kFp8 ? sc->v[(base + t) & 7] : nullptr;
       if (!busy) {
       } else if (span == 128) {
         softmax_step<C, 4>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, 0, first, g, done, r);
@@ -1043,7 +1067,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       if (both) d0 = g * (C::D / 2), d1 = d0 + C::D / 2;  // a half of the dims each
     }
     const bool whole = w.i0 == 0 && w.i1 == w.tiles;
-    const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (C::kFp8 ? kTwo68 : 1.f);  // O is 0 where the sum is
+    const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (C::kFp8 ? kTwo120 : 1.f);  // O is 0 where the sum is
     const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0), qh = static_cast<int64_t>(w.head) * k.l.group + x0 - node * k.l.group;
     const int64_t t = w.q.first + node;
     const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
@@ -1112,7 +1136,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       if (!whole)
         *reinterpret_cast<float2*>(k.stat + (slot * C::kBlockRows + m0) * 2) = make_float2(ref, total);
       else if (a.lse != nullptr)
-        a.lse[t * a.c.num_q_heads + qh] = total == 0.f ? -INFINITY : (ref + log2f(total)) * 0.6931471805599453f;
+        a.lse[t * a.c.num_q_heads + qh] = total == 0.f ? -INFINITY : (ref - (C::kFp8 ? kLift : 0.f) + log2f(total)) * 0.6931471805599453f;
     }
     if (!whole && w.i0 == 0 && g == 0 && row == 0)  // (the segment ends where the range does)
       k.part[blockIdx.x] = Part{w.r, w.head, s.block, team_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.teams)};
@@ -1136,9 +1160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     draft_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args k) {
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t mem = smem_u32(raw);  // (checked below: the swizzle is one of address bits)
-  constexpr int kOpAt = C::kTiles * C::kQ, kLoadAt = kOpAt + C::kOps * C::kOperand, kScaleAt = kLoadAt + C::kLoads * C::kRaw,
-                kEnd = kScaleAt + C::kLoads * C::kScales, kSharedAt = kEnd + (C::kFp8 ? static_cast<int>(sizeof(Scales)) : 0);
-  const Buffers b{mem, mem + kLoadAt, mem + kOpAt, mem + kScaleAt, C::kFp8 ? reinterpret_cast<Scales*>(raw + kEnd) : nullptr};
+  constexpr int kOpAt = C::kTiles * C::kQ, kLoadAt = kOpAt + C::kOps * C::kOperand,
+                kEnd = kLoadAt + C::kLoads * C::kRaw, kSharedAt = kEnd + (C::kFp8 ? static_cast<int>(sizeof(Scales)) : 0);
+  const Buffers b{mem, mem + kLoadAt, mem + kOpAt, C::kFp8 ? reinterpret_cast<Scales*>(raw + kEnd) : nullptr};
   Shared& sh = *reinterpret_cast<Shared*>(raw + kSharedAt);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (warp == 12) {
