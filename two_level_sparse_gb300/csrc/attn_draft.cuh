@@ -345,25 +345,81 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          ((128u >> 4) << 24);
 }
+// N products issued by one lane (one election for all of them: the warp shares its
+// scheduler with the softmax's); step j reads the operands at a + S::a(j) and b +
+// S::b(j), in 16 bytes, or columns for an A in tensor memory.
+template <class S, int N, bool kE4m3>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+  static_assert(N == 8 || N == 4, "");
+  if constexpr (kE4m3 && N == 8)
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %12;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %13;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %14;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::a(4)), "n"(S::a(5)), "n"(S::a(6)), "n"(S::a(7)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "n"(S::b(4)), "n"(S::b(5)), "n"(S::b(6)), "n"(S::b(7))
+      : "memory");
+  else if constexpr (kE4m3)
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %8;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3))
+      : "memory");
+  else if constexpr (N == 8)
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %12;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %13;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %14;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::a(4)), "n"(S::a(5)), "n"(S::a(6)), "n"(S::a(7)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "n"(S::b(4)), "n"(S::b(5)), "n"(S::b(6)), "n"(S::b(7))
+      : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %8;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3))
       : "memory");
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
-      : "memory");
-}
+template <class S, int N>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+  static_assert(N == 8 || N == 4, "");
+  if constexpr (N == 8)
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 x, %1, %5;\n\tadd.s64 y, %2, %12;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %6;\n\tadd.s64 y, %2, %13;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %7;\n\tadd.s64 y, %2, %14;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::a(4)), "n"(S::a(5)), "n"(S::a(6)), "n"(S::a(7)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "n"(S::b(4)), "n"(S::b(5)), "n"(S::b(6)), "n"(S::b(7))
+      : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred p, e, o;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 x, %1, %5;\n\tadd.s64 y, %2, %8;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -695,6 +751,22 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
 }
 
 // ------------------------------------------------------------------ products
+// Steps of Q K^T: 32 bytes of the rows at a time, blocks of 128 bytes of all rows;
+// e4m3: the query's two parts in turn.
+template <class C>
+struct ScoreSteps {
+  static constexpr int kCount = C::D / 16;  // e4m3: half as many, twice
+  __host__ __device__ static constexpr int e(int j) { return C::kFp8 ? j >> 1 : j; }
+  __host__ __device__ static constexpr int a(int j) {
+    return (C::kFp8 && (j & 1) ? 128 * C::D / 16 : 0) + (e(j) >> 2) * (128 * 128 / 16) + (e(j) & 3) * 2;
+  }
+  __host__ __device__ static constexpr int b(int j) { return (e(j) >> 2) * (C::kSlotKeys * 128 / 16) + (e(j) & 3) * 2; }
+};
+// Steps of P V: 16 positions at a time.
+struct ValueSteps {
+  __host__ __device__ static constexpr int a(int j) { return 8 * j; }
+  __host__ __device__ static constexpr int b(int j) { return 128 * j; }
+};
 template <class C>
 __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, const Buffers& b, uint32_t tmem) {
   constexpr uint32_t kIdQ = idesc(C::kSlotKeys, !C::kFp8, false), kIdP = idesc(C::D, true, true);
@@ -728,16 +800,10 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
             constexpr int kBytes = C::kRow < 128 ? C::kRow : 128;  // of an operand's rows; 32 of them per product
             const uint64_t da = desc_rows(q, kBytes), db = desc_rows(b.load + slot * C::kRaw, kBytes);
             const uint32_t d = tmem + 128 * (i & 1) + x * C::kSlotKeys;
-#pragma unroll
-            for (int e = 0; e < C::kRow / 32; ++e) {
-              const uint64_t ea = da + (e >> 2) * (128 * 128 / 16) + (e & 3) * 2, eb = db + (e >> 2) * (C::kSlotKeys * 128 / 16) + (e & 3) * 2;
-              if (C::kFp8) {
-                mma_f8(d, ea, eb, kIdQ, e > 0);
-                mma_f8(d, ea + 128 * C::D / 16, eb, kIdQ, 1);
-              } else {
-                mma_ss(d, ea, eb, kIdQ, e > 0);
-              }
-            }
+            using S = ScoreSteps<C>;
+            constexpr int kSteps = S::kCount > 8 ? 8 : S::kCount;
+            mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, 0);
+            if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kIdQ, 1);  // (a step's offsets repeat)
             if (last)
               for (int y = 0; y < (C::kFp8 ? kPrepWarps : 1); ++y) mma_commit_elect(&sh.empty[slot]);
           }
@@ -768,10 +834,8 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
         if (wait.alive) {
           tc_fence_after();
           const uint64_t db = desc128(C::kFp8 ? b.op + slot * C::kOperand : b.load + slot * C::kRaw, C::kSlotKeys * 128);
-#pragma unroll
-          for (int e = 0; e < C::kSlotKeys / 16; ++e)
-            mma_ts(tmem + kColO + o * C::D, tmem + 128 * (p & 1) + x * (C::kSlotKeys / 2) + e * 8, db + e * 128, kIdP,
-                   x > 0 || e > 0 || p >= (C::kTwo ? 2 : 1));
+          mma_ts<ValueSteps, C::kSlotKeys / 16>(tmem + kColO + o * C::D, tmem + 128 * (p & 1) + x * (C::kSlotKeys / 2), db, kIdP,
+                                                x > 0 || p >= (C::kTwo ? 2 : 1));
           if (last) mma_commit_elect(C::kFp8 ? &sh.op_empty[slot] : &sh.empty[slot]);
         }
         if (fresh) at.advance(), op.advance();
