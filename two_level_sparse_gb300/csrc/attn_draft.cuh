@@ -101,6 +101,8 @@ struct Shared {
   // or that is not waited for by those that free the slot, would take one phase for another.
   uint64_t full[kMaxSlots], v_full[kMaxSlots], empty[kMaxSlots];
   uint64_t ready[kMaxSlots], op_empty[kMaxSlots];  // values looked over (bf16), operands (FP8)
+  // pv_done: two streams: of a segment's last step (a score buffer that is full says that what was issued before is done,
+  // the stream's last product among it); one stream: of every step
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
   float ref[2][128], sums[2][128];  // the streams' references and sums, when they are put together
   float fold[2][8][96];              // and eight dims of the copies of rows
@@ -310,7 +312,8 @@ __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
 
 // ------------------------------------------------------------------ small things
 // One role's waits: false once anything has given up; the role then goes on
-// through its loop without touching memory.
+// through its loop without touching memory.  (By one lane and a shuffle instead of
+// all: 1.4 times the time of the whole.)
 struct Waiter {
   Shared& sh;
   int32_t* dev_err;
@@ -767,6 +770,10 @@ struct ValueSteps {
   __host__ __device__ static constexpr int a(int j) { return 8 * j; }
   __host__ __device__ static constexpr int b(int j) { return 128 * j; }
 };
+// Step i is Q K^T into score buffer i % 2, the softmax, then P V.  A wait costs some
+// 200 cycles even where it is for something done, so a step's keys and values are
+// waited for before its probabilities: P V and, as the buffer is free then, the
+// scores of the step after next follow at once.
 template <class C>
 __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, const Buffers& b, uint32_t tmem) {
   constexpr uint32_t kIdQ = idesc(C::kSlotKeys, !C::kFp8, false), kIdP = idesc(C::D, true, true);
@@ -780,68 +787,74 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
     if (s.rows == 0) continue;
+    auto keys = [&](int i) {  // waits for step i's keys
+      if (i >= s.steps || (s.two && (i & 1))) return;
+      k_slot = at.slot;
+#pragma unroll 1
+      for (int x = 0; x < C::kParts; ++x, at.advance()) {
+        wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
+        k_turn ^= 1u << at.slot;
+      }
+    };
+    auto scores = [&](int i) {
+      if (i >= s.steps || !wait.alive) return;
+      const bool last = !s.two || (i & 1);  // of the tile's
+      const uint32_t q = b.q + (s.two ? (i & 1) * C::kQ : 0);
+      tc_fence_after();
+#pragma unroll 1
+      for (int x = 0, slot = k_slot; x < C::kParts; ++x) {
+        constexpr int kBytes = C::kRow < 128 ? C::kRow : 128;  // of an operand's rows; 32 of them per product
+        const uint64_t da = desc_rows(q, kBytes), db = desc_rows(b.load + slot * C::kRaw, kBytes);
+        const uint32_t d = tmem + 128 * (i & 1) + x * C::kSlotKeys;
+        using S = ScoreSteps<C>;
+        constexpr int kSteps = S::kCount > 8 ? 8 : S::kCount;
+        mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, 0);
+        if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kIdQ, 1);  // (a step's offsets repeat)
+        if (x == C::kParts - 1) mma_commit_elect(&sh.s_full[i & 1]);
+        if (last)
+          for (int y = 0; y < (C::kFp8 ? kPrepWarps : 1); ++y) mma_commit_elect(&sh.empty[slot]);
+        if (++slot == C::kLoads) slot = 0;
+      }
+      if (i == s.steps - 1) mma_commit_elect(&sh.q_empty);
+    };
+    keys(0);
     wait(&sh.q_full, segments & 1);
     ++segments;
+    scores(0);
+    keys(1);
+    scores(1);
 #pragma unroll 1
-    for (int i = 0; i <= s.steps; ++i) {
-      if (i < s.steps) {
-        const bool fresh = !s.two || (i & 1) == 0, last = !s.two || (i & 1) == 1;
-        const uint32_t q = b.q + (s.two ? (i & 1) * C::kQ : 0);
-        if (fresh) k_slot = at.slot;
-        int slot = k_slot;
+    for (int i = 0; i < s.steps; ++i) {
+      const int o = C::kTwo ? i & 1 : 0;
+      const bool fresh = !s.two || (i & 1) == 0, last = !s.two || (i & 1) == 1;
+      if (fresh) {
+        v_slot = C::kFp8 ? op.slot : at.slot;
 #pragma unroll 1
-        for (int x = 0; x < C::kParts; ++x) {
-          if (fresh) {
-            wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
-            k_turn ^= 1u << at.slot;
+        for (int x = 0; x < C::kParts; ++x, at.advance(), op.advance()) {
+          if (C::kFp8) {
+            wait(&sh.ready[op.slot], op.phase);
+          } else {
+            const uint32_t turn = (v_turn >> at.slot) & 1;
+            if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
+            v_turn ^= 1u << at.slot;
           }
-          if (wait.alive) {
-            tc_fence_after();
-            constexpr int kBytes = C::kRow < 128 ? C::kRow : 128;  // of an operand's rows; 32 of them per product
-            const uint64_t da = desc_rows(q, kBytes), db = desc_rows(b.load + slot * C::kRaw, kBytes);
-            const uint32_t d = tmem + 128 * (i & 1) + x * C::kSlotKeys;
-            using S = ScoreSteps<C>;
-            constexpr int kSteps = S::kCount > 8 ? 8 : S::kCount;
-            mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, 0);
-            if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kIdQ, 1);  // (a step's offsets repeat)
-            if (last)
-              for (int y = 0; y < (C::kFp8 ? kPrepWarps : 1); ++y) mma_commit_elect(&sh.empty[slot]);
-          }
-          if (fresh) at.advance();
-          if (++slot == C::kLoads) slot = 0;
-        }
-        if (wait.alive) {
-          mma_commit_elect(&sh.s_full[i & 1]);
-          if (i == s.steps - 1) mma_commit_elect(&sh.q_empty);
         }
       }
-      if (i == 0) continue;
-      const int p = i - 1, o = C::kTwo ? p & 1 : 0;
-      const bool fresh = !s.two || (p & 1) == 0, last = !s.two || (p & 1) == 1;
-      wait(&sh.p_full[p & 1], (p_turn >> (p & 1)) & 1);
-      p_turn ^= 1u << (p & 1);
-      if (fresh) v_slot = C::kFp8 ? op.slot : at.slot;
-      int slot = v_slot;
+      keys(i + 2);
+      wait(&sh.p_full[i & 1], (p_turn >> (i & 1)) & 1);
+      p_turn ^= 1u << (i & 1);
+      if (!wait.alive) continue;
+      tc_fence_after();
 #pragma unroll 1
-      for (int x = 0; x < C::kParts; ++x) {
-        if (fresh && C::kFp8) {
-          wait(&sh.ready[op.slot], op.phase);
-        } else if (fresh) {
-          const uint32_t turn = (v_turn >> at.slot) & 1;
-          if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
-          v_turn ^= 1u << at.slot;
-        }
-        if (wait.alive) {
-          tc_fence_after();
-          const uint64_t db = desc128(C::kFp8 ? b.op + slot * C::kOperand : b.load + slot * C::kRaw, C::kSlotKeys * 128);
-          mma_ts<ValueSteps, C::kSlotKeys / 16>(tmem + kColO + o * C::D, tmem + 128 * (p & 1) + x * (C::kSlotKeys / 2), db, kIdP,
-                                                x > 0 || p >= (C::kTwo ? 2 : 1));
-          if (last) mma_commit_elect(C::kFp8 ? &sh.op_empty[slot] : &sh.empty[slot]);
-        }
-        if (fresh) at.advance(), op.advance();
+      for (int x = 0, slot = v_slot; x < C::kParts; ++x) {
+        const uint64_t db = desc128(C::kFp8 ? b.op + slot * C::kOperand : b.load + slot * C::kRaw, C::kSlotKeys * 128);
+        mma_ts<ValueSteps, C::kSlotKeys / 16>(tmem + kColO + o * C::D, tmem + 128 * (i & 1) + x * (C::kSlotKeys / 2), db, kIdP,
+                                              x > 0 || i >= (C::kTwo ? 2 : 1));
+        if (last) mma_commit_elect(C::kFp8 ? &sh.op_empty[slot] : &sh.empty[slot]);
         if (++slot == (C::kFp8 ? C::kOps : C::kLoads)) slot = 0;
       }
-      if (wait.alive) mma_commit_elect(&sh.pv_done[o]);
+      if (!C::kTwo || i + 2 >= s.steps) mma_commit_elect(&sh.pv_done[o]);
+      scores(i + 2);
     }
   }
   if (!wait.alive) {  // the products in flight end before the CTA's memory goes
@@ -1025,7 +1038,7 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     const float up = fmaxf(r.ref, fminf(top, kFar)), by = exp2_approx(r.ref - up);
     r.ref = up;
     r.sum = mul2(r.sum, make_float2(by, by));
-    if (wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1)) {
+    if (C::kTwo || wait(&sh.pv_done[0], (done - 1) & 1)) {
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < C::D; c += 32) {
@@ -1098,11 +1111,11 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
         softmax_step<C, 1>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, first, g, done, r);
       }
       // every phase is waited for in turn, as a wait tells only the present one from the one before
-      if (!first) wait(&sh.pv_done[C::kTwo ? g : 0], (done - 1) & 1);
+      if (!C::kTwo && !first) wait(&sh.pv_done[0], (done - 1) & 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[buf]);
-      ++done;
+      if (!C::kTwo || i + kStride >= s.steps) ++done;
     }
     base += s.tiles;
     // ---- the segment's end
