@@ -111,6 +111,7 @@ struct Shared {
   int64_t warp_sum[16];
   int32_t first, end, total, teams;  // the team's range of the list
   int32_t req, head, block, tile;    // where it starts
+  int32_t row0, n, len, limit;       // and that request
   uint32_t tmem;
   int32_t abort;
 };
@@ -132,6 +133,9 @@ struct Request {
   int blocks;
 };
 enum { kGood = 0, kBadLen = 1, kBadReq = 2 };
+__device__ __forceinline__ int blocks_of(const Args& k, int n) {  // (the host has checked that rows * G fit)
+  return static_cast<int>((static_cast<int64_t>(n) * k.l.group + k.l.block_rows - 1) / k.l.block_rows);
+}
 __device__ __forceinline__ Request request_of(const Args& k, int r, int& bad) {
   const DraftArgs& a = k.a;
   Request q;
@@ -150,7 +154,7 @@ __device__ __forceinline__ Request request_of(const Args& k, int r, int& bad) {
     bad = kBadLen;
     q.len = q.limit = 0;
   }
-  q.blocks = static_cast<int>((static_cast<int64_t>(q.n) * k.l.group + k.l.block_rows - 1) / k.l.block_rows);
+  q.blocks = blocks_of(k, q.n);
   return q;
 }
 // The last node of a team's blocks b, b + 1, ...
@@ -273,6 +277,7 @@ __device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
       for (int t; at >= (t = block_tiles(k, q, b)); b += k.l.team) at -= t;
     }
     sh.req = r, sh.head = head, sh.block = b, sh.tile = at;
+    sh.row0 = q.first, sh.n = q.n, sh.len = q.len, sh.limit = q.limit;
   }
   __syncthreads();
 }
@@ -280,9 +285,8 @@ __device__ __forceinline__ Walk walk_of(const Args& k, const Shared& sh) {
   Walk w{};
   w.left = sh.end - sh.first;
   if (w.left == 0) return w;
-  int bad;
   w.r = sh.req, w.head = sh.head, w.block = sh.block, w.tile = sh.tile;
-  w.q = request_of(k, w.r, bad);
+  w.q = Request{sh.row0, sh.n, sh.len, sh.limit, blocks_of(k, sh.n)};
   w.tiles = block_tiles(k, w.q, w.block);
   return w;
 }
@@ -424,6 +428,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "add.s32 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3))
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -888,10 +899,10 @@ __device__ __forceinline__ uint32_t seen_of(const RowMask& m, int64_t pos) {
   return __funnelshift_r(mask_word(m, i), mask_word(m, i + 1), static_cast<int>(rel) & 31);
 }
 
-// What a row sees that is not finite, of 32 dims from d0 on and positions from
+// What a row sees that is not finite, of 16 dims from d0 on and positions from
 // `first` on: added as it is.
 template <class C>
-__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int64_t first, int d0, uint32_t (&o)[32]) {
+__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int64_t first, int d0, float (&o)[16]) {
   const CacheArgs& c = k.a.c;
   const int64_t end = min(static_cast<int64_t>(w.i1) * kKeys, static_cast<int64_t>(w.q.limit));
 #pragma unroll 1
@@ -902,29 +913,41 @@ __device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask
     const uint4* v = reinterpret_cast<const uint4*>(
         c.v_pool + (static_cast<int64_t>(page) * c.num_kv_heads + w.head) * C::kPageBytes + ((pos & (kPage - 1)) * C::D + d0) * 2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const uint4 x = v[i];
       const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t &lo = o[8 * i + 2 * j], &hi = o[8 * i + 2 * j + 1];
-        if ((u[j] & 0x7F80u) == 0x7F80u) lo = __float_as_uint(__uint_as_float(lo) + bf16_lo(u[j]));
-        if ((u[j] & 0x7F800000u) == 0x7F800000u) hi = __float_as_uint(__uint_as_float(hi) + bf16_hi(u[j]));
+        float &lo = o[8 * i + 2 * j], &hi = o[8 * i + 2 * j + 1];
+        if ((u[j] & 0x7F80u) == 0x7F80u) lo += bf16_lo(u[j]);
+        if ((u[j] & 0x7F800000u) == 0x7F800000u) hi += bf16_hi(u[j]);
       }
     }
   }
 }
 
-// 32 N of a row's scores, 32 columns at a time, the next ones on their way.
-template <int N, class F>
+// A row's 128 scores, 32 columns at a time, the next ones on their way.
+template <class F>
 __device__ __forceinline__ void over_scores(uint32_t at, F f) {
   uint32_t x[2][32];
   tmem_ld32(at, x[0]);
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
+  for (int c = 0; c < 4; ++c) {
     tmem_ld_wait();
-    if (c < N - 1) tmem_ld32(at + 32 * (c + 1), x[(c + 1) & 1]);
+    if (c < 3) tmem_ld32(at + 32 * (c + 1), x[(c + 1) & 1]);
     f(c, x[c & 1]);
+  }
+}
+// n times 32 of them, one after another: the code is a quarter, and a call's first
+// tiles and its masked ones run it cold.
+template <class F>
+__device__ __forceinline__ void over_some_scores(uint32_t at, int n, F f) {
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    uint32_t x[32];
+    tmem_ld32(at + 32 * c, x);
+    tmem_ld_wait();
+    f(c, x);
   }
 }
 // Two scores, times their keys' scales.
@@ -935,102 +958,95 @@ __device__ __forceinline__ float2 scores_of(uint32_t s0, uint32_t s1, float k0, 
 }
 __device__ __forceinline__ bool bit(uint32_t bits, int j) { return (bits >> j) & 1; }
 
-// The row's largest logit (base 2) of a tile: of the scores, as rounding keeps their order.
-template <class C, bool kMasked, int N>
-__device__ __forceinline__ float tile_top(uint32_t at, const uint32_t (&bits)[N], const float* ks, float factor) {
-  const bool down = factor < 0.f;
-  float top = down ? INFINITY : -INFINITY, other = top;
-  over_scores<N>(at, [&](int c, const uint32_t (&x)[32]) {
-    const float none = down ? INFINITY : -INFINITY;
+// The largest of 32 scores and `top` (kDown: the smallest).
+template <class C, bool kCareful, bool kDown>
+__device__ __forceinline__ float top_of(const uint32_t (&x)[32], uint32_t bits, const float* ks, float top) {
+  float other = top;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
-      float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
-      if (kMasked) {
-        y.x = bit(bits[c], j) ? y.x : none, y.y = bit(bits[c], j + 1) ? y.y : none;
-        z.x = bit(bits[c], j + 2) ? z.x : none, z.y = bit(bits[c], j + 3) ? z.y : none;
-      }
-      if (down) {
-        top = fminf(top, fminf(y.x, y.y)), other = fminf(other, fminf(z.x, z.y));
-      } else {
-        top = fmaxf(top, fmaxf(y.x, y.y)), other = fmaxf(other, fmaxf(z.x, z.y));
-      }
+  for (int j = 0; j < 32; j += 4) {
+    float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + j);
+    float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
+    if (kCareful) {
+      const float none = kDown ? INFINITY : -INFINITY;
+      y.x = bit(bits, j) ? y.x : none, y.y = bit(bits, j + 1) ? y.y : none;
+      z.x = bit(bits, j + 2) ? z.x : none, z.y = bit(bits, j + 3) ? z.y : none;
     }
-  });
-  top = down ? fminf(top, other) : fmaxf(top, other);
-  return kMasked && (top == INFINITY || top == -INFINITY) && factor == 0.f ? -INFINITY : top * factor;
+    top = kDown ? fminf(top, fminf(y.x, y.y)) : fmaxf(top, fmaxf(y.x, y.y));
+    other = kDown ? fminf(other, fminf(z.x, z.y)) : fmaxf(other, fmaxf(z.x, z.y));
+  }
+  return kDown ? fminf(top, other) : fmaxf(top, other);
 }
 
-// The row's probabilities of a tile, over its scores, and their sum.  kCareful:
-// masked, or logits that are rounded by themselves, as the reference is (a
-// product and a difference in one step are off by half of the reference's last
-// place, which only counts where logits pass 2^22).
-template <class C, bool kCareful, int N>
-__device__ __forceinline__ void tile_probabilities(uint32_t at, uint32_t to, const uint32_t (&bits)[N], const float* ks, const float* vs,
-                                                   float factor, float ref, float2& sum) {
+// 32 probabilities, over their scores, and their sum.  kCareful: masked, or
+// logits that are rounded by themselves, as the reference is (a product and a
+// difference in one step are off by half of the reference's last place, which
+// only counts where logits pass 2^22).
+template <class C, bool kCareful>
+__device__ __forceinline__ void probabilities_of(const uint32_t (&x)[32], uint32_t to, uint32_t bits, const float* ks,
+                                                 const float* vs, float factor, float ref, float2& sum, float2& other) {
   const float up = C::kFp8 ? kLift - ref : -ref;
   const float2 less = make_float2(up, up), by = make_float2(factor, factor);
-  float2 other = make_float2(0.f, 0.f);
-  over_scores<N>(at, [&](int c, const uint32_t (&x)[32]) {
-    uint32_t p[16];
+  uint32_t p[16];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
-      if (C::kFp8) {
-        f = *reinterpret_cast<const float4*>(ks + 32 * c + j);
-        h = *reinterpret_cast<const float4*>(vs + 32 * c + j);
-      }
-      float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
-      if (kCareful) {
-        y = add2(make_float2(__fmul_rn(y.x, factor), __fmul_rn(y.y, factor)), make_float2(-ref, -ref));
-        z = add2(make_float2(__fmul_rn(z.x, factor), __fmul_rn(z.y, factor)), make_float2(-ref, -ref));
-        if (C::kFp8) y = add2(y, make_float2(kLift, kLift)), z = add2(z, make_float2(kLift, kLift));
-      } else {
-        y = fma2(y, by, less), z = fma2(z, by, less);
-      }
-      y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-      z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-      if (kCareful) {
-        y.x = bit(bits[c], j) ? y.x : 0.f, y.y = bit(bits[c], j + 1) ? y.y : 0.f;
-        z.x = bit(bits[c], j + 2) ? z.x : 0.f, z.y = bit(bits[c], j + 3) ? z.y : 0.f;
-      }
-      sum = add2(sum, y), other = add2(other, z);
-      if (C::kFp8) {
-        y = mul2(y, make_float2(h.x, h.y)), z = mul2(z, make_float2(h.z, h.w));
-        if (kCareful) {  // (a scale that is not finite must not meet a 0)
-          y.x = bit(bits[c], j) ? y.x : 0.f, y.y = bit(bits[c], j + 1) ? y.y : 0.f;
-          z.x = bit(bits[c], j + 2) ? z.x : 0.f, z.y = bit(bits[c], j + 3) ? z.y : 0.f;
-        }
-      }
-      p[j / 2] = bf16x2(y.x, y.y), p[j / 2 + 1] = bf16x2(z.x, z.y);
+  for (int j = 0; j < 32; j += 4) {
+    float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
+    if (C::kFp8) {
+      f = *reinterpret_cast<const float4*>(ks + j);
+      h = *reinterpret_cast<const float4*>(vs + j);
     }
-    tmem_st16(to + 16 * c, p);
-  });
-  sum = add2(sum, other);
+    float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
+    if (kCareful) {
+      y = add2(make_float2(__fmul_rn(y.x, factor), __fmul_rn(y.y, factor)), make_float2(-ref, -ref));
+      z = add2(make_float2(__fmul_rn(z.x, factor), __fmul_rn(z.y, factor)), make_float2(-ref, -ref));
+      if (C::kFp8) y = add2(y, make_float2(kLift, kLift)), z = add2(z, make_float2(kLift, kLift));
+    } else {
+      y = fma2(y, by, less), z = fma2(z, by, less);
+    }
+    y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+    if (kCareful) {
+      y.x = bit(bits, j) ? y.x : 0.f, y.y = bit(bits, j + 1) ? y.y : 0.f;
+      z.x = bit(bits, j + 2) ? z.x : 0.f, z.y = bit(bits, j + 3) ? z.y : 0.f;
+    }
+    sum = add2(sum, y), other = add2(other, z);
+    if (C::kFp8) {
+      y = mul2(y, make_float2(h.x, h.y)), z = mul2(z, make_float2(h.z, h.w));
+      if (kCareful) {  // (a scale that is not finite must not meet a 0)
+        y.x = bit(bits, j) ? y.x : 0.f, y.y = bit(bits, j + 1) ? y.y : 0.f;
+        z.x = bit(bits, j + 2) ? z.x : 0.f, z.y = bit(bits, j + 3) ? z.y : 0.f;
+      }
+    }
+    p[j / 2] = bf16x2(y.x, y.y), p[j / 2 + 1] = bf16x2(z.x, z.y);
+  }
+  tmem_st16(to, p);
 }
 
-// A step of the softmax for a warp that has the 32 N columns of the buffer `at` from
+// A step of the softmax for a warp that has the 32 n columns of the buffer `at` from
 // 32 c0 on: reference, rescaling of O, probabilities; zeros in the other columns.
 struct Row {
   float factor, ref;
   float2 sum;
 };
-template <class C, int N>
+template <class C>
 __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const RowMask& mask, int64_t pos0, uint32_t pages,
                                              int seen, const float* ks, const float* vs, uint32_t at, uint32_t own, int c0,
-                                             bool first, int g, uint32_t done, Row& r) {
-  const bool masked = pages != 3 || pos0 + kKeys > seen;
-  uint32_t bits[N];
-#pragma unroll
-  for (int c = 0; c < N; ++c) bits[c] = ~0u;
-  if (masked) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) bits[c] = (pages >> ((c0 + c) >> 1)) & 1 ? seen_of(mask, pos0 + 32 * (c0 + c)) : 0;
-  }
+                                             int n, bool first, uint32_t done, Row& r) {
+  const bool masked = pages != 3 || pos0 + kKeys > seen, plain = !masked && n == 4, down = r.factor < 0.f;
   const uint32_t scores = at + 32 * c0, to = at + 16 * c0;
   if (C::kFp8) ks += 32 * c0, vs += 32 * c0;
-  float top = masked ? tile_top<C, true, N>(scores, bits, ks, r.factor) : tile_top<C, false, N>(scores, bits, ks, r.factor);
+  auto bits_of = [&](int c) {
+    return !masked ? ~0u : (pages >> ((c0 + c) >> 1)) & 1 ? seen_of(mask, pos0 + 32 * (c0 + c)) : 0;
+  };
+  // the largest logit (base 2): of the scores, as rounding keeps their order
+  float top = down ? INFINITY : -INFINITY;
+  if (plain && !down)
+    over_scores(scores, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
+  else if (!down)
+    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, true, false>(x, bits_of(c), ks + 32 * c, top); });
+  else
+    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, true, true>(x, bits_of(c), ks + 32 * c, top); });
+  top = r.factor == 0.f && fabsf(top) == INFINITY ? -INFINITY : top * r.factor;
   if (C::kFp8) top = ceilf(top);  // so that kLift less a reference is exact
   if (first) {
     r.ref = fmaxf(fminf(top, kFar), -kFar);
@@ -1052,16 +1068,22 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
       tmem_st_wait();
     }
   }
-  if (masked || __any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f))
-    tile_probabilities<C, true, N>(scores, to, bits, ks, vs, r.factor, r.ref, r.sum);
+  float2 other = make_float2(0.f, 0.f);
+  if (plain && !__any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f))
+    over_scores(scores, [&](int c, const uint32_t (&x)[32]) {
+      probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+    });
   else
-    tile_probabilities<C, false, N>(scores, to, bits, ks, vs, r.factor, r.ref, r.sum);
-  if (N < 4) {
+    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) {
+      probabilities_of<C, true>(x, to + 16 * c, bits_of(c), ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+    });
+  r.sum = add2(r.sum, other);
+#pragma unroll 1
+  for (int c = n; c < 4; ++c) {
     uint32_t none[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) none[j] = 0;
-#pragma unroll
-    for (int c = N; c < 4; ++c) tmem_st16(at + 16 * ((c0 + c) & 3), none);
+    tmem_st16(at + 16 * ((c0 + c) & 3), none);
   }
   tmem_st_wait();
 }
@@ -1102,14 +1124,8 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       const uint32_t pages = sh.pages[(base + t) & 15];
       const int64_t pos0 = static_cast<int64_t>(w.i0 + t) * kKeys;
       const float *ks = C::kFp8 ? sc->k[(base + t) & 7] : nullptr, *vs = C::kFp8 ? sc->v[(base + t) & 7] : nullptr;
-      if (!busy) {
-      } else if (span == 128) {
-        softmax_step<C, 4>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, 0, first, g, done, r);
-      } else if (span == 64) {
-        softmax_step<C, 2>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, first, g, done, r);
-      } else {
-        softmax_step<C, 1>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, first, g, done, r);
-      }
+      if (busy)
+        softmax_step<C>(sh, wait, mask, pos0, pages, seen, ks, vs, at, own, c0, span >> 5, first, done, r);
       // every phase is waited for in turn, as a wait tells only the present one from the one before
       if (!C::kTwo && !first) wait(&sh.pv_done[0], (done - 1) & 1);
       tc_fence_before();
@@ -1150,33 +1166,31 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
     const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
     const uint32_t from = both ? lanes + kColO : own;
 #pragma unroll 1
-    for (int c = busy ? d0 : d1; c < d1; c += 32) {
-      uint32_t o[32];
-      tmem_ld32(from + c, o);
+    for (int c = busy ? d0 : d1; c < d1; c += 16) {
+      uint32_t o[16], y[16];
+      tmem_ld16(from + c, o);
+      if (both && s.steps > 1) tmem_ld16(from + C::D + c, y);
       tmem_ld_wait();
-      if (joined) {
-        uint32_t y[32];
+      float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = 0;
-        if (both && s.steps > 1) tmem_ld32(from + C::D + c, y);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fa + __uint_as_float(y[j]) * fb);
+      for (int j = 0; j < 16; ++j) {
+        v[j] = __uint_as_float(o[j]);
+        if (joined) v[j] *= fa;
+        if (both && s.steps > 1) v[j] += __uint_as_float(y[j]) * fb;
       }
       if (span < 128) {  // the copies' sums, eight dims at a time (all of the stream's warps are busy)
 #pragma unroll
-        for (int j0 = 0; j0 < 32; j0 += 8) {
+        for (int j0 = 0; j0 < 16; j0 += 8) {
           if (c0 != 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sh.fold[g][j][row - span] = __uint_as_float(o[j0 + j]);
+            for (int j = 0; j < 8; ++j) sh.fold[g][j][row - span] = v[j0 + j];
           }
           named_sync(2 + g, 128);
           if (c0 == 0) {
+#pragma unroll 1
+            for (int x = row; x < 128 - span; x += span) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float v = __uint_as_float(o[j0 + j]);
-              for (int y = row; y < 128 - span; y += span) v += sh.fold[g][j][y];
-              o[j0 + j] = __float_as_uint(v);
+              for (int j = 0; j < 8; ++j) v[j0 + j] += sh.fold[g][j][x];
             }
           }
           named_sync(2 + g, 128);
@@ -1184,26 +1198,25 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       }
       if (live) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = total == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * by);
+        for (int j = 0; j < 16; ++j) v[j] = total == 0.f ? 0.f : v[j] * by;
         if (odd) {
-          uint32_t y[32];
+          float z[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] = o[j];
-          add_odd<C>(k, w, mask, span < 128 ? 0 : w.q.len, c, y);
+          for (int j = 0; j < 16; ++j) z[j] = v[j];
+          add_odd<C>(k, w, mask, span < 128 ? 0 : w.q.len, c, z);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = y[j];
+          for (int j = 0; j < 16; ++j) v[j] = z[j];
         }
         if (whole) {
           uint16_t* dst = a.out + t * a.out_stride + qh * C::D + c;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            *reinterpret_cast<uint4*>(dst + j) = make_uint4(
-                bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
-                bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])), bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
+          for (int j = 0; j < 16; j += 8)
+            *reinterpret_cast<uint4*>(dst + j) = make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
+                                                            bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
         } else {
           float* dst = k.sum + (slot * C::kBlockRows + m0) * C::D + c;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
       }
       __syncwarp();
