@@ -23,73 +23,67 @@ Layout layout_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, in
 // With the parts' references m_i, sums l_i and unnormalised sums o_i:
 //   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
 // CTA (x, y) takes the unit that begins in CTA x and goes on, and every
-// gridDim.y-th group of its rows; a row's parts are dealt to `ways` warps, whose
-// sums are added in order.
+// gridDim.y-th run of its (row, four dims); neighbouring lanes have neighbouring
+// rows.  The parts are dealt to `ways` groups of warps, whose sums are added in
+// order.  Bound by latency: the parts sit in L2.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Args k) {
-  constexpr int kPer = D / 32;
-  __shared__ float sums[kJoinWarps][D];
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Args k) {
+  __shared__ float sums[kJoinWarps][32][7];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   release_successor();
   wait_predecessor();
   const Part p = k.part[blockIdx.x];
   if (p.last < 0) return;
   const int team = static_cast<int>(blockIdx.x) / k.l.team, member = static_cast<int>(blockIdx.x) % k.l.team;
-  const int n = p.last - team + 1, ways = n > 32 ? 16 : n > 4 ? 4 : 1, per = kJoinWarps / ways;
-  const int hw = warp / ways, way = warp % ways;
+  const int n = p.last - team + 1, ways = n > 32 ? 16 : n > 4 ? 4 : 1, per = 32 * (kJoinWarps / ways);
+  const int way = warp % ways, group = warp / ways;
   const int first = k.a.c.req_start[p.req], row0 = p.block * k.l.block_rows;
   const int rows = min(k.l.block_rows, (k.a.c.req_start[p.req + 1] - first) * k.l.group - row0);
+  const float2* stats = reinterpret_cast<const float2*>(k.stat);
+  const float4* parts = reinterpret_cast<const float4*>(k.sum);
   auto slot = [&](int i) { return 2ll * ((team + i) * k.l.team + member) + (i == 0 ? 1 : 0); };
 #pragma unroll 1
-  for (int base = blockIdx.y * per; base < rows; base += gridDim.y * per) {
-    const int m = base + hw;
-    const bool live = m < rows;
-    float top = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] = 0.f;
-    if (live) {
-      auto stat = [&](int i) { return reinterpret_cast<const float2*>(k.stat)[slot(i) * k.l.block_rows + m]; };
-      for (int i = lane; i < n; i += 32) {
-        const float2 st = stat(i);
-        const float up = fmaxf(top, st.x);
-        l = l * draft::exp2_approx(top - up) + st.y * draft::exp2_approx(st.x - up);  // (references are finite)
-        top = up;
-      }
-      float up = top;
-#pragma unroll
-      for (int b = 16; b > 0; b >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, b));
-      l *= draft::exp2_approx(top - up);
-      top = up;
-#pragma unroll
-      for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+  for (int base = blockIdx.y * per; base < rows * (D / 4); base += gridDim.y * per) {
+    const int x = base + group * 32 + lane;
+    const bool live = x < rows * (D / 4);
+    const int c = live ? x / rows : 0, m = live ? x - c * rows : 0;
+    // this way's parts: running reference and sums
+    float top = -draft::kFar, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int i = way; i < n; i += ways) {
-        const float f = draft::exp2_approx(stat(i).x - top);
-        const float* src = k.sum + (slot(i) * k.l.block_rows + m) * D + lane;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] += f * src[32 * j];
-      }
+    for (int i = way; i < n; i += ways) {
+      const float2 st = stats[slot(i) * k.l.block_rows + m];
+      const float4 v = parts[(slot(i) * (D / 4) + c) * k.l.block_rows + m];
+      const float up = fmaxf(top, st.x), f = draft::exp2_approx(top - up), g = draft::exp2_approx(st.x - up);
+      top = up;
+      l = l * f + st.y * g;
+      o.x = o.x * f + v.x * g, o.y = o.y * f + v.y * g, o.z = o.z * f + v.z * g, o.w = o.w * f + v.w * g;
     }
     if (ways > 1) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) sums[warp][32 * j + lane] = o[j];
+      float* mine = sums[warp][lane];
+      mine[0] = top, mine[1] = l, mine[2] = o.x, mine[3] = o.y, mine[4] = o.z, mine[5] = o.w;
       __syncthreads();
       if (way == 0)
 #pragma unroll 1
-        for (int x = 1; x < ways; ++x)
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) o[j] += sums[warp + x][32 * j + lane];
+        for (int y = 1; y < ways; ++y) {
+          const float* v = sums[warp + y][lane];
+          const float up = fmaxf(top, v[0]), f = draft::exp2_approx(top - up), g = draft::exp2_approx(v[0] - up);
+          top = up;
+          l = l * f + v[1] * g;
+          o.x = o.x * f + v[2] * g, o.y = o.y * f + v[3] * g, o.z = o.z * f + v[4] * g, o.w = o.w * f + v[5] * g;
+        }
       __syncthreads();
     }
     if (!live || way != 0) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int x = row0 + m, node = x / k.l.group;
-    const int64_t t = first + node, qh = static_cast<int64_t>(p.head) * k.l.group + x - node * k.l.group;
-    uint16_t* dst = k.a.out + t * k.a.out_stride + qh * D;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o[j] * inv));
-    if (k.a.lse != nullptr && lane == 0)
-      k.a.lse[t * k.a.c.num_q_heads + qh] = l == 0.f ? -INFINITY : (top - (k.a.c.fp8 ? draft::kLift : 0.f) + log2f(l)) * 0.6931471805599453f;
+    const int row = row0 + m, node = row / k.l.group;
+    const int64_t t = first + node, qh = static_cast<int64_t>(p.head) * k.l.group + row - node * k.l.group;
+    const bool none = l == 0.f;
+    *reinterpret_cast<uint2*>(k.a.out + t * k.a.out_stride + qh * D + 4 * c) =
+        make_uint2(none ? 0u : draft::bf16x2(o.x * inv, o.y * inv), none ? 0u : draft::bf16x2(o.z * inv, o.w * inv));
+    if (k.a.lse != nullptr && c == 0)
+      k.a.lse[t * k.a.c.num_q_heads + qh] =
+          none ? -INFINITY : (top - (k.a.c.fp8 ? draft::kLift : 0.f) + log2f(l)) * 0.6931471805599453f;
   }
 }
 

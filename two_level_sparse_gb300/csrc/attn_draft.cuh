@@ -71,7 +71,7 @@ struct Args {
   Layout l;
   Part* part;   // [ctas]
   float* stat;  // [2 ctas][block_rows][2]: reference (base 2) and sum
-  float* sum;   // [2 ctas][block_rows][D]
+  float* sum;   // [2 ctas][D / 4][block_rows][4]: neighbouring rows are neighbouring lanes
 };
 
 template <int D_, bool kFp8_>
@@ -1214,9 +1214,9 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
             *reinterpret_cast<uint4*>(dst + j) = make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
                                                             bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
         } else {
-          float* dst = k.sum + (slot * C::kBlockRows + m0) * C::D + c;
+          float4* dst = reinterpret_cast<float4*>(k.sum) + (slot * (C::D / 4) + c / 4) * C::kBlockRows + m0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          for (int j = 0; j < 16; j += 4) dst[j / 4 * C::kBlockRows] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
       }
       __syncwarp();
