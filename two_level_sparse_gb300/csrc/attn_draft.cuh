@@ -1032,7 +1032,7 @@ template <class C>
 __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const RowMask& mask, int64_t pos0, uint32_t pages,
                                              int seen, const float* ks, const float* vs, uint32_t at, uint32_t own, int c0,
                                              int n, bool first, uint32_t done, Row& r) {
-  const bool masked = pages != 3 || pos0 + kKeys > seen, plain = !masked && n == 4, down = r.factor < 0.f;
+  const bool masked = pages != 3 || pos0 + kKeys > seen, plain = !masked, down = r.factor < 0.f;
   const uint32_t scores = at + 32 * c0, to = at + 16 * c0;
   if (C::kFp8) ks += 32 * c0, vs += 32 * c0;
   auto bits_of = [&](int c) {
@@ -1040,8 +1040,10 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
   };
   // the largest logit (base 2): of the scores, as rounding keeps their order
   float top = down ? INFINITY : -INFINITY;
-  if (plain && !down)
+  if (plain && n == 4 && !down)
     over_scores(scores, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
+  else if (plain && !down)
+    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
   else if (!down)
     over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, true, false>(x, bits_of(c), ks + 32 * c, top); });
   else
@@ -1069,8 +1071,13 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     }
   }
   float2 other = make_float2(0.f, 0.f);
-  if (plain && !__any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f))
+  const bool near = plain && !__any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f);
+  if (near && n == 4)
     over_scores(scores, [&](int c, const uint32_t (&x)[32]) {
+      probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+    });
+  else if (near)
+    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) {
       probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
     });
   else
@@ -1243,7 +1250,9 @@ __device__ __forceinline__ void drain_copies(Shared& sh) {
     mbar_wait(i & 1 ? &sh.v_full[i >> 2] : &sh.full[i >> 2], (i >> 1) & 1, nullptr, 1000000ull);
 }
 
-constexpr int kThreads = 512;
+// 14 warps of 128 registers: 8 softmax, 4 preparation, products, loads.  (A split by
+// setmaxnreg, 160 and 96, spilled in the products' and loads' warps: 8% more time.)
+constexpr int kThreads = 448;
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1284,11 +1293,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_range<kThreads>(k, sh);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  // 512 x 128 registers at launch: 256 x 168 and 256 x 88
-  if (warp < 8)
-    regs_inc<160>();
-  else
-    regs_dec<96>();
   if ((mem & 1023u) != 0) {  // not by the launch's rules: nothing is read
     if (tid == 0) report(k.a.c.dev_err, kDevErrTimeout);
   } else if (warp < 8) {
