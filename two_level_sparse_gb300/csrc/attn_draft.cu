@@ -1,5 +1,5 @@
 // Attention of drafted rows over the paged cache: dispatch, the workspace's
-// layout, and the join of units that several teams worked on (contract in
+// layout, and the join of units that several CTAs worked on (contract in
 // include/ci_draft.h; the main kernel is in attn_draft.cuh).
 #include "attn_draft.cuh"
 
@@ -14,10 +14,8 @@ constexpr int kJoinWarps = 16, kJoinRows = 8;
 
 int block_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 
-Layout layout_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-  const int group = num_q_heads / num_kv_heads, rows = block_rows(head_dim);
-  const int64_t blocks = (static_cast<int64_t>(max_rows) * group + rows - 1) / rows;
-  return Layout{device_sm_count(), static_cast<int>(blocks < 2 ? blocks : 2), group, rows};
+Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  return Layout{device_sm_count(), num_q_heads / num_kv_heads, block_rows(head_dim)};
 }
 
 // With the parts' references m_i, sums l_i and unnormalised sums o_i:
@@ -34,14 +32,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   wait_predecessor();
   const Part p = k.part[blockIdx.x];
   if (p.last < 0) return;
-  const int team = static_cast<int>(blockIdx.x) / k.l.team, member = static_cast<int>(blockIdx.x) % k.l.team;
-  const int n = p.last - team + 1, ways = n > 32 ? 16 : n > 4 ? 4 : 1, per = 32 * (kJoinWarps / ways);
+  const int n = p.last - static_cast<int>(blockIdx.x) + 1, ways = n > 32 ? 16 : n > 4 ? 4 : 1, per = 32 * (kJoinWarps / ways);
   const int way = warp % ways, group = warp / ways;
   const int first = k.a.c.req_start[p.req], row0 = p.block * k.l.block_rows;
   const int rows = min(k.l.block_rows, (k.a.c.req_start[p.req + 1] - first) * k.l.group - row0);
   const float2* stats = reinterpret_cast<const float2*>(k.stat);
   const float4* parts = reinterpret_cast<const float4*>(k.sum);
-  auto slot = [&](int i) { return 2ll * ((team + i) * k.l.team + member) + (i == 0 ? 1 : 0); };
+  auto slot = [&](int i) { return 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
 #pragma unroll 1
   for (int base = blockIdx.y * per; base < rows * (D / 4); base += gridDim.y * per) {
     const int x = base + group * 32 + lane;
@@ -92,14 +89,14 @@ int64_t stat_bytes(const Layout& l) { return 2ll * l.ctas * l.block_rows * 2 * 4
 
 }  // namespace
 
-int64_t attn_draft_workspace_bytes(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-  const Layout l = layout_of(max_rows, num_q_heads, num_kv_heads, head_dim);
+int64_t attn_draft_workspace_bytes(int32_t, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const Layout l = layout_of(num_q_heads, num_kv_heads, head_dim);
   return part_bytes(l) + stat_bytes(l) + 2ll * l.ctas * l.block_rows * head_dim * 4;
 }
 
 cudaError_t launch_attn_draft(const DraftArgs& a, cudaStream_t stream) {
   const CacheArgs& c = a.c;
-  Args k{a, layout_of(a.max_rows, c.num_q_heads, c.num_kv_heads, c.head_dim), nullptr, nullptr, nullptr};
+  Args k{a, layout_of(c.num_q_heads, c.num_kv_heads, c.head_dim), nullptr, nullptr, nullptr};
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   k.part = reinterpret_cast<Part*>(ws);
   k.stat = reinterpret_cast<float*>(ws + part_bytes(k.l));

@@ -7,10 +7,11 @@
 // query heads, are one matrix Q of n G rows (row m is node m / G, head m % G).
 // A unit is (request, key-value head, block of 128 or 256 of those rows); it
 // reads the request's positions in tiles of 128.  The units' tiles, in order,
-// are one list, split evenly over teams of CTAs (one CTA per SM); the CTAs of
-// a team take neighbouring blocks of the same rows and read the same tiles at
-// the same time, once from HBM.  A unit that several teams worked on is joined
-// in a second launch, in order.
+// are one list, split evenly over the CTAs, one per SM.  A unit that several
+// worked on is joined in a second launch, in order.  (CTAs that take a request's
+// neighbouring blocks in step read each tile once from HBM, which is 2 to 3% of
+// the time where all requests have as many blocks, and loses a fifth where they
+// have not.)
 //
 // A tile, on the fifth-generation tensor cores:
 //   S [128 rows x 128 positions] = Q K^T   both from shared memory, S in tensor memory
@@ -62,7 +63,7 @@ struct Part {  // the unit that goes on past the end of a CTA's range; last < 0:
   int32_t req, head, block, last;
 };
 struct Layout {
-  int32_t ctas, team;  // CTAs, and how many make a team
+  int32_t ctas;
   int32_t group;       // query heads per key-value head
   int32_t block_rows;  // rows of a block: 128 or 256
 };
@@ -91,6 +92,7 @@ struct Config {
   // K is read from the loaded slots, and so is V in bf16; FP8: V from operand slots
   static constexpr int kLoads = kFp8 ? (D == 64 ? 10 : 5) : (D == 64 ? 8 : 4);
   static constexpr int kOps = kFp8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kPrepWarps = kTwo ? 4 : 8;  // (one stream: those of the other one, too)
   static constexpr int kStreamThreads = kTwo ? 256 : 128;  // of the softmax
   static constexpr int kPageBytes = kFp8 ? 64 * D + 256 : 128 * D;
 };
@@ -109,7 +111,7 @@ struct Shared {
   uint32_t pages[16];                // of the last sixteen tiles: which of the two pages are there
   int32_t odd[4];                    // of the last four segments: the one where a value was not finite
   int64_t warp_sum[16];
-  int32_t first, end, total, teams;  // the team's range of the list
+  int32_t first, end, total, ctas;   // the CTA's range of the list, and how many share it
   int32_t req, head, block, tile;    // where it starts
   int32_t row0, n, len, limit;       // and that request
   uint32_t tmem;
@@ -157,36 +159,35 @@ __device__ __forceinline__ Request request_of(const Args& k, int r, int& bad) {
   q.blocks = blocks_of(k, q.n);
   return q;
 }
-// The last node of a team's blocks b, b + 1, ...
+// The last node of block b.
 __device__ __forceinline__ int last_node(const Args& k, const Request& q, int b) {
-  return static_cast<int>(min(static_cast<int64_t>(q.n), (static_cast<int64_t>(b + k.l.team) * k.l.block_rows - 1) / k.l.group + 1)) - 1;
+  return static_cast<int>(min(static_cast<int64_t>(q.n), (static_cast<int64_t>(b + 1) * k.l.block_rows - 1) / k.l.group + 1)) - 1;
 }
-// Tiles of the team's blocks from b on.
+// Tiles of block b.
 __device__ __forceinline__ int block_tiles(const Args& k, const Request& q, int b) {
   const int keys = q.limit == 0 ? 1 : k.a.mask != nullptr ? q.limit : q.len + last_node(k, q, b) + 1;
   return (keys - 1) / kKeys + 1;
 }
 // Tiles of one key-value head.
 __device__ __forceinline__ int head_tiles(const Args& k, const Request& q) {
-  if (k.a.mask != nullptr || q.limit == 0) return q.n == 0 ? 0 : (q.blocks + k.l.team - 1) / k.l.team * block_tiles(k, q, 0);
+  if (k.a.mask != nullptr || q.limit == 0) return q.n == 0 ? 0 : q.blocks * block_tiles(k, q, 0);
   int n = 0;
 #pragma unroll 1
-  for (int b = 0; b < q.blocks; b += k.l.team) n += block_tiles(k, q, b);
+  for (int b = 0; b < q.blocks; ++b) n += block_tiles(k, q, b);
   return n;
 }
 
-// A CTA's way through its team's range: tiles [i0, i1) of a unit at a time.
+// A CTA's way through its range: tiles [i0, i1) of a unit at a time.
 struct Walk {
   int left;                         // tiles of the range behind the segment
-  int r, head, block, tile, tiles;  // where the next segment starts; block: the team's first
+  int r, head, block, tile, tiles;  // where the next segment starts
   Request q;
   int i0, i1;
   __device__ __forceinline__ bool next(const Args& k) {
     if (left == 0) return false;
     if (tile == tiles) {
       tile = 0;
-      block += k.l.team;
-      if (block >= q.blocks) {
+      if (++block == q.blocks) {
         block = 0;
         if (++head == k.a.c.num_kv_heads) {
           head = 0;
@@ -206,14 +207,14 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int share_start(int team, int per, int rest) { return team * per + min(team, rest); }
-// The team that has tile x of the list.
-__device__ __forceinline__ int team_of(int x, int total, int teams) {
-  const int per = total / teams, rest = total - per * teams, longer = rest * (per + 1);
+__device__ __forceinline__ int share_start(int cta, int per, int rest) { return cta * per + min(cta, rest); }
+// The CTA that has tile x of the list.
+__device__ __forceinline__ int cta_of(int x, int total, int ctas) {
+  const int per = total / ctas, rest = total - per * ctas, longer = rest * (per + 1);
   return x < longer ? x / (per + 1) : rest + (x - longer) / per;
 }
 
-// The range of this CTA's team: every thread adds up a run of requests, a scan
+// The range of this CTA: every thread adds up a run of requests, a scan
 // over the threads gives the total, and the thread whose run holds the range's
 // first tile walks to it.
 template <int kThreads>
@@ -251,10 +252,10 @@ __device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
     sum = 0;
   }
   const int total = static_cast<int>(sum);
-  const int teams = min(k.l.ctas / k.l.team, total), per = teams > 0 ? total / teams : 0, rest = total - per * teams;
-  const int team = static_cast<int>(blockIdx.x) / k.l.team;
-  const int first = share_start(min(team, teams), per, rest), end = share_start(min(team + 1, teams), per, rest);
-  if (tid == 0) sh.first = first, sh.end = end, sh.total = total, sh.teams = teams;
+  const int ctas = min(k.l.ctas, total), per = ctas > 0 ? total / ctas : 0, rest = total - per * ctas;
+  const int cta = static_cast<int>(blockIdx.x);
+  const int first = share_start(min(cta, ctas), per, rest), end = share_start(min(cta + 1, ctas), per, rest);
+  if (tid == 0) sh.first = first, sh.end = end, sh.total = total, sh.ctas = ctas;
   if (first < end && before <= first && first < before + mine) {
     int at = static_cast<int>(first - before), r = r0, bad;
     Request q = request_of(k, r, bad);
@@ -270,11 +271,11 @@ __device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
     int b = 0;
     if (k.a.mask != nullptr || q.limit == 0) {
       const int t = block_tiles(k, q, 0);
-      b = at / t * k.l.team;
+      b = at / t;
       at -= at / t * t;
     } else {
 #pragma unroll 1
-      for (int t; at >= (t = block_tiles(k, q, b)); b += k.l.team) at -= t;
+      for (int t; at >= (t = block_tiles(k, q, b)); ++b) at -= t;
     }
     sh.req = r, sh.head = head, sh.block = b, sh.tile = at;
     sh.row0 = q.first, sh.n = q.n, sh.len = q.len, sh.limit = q.limit;
@@ -291,9 +292,8 @@ __device__ __forceinline__ Walk walk_of(const Args& k, const Shared& sh) {
   return w;
 }
 
-// A segment as one CTA of the team has it.
 struct Segment {
-  int block, rows;  // its block, and how many rows that has (0: nothing to do)
+  int rows;         // of its block
   int row0;         // its first row of the request's matrix
   bool two;         // two tiles of rows, over the same positions
   int span;         // else rows are there 128 / span times, each copy for its own span positions of a tile
@@ -303,9 +303,8 @@ struct Segment {
 template <class C>
 __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
   Segment s;
-  s.block = w.block + static_cast<int>(blockIdx.x) % k.l.team;
-  s.row0 = s.block * C::kBlockRows;
-  s.rows = s.block < w.q.blocks ? min(C::kBlockRows, w.q.n * k.l.group - s.row0) : 0;
+  s.row0 = w.block * C::kBlockRows;
+  s.rows = min(C::kBlockRows, w.q.n * k.l.group - s.row0);
   s.two = C::kTwo && s.rows > 128;
   s.span = s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
   s.tiles = w.i1 - w.i0;
@@ -515,7 +514,6 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
-    if (s.rows == 0) continue;
     const int32_t* table = c.page_table + static_cast<int64_t>(w.r) * c.max_pages;
     const int lag = s.two ? 0 : 1;
     // the pages of 32 tiles, two per lane; those of the 32 before, for V
@@ -577,15 +575,13 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 }
 
 // ------------------------------------------------------------------ preparation
-constexpr int kPrepWarps = 4;
-
 // The rows of Q: row m of the request's matrix is node m / G.  FP8: each row
 // scaled by a power of two, 1 / factor, and split into two e4m3 numbers per
 // element, one tile of each.
 template <class C>
 __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const Segment& s, const Buffers& b,
                                              float (*factor)[128], int tid) {
-  constexpr int kChunks = C::D / 8, kRowsAtOnce = 32 * kPrepWarps / kChunks;
+  constexpr int kChunks = C::D / 8, kRowsAtOnce = 32 * C::kPrepWarps / kChunks;
   const int chunk = tid % kChunks;
   const int rows = s.two ? 256 : 128;
 #pragma unroll 4
@@ -640,7 +636,7 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
 template <class C>
 __device__ __forceinline__ void prep_values(Shared& sh, const Walk& w, const Segment& s, uint32_t slot, int64_t pos0,
                                             uint32_t pages, int x, int warp, int lane, int segment) {
-  constexpr int kChunks = C::D / 8, kPer = C::kSlotKeys / kPrepWarps;
+  constexpr int kChunks = C::D / 8, kPer = C::kSlotKeys / C::kPrepWarps;
   const bool copies = !s.two && s.span < 128;
   bool odd = false;
 #pragma unroll 4
@@ -681,8 +677,8 @@ __device__ __forceinline__ uint2 widen_bf16(uint32_t r) {
 // positions q and q ^ 5, which the swizzles of both layouts put on different banks.
 template <class C>
 __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int lane) {
-  constexpr int kBlocks = C::D / 64, kCount = C::kSlotKeys / 8 * kBlocks / kPrepWarps;
-  static_assert(kPrepWarps % kBlocks == 0, "");
+  constexpr int kBlocks = C::D / 64, kCount = C::kSlotKeys / 8 * kBlocks / C::kPrepWarps;
+  static_assert(C::kPrepWarps % kBlocks == 0, "");
   const int u = lane & 3, p = (lane >> 3) ^ ((lane & 4) ? 5 : 0), block = warp % kBlocks;
   raw += C::kBox == 128 ? (block >> 1) * (C::kSlotKeys * 128) + p * 128 + (((4 * (block & 1) + u) ^ p) << 4)
                         : p * 64 + ((u ^ ((p >> 1) & 3)) << 4);
@@ -693,14 +689,14 @@ __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int l
   for (int j = 0; j < kCount; j += 4) {
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lds128(raw + (first + (j + i) * (kPrepWarps / kBlocks)) * (8 * C::kBox));
+    for (int i = 0; i < 4; ++i) v[i] = lds128(raw + (first + (j + i) * (C::kPrepWarps / kBlocks)) * (8 * C::kBox));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       uint2 r[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) r[x] = widen_bf16(c[x]);
-      const uint32_t at = (first + (j + i) * (kPrepWarps / kBlocks)) * 1024;
+      const uint32_t at = (first + (j + i) * (C::kPrepWarps / kBlocks)) * 1024;
       sts128(op0 + at, make_uint4(r[0].x, r[0].y, r[1].x, r[1].y));
       sts128(op1 + at, make_uint4(r[2].x, r[2].y, r[3].x, r[3].y));
     }
@@ -709,7 +705,7 @@ __device__ __forceinline__ void widen(uint32_t raw, uint32_t op, int warp, int l
 
 template <class C>
 __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const Buffers& b) {
-  const int tid = threadIdx.x & (32 * kPrepWarps - 1), lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x - (384 - 32 * C::kPrepWarps), lane = tid & 31, warp = tid >> 5;
   Waiter wait{sh, k.a.c.dev_err};
   Place<C::kLoads> at;
   Place<C::kFp8 ? C::kOps : 1> op;
@@ -717,7 +713,6 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
-    if (s.rows == 0) continue;
     if (wait(&sh.q_empty, (segments & 1) ^ 1)) {
       prep_queries<C>(k, w, s, b, C::kFp8 ? b.sc->factor[(segments + 1) & 1] : nullptr, tid);
       __syncwarp();
@@ -750,12 +745,9 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
           if (wait(&sh.v_full[at.slot], turn) && wait(&sh.op_empty[op.slot], op.phase ^ 1)) {
             widen<C>(raw, b.op + op.slot * C::kOperand, warp, lane);
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sh.ready[op.slot]);
-              mbar_arrive(&sh.empty[at.slot]);
-            }
           }
+          named_sync(4, 32 * C::kPrepWarps);
+          if (tid == 0 && wait.alive) mbar_arrive(&sh.ready[op.slot]), mbar_arrive(&sh.empty[at.slot]);
           op.advance();
         }
       }
@@ -797,7 +789,6 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
-    if (s.rows == 0) continue;
     auto keys = [&](int i) {  // waits for step i's keys
       if (i >= s.steps || (s.two && (i & 1))) return;
       k_slot = at.slot;
@@ -822,8 +813,7 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
         mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, 0);
         if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kIdQ, 1);  // (a step's offsets repeat)
         if (x == C::kParts - 1) mma_commit_elect(&sh.s_full[i & 1]);
-        if (last)
-          for (int y = 0; y < (C::kFp8 ? kPrepWarps : 1); ++y) mma_commit_elect(&sh.empty[slot]);
+        if (last) mma_commit_elect(&sh.empty[slot]);
         if (++slot == C::kLoads) slot = 0;
       }
       if (i == s.steps - 1) mma_commit_elect(&sh.q_empty);
@@ -1106,7 +1096,6 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
 #pragma unroll 1
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
-    if (s.rows == 0) continue;
     ++segment;
     // this thread's row of the block, and its copy's first 32 columns of a tile
     const int m0 = s.two ? g * 128 + row : row & (s.span - 1), c0 = s.two ? 0 : (row & ~(s.span - 1)) >> 5;
@@ -1236,7 +1225,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
         a.lse[t * a.c.num_q_heads + qh] = total == 0.f ? -INFINITY : (ref - (C::kFp8 ? kLift : 0.f) + log2f(total)) * 0.6931471805599453f;
     }
     if (!whole && w.i0 == 0 && g == 0 && row == 0)  // (the segment ends where the range does)
-      k.part[blockIdx.x] = Part{w.r, w.head, s.block, team_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.teams)};
+      k.part[blockIdx.x] = Part{w.r, w.head, w.block, cta_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.ctas)};
     if (joined) named_sync(1, C::kStreamThreads);  // all have read the sums
   }
 }
@@ -1272,15 +1261,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kLoads; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.empty[i], C::kFp8 ? kPrepWarps : 1);
-      mbar_init(&sh.ready[i], kPrepWarps);
-    }
-    for (int i = 0; i < C::kOps; ++i) {
-      if (i >= C::kLoads) mbar_init(&sh.ready[i], kPrepWarps);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.ready[i], C::kFp8 ? 1 : C::kPrepWarps);
       mbar_init(&sh.op_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4), mbar_init(&sh.pv_done[i], 1);
-    mbar_init(&sh.q_full, kPrepWarps);
+    mbar_init(&sh.q_full, C::kPrepWarps);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
@@ -1295,8 +1281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem;
   if ((mem & 1023u) != 0) {  // not by the launch's rules: nothing is read
     if (tid == 0) report(k.a.c.dev_err, kDevErrTimeout);
-  } else if (warp < 8) {
-    if (C::kTwo || warp < 4) softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, warp >> 2);
+  } else if (warp < C::kStreamThreads / 32) {
+    softmax<C>(k, sh, walk_of(k, sh), b.sc, tmem, warp >> 2);
   } else if (warp < 12) {
     prepare<C>(k, sh, walk_of(k, sh), b);
   } else if (warp == 12) {
