@@ -494,3 +494,179 @@ def test_trim(draft):
     draft.ci_pages_trim(t, f, i32([128, 128, 128, 129]), i32([129, 0, 65 - 64, 0]), dev_err=bits)
     assert t.tolist() == [[0, 1], [-1, -1], [3, -1], [5, 5]] and f.tolist() == [1, 1, 0, 1, 0, 1]
     assert int(bits) == LEN | PAGE_ERR
+
+
+# ------------------------------------------------------------------ together
+def test_attention_on_two_streams_and_from_graphs(draft):
+    """Calls at the same time on two streams, and replayed graphs, give what calls one after another do."""
+    ps = [Drafted([3000 + 50 * i for i in range(20)], [4 + s] * 20, 8, 2, 128, BF16, seed=s) for s in range(2)]
+    want = [p.run(draft) for p in ps]
+    args, outs = [], []
+    for p in ps:
+        out, lse = torch.empty_like(want[len(outs)][0]), torch.empty_like(want[len(outs)][1])
+        args.append((p.q.cuda(), p.k.cuda(), p.v.cuda(), p.table.cuda(), i32(p.starts), i32(p.lens), p.max_len, p.max_rows,
+                     p.scale, out, torch.as_tensor(p.mask.view(np.int32)).cuda(), lse))
+        outs.append((out, lse))
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, stream in zip(args, streams):
+            draft.ci_attn_draft(*a[:10], mask=a[10], lse=a[11], stream=stream)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    graphs = []
+    for a, stream in zip(args, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            draft.ci_attn_draft(*a[:10], mask=a[10], lse=a[11])
+        graphs.append(graph)
+    for out, lse in outs:
+        out.zero_(), lse.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+def entries(cache, r, n):
+    """A request's first n cached entries, keys and values of all layers, and their scales."""
+    at = torch.arange(n, device="cuda")
+    page, slot = cache.page_table[r].long()[at // 64], at % 64
+    d = cache.head_dim
+    width = 2 * d if cache.k.shape[-1] == 64 * 2 * d else d
+    got = []
+    for pool in (cache.k, cache.v):
+        got.append(pool[..., :64 * width].unflatten(-1, (64, width))[:, page, :, slot])
+        if width == d:
+            got.append(pool[..., 64 * d:].unflatten(-1, (64, 4))[:, page, :, slot])
+    return got
+
+
+@pytest.mark.parametrize("fmt,d,tree,graph", [(BF16, 128, True, False), (FP8, 128, True, False), (BF16, 64, False, False),
+                                              (FP8, 256, True, False), (BF16, 128, True, True), (FP8, 64, False, True)])
+def test_drafted_steps(fmt, d, tree, graph):
+    """Drafted steps leave the cache and give the results that decoding the kept tokens one by one does."""
+    from two_level_sparse_gb300.paged import PagedCache, drafted_step
+
+    rng = np.random.default_rng(d + fmt)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    hq, hkv, layers, most, steps = 8, 2, 2, 9, 4
+    lens = [126, 0, 61, 300]
+    caches = [PagedCache(layers, 4, 8, 40, hkv, d, fmt) for _ in range(2)]
+    drafted, plain = caches
+    companion = torch.randint(0, 256, (40, 8448), dtype=torch.int32, generator=gen, device="cuda").to(torch.uint8)
+    drafted.companions.append(companion)
+    norm = 1 + 0.1 * torch.randn(d, device="cuda", generator=gen)
+    angle = torch.arange(600, device="cuda")[:, None] * 10000.0 ** (-torch.arange(d // 2, device="cuda") / (d // 2))
+    cs = torch.cat([angle.cos(), angle.sin()], 1)
+    x = torch.randn(sum(lens), hq + 2 * hkv, d, device="cuda", generator=gen).bfloat16()
+    starts, at = i32(np.cumsum([0, *lens])), i32([i for n in lens for i in range(n)])
+    for c in caches:
+        c.grow(i32(lens))
+        for j in range(layers):
+            c.append(j, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], norm, norm, 1e-6, cs, True, at, 2, req_start=starts)
+    buf = dict(count=i32([0] * 4), parent=i32(np.full((4, most), -1)), token=i32(np.zeros((4, most))),
+               qkv=torch.zeros(layers, 4 * most, hq + 2 * hkv, d, dtype=torch.bfloat16, device="cuda"),
+               target=i32(np.zeros(4 * most)))
+
+    def step():
+        dr = drafted.draft(buf["count"], buf["parent"] if tree else None, buf["token"])
+        outs = drafted_step(drafted, dr, buf["qkv"], norm, norm, 1e-6, cs)
+        return dr, outs, drafted.commit(dr, buf["target"])
+
+    run = step
+    if graph:
+        step()  # with no tokens
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = step()
+
+        def run():
+            g.replay()
+            return held
+
+    for s in range(steps):
+        count = [3, most if s else 0, s, 7 - s]
+        up = random_trees(rng, count, most, wide=3)
+        token, target = rng.integers(0, 2, (4, most)), rng.integers(0, 2, 4 * most)
+        buf["count"].copy_(i32(count)), buf["parent"].copy_(i32(up)), buf["token"].copy_(i32(token))
+        buf["target"].copy_(i32(target))
+        buf["qkv"].copy_(torch.randn(buf["qkv"].shape, device="cuda", generator=gen))
+        index_before = companion.clone()
+        dr, outs, (path, kept, after) = run()
+        drafted.check()
+        start = np.concatenate([[0], np.cumsum(count)])
+        flat = [int(t) for r in range(4) for t in token[r, :count[r]]]
+        want = D.accept(start, lens, up if tree else None, flat, target, None, most)
+        np.testing.assert_array_equal(path.cpu().numpy(), want[0])
+        assert kept.tolist() == want[1] and after.tolist() == want[2] and drafted.length.tolist() == want[3]
+        # the kept tokens, one by one
+        for i in range(max(want[1])):
+            there = [i < n for n in want[1]]
+            pos = [lens[r] + i if there[r] else 0 for r in range(4)]
+            plain.grow(i32([lens[r] + min(i + 1, want[1][r]) for r in range(4)]))
+            rows = [int(start[r] + want[0][r][i]) if there[r] else 0 for r in range(4)]
+            for j in range(layers):
+                y = buf["qkv"][j, rows]
+                q = plain.append(j, y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:], norm, norm, 1e-6, cs, True, i32(pos), 0,
+                                 cache_pos=i32([p if t else -1 for p, t in zip(pos, there)]))
+                o = plain.attend(j, q, 0, i32([p + 1 if t else 0 for p, t in zip(pos, there)]))
+                for r in range(4):
+                    if there[r]:  # each is within its own rounding and its probabilities' of the exact result
+                        torch.testing.assert_close(outs[j][rows[r]].float(), o[r].float(), rtol=2 ** -7, atol=2 ** -6)
+        lens = want[3]
+        for r in range(4):
+            for a, b in zip(entries(drafted, r, lens[r]), entries(plain, r, lens[r])):
+                assert torch.equal(a, b), r
+            pages = -(-lens[r] // 64)
+            assert (drafted.page_table[r, :pages] >= 0).all() and (drafted.page_table[r, pages:] == -1).all()
+        used = drafted.page_table[drafted.page_table >= 0].long()
+        ref = torch.zeros(40, dtype=torch.int32, device="cuda").index_add_(0, used, torch.ones_like(used, dtype=torch.int32))
+        assert torch.equal(ref, drafted.ref_count)
+        if not graph:  # the index keys moved along (looked at where both pages are still there)
+            table = drafted.page_table.cpu().numpy()
+            for r in range(4):
+                old = lens[r] - want[1][r]
+                for i in range(want[1][r]):
+                    src, dst = old + int(want[0][r][i]), old + i
+                    a, b = table[r, src // 64], table[r, dst // 64]
+                    if a >= 0:
+                        for row, base in ((128, 0), (4, 64 * 128)):
+                            x, y = base + row * (dst % 64), base + row * (src % 64)
+                            assert torch.equal(companion[b, x:x + row], index_before[a, y:y + row])
+
+
+def test_draft_bookkeeping(draft):
+    """Drafts that do not fit, pages that run out, an open draft, drafts without tokens."""
+    from two_level_sparse_gb300.paged import PagedCache
+
+    cache = PagedCache(1, 3, 2, 4, 1, 64)
+    cache.grow(i32([60, 64, 120]))
+    assert (cache.ref_count > 0).all()
+    d = cache.draft(i32([3, 2, 4]), token=i32(np.ones((3, 9))))  # the second request gets no page
+    assert d.cache_pos[:9].tolist() == [60, 61, 62, -1, -1, 120, 121, 122, 123] and int(cache.dev_err) == PAGE_ERR
+    for f in (lambda: cache.grow(i32([60, 64, 120])), lambda: cache.free(i32([0])), cache.compact,
+              lambda: cache.fork(i32([0]), i32([1]), i32([3])), lambda: cache.draft(i32([1, 1, 1]), max_nodes=1)):
+        with pytest.raises(RuntimeError, match="open"):
+            f()
+    path, kept, after = cache.commit(d, i32([1] * 27))
+    assert kept.tolist() == [3, 0, 4] and after.tolist() == [1, -1, 1] and cache.length.tolist() == [63, 64, 124]
+    with pytest.raises(RuntimeError):
+        cache.commit(d, i32([1] * 27))
+    cache.dev_err.zero_()
+    d = cache.draft(i32([2, -1, 5]), token=i32(np.ones((3, 9))), rows=7)  # 124 + 5 positions do not fit two pages
+    assert d.req_start.tolist() == [0, 2, 2, 2] and int(cache.dev_err) == LEN | PAGE_ERR
+    assert d.end.tolist() == [65, 64, 124] and d.cache_pos.tolist() == [63, -1, -1, -1, -1, -1, -1]  # no page is left
+    cache.commit(d, i32([0] * 7))
+    assert cache.length.tolist() == [64, 64, 124]
+    with pytest.raises(ValueError):
+        cache.draft(i32([1, 1, 1]))
+    cache.dev_err.zero_()
+    d = cache.draft(i32([0, 0, 1]), max_nodes=1)
+    with pytest.raises(ValueError, match="tokens"):
+        cache.commit(d, i32([0] * 3))

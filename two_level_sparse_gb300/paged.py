@@ -11,19 +11,43 @@ others fill (the indexer's keys) are copied along as ``companions``.
 the new tokens' keys and values into every layer's pages, the indexer's
 positions (``step.IndexerStep``), every layer's attention over its positions.
 
+A drafted step checks several guessed tokens of every request at once:
+``PagedCache.draft`` lays the guesses' trees out behind the caches,
+``append`` and ``attend_draft`` take their rows layer by layer
+(``drafted_step``: all layers), ``commit`` keeps what the model agrees with.
+
 ``python -m two_level_sparse_gb300.paged`` serves a few synthetic requests:
-prompts, a fork, decode steps, a release and a compaction.
+prompts, a fork, decode steps, a release, a compaction and drafted steps.
 
 As in ``step``, this module allocates buffers and marshals arguments; the
 computation runs in libci.so.
 """
 from __future__ import annotations
 
+import dataclasses
+
 import torch
 
 from . import cache as ops
+from . import draft as drafts
 
 _I32 = torch.int32
+
+
+@dataclasses.dataclass(frozen=True)
+class Draft:
+    """A drafted step's rows (``PagedCache.draft``): request r's are
+    req_start[r] .. req_start[r + 1] - 1, one per node; those behind the last
+    request's belong to nobody."""
+
+    parent: torch.Tensor | None  # [requests, max_nodes]; None: chains
+    max_nodes: int
+    req_start: torch.Tensor      # [requests + 1]
+    positions: torch.Tensor      # [rows]: for the rotation
+    cache_pos: torch.Tensor      # [rows]: where the row's key and value are kept; -1: nowhere
+    mask: torch.Tensor | None    # [rows, words]: the nodes that a row sees; None: chains
+    token: torch.Tensor | None   # [rows]
+    end: torch.Tensor            # [requests]: the positions that there are pages for until the step ends
 
 
 class PagedCache:
@@ -33,8 +57,9 @@ class PagedCache:
     are int32 tensors on the cache's device; nothing but ``check`` waits.
     ``length`` [requests] is what every request holds; ``short`` is 1 where its
     last growth or fork got less than it asked for.
-    ``append`` and ``attend`` run on ``stream`` (None: the current one), whose
-    memory their results are."""
+    ``append``, ``attend`` and ``attend_draft`` run on ``stream`` (None: the
+    current one), whose memory their results are.
+    From ``draft`` to its ``commit`` no other method changes the requests."""
 
     def __init__(self, layers: int, requests: int, max_pages: int, num_pages: int, kv_heads: int, head_dim: int,
                  cache_format: int = ops.CACHE_BF16, companions=(), device="cuda"):
@@ -53,6 +78,7 @@ class PagedCache:
         self._pairs = torch.empty(3, num_pages, dtype=_I32, device=device)  # remap, copy_src, copy_dst
         self._count = torch.empty(1, dtype=_I32, device=device)
         self._workspace = {}
+        self._open = None  # the draft that is not committed yet
 
     def _copy(self, src, dst, count=None):
         pools = [*self.k, *self.v, *self.companions]
@@ -62,6 +88,10 @@ class PagedCache:
     def _limit(self):
         return ops.PAGE * self.page_table.shape[1]
 
+    def _closed(self):
+        if self._open is not None:
+            raise RuntimeError("a draft is open: commit it first")
+
     def _room(self, rows):
         """The positions for which rows of the page table have pages, from the first on."""
         return ops.PAGE * torch.where(rows < 0, self._column, self._column.shape[0]).amin(1)
@@ -70,6 +100,7 @@ class PagedCache:
         """Pages up to ``new_len`` [requests] positions; a request that is not to grow has its present length.
         Where the pages run out the length goes as far as they do, where the call refuses (fewer positions than
         there are, or more than a row has) it stays; either is ``short`` then, and in ``dev_err``."""
+        self._closed()
         ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, new_len, dev_err=self.dev_err)
         asked = torch.where(new_len <= self._limit(), new_len, 0)
         torch.maximum(self.length, torch.minimum(asked, self._room(self.page_table)), out=self.length)
@@ -86,6 +117,7 @@ class PagedCache:
         """``child[i]`` becomes the first ``length[i]`` positions of ``parent[i]``; what it held is released.
         A fork that the call refuses (its bits are in ``dev_err``) leaves both as they are; a child without a page
         for its end is ``short`` of it."""
+        self._closed()
         done = self._known(parent) & self._known(child) & (parent != child)
         done &= (length >= 0) & (length <= self._limit())
         child_done = torch.where(done, child, -1)
@@ -100,11 +132,13 @@ class PagedCache:
         self._state.index_copy_(1, at, torch.stack([got, (got != length).to(_I32)]))
 
     def free(self, req):
+        self._closed()
         ops.ci_pages_free(self.page_table, self.ref_count, req, dev_err=self.dev_err)
         self._state.index_fill_(1, self._at(req, self._known(req)), 0)
 
     def compact(self):
         """Every live page into the lowest ids."""
+        self._closed()
         remap, src, dst = self._pairs
         ops.ci_pages_compact(self.page_table, self.ref_count, remap, src, dst, self._count, dev_err=self.dev_err)
         self._copy(src, dst, self._count)
@@ -131,6 +165,88 @@ class PagedCache:
                            d ** -0.5 if scale is None else scale, out, pos=pos, workspace=self._workspace[key],
                            dev_err=self.dev_err, stream=stream, **kw)
         return out
+
+    def _pool_forms(self):
+        """Bytes of a position's row and of its scale, of every pool that a commit moves entries in."""
+        fp8 = ops.cache_format(self.k[0], self.head_dim) == ops.CACHE_FP8
+        own = (self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)
+        forms = [own] * (2 * self.k.shape[0])
+        for p in self.companions:
+            row = p.shape[-1] // ops.PAGE - 4
+            if p.dim() not in (2, 3) or row not in (64, 128) or p.shape[-1] != ops.PAGE * (row + 4):
+                raise ValueError("drafts need companions that are index-K pools: [num_pages, 8448 or 4352]")
+            forms.append((row, 4))
+        return forms
+
+    def draft(self, count, parent=None, token=None, max_nodes=None, rows=None):
+        """``count[r]`` drafted tokens of every request: a tree ``parent`` [requests, max_nodes] (None: chains), node 0
+        the token that the request goes on with, ``token`` alike.  Pages for them, and their rows; ``rows``: at
+        most so many (None: requests * max_nodes).  A count or a length that does not fit counts as no tokens, a token
+        for which the pages run out is kept nowhere and not accepted; both are in ``dev_err``."""
+        self._closed()
+        self._pool_forms()
+        requests = self.length.shape[0]
+        given = parent if parent is not None else token
+        max_nodes = given.shape[1] if given is not None else max_nodes
+        if max_nodes is None or not 1 <= max_nodes <= drafts.MAX_NODES:
+            raise ValueError(f"a tree has 1 to {drafts.MAX_NODES} nodes at most")
+        rows = requests * max_nodes if rows is None else rows
+        ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
+        fits = (count >= 0) & (count <= max_nodes) & (count <= self._limit() - self.length)
+        end = self.length + torch.where(fits, count, 0)
+        ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, end, dev_err=self.dev_err)
+        d = Draft(parent, max_nodes, ints(requests + 1), ints(rows), ints(rows),
+                  None if parent is None else ints(rows, (max_nodes + 31) // 32), None if token is None else ints(rows), end)
+        drafts.ci_draft_plan(self.length, count, parent, self.page_table, self.ref_count.shape[0], d.req_start,
+                             d.positions, d.cache_pos, mask=d.mask, token=token, row_token=d.token,
+                             max_nodes=max_nodes, dev_err=self.dev_err)
+        self._open = d
+        return d
+
+    def attend_draft(self, layer, q, draft, scale=None, out=None, stream=None, **kw):
+        """Attention of the draft's rows q [rows, heads, head_dim] over their requests' caches and their ancestors.
+        Rows of nobody get zeros (or, where ``out`` is given, are left as they are)."""
+        rows, heads, d = q.shape
+        if out is None:
+            out = ops.empty_on(stream, q.shape, q.dtype, q.device)
+            with torch.cuda.stream(stream):
+                out.zero_()
+        workspace = None  # a captured call's is the graph's own: graphs may run at the same time
+        if not torch.cuda.is_current_stream_capturing():
+            on = stream if stream is not None else torch.cuda.current_stream(q.device)
+            key = ("draft", heads, on.cuda_stream)
+            n = drafts.attn_draft_workspace_bytes(draft.max_nodes, heads, self.k.shape[2], d)
+            if key not in self._workspace or self._workspace[key].numel() < n:
+                self._workspace[key] = ops.empty_on(stream, (n,), torch.uint8, q.device)
+            workspace = self._workspace[key]
+        drafts.ci_attn_draft(q, self.k[layer], self.v[layer], self.page_table, draft.req_start, self.length, self._limit(),
+                             draft.max_nodes, d ** -0.5 if scale is None else scale, out, mask=draft.mask,
+                             workspace=workspace, dev_err=self.dev_err, stream=stream, **kw)
+        return out
+
+    def commit(self, draft, target):
+        """Ends a drafted step: ``target`` [rows] is the token that the model puts behind each row.  From node 0 on,
+        the child that the model names is kept as long as there is one; a request's length grows by what is kept.
+        Returns (path [requests, max_nodes], the kept nodes, -1 behind them; their number; the token behind the
+        last one, -1 where nothing was drafted)."""
+        if self._open is not draft:
+            raise RuntimeError("this draft is not open")
+        if draft.token is None:
+            raise ValueError("this draft was made without tokens")
+        requests = self.length.shape[0]
+        ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
+        path, kept, after, length = ints(requests, draft.max_nodes), ints(requests), ints(requests), ints(requests)
+        drafts.ci_draft_accept(draft.req_start, self.length, draft.parent, draft.token, target, path, kept, after, length,
+                               cache_pos=draft.cache_pos, dev_err=self.dev_err)
+        pools, forms = [*self.k, *self.v, *self.companions], self._pool_forms()
+        for at in range(0, len(pools), ops.MAX_POOLS):
+            part = slice(at, at + ops.MAX_POOLS)
+            drafts.ci_slots_move(pools[part], *zip(*forms[part]), self.page_table, self.length, path, kept,
+                                 dev_err=self.dev_err)
+        drafts.ci_pages_trim(self.page_table, self.ref_count, draft.end, length, dev_err=self.dev_err)
+        self.length.copy_(length)
+        self._open = None
+        return path, kept, after
 
     def check(self):
         """Waits for the device; raises if any call so far met bad data."""
@@ -162,6 +278,19 @@ def sparse_decode_step(cache: PagedCache, step, qkv, q_norm, k_norm, eps, cos_si
             for j, q in enumerate(queries)]
 
 
+def drafted_step(cache: PagedCache, draft: Draft, qkv, q_norm, k_norm, eps, cos_sin, is_neox=True):
+    """The layers of a drafted step where every layer's inputs are at hand, as ``sparse_decode_step``.
+    ``qkv[layer]``: bf16 [rows, q_heads + 2 kv_heads, head_dim].  Returns the layers' attention outputs."""
+    hkv = cache.k.shape[2]
+    hq = qkv[0].shape[1] - 2 * hkv
+    outs = []
+    for j, x in enumerate(qkv):
+        q = cache.append(j, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], q_norm, k_norm, eps, cos_sin, is_neox,
+                         draft.positions, ops.LAYOUT_VARLEN, req_start=draft.req_start, cache_pos=draft.cache_pos)
+        outs.append(cache.attend_draft(j, q, draft))
+    return outs
+
+
 def main():
     from . import synth
     from .step import IndexerStep
@@ -179,7 +308,7 @@ def main():
     step = IndexerStep(wl)  # its buffers are for the lengths to come
     wl.page_table, wl.seq_len = cache.page_table, cache.length
     norm = torch.ones(d, device=dev)
-    angle = torch.arange(max(end), device=dev)[:, None] * 10000.0 ** (-torch.arange(d // 2, device=dev) / (d // 2))
+    angle = torch.arange(max(end) + 6 * steps, device=dev)[:, None] * 10000.0 ** (-torch.arange(d // 2, device=dev) / (d // 2))
     cos_sin = torch.cat([angle.cos(), angle.sin()], 1)
     tokens = lambda n: torch.randn(n, hq + 2 * hkv, d, device=dev, generator=gen).bfloat16()  # noqa: E731
 
@@ -204,6 +333,18 @@ def main():
     cache.check()
     print(f"lengths {cache.length.tolist()}, {used} pages in use, {left} after the release; largest output "
           f"{max(float(o.abs().max()) for o in outs):.3f}")
+
+    # drafted steps: trees of six tokens for the requests that are left, a vocabulary of two
+    live = (cache.length > 0).to(_I32)
+    tree = ints(-1, 0, 0, 1, 1, 2).expand(len(end), -1).contiguous()
+    for _ in range(steps):
+        vocab = lambda *shape: torch.randint(0, 2, shape, device=dev, generator=gen, dtype=_I32)  # noqa: E731
+        now = cache.draft(6 * live, tree, vocab(len(end), 6))
+        rows = now.positions.shape[0]
+        drafted_step(cache, now, [tokens(rows) for _ in range(layers)], norm, norm, 1e-6, cos_sin)
+        _, kept, _ = cache.commit(now, vocab(rows))
+    cache.check()
+    print(f"lengths {cache.length.tolist()} after {steps} drafted steps, {kept.tolist()} tokens kept in the last")
 
 
 if __name__ == "__main__":
