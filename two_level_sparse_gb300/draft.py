@@ -35,20 +35,24 @@ for _name, _argtypes in SIGNATURES.items():
     _fn.restype = _I64 if _name.endswith("_bytes") else ctypes.c_int
 
 
+_current_device = torch._C._cuda_getDevice  # torch.cuda.current_device(), without the check that CUDA is up
+
+
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != shape:
+    """The device pointer of a contiguous int32 GPU tensor of the shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _dev(t, _I32T, name)
+    if t.dtype is not _I32T or not t.is_cuda or not t.is_contiguous():
+        return _dev(t, _I32T, name)  # says what is wrong
+    return t.data_ptr()
 
 
 def _here(t, name):
     """The launch goes to the current device: the tensors have to be there."""
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} must live on the current device")
-
-
-def _per_request(num_req, **tensors):
-    return [_shape(t, (num_req,), name) for name, t in tensors.items()]
 
 
 def ci_draft_plan(length, count, parent, page_table, num_pages, req_start, positions, cache_pos, mask=None, token=None,
@@ -66,8 +70,8 @@ def ci_draft_plan(length, count, parent, page_table, num_pages, req_start, posit
     if (token is None) != (row_token is None):
         raise ValueError("token and row_token come together")
     words = 0 if mask is None else mask.shape[1]
-    args = [*_per_request(num_req, length=length, count=count), _shape(parent, (num_req, max_nodes), "parent"),
-            _shape(token, (num_req, max_nodes), "token"), num_req, max_nodes, _ints(page_table, "page_table"),
+    args = [_shape(length, (num_req,), "length"), _shape(count, (num_req,), "count"),
+            _shape(parent, (num_req, max_nodes), "parent"), _shape(token, (num_req, max_nodes), "token"), num_req, max_nodes, _ints(page_table, "page_table"),
             max_pages, num_pages, rows, _shape(req_start, (num_req + 1,), "req_start"),
             _shape(positions, (rows,), "positions"), _shape(cache_pos, (rows,), "cache_pos"),
             _shape(mask, (rows, words), "mask"), words, _shape(row_token, (rows,), "row_token"),
@@ -128,7 +132,8 @@ def ci_draft_accept(req_start, length, parent, row_token, target, path, accepted
             _shape(parent, (num_req, max_nodes), "parent"), num_req, max_nodes, rows,
             _shape(row_token, (rows,), "row_token"), _shape(target, (rows,), "target"),
             _shape(cache_pos, (rows,), "cache_pos"), _ints(path, "path"),
-            *_per_request(num_req, accepted=accepted, next=next, new_len=new_len), _dev(dev_err, _I32T, "dev_err"),
+            _shape(accepted, (num_req,), "accepted"), _shape(next, (num_req,), "next"),
+            _shape(new_len, (num_req,), "new_len"), _dev(dev_err, _I32T, "dev_err"),
             _on(stream, path)]
     _here(path, "path")
     _check("ci_draft_accept", lib.ci_draft_accept(*args))
@@ -143,27 +148,27 @@ def ci_slots_move(pools, row_bytes, scale_bytes, page_table, length, path, count
     n = len(pools)
     if not 1 <= n <= MAX_POOLS:
         raise ValueError(f"1 to {MAX_POOLS} pools per call")
-    rows = [row_bytes] * n if isinstance(row_bytes, int) else list(row_bytes)
-    scales = [scale_bytes] * n if isinstance(scale_bytes, int) else list(scale_bytes)
+    rows = array("i", [row_bytes]) * n if isinstance(row_bytes, int) else array("i", row_bytes)
+    scales = array("i", [scale_bytes]) * n if isinstance(scale_bytes, int) else array("i", scale_bytes)
+    if len(rows) != n or len(scales) != n:
+        raise ValueError("row_bytes and scale_bytes: a number, or one for each pool")
     if isinstance(pools, torch.Tensor):
-        if pools.dim() not in (3, 4):
-            raise ValueError("pools must be [pools, num_pages, heads, bytes]")
-        base, shapes = _dev(pools, _U8, "pools"), [tuple(pools.shape[1:])] * n
+        base, shapes = _dev(pools, _U8, "pools"), [pools.shape[1:]]
         step = pools.numel() // n
-        ptrs = array("Q", [base + i * step for i in range(n)])
+        ptrs = array("Q", range(base, base + n * step, step) if step else [base] * n)
     else:
-        shapes = [tuple(p.shape) for p in pools]
+        shapes = [p.shape for p in pools]
         ptrs = array("Q", [_dev(p, _U8, "pools") for p in pools])
     num_pages = shapes[0][0]
-    heads = []
-    for shape, row, scale in zip(shapes, rows, scales, strict=True):
+    heads = array("i")
+    for shape, row, scale in {(shape, row, scale): None for shape, row, scale in
+                              zip(shapes * (n // len(shapes)), rows, scales)}:
         if len(shape) not in (2, 3) or shape[0] != num_pages or shape[-1] != PAGE * (row + scale):
             raise ValueError(f"a pool must be [{num_pages}, heads, {PAGE * (row + scale)}], got {list(shape)}")
-        heads.append(shape[1] if len(shape) == 3 else 1)
+    heads.extend([shape[1] if len(shape) == 3 else 1 for shape in shapes] * (n // len(shapes)))
     num_req, max_pages = page_table.shape
     if path.dim() != 2 or path.shape[0] != num_req:
         raise ValueError(f"path must be [{num_req}, n]")
-    heads, rows, scales = array("i", heads), array("i", rows), array("i", scales)
     _here(path, "path")
     _check("ci_slots_move", lib.ci_slots_move(
         ptrs.buffer_info()[0], heads.buffer_info()[0], rows.buffer_info()[0], scales.buffer_info()[0], n, num_pages,
@@ -175,7 +180,7 @@ def ci_slots_move(pools, row_bytes, scale_bytes, page_table, length, path, count
 def ci_pages_trim(page_table, ref_count, old_len, new_len, dev_err=None, stream=None):
     """The pages behind new_len released, where a request had old_len positions (see include/ci_draft.h)."""
     num_req = page_table.shape[0]
-    old, new = _per_request(num_req, old_len=old_len, new_len=new_len)
+    old, new = _shape(old_len, (num_req,), "old_len"), _shape(new_len, (num_req,), "new_len")
     _here(page_table, "page_table")
     _check("ci_pages_trim", lib.ci_pages_trim(*_table(page_table, ref_count), old, new, _dev(dev_err, _I32T, "dev_err"),
                                               _on(stream, page_table)))
