@@ -298,6 +298,7 @@ struct Segment {
   bool two;         // two tiles of rows, over the same positions
   int span;         // else rows are there 128 / span times, each copy for its own span positions of a tile
   int tiles, steps;
+  int lag;          // by how many tiles V's loads are behind K's
   int seen;         // positions that every row of the block sees
 };
 template <class C>
@@ -306,6 +307,7 @@ __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
   s.row0 = w.block * C::kBlockRows;
   s.rows = min(C::kBlockRows, w.q.n * k.l.group - s.row0);
   s.two = C::kTwo && s.rows > 128;
+  s.lag = C::kFp8 || s.two ? 0 : 1;
   s.span = s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
   s.tiles = w.i1 - w.i0;
   s.steps = s.two ? 2 * s.tiles : s.tiles;
@@ -500,8 +502,9 @@ __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;
 
 
 // ------------------------------------------------------------------ loads
-// K and V of the tiles, in the order in which the products take them: with two
-// tiles of rows K and V of a tile, else V a tile behind K.
+// K and V of the tiles, in the order in which they are taken: with two tiles of
+// rows K and V of a tile, else V a tile behind K; FP8: K and V of a tile, as V is
+// prepared while the tile's scores are computed.
 template <class C>
 __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, const Buffers& b, const CUtensorMap* kmap,
                                            const CUtensorMap* vmap) {
@@ -515,7 +518,7 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
   while (w.next(k)) {
     const Segment s = segment_of<C>(k, w);
     const int32_t* table = c.page_table + static_cast<int64_t>(w.r) * c.max_pages;
-    const int lag = s.two ? 0 : 1;
+    const int lag = s.lag;
     // the pages of 32 tiles, two per lane; those of the 32 before, for V
     int lo = -1, hi = -1, lo0 = -1, hi0 = -1;
 #pragma unroll 1
@@ -719,7 +722,7 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
       if (lane == 0) mbar_arrive(&sh.q_full);
     }
     ++segments;
-    const int lag = s.two ? 0 : 1;
+    const int lag = s.lag;
 #pragma unroll 1
     for (int j = 0; j < s.tiles + lag; ++j) {
 #pragma unroll 1
@@ -797,6 +800,8 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
         wait(&sh.full[at.slot], (k_turn >> at.slot) & 1);
         k_turn ^= 1u << at.slot;
       }
+      if (C::kFp8)  // (the values' slots are the preparation's)
+        for (int x = 0; x < C::kParts; ++x) at.advance();
     };
     auto scores = [&](int i) {
       if (i >= s.steps || !wait.alive) return;
@@ -831,13 +836,15 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
       if (fresh) {
         v_slot = C::kFp8 ? op.slot : at.slot;
 #pragma unroll 1
-        for (int x = 0; x < C::kParts; ++x, at.advance(), op.advance()) {
+        for (int x = 0; x < C::kParts; ++x) {
           if (C::kFp8) {
             wait(&sh.ready[op.slot], op.phase);
+            op.advance();
           } else {
             const uint32_t turn = (v_turn >> at.slot) & 1;
             if (wait(&sh.v_full[at.slot], turn)) wait(&sh.ready[at.slot], turn);
             v_turn ^= 1u << at.slot;
+            at.advance();
           }
         }
       }
