@@ -848,20 +848,20 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
           }
         }
       }
-      keys(i + 2);
+      if (C::kTwo) keys(i + 2);
       wait(&sh.p_full[i & 1], (p_turn >> (i & 1)) & 1);
       p_turn ^= 1u << (i & 1);
-      if (!wait.alive) continue;
-      tc_fence_after();
+      if (wait.alive) tc_fence_after();
 #pragma unroll 1
-      for (int x = 0, slot = v_slot; x < C::kParts; ++x) {
+      for (int x = 0, slot = v_slot; wait.alive && x < C::kParts; ++x) {
         const uint64_t db = desc128(C::kFp8 ? b.op + slot * C::kOperand : b.load + slot * C::kRaw, C::kSlotKeys * 128);
         mma_ts<ValueSteps, C::kSlotKeys / 16>(tmem + kColO + o * C::D, tmem + 128 * (i & 1) + x * (C::kSlotKeys / 2), db, kIdP,
                                               x > 0 || i >= (C::kTwo ? 2 : 1));
         if (last) mma_commit_elect(C::kFp8 ? &sh.op_empty[slot] : &sh.empty[slot]);
         if (++slot == (C::kFp8 ? C::kOps : C::kLoads)) slot = 0;
       }
-      if (!C::kTwo || i + 2 >= s.steps) mma_commit_elect(&sh.pv_done[o]);
+      if (wait.alive && (!C::kTwo || i + 2 >= s.steps)) mma_commit_elect(&sh.pv_done[o]);
+      if (!C::kTwo) keys(i + 2);  // (its slots may be those that this product frees)
       scores(i + 2);
     }
   }
@@ -1024,6 +1024,7 @@ __device__ __forceinline__ void probabilities_of(const uint32_t (&x)[32], uint32
 struct Row {
   float factor, ref;
   float2 sum;
+  bool far;  // whether a reference of the warp's rows is too large for a product and a difference in one step
 };
 template <class C>
 __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const RowMask& mask, int64_t pos0, uint32_t pages,
@@ -1049,9 +1050,11 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
   if (C::kFp8) top = ceilf(top);  // so that kLift less a reference is exact
   if (first) {
     r.ref = fmaxf(fminf(top, kFar), -kFar);
+    r.far = __any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f);
   } else if (__any_sync(0xffffffffu, top > r.ref + kSlack)) {
     const float up = fmaxf(r.ref, fminf(top, kFar)), by = exp2_approx(r.ref - up);
     r.ref = up;
+    r.far = __any_sync(0xffffffffu, fabsf(up) >= 4194304.f);
     r.sum = mul2(r.sum, make_float2(by, by));
     if (C::kTwo || wait(&sh.pv_done[0], (done - 1) & 1)) {
       tc_fence_after();
@@ -1068,7 +1071,7 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     }
   }
   float2 other = make_float2(0.f, 0.f);
-  const bool near = plain && !__any_sync(0xffffffffu, fabsf(r.ref) >= 4194304.f);
+  const bool near = plain && !r.far;
   if (near && n == 4)
     over_scores(scores, [&](int c, const uint32_t (&x)[32]) {
       probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
@@ -1112,7 +1115,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
                        node, w.q.n, w.q.len, w.q.limit, a.mask_words};
     const int seen = C::kTwo && s.two && g == 1 && a.mask == nullptr && w.q.limit > 0
                          ? w.q.len + (s.row0 + 128) / k.l.group + 1 : s.seen;
-    Row r{a.scale * attn::kLog2e, -kFar, make_float2(0.f, 0.f)};
+    Row r{a.scale * attn::kLog2e, -kFar, make_float2(0.f, 0.f), false};
     const int span = s.two ? 128 : s.span;
     const bool busy = (m0 & ~31) < s.rows;  // whether the warp has rows
 #pragma unroll 1
