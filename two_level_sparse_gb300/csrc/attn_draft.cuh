@@ -308,7 +308,10 @@ __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
   s.rows = min(C::kBlockRows, w.q.n * k.l.group - s.row0);
   s.two = C::kTwo && s.rows > 128;
   s.lag = C::kFp8 || s.two ? 0 : 1;
-  s.span = s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
+  // Copies: FP8 alone, where the softmax and the scales are what counts (32 requests of 16k, 4 nodes of 8 heads: without
+  // 327 us, with 258); in bf16 they are slower (351 and 476 us), as a copy's zeros may not meet values that are not
+  // finite, so that every tile's would have to be looked over.
+  s.span = !C::kFp8 || s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
   s.tiles = w.i1 - w.i0;
   s.steps = s.two ? 2 * s.tiles : s.tiles;
   s.seen = w.q.limit == 0 ? 0 : w.q.len + (k.a.mask != nullptr ? 0 : s.row0 / k.l.group + 1);
@@ -633,21 +636,18 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
 }
 
 // Values of a slot that not every row of the block sees (positions from s.seen
-// on; any, where rows are there more than once, as each copy has zeros for the
-// others' positions): zeros where there are none or where they are not finite,
-// which is noted.
+// on): zeros where there are none or where they are not finite, which is noted.
 template <class C>
 __device__ __forceinline__ void prep_values(Shared& sh, const Walk& w, const Segment& s, uint32_t slot, int64_t pos0,
                                             uint32_t pages, int x, int warp, int lane, int segment) {
   constexpr int kChunks = C::D / 8, kPer = C::kSlotKeys / C::kPrepWarps;
-  const bool copies = !s.two && s.span < 128;
   bool odd = false;
 #pragma unroll 4
   for (int e = lane; e < kPer * kChunks; e += 32) {
     const int p = warp * kPer + e / kChunks;
     const int64_t pos = pos0 + p;
     const bool page = (pages >> (C::kParts == 1 ? p / kPage : x)) & 1;
-    if (page && pos < s.seen && !copies) continue;
+    if (page && pos < s.seen) continue;
     const uint32_t at = slot + operand_offset(C::kSlotKeys, p, e % kChunks);
     if (!page || pos >= w.q.limit) {
       sts128(at, make_uint4(0, 0, 0, 0));
@@ -739,7 +739,7 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
           if (!C::kFp8) {
             if (!wait(&sh.v_full[at.slot], turn)) continue;
             const uint32_t pages = sh.pages[(base + t) & 15];
-            if (pages != 3 || pos0 + C::kSlotKeys > s.seen || (!s.two && s.span < 128))
+            if (pages != 3 || pos0 + C::kSlotKeys > s.seen)
               prep_values<C>(sh, w, s, raw, pos0, pages, x, warp, lane, static_cast<int>(segments));
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.ready[at.slot]);
@@ -896,14 +896,14 @@ __device__ __forceinline__ uint32_t seen_of(const RowMask& m, int64_t pos) {
   return __funnelshift_r(mask_word(m, i), mask_word(m, i + 1), static_cast<int>(rel) & 31);
 }
 
-// What a row sees that is not finite, of 16 dims from d0 on and positions from
-// `first` on: added as it is.
+// What a row sees that is not finite, of the nodes and of 16 dims from d0 on: added
+// as it is.
 template <class C>
-__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int64_t first, int d0, float (&o)[16]) {
+__device__ __noinline__ void add_odd(const Args& k, const Walk& w, const RowMask& m, int d0, float (&o)[16]) {
   const CacheArgs& c = k.a.c;
   const int64_t end = min(static_cast<int64_t>(w.i1) * kKeys, static_cast<int64_t>(w.q.limit));
 #pragma unroll 1
-  for (int64_t pos = max(first, static_cast<int64_t>(w.i0) * kKeys); pos < end; ++pos) {
+  for (int64_t pos = max(static_cast<int64_t>(w.q.len), static_cast<int64_t>(w.i0) * kKeys); pos < end; ++pos) {
     if ((seen_of(m, pos) & 1) == 0) continue;
     const int page = c.page_table[static_cast<int64_t>(w.r) * c.max_pages + pos / kPage];
     if (page < 0 || page >= c.num_pages) continue;
@@ -1209,7 +1209,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = v[j];
-          add_odd<C>(k, w, mask, span < 128 ? 0 : w.q.len, c, z);
+          add_odd<C>(k, w, mask, c, z);
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = z[j];
         }
