@@ -25,7 +25,21 @@
 //
 // The reference m of a row is the largest logit of its first tile, raised where
 // a later one passes it by 8 (in base 2): probabilities are at most 2^8, and O
-// is rescaled only then.
+// is rescaled only then.  P is rounded to bf16, an error of its size of 2^-9 for
+// the positions that carry a row, and divided by the sum of the unrounded ones.
+//
+// What bounds it.  Few rows in bf16: the HBM (32 requests of 16k, 4 nodes, 64
+// heads over 8 of 128: 2.15 GB in 338 us, 6.4 TB/s of a copy's 6.8).  Many rows: a
+// step's chain of softmax and products (64 trees of 64 nodes over 4k-16k: 1.15 ms,
+// 1200 TFLOP/s; a chunk of 2048 behind 16k: 0.875 ms, 1340 TFLOP/s).  A pair of
+// steps takes 3700 cycles, of which the tensor cores work half: a softmax of 128
+// columns is 2000 (500 the largest, 1130 the exponentials, the rest waits and
+// stores), P V and the next Q K^T behind it 1500.  Neither shared memory (38%) nor
+// exponentials (26%) nor issue slots (35%) are full.  FP8: V's widening and the
+// issuing warp's waits, 1950 cycles a tile where the HBM's rate is 1460 (64 chains
+// of 4 over 16k-64k: 1.15-1.18 ms, 4.8 TB/s).  Short calls: the start, 8000 cycles
+// until the first tile arrives, cold code, and the join (4 requests of 16 nodes
+// over 1k-4k: 32 us; one row over 16 positions: 11 us).
 //
 // Masks.  Only tiles that reach past the positions that all rows of a block see
 // have any: there a row's 128 bits come from its mask words, shifted to the
@@ -308,9 +322,10 @@ __device__ __forceinline__ Segment segment_of(const Args& k, const Walk& w) {
   s.rows = min(C::kBlockRows, w.q.n * k.l.group - s.row0);
   s.two = C::kTwo && s.rows > 128;
   s.lag = C::kFp8 || s.two ? 0 : 1;
-  // Copies: FP8 alone, where the softmax and the scales are what counts (32 requests of 16k, 4 nodes of 8 heads: without
-  // 327 us, with 258); in bf16 they are slower (351 and 476 us), as a copy's zeros may not meet values that are not
-  // finite, so that every tile's would have to be looked over.
+  // Copies: FP8 alone, where a tile's softmax and scales are what counts (32 requests of 16k, 4 nodes of 8 heads: without
+  // 311 us, with 258); in bf16 they are slower (338 and 476 us), as a copy's zeros may not meet values that are not
+  // finite, so that every tile's would have to be looked over.  (A copy's span holds at least one of the rows, so that
+  // every warp of a stream is busy where there are copies: they meet at barriers.)
   s.span = !C::kFp8 || s.rows > 64 ? 128 : s.rows > 32 ? 64 : 32;
   s.tiles = w.i1 - w.i0;
   s.steps = s.two ? 2 * s.tiles : s.tiles;

@@ -1,7 +1,10 @@
 // A drafted step's bookkeeping over the paged cache: its rows, the accepted
 // path, the moves of what is kept, the release of what is not (contract in
 // include/ci_draft.h).  All of it is bound by latency: a launch, and a chain of
-// dependent loads as long as a tree is deep.
+// dependent loads as long as a tree is deep.  200 requests of up to 64 nodes (8
+// of 16), by the kernels' own clock: plan 6.8 us (3.1), accept 2.3 (1.7), trim 1.3
+// (1.3), the moves of three tokens a request in 40 pools 10.0 (in 2: 2.5); 30 and
+// 45 us for plan and commit as Python calls, which are as long as their host side.
 #include "cache_common.cuh"
 #include "draft_internal.h"
 
