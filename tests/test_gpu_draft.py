@@ -259,6 +259,14 @@ def test_attention_strides_and_rows_of_no_request(draft, fmt):
     p.check(out, lse)
 
 
+@pytest.mark.parametrize("words", [1, 2, 5])
+@pytest.mark.parametrize("fmt", [BF16, FP8])
+def test_attention_mask_words(draft, words, fmt):
+    """Fewer words than a request has nodes (what they do not name is not seen), more, and bits behind its nodes."""
+    p = Drafted([200, 33, 0], [40, 7, 70], 8, 2, 128, fmt, "any", seed=words, words=words)
+    p.check(*p.run(draft))
+
+
 def test_attention_reports(draft):
     p = Drafted([100, 200, 50], [4, 5, 3], 4, 2, 128, BF16, seed=5)
     want, wlse = p.run(draft)
@@ -268,6 +276,11 @@ def test_attention_reports(draft):
     assert torch.equal(out[:4], want[:4]) and torch.equal(out[9:], want[9:])
     out, lse = p.run(draft, length=i32([-1, 200, 50]))
     assert int(p.err) == LEN and (out[:4] == 0).all() and torch.equal(out[4:], want[4:])
+    # more rows than was said
+    p.max_rows = 4
+    out, lse = p.run(draft)
+    assert int(p.err) == LEN and (out[4:9] == 0).all() and torch.equal(out[:4], want[:4]) and torch.equal(out[9:], want[9:])
+    p.max_rows = 5
     # starts that descend or leave the rows: none of that request's
     res = torch.full_like(want, 5.0)
     out, _ = p.run(draft, out=res, req_start=i32([0, 4, 99, 12]))
@@ -575,7 +588,7 @@ def test_drafted_steps(fmt, d, tree, graph):
                target=i32(np.zeros(4 * most)))
 
     def step():
-        dr = drafted.draft(buf["count"], buf["parent"] if tree else None, buf["token"])
+        dr = drafted.draft(buf["count"], buf["token"], buf["parent"] if tree else None)
         outs = drafted_step(drafted, dr, buf["qkv"], norm, norm, 1e-6, cs)
         return dr, outs, drafted.commit(dr, buf["target"])
 
@@ -642,31 +655,38 @@ def test_drafted_steps(fmt, d, tree, graph):
 
 
 def test_draft_bookkeeping(draft):
-    """Drafts that do not fit, pages that run out, an open draft, drafts without tokens."""
+    """Drafts that do not fit, pages that run out, an open draft, one that is dropped."""
     from two_level_sparse_gb300.paged import PagedCache
 
-    cache = PagedCache(1, 3, 2, 4, 1, 64)
+    cache, ones = PagedCache(1, 3, 2, 4, 1, 64), i32(np.ones((3, 9)))
     cache.grow(i32([60, 64, 120]))
     assert (cache.ref_count > 0).all()
-    d = cache.draft(i32([3, 2, 4]), token=i32(np.ones((3, 9))))  # the second request gets no page
+    d = cache.draft(i32([3, 2, 4]), ones)  # the second request gets no page
     assert d.cache_pos[:9].tolist() == [60, 61, 62, -1, -1, 120, 121, 122, 123] and int(cache.dev_err) == PAGE_ERR
     for f in (lambda: cache.grow(i32([60, 64, 120])), lambda: cache.free(i32([0])), cache.compact,
-              lambda: cache.fork(i32([0]), i32([1]), i32([3])), lambda: cache.draft(i32([1, 1, 1]), max_nodes=1)):
+              lambda: cache.fork(i32([0]), i32([1]), i32([3])), lambda: cache.draft(i32([1, 1, 1]), ones)):
         with pytest.raises(RuntimeError, match="open"):
             f()
     path, kept, after = cache.commit(d, i32([1] * 27))
     assert kept.tolist() == [3, 0, 4] and after.tolist() == [1, -1, 1] and cache.length.tolist() == [63, 64, 124]
-    with pytest.raises(RuntimeError):
-        cache.commit(d, i32([1] * 27))
+    q = torch.zeros(27, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for f in (lambda: cache.commit(d, i32([1] * 27)), lambda: cache.drop(d), lambda: cache.attend_draft(0, q, d)):
+        with pytest.raises(RuntimeError, match="not open"):
+            f()
     cache.dev_err.zero_()
-    d = cache.draft(i32([2, -1, 5]), token=i32(np.ones((3, 9))), rows=7)  # 124 + 5 positions do not fit two pages
+    d = cache.draft(i32([2, -1, 5]), ones, rows=7)  # 124 + 5 positions do not fit two pages, no page is left for 63 + 2
     assert d.req_start.tolist() == [0, 2, 2, 2] and int(cache.dev_err) == LEN | PAGE_ERR
-    assert d.end.tolist() == [65, 64, 124] and d.cache_pos.tolist() == [63, -1, -1, -1, -1, -1, -1]  # no page is left
+    assert d.end.tolist() == [65, 64, 124] and d.cache_pos.tolist() == [63, -1, -1, -1, -1, -1, -1]
     cache.commit(d, i32([0] * 7))
     assert cache.length.tolist() == [64, 64, 124]
+    cache = PagedCache(1, 2, 4, 8, 1, 64)
+    cache.grow(i32([60, 1]))
+    before = cache.page_table.clone(), cache.ref_count.clone()
+    cache.drop(cache.draft(i32([9, 9]), i32(np.ones((2, 9)))))
+    assert torch.equal(cache.page_table, before[0]) and torch.equal(cache.ref_count, before[1])
+    assert cache.length.tolist() == [60, 1] and int(cache.dev_err) == 0
     with pytest.raises(ValueError):
-        cache.draft(i32([1, 1, 1]))
-    cache.dev_err.zero_()
-    d = cache.draft(i32([0, 0, 1]), max_nodes=1)
-    with pytest.raises(ValueError, match="tokens"):
-        cache.commit(d, i32([0] * 3))
+        cache.draft(i32([1, 1]), i32(np.ones((2, 257))))
+    cache.companions.append(torch.zeros(8, 100, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="companions"):
+        cache.draft(i32([1, 1]), i32(np.ones((2, 2))))

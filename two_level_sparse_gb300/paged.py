@@ -46,7 +46,7 @@ class Draft:
     positions: torch.Tensor      # [rows]: for the rotation
     cache_pos: torch.Tensor      # [rows]: where the row's key and value are kept; -1: nowhere
     mask: torch.Tensor | None    # [rows, words]: the nodes that a row sees; None: chains
-    token: torch.Tensor | None   # [rows]
+    token: torch.Tensor          # [rows]
     end: torch.Tensor            # [requests]: the positions that there are pages for until the step ends
 
 
@@ -59,7 +59,7 @@ class PagedCache:
     last growth or fork got less than it asked for.
     ``append``, ``attend`` and ``attend_draft`` run on ``stream`` (None: the
     current one), whose memory their results are.
-    From ``draft`` to its ``commit`` no other method changes the requests."""
+    From ``draft`` to its ``commit`` or ``drop`` no other method changes the requests."""
 
     def __init__(self, layers: int, requests: int, max_pages: int, num_pages: int, kv_heads: int, head_dim: int,
                  cache_format: int = ops.CACHE_BF16, companions=(), device="cuda"):
@@ -90,7 +90,7 @@ class PagedCache:
 
     def _closed(self):
         if self._open is not None:
-            raise RuntimeError("a draft is open: commit it first")
+            raise RuntimeError("a draft is open: commit or drop it first")
 
     def _room(self, rows):
         """The positions for which rows of the page table have pages, from the first on."""
@@ -178,17 +178,19 @@ class PagedCache:
             forms.append((row, 4))
         return forms
 
-    def draft(self, count, parent=None, token=None, max_nodes=None, rows=None):
-        """``count[r]`` drafted tokens of every request: a tree ``parent`` [requests, max_nodes] (None: chains), node 0
-        the token that the request goes on with, ``token`` alike.  Pages for them, and their rows; ``rows``: at
+    def _is_open(self, draft):
+        if self._open is not draft:
+            raise RuntimeError("this draft is not open")
+
+    def draft(self, count, token, parent=None, rows=None):
+        """``count[r]`` drafted tokens ``token`` [requests, max_nodes] of every request: a tree ``parent``, alike
+        (None: chains), node 0 the token that the request goes on with.  Pages for them, and their rows; ``rows``: at
         most so many (None: requests * max_nodes).  A count or a length that does not fit counts as no tokens, a token
         for which the pages run out is kept nowhere and not accepted; both are in ``dev_err``."""
         self._closed()
         self._pool_forms()
-        requests = self.length.shape[0]
-        given = parent if parent is not None else token
-        max_nodes = given.shape[1] if given is not None else max_nodes
-        if max_nodes is None or not 1 <= max_nodes <= drafts.MAX_NODES:
+        requests, max_nodes = token.shape
+        if not 1 <= max_nodes <= drafts.MAX_NODES:
             raise ValueError(f"a tree has 1 to {drafts.MAX_NODES} nodes at most")
         rows = requests * max_nodes if rows is None else rows
         ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
@@ -196,16 +198,17 @@ class PagedCache:
         end = self.length + torch.where(fits, count, 0)
         ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, end, dev_err=self.dev_err)
         d = Draft(parent, max_nodes, ints(requests + 1), ints(rows), ints(rows),
-                  None if parent is None else ints(rows, (max_nodes + 31) // 32), None if token is None else ints(rows), end)
+                  None if parent is None else ints(rows, (max_nodes + 31) // 32), ints(rows), end)
         drafts.ci_draft_plan(self.length, count, parent, self.page_table, self.ref_count.shape[0], d.req_start,
                              d.positions, d.cache_pos, mask=d.mask, token=token, row_token=d.token,
-                             max_nodes=max_nodes, dev_err=self.dev_err)
+                             dev_err=self.dev_err)
         self._open = d
         return d
 
     def attend_draft(self, layer, q, draft, scale=None, out=None, stream=None, **kw):
         """Attention of the draft's rows q [rows, heads, head_dim] over their requests' caches and their ancestors.
         Rows of nobody get zeros (or, where ``out`` is given, are left as they are)."""
+        self._is_open(draft)
         rows, heads, d = q.shape
         if out is None:
             out = ops.empty_on(stream, q.shape, q.dtype, q.device)
@@ -229,10 +232,7 @@ class PagedCache:
         the child that the model names is kept as long as there is one; a request's length grows by what is kept.
         Returns (path [requests, max_nodes], the kept nodes, -1 behind them; their number; the token behind the
         last one, -1 where nothing was drafted)."""
-        if self._open is not draft:
-            raise RuntimeError("this draft is not open")
-        if draft.token is None:
-            raise ValueError("this draft was made without tokens")
+        self._is_open(draft)
         requests = self.length.shape[0]
         ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
         path, kept, after, length = ints(requests, draft.max_nodes), ints(requests), ints(requests), ints(requests)
@@ -247,6 +247,12 @@ class PagedCache:
         self.length.copy_(length)
         self._open = None
         return path, kept, after
+
+    def drop(self, draft):
+        """Ends a drafted step of which nothing is kept."""
+        self._is_open(draft)
+        drafts.ci_pages_trim(self.page_table, self.ref_count, draft.end, self.length, dev_err=self.dev_err)
+        self._open = None
 
     def check(self):
         """Waits for the device; raises if any call so far met bad data."""
@@ -339,7 +345,7 @@ def main():
     tree = ints(-1, 0, 0, 1, 1, 2).expand(len(end), -1).contiguous()
     for _ in range(steps):
         vocab = lambda *shape: torch.randint(0, 2, shape, device=dev, generator=gen, dtype=_I32)  # noqa: E731
-        now = cache.draft(6 * live, tree, vocab(len(end), 6))
+        now = cache.draft(6 * live, vocab(len(end), 6), tree)
         rows = now.positions.shape[0]
         drafted_step(cache, now, [tokens(rows) for _ in range(layers)], norm, norm, 1e-6, cos_sin)
         _, kept, _ = cache.commit(now, vocab(rows))
