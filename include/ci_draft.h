@@ -95,7 +95,7 @@ CI_API int ci_draft_plan(const int32_t* length, const int32_t* count, const int3
  * Any finite logits; values |v| <= 2^80; FP8: scales finite, |scale| <= 2^60,
  * and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *
- * max_len <= 64 * max_pages; max_rows >= 1: no request has more rows;
+ * max_len <= 64 * max_pages; max_rows >= 0: no request has more rows;
  * mask_words >= 1 (ignored for NULL).  rows * G < 2^31, and with B = min(num_req * ceil(max_rows *
  * G / 128), ceil(rows * G / 128) + num_req), G = num_q_heads / num_kv_heads:
  * num_kv_heads * B * (max_len / 128 + 1) < 2^31.

@@ -259,6 +259,22 @@ def test_attention_strides_and_rows_of_no_request(draft, fmt):
     p.check(out, lse)
 
 
+def test_calls_with_no_rows(draft):
+    """A step in which nobody drafts: every call runs and changes nothing."""
+    p = Drafted([100, 30], [0, 0], 8, 2, 128, BF16)
+    p.max_rows = 0
+    out, lse = p.run(draft)
+    assert out.shape == (0, 8, 128) and int(p.err) == 0
+    empty, bits = i32([]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    path, kept, after, new = i32([[9, 9]] * 2), i32([9, 9]), i32([9, 9]), i32([9, 9])
+    draft.ci_draft_accept(i32([0, 0, 0]), i32([100, 30]), None, empty, empty, path, kept, after, new, dev_err=bits)
+    assert path.tolist() == [[-1, -1]] * 2 and kept.tolist() == [0, 0] and after.tolist() == [-1, -1]
+    assert new.tolist() == [100, 30]
+    pool = p.k.cuda()
+    draft.ci_slots_move([pool], 256, 0, p.table.cuda(), i32([100, 30]), path, kept, dev_err=bits)
+    assert torch.equal(pool.cpu(), p.k) and int(bits) == 0
+
+
 @pytest.mark.parametrize("words", [1, 2, 5])
 @pytest.mark.parametrize("fmt", [BF16, FP8])
 def test_attention_mask_words(draft, words, fmt):

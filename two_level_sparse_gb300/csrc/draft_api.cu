@@ -47,7 +47,7 @@ int ci_draft_plan(const int32_t* length, const int32_t* count, const int32_t* pa
 int64_t ci_attn_draft_workspace_bytes(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
   const int st = check_heads(num_q_heads, num_kv_heads, head_dim);
   if (st != CI_OK) return st;
-  if (max_rows < 1) return CI_ERR_SHAPE;
+  if (max_rows < 0) return CI_ERR_SHAPE;
   return ci::attn_draft_workspace_bytes(max_rows, num_q_heads, num_kv_heads, head_dim);
 }
 
@@ -64,8 +64,9 @@ int ci_attn_draft(const uint16_t* q, int64_t q_stride, int32_t rows, int32_t num
   st = check_requests(num_req, max_pages, num_pages);
   if (st != CI_OK) return st;
   if (num_req < 1) return CI_ERR_RANGE;
-  if (max_rows < 1 || (mask && mask_words < 1)) return CI_ERR_SHAPE;
+  if (max_rows < 0) return CI_ERR_SHAPE;
   if (rows == 0) return CI_OK;
+  if (mask && mask_words < 1) return CI_ERR_SHAPE;
   if (!q || !k_pool || !v_pool || !page_table || !req_start || !length || !out || !ws) return CI_ERR_NULL;
   if (num_pages < 1 || num_pages * num_kv_heads * (CI_PAGE + 256 / head_dim) > INT32_MAX) return CI_ERR_RANGE;
   if (static_cast<int64_t>(max_len) > static_cast<int64_t>(max_pages) * CI_PAGE) return CI_ERR_SHAPE;
