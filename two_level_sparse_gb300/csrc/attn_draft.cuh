@@ -55,7 +55,6 @@
 // probability.
 #pragma once
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "attn.cuh"
 #include "draft_internal.h"
@@ -596,6 +595,16 @@ __device__ __forceinline__ void load_tiles(const Args& k, Shared& sh, Walk w, co
 }
 
 // ------------------------------------------------------------------ preparation
+__device__ __forceinline__ uint32_t f16x2_to_e4m3(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ __half2 e4m3x2_to_f16(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
+  return *reinterpret_cast<const __half2*>(&r);
+}
 // The rows of Q: row m of the request's matrix is node m / G.  FP8: each row
 // scaled by a power of two, 1 / factor, and split into two e4m3 numbers per
 // element, one tile of each.
@@ -604,13 +613,17 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
                                              float (*factor)[128], int tid) {
   constexpr int kChunks = C::D / 8, kRowsAtOnce = 32 * C::kPrepWarps / kChunks;
   const int chunk = tid % kChunks;
-  const int rows = s.two ? 256 : 128;
+  const int rows = s.two ? 256 : 128, group = k.l.group;
+  // y / group = y inv / 2^16 rounded down, for y < 384 and group <= 128
+  const uint32_t inv = (65535u + group) / group;
+  const int node0 = s.row0 / group, rest0 = s.row0 - node0 * group;
+  const uint16_t* first = k.a.q + (w.q.first + node0) * k.a.q_stride + static_cast<int64_t>(w.head) * group * C::D + chunk * 8;
 #pragma unroll 4
   for (int m = tid / kChunks; m < rows; m += kRowsAtOnce) {
-    const int of = s.two ? m : m & (s.span - 1), x = s.row0 + of, node = x / k.l.group;
+    const int of = s.two ? m : m & (s.span - 1);
     const bool there = of < s.rows;
-    const uint16_t* src = k.a.q + (w.q.first + (there ? node : 0)) * k.a.q_stride +
-                          (static_cast<int64_t>(w.head) * k.l.group + (there ? x - node * k.l.group : 0)) * C::D + chunk * 8;
+    const uint32_t y = there ? rest0 + of : 0, node = (y * inv) >> 16;
+    const uint16_t* src = first + node * k.a.q_stride + (y - node * group) * C::D;
     const int row = m & 127;
     const uint32_t tile = b.q + (m >> 7) * C::kQ;
     if (!C::kFp8) {
@@ -620,9 +633,10 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
     uint4 v = make_uint4(0, 0, 0, 0);
     if (there) v = *reinterpret_cast<const uint4*>(src);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // the largest magnitude's bits
+    uint32_t top = 0;  // the largest magnitudes' bits, of even and of odd dims
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, u[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
     for (int o = 1; o < kChunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = static_cast<int>(top >> 7);  // biased; 255: not finite
@@ -630,11 +644,11 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
     const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -120 <= up <= 126
     uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = make_float2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
-      uint32_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-      const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3)));
-      const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {  // (f16 has the scaled elements exactly, down to 2^-32 of the largest)
+      const uint32_t x = attn::f16x2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
+      uint32_t h = f16x2_to_e4m3(x);
+      const __half2 less = __hsub2(*reinterpret_cast<const __half2*>(&x), e4m3x2_to_f16(h));
+      const uint32_t l = f16x2_to_e4m3(*reinterpret_cast<const uint32_t*>(&less));
       if (e == 255) h = 0x7F7F;  // a row that is not finite: NaN
       hi[i >> 1] |= h << (16 * (i & 1)), lo[i >> 1] |= l << (16 * (i & 1));
     }
