@@ -965,15 +965,21 @@ __device__ __forceinline__ void over_scores(uint32_t at, F f) {
   }
 }
 // n times 32 of them, one after another: the code is a quarter, and a call's first
-// tiles and its masked ones run it cold.
-template <class F>
-__device__ __forceinline__ void over_some_scores(uint32_t at, int n, F f) {
+// tiles and its masked ones run it cold.  bits(c) are those that the row sees; where
+// no row of the warp sees any, none(c) instead, and f is told where all see all.
+template <class B, class F, class N>
+__device__ __forceinline__ void over_some_scores(uint32_t at, int n, bool masked, B bits, F f, N none) {
 #pragma unroll 1
   for (int c = 0; c < n; ++c) {
+    const uint32_t seen = masked ? bits(c) : ~0u;
+    if (masked && !__any_sync(0xffffffffu, seen != 0)) {
+      none(c);
+      continue;
+    }
     uint32_t x[32];
     tmem_ld32(at + 32 * c, x);
     tmem_ld_wait();
-    f(c, x);
+    f(c, x, seen, !masked || __all_sync(0xffffffffu, seen == ~0u));
   }
 }
 // Two scores, times their keys' scales.
@@ -1062,19 +1068,21 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
   const bool masked = pages != 3 || pos0 + kKeys > seen, plain = !masked, down = r.factor < 0.f;
   const uint32_t scores = at + 32 * c0, to = at + 16 * c0;
   if (C::kFp8) ks += 32 * c0, vs += 32 * c0;
-  auto bits_of = [&](int c) {
-    return !masked ? ~0u : (pages >> ((c0 + c) >> 1)) & 1 ? seen_of(mask, pos0 + 32 * (c0 + c)) : 0;
-  };
+  auto bits_of = [&](int c) { return (pages >> ((c0 + c) >> 1)) & 1 ? seen_of(mask, pos0 + 32 * (c0 + c)) : 0; };
   // the largest logit (base 2): of the scores, as rounding keeps their order
   float top = down ? INFINITY : -INFINITY;
   if (plain && n == 4 && !down)
     over_scores(scores, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
-  else if (plain && !down)
-    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
-  else if (!down)
-    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, true, false>(x, bits_of(c), ks + 32 * c, top); });
   else
-    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, true, true>(x, bits_of(c), ks + 32 * c, top); });
+    over_some_scores(
+        scores, n, masked, bits_of,
+        [&](int c, const uint32_t (&x)[32], uint32_t bits, bool all) {
+          if (down)
+            top = top_of<C, true, true>(x, bits, ks + 32 * c, top);
+          else
+            top = all ? top_of<C, false, false>(x, 0, ks + 32 * c, top) : top_of<C, true, false>(x, bits, ks + 32 * c, top);
+        },
+        [](int) {});
   top = r.factor == 0.f && fabsf(top) == INFINITY ? -INFINITY : top * r.factor;
   if (C::kFp8) top = ceilf(top);  // so that kLift less a reference is exact
   if (first) {
@@ -1100,27 +1108,29 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     }
   }
   float2 other = make_float2(0.f, 0.f);
-  const bool near = plain && !r.far;
-  if (near && n == 4)
-    over_scores(scores, [&](int c, const uint32_t (&x)[32]) {
-      probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
-    });
-  else if (near)
-    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) {
-      probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
-    });
-  else
-    over_some_scores(scores, n, [&](int c, const uint32_t (&x)[32]) {
-      probabilities_of<C, true>(x, to + 16 * c, bits_of(c), ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
-    });
-  r.sum = add2(r.sum, other);
-#pragma unroll 1
-  for (int c = n; c < 4; ++c) {
+  auto zeros = [&](int c) {
     uint32_t none[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) none[j] = 0;
     tmem_st16(at + 16 * ((c0 + c) & 3), none);
-  }
+  };
+  if (plain && !r.far && n == 4)
+    over_scores(scores, [&](int c, const uint32_t (&x)[32]) {
+      probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+    });
+  else
+    over_some_scores(
+        scores, n, masked, bits_of,
+        [&](int c, const uint32_t (&x)[32], uint32_t bits, bool all) {
+          if (all && !r.far)
+            probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+          else
+            probabilities_of<C, true>(x, to + 16 * c, bits, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+        },
+        zeros);
+  r.sum = add2(r.sum, other);
+#pragma unroll 1
+  for (int c = n; c < 4; ++c) zeros(c);
   tmem_st_wait();
 }
 
