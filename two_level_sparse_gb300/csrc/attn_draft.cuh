@@ -454,6 +454,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -965,21 +970,30 @@ __device__ __forceinline__ void over_scores(uint32_t at, F f) {
   }
 }
 // n times 32 of them, one after another: the code is a quarter, and a call's first
-// tiles and its masked ones run it cold.  bits(c) are those that the row sees; where
-// no row of the warp sees any, none(c) instead, and f is told where all see all.
-template <class B, class F, class N>
-__device__ __forceinline__ void over_some_scores(uint32_t at, int n, bool masked, B bits, F f, N none) {
+// tiles and its masked ones run it cold.  bits(c) are those that the row sees: where
+// no row of the warp sees any, none(c); where some see some or `careful` asks for
+// it, part(c, j, x, bits) for 16 from j on.
+template <class B, class F, class P, class N>
+__device__ __forceinline__ void over_some_scores(uint32_t at, int n, bool masked, bool careful, B bits, F all, P part, N none) {
 #pragma unroll 1
   for (int c = 0; c < n; ++c) {
     const uint32_t seen = masked ? bits(c) : ~0u;
     if (masked && !__any_sync(0xffffffffu, seen != 0)) {
       none(c);
-      continue;
+    } else if (!careful && (!masked || __all_sync(0xffffffffu, seen == ~0u))) {
+      uint32_t x[32];
+      tmem_ld32(at + 32 * c, x);
+      tmem_ld_wait();
+      all(c, x);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < 32; j += 16) {
+        uint32_t x[16];
+        tmem_ld16(at + 32 * c + j, x);
+        tmem_ld_wait();
+        part(c, j, x, seen >> j);
+      }
     }
-    uint32_t x[32];
-    tmem_ld32(at + 32 * c, x);
-    tmem_ld_wait();
-    f(c, x, seen, !masked || __all_sync(0xffffffffu, seen == ~0u));
   }
 }
 // Two scores, times their keys' scales.
@@ -990,12 +1004,12 @@ __device__ __forceinline__ float2 scores_of(uint32_t s0, uint32_t s1, float k0, 
 }
 __device__ __forceinline__ bool bit(uint32_t bits, int j) { return (bits >> j) & 1; }
 
-// The largest of 32 scores and `top` (kDown: the smallest).
-template <class C, bool kCareful, bool kDown>
-__device__ __forceinline__ float top_of(const uint32_t (&x)[32], uint32_t bits, const float* ks, float top) {
+// The largest of N scores and `top` (kDown: the smallest).
+template <class C, bool kCareful, bool kDown, int N>
+__device__ __forceinline__ float top_of(const uint32_t (&x)[N], uint32_t bits, const float* ks, float top) {
   float other = top;
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
+  for (int j = 0; j < N; j += 4) {
     float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
     if (C::kFp8) f = *reinterpret_cast<const float4*>(ks + j);
     float2 y = scores_of<C>(x[j], x[j + 1], f.x, f.y), z = scores_of<C>(x[j + 2], x[j + 3], f.z, f.w);
@@ -1010,18 +1024,18 @@ __device__ __forceinline__ float top_of(const uint32_t (&x)[32], uint32_t bits, 
   return kDown ? fminf(top, other) : fmaxf(top, other);
 }
 
-// 32 probabilities, over their scores, and their sum.  kCareful: masked, or
+// N probabilities, over their scores, and their sum.  kCareful: masked, or
 // logits that are rounded by themselves, as the reference is (a product and a
 // difference in one step are off by half of the reference's last place, which
 // only counts where logits pass 2^22).
-template <class C, bool kCareful>
-__device__ __forceinline__ void probabilities_of(const uint32_t (&x)[32], uint32_t to, uint32_t bits, const float* ks,
+template <class C, bool kCareful, int N>
+__device__ __forceinline__ void probabilities_of(const uint32_t (&x)[N], uint32_t to, uint32_t bits, const float* ks,
                                                  const float* vs, float factor, float ref, float2& sum, float2& other) {
   const float up = C::kFp8 ? kLift - ref : -ref;
   const float2 less = make_float2(up, up), by = make_float2(factor, factor);
-  uint32_t p[16];
+  uint32_t p[N / 2];
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
+  for (int j = 0; j < N; j += 4) {
     float4 f = make_float4(1.f, 1.f, 1.f, 1.f), h = f;
     if (C::kFp8) {
       f = *reinterpret_cast<const float4*>(ks + j);
@@ -1051,7 +1065,10 @@ __device__ __forceinline__ void probabilities_of(const uint32_t (&x)[32], uint32
     }
     p[j / 2] = bf16x2(y.x, y.y), p[j / 2 + 1] = bf16x2(z.x, z.y);
   }
-  tmem_st16(to, p);
+  if constexpr (N == 32)
+    tmem_st16(to, p);
+  else
+    tmem_st8(to, p);
 }
 
 // A step of the softmax for a warp that has the 32 n columns of the buffer `at` from
@@ -1075,12 +1092,10 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     over_scores(scores, [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); });
   else
     over_some_scores(
-        scores, n, masked, bits_of,
-        [&](int c, const uint32_t (&x)[32], uint32_t bits, bool all) {
-          if (down)
-            top = top_of<C, true, true>(x, bits, ks + 32 * c, top);
-          else
-            top = all ? top_of<C, false, false>(x, 0, ks + 32 * c, top) : top_of<C, true, false>(x, bits, ks + 32 * c, top);
+        scores, n, masked, down, bits_of,
+        [&](int c, const uint32_t (&x)[32]) { top = top_of<C, false, false>(x, 0, ks + 32 * c, top); },
+        [&](int c, int j, const uint32_t (&x)[16], uint32_t bits) {
+          top = down ? top_of<C, true, true>(x, bits, ks + 32 * c + j, top) : top_of<C, true, false>(x, bits, ks + 32 * c + j, top);
         },
         [](int) {});
   top = r.factor == 0.f && fabsf(top) == INFINITY ? -INFINITY : top * r.factor;
@@ -1120,12 +1135,12 @@ __device__ __forceinline__ void softmax_step(Shared& sh, Waiter& wait, const Row
     });
   else
     over_some_scores(
-        scores, n, masked, bits_of,
-        [&](int c, const uint32_t (&x)[32], uint32_t bits, bool all) {
-          if (all && !r.far)
-            probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
-          else
-            probabilities_of<C, true>(x, to + 16 * c, bits, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+        scores, n, masked, r.far, bits_of,
+        [&](int c, const uint32_t (&x)[32]) {
+          probabilities_of<C, false>(x, to + 16 * c, 0, ks + 32 * c, vs + 32 * c, r.factor, r.ref, r.sum, other);
+        },
+        [&](int c, int j, const uint32_t (&x)[16], uint32_t bits) {
+          probabilities_of<C, true>(x, to + 16 * c + j / 2, bits, ks + 32 * c + j, vs + 32 * c + j, r.factor, r.ref, r.sum, other);
         },
         zeros);
   r.sum = add2(r.sum, other);
