@@ -623,49 +623,81 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
   const uint32_t inv = (65535u + group) / group;
   const int node0 = s.row0 / group, rest0 = s.row0 - node0 * group;
   const uint16_t* first = k.a.q + (w.q.first + node0) * k.a.q_stride + static_cast<int64_t>(w.head) * group * C::D + chunk * 8;
-#pragma unroll 4
-  for (int m = tid / kChunks; m < rows; m += kRowsAtOnce) {
+  auto row_of = [&](int m, bool& there) {
     const int of = s.two ? m : m & (s.span - 1);
-    const bool there = of < s.rows;
+    there = of < s.rows;
     const uint32_t y = there ? rest0 + of : 0, node = (y * inv) >> 16;
-    const uint16_t* src = first + node * k.a.q_stride + (y - node * group) * C::D;
-    const int row = m & 127;
-    const uint32_t tile = b.q + (m >> 7) * C::kQ;
-    if (!C::kFp8) {
-      attn::copy16(tile + operand_offset(128, row, chunk), reinterpret_cast<const uint8_t*>(src), there);
-      continue;
+    return first + node * k.a.q_stride + (y - node * group) * C::D;
+  };
+  if (!C::kFp8) {
+#pragma unroll 4
+    for (int m = tid / kChunks; m < rows; m += kRowsAtOnce) {
+      bool there;
+      const uint16_t* src = row_of(m, there);
+      attn::copy16(b.q + (m >> 7) * C::kQ + operand_offset(128, m & 127, chunk), reinterpret_cast<const uint8_t*>(src), there);
     }
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (there) v = *reinterpret_cast<const uint4*>(src);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // the largest magnitudes' bits, of even and of odd dims
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, u[i] & 0x7FFF7FFFu);
-    top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-    for (int o = 1; o < kChunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = static_cast<int>(top >> 7);  // biased; 255: not finite
-    const int up = e == 255 || top == 0 ? 0 : min(7 - (e - 127), 126);
-    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -120 <= up <= 126
-    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // (f16 has the scaled elements exactly, down to 2^-32 of the largest)
-      const uint32_t x = attn::f16x2(bf16_lo(u[i]) * f, bf16_hi(u[i]) * f);
-      uint32_t h = f16x2_to_e4m3(x);
-      const __half2 less = __hsub2(*reinterpret_cast<const __half2*>(&x), e4m3x2_to_f16(h));
-      const uint32_t l = f16x2_to_e4m3(*reinterpret_cast<const uint32_t*>(&less));
-      if (e == 255) h = 0x7F7F;  // a row that is not finite: NaN
-      hi[i >> 1] |= h << (16 * (i & 1)), lo[i >> 1] |= l << (16 * (i & 1));
-    }
-    const int c16 = chunk >> 1;
-    const uint32_t at = tile + (chunk & 1) * 8 +
-                        (C::D == 64 ? row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4)
-                                    : (c16 >> 3) * (128 * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
-    sts64(at, hi[0], hi[1]);
-    sts64(at + 128 * C::D, lo[0], lo[1]);
-    if (chunk == 0) factor[m >> 7][row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    wait_copies();
   }
-  if (!C::kFp8) wait_copies();
+  // four rows at a time, so that their steps fill each other's waits, and the next four on their way
+  constexpr int kAtOnce = 4, kStep = kAtOnce * kRowsAtOnce;
+  static_assert(128 % kStep == 0, "");
+  uint4 next[kAtOnce];
+  auto load = [&](int m0) {
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      bool there;
+      const uint16_t* src = row_of(m0 + x * kRowsAtOnce, there);
+      next[x] = make_uint4(0, 0, 0, 0);
+      if (there) next[x] = *reinterpret_cast<const uint4*>(src);
+    }
+  };
+  if (C::kFp8) load(tid / kChunks);
+#pragma unroll 1
+  for (int m0 = tid / kChunks; C::kFp8 && m0 < rows; m0 += kStep) {
+    uint32_t u[kAtOnce][4], top[kAtOnce];  // top: the largest magnitudes' bits, of even and of odd dims
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      u[x][0] = next[x].x, u[x][1] = next[x].y, u[x][2] = next[x].z, u[x][3] = next[x].w;
+      top[x] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[x] = __vmaxu2(top[x], u[x][i] & 0x7FFF7FFFu);
+      top[x] = max(top[x] & 0xFFFFu, top[x] >> 16);
+    }
+    if (m0 + kStep < rows) load(m0 + kStep);
+#pragma unroll
+    for (int o = 1; o < kChunks; o <<= 1) {
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], o));
+    }
+    uint32_t hi[kAtOnce][2] = {}, lo[kAtOnce][2] = {};
+    float down[kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int e = static_cast<int>(top[x] >> 7);  // biased; 255: not finite
+      const int up = e == 255 || top[x] == 0 ? 0 : min(7 - (e - 127), 126);
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -120 <= up <= 126
+      down[x] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (f16 has the scaled elements exactly, down to 2^-32 of the largest)
+        const uint32_t y = attn::f16x2(bf16_lo(u[x][i]) * f, bf16_hi(u[x][i]) * f);
+        uint32_t h = f16x2_to_e4m3(y);
+        const __half2 less = __hsub2(*reinterpret_cast<const __half2*>(&y), e4m3x2_to_f16(h));
+        const uint32_t l = f16x2_to_e4m3(*reinterpret_cast<const uint32_t*>(&less));
+        if (e == 255) h = 0x7F7F;  // a row that is not finite: NaN
+        hi[x][i >> 1] |= h << (16 * (i & 1)), lo[x][i >> 1] |= l << (16 * (i & 1));
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int m = m0 + x * kRowsAtOnce, row = m & 127, c16 = chunk >> 1;
+      const uint32_t at = b.q + (m >> 7) * C::kQ + (chunk & 1) * 8 +
+                          (C::D == 64 ? row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4)
+                                      : (c16 >> 3) * (128 * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+      sts64(at, hi[x][0], hi[x][1]);
+      sts64(at + 128 * C::D, lo[x][0], lo[x][1]);
+      if (chunk == 0) factor[m >> 7][row] = down[x];
+    }
+  }
   fence_proxy_async_smem();
 }
 
