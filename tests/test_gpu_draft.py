@@ -153,6 +153,22 @@ def test_attention_many_tiles_per_cta(draft, d, hq, hkv, nodes, fmt):
 
 
 @pytest.mark.parametrize("fmt", [BF16, FP8])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("some", [[1, 40, 17, 3], [16, 33], [0, 1, 0, 200]])
+def test_attention_blocks_of_one_and_of_two_tiles_of_rows(draft, some, d, kind, fmt):
+    """Blocks that weigh unlike in the split over the CTAs, whole ones and such that several share."""
+    nodes = some * (96 // len(some))
+    lens = [1 + 211 * i % 3001 for i in range(96)]
+    p = Drafted(lens, nodes, 8, 1, d, fmt, kind, seed=d + len(some))
+    out, lse = p.run(draft)
+    rows = {int(p.starts[r]) + i for r in range(0, 96, 5) if nodes[r] for i in {0, nodes[r] // 2, nodes[r] - 1}}
+    p.check(out, lse, rows=rows)
+    again = p.run(draft)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8])
 @pytest.mark.parametrize("d,hq,hkv", [(128, 16, 2), (64, 6, 2), (256, 4, 1)])
 def test_attention_long_chain(draft, d, hq, hkv, fmt):
     """A prompt's chunk behind its prefix, and a prompt with none: sampled rows."""

@@ -123,8 +123,10 @@ struct Shared {
   float fold[2][8][96];              // and eight dims of the copies of rows
   uint32_t pages[16];                // of the last sixteen tiles: which of the two pages are there
   int32_t odd[4];                    // of the last four segments: the one where a value was not finite
-  int64_t warp_sum[16];
-  int32_t first, end, total, ctas;   // the CTA's range of the list, and how many share it
+  int64_t warp_sum[2][16];
+  int32_t tile_at[2];                // the CTA's range of the list
+  int32_t end, total, ctas;          // where its share of the weight ends, the weight of all, how many share it
+  int32_t weighted, skip;            // whether a tile weighs more than 1; the first one behind the range begins `skip` behind `end`
   int32_t req, head, block, tile;    // where it starts
   int32_t row0, n, len, limit;       // and that request
   uint32_t tmem;
@@ -190,6 +192,24 @@ __device__ __forceinline__ int head_tiles(const Args& k, const Request& q) {
   return n;
 }
 
+// Whether block b, a request's last, has no more than 128 rows (of 256).
+__device__ __forceinline__ bool is_light(const Args& k, const Request& q, int b) {
+  return static_cast<int64_t>(q.n) * k.l.group - static_cast<int64_t>(b) * k.l.block_rows <= 128;
+}
+// Tiles of such a block of one key-value head.
+__device__ __forceinline__ int light_tiles(const Args& k, const Request& q) {
+  return q.n > 0 && is_light(k, q, q.blocks - 1) ? block_tiles(k, q, q.blocks - 1) : 0;
+}
+// What a tile weighs in the split of the list: where some blocks are light, 2 in
+// those and 3 in others, else 1.  (bf16, without, with, and with weights of 1 and 2:
+// 60 requests of one row behind 8192 beside two chunks of 1024 behind 4096, 64 / 8
+// heads of 128, 641, 534 and 536 us; 17 trees of 1 to 20 nodes, 64 heads over one,
+// 272, 264 and 305; 9 chains of 1 to 1024 behind 16k, 1460, 1505 and 1479.)
+constexpr int kLight = 2, kHeavy = 3;
+__device__ __forceinline__ int weight_of(const Args& k, const Request& q, int b, bool weighted) {
+  return !weighted ? 1 : is_light(k, q, b) ? kLight : kHeavy;
+}
+
 // A CTA's way through its range: tiles [i0, i1) of a unit at a time.
 struct Walk {
   int left;                         // tiles of the range behind the segment
@@ -229,13 +249,14 @@ __device__ __forceinline__ int cta_of(int x, int total, int ctas) {
 
 // The range of this CTA: every thread adds up a run of requests, a scan
 // over the threads gives the total, and the thread whose run holds the range's
-// first tile walks to it.
-template <int kThreads>
+// first tile walks to it.  Split by weight, a range has the tiles that begin in its
+// share of the whole weight, and the one that holds the share's end counts to it.
+template <int kThreads, bool kTwo>
 __device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = k.a.c.num_kv_heads;
   const int per_thread = (k.a.c.num_req + kThreads - 1) / kThreads;
   const int r0 = min(tid * per_thread, k.a.c.num_req), r1 = min(r0 + per_thread, k.a.c.num_req);
-  int64_t mine = 0;
+  int64_t mine = 0, light = 0;  // tiles
   int bits = 0;
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
@@ -243,61 +264,91 @@ __device__ __forceinline__ void find_range(const Args& k, Shared& sh) {
     const Request q = request_of(k, r, bad);
     bits |= bad;
     mine += static_cast<int64_t>(head_tiles(k, q)) * heads;
+    if (kTwo) light += static_cast<int64_t>(light_tiles(k, q)) * heads;
   }
   if (bits != 0 && blockIdx.x == 0)
     report(k.a.c.dev_err, (bits & kBadLen ? kDevErrLen : 0) | (bits & kBadReq ? kDevErrReq : 0));
-  int64_t incl = mine;
+  int64_t incl = mine, light_incl = light;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o), y = kTwo ? __shfl_up_sync(0xffffffffu, light_incl, o) : 0;
+    if (lane >= o) incl += v, light_incl += y;
   }
-  if (lane == 31) sh.warp_sum[warp] = incl;
+  if (lane == 31) sh.warp_sum[0][warp] = incl, sh.warp_sum[1][warp] = light_incl;
   __syncthreads();
-  int64_t before = incl - mine, sum = 0;
+  int64_t before = incl - mine, sum = 0, light_before = light_incl - light, light_sum = 0;
 #pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sh.warp_sum[w];
-    sum += sh.warp_sum[w];
+    if (w < warp) before += sh.warp_sum[0][w], light_before += sh.warp_sum[1][w];
+    sum += sh.warp_sum[0][w], light_sum += sh.warp_sum[1][w];
   }
   if (sum > INT32_MAX) {  // starts that descend: requests with the same rows
     if (blockIdx.x == 0 && tid == 0) report(k.a.c.dev_err, kDevErrReq);
     sum = 0;
   }
+  // by weight where tiles differ and every CTA's share weighs a tile, so that one begins in each
+  const int tiles = static_cast<int>(sum), tiles_before = static_cast<int>(before);
+  const int64_t weights = kHeavy * sum - (kHeavy - kLight) * light_sum;
+  const bool weighted =
+      kTwo && 0 < light_sum && light_sum < sum && weights >= static_cast<int64_t>(kHeavy) * k.l.ctas && weights <= INT32_MAX;
+  if (weighted) {
+    sum = weights;
+    mine = kHeavy * mine - (kHeavy - kLight) * light;
+    before = kHeavy * before - (kHeavy - kLight) * light_before;
+  }
   const int total = static_cast<int>(sum);
   const int ctas = min(k.l.ctas, total), per = ctas > 0 ? total / ctas : 0, rest = total - per * ctas;
   const int cta = static_cast<int>(blockIdx.x);
   const int first = share_start(min(cta, ctas), per, rest), end = share_start(min(cta + 1, ctas), per, rest);
-  if (tid == 0) sh.first = first, sh.end = end, sh.total = total, sh.ctas = ctas;
-  if (first < end && before <= first && first < before + mine) {
-    int at = static_cast<int>(first - before), r = r0, bad;
-    Request q = request_of(k, r, bad);
-    int n = head_tiles(k, q);
+  if (tid == 0) {
+    sh.end = end, sh.total = total, sh.ctas = ctas, sh.weighted = weighted;
+    if (!weighted || end == total) sh.tile_at[1] = weighted ? tiles : end, sh.skip = 0;
+  }
 #pragma unroll 1
-    while (at >= static_cast<int64_t>(n) * heads) {
-      at -= n * heads;
-      q = request_of(k, ++r, bad);
-      n = head_tiles(k, q);
+  for (int e = 0; e <= weighted; ++e) {
+    const int pos = e ? end : first;
+    if (first == end || pos < before || pos >= before + mine) continue;
+    int at = static_cast<int>(pos - before), r = r0, bad, index = tiles_before;
+    Request q;
+    int of_head, n;  // a head's tiles and their weight
+#pragma unroll 1
+    for (;; ++r) {
+      q = request_of(k, r, bad);
+      n = of_head = head_tiles(k, q);
+      if (weighted) n = kHeavy * of_head - (kHeavy - kLight) * light_tiles(k, q);
+      if (at < static_cast<int64_t>(n) * heads) break;
+      at -= n * heads, index += of_head * heads;
     }
     const int head = at / n;
-    at -= head * n;
+    at -= head * n, index += head * of_head;
     int b = 0;
-    if (k.a.mask != nullptr || q.limit == 0) {
-      const int t = block_tiles(k, q, 0);
-      b = at / t;
-      at -= at / t * t;
+    if (k.a.mask != nullptr || q.limit == 0) {  // (the light block is the last)
+      const int t = block_tiles(k, q, 0), weight = t * weight_of(k, q, 0, weighted);
+      b = at / weight;
+      at -= b * weight;
+      index += b * t;
     } else {
 #pragma unroll 1
-      for (int t; at >= (t = block_tiles(k, q, b)); ++b) at -= t;
+      for (;; ++b) {
+        const int t = block_tiles(k, q, b), weight = t * weight_of(k, q, b, weighted);
+        if (at < weight) break;
+        at -= weight;
+        index += t;
+      }
     }
-    sh.req = r, sh.head = head, sh.block = b, sh.tile = at;
+    const int weight = weight_of(k, q, b, weighted), tile = (at + weight - 1) / weight;
+    sh.tile_at[e] = weighted ? index + tile : first;
+    if (e) sh.skip = tile * weight - at;
+    if (e) continue;
+    sh.req = r, sh.head = head, sh.block = b, sh.tile = tile;
     sh.row0 = q.first, sh.n = q.n, sh.len = q.len, sh.limit = q.limit;
   }
+  if (first == end && tid == 0) sh.tile_at[0] = sh.tile_at[1] = 0;
   __syncthreads();
 }
 __device__ __forceinline__ Walk walk_of(const Args& k, const Shared& sh) {
   Walk w{};
-  w.left = sh.end - sh.first;
+  w.left = sh.tile_at[1] - sh.tile_at[0];
   if (w.left == 0) return w;
   w.r = sh.req, w.head = sh.head, w.block = sh.block, w.tile = sh.tile;
   w.q = Request{sh.row0, sh.n, sh.len, sh.limit, blocks_of(k, sh.n)};
@@ -1321,7 +1372,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
         a.lse[t * a.c.num_q_heads + qh] = total == 0.f ? -INFINITY : (ref - (C::kFp8 ? kLift : 0.f) + log2f(total)) * 0.6931471805599453f;
     }
     if (!whole && w.i0 == 0 && g == 0 && row == 0)  // (the segment ends where the range does)
-      k.part[blockIdx.x] = Part{w.r, w.head, w.block, cta_of(sh.end - 1 + w.tiles - w.i1, sh.total, sh.ctas)};
+      k.part[blockIdx.x] = Part{w.r, w.head, w.block, cta_of(sh.end + sh.skip + (w.tiles - 1 - w.i1) * weight_of(k, w.q, w.block, sh.weighted != 0), sh.total, sh.ctas)};
     if (joined) named_sync(1, C::kStreamThreads);  // all have read the sums
   }
 }
@@ -1372,7 +1423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_predecessor();
   if (tid == 0) k.part[blockIdx.x].last = -1;
   tc_fence_before();
-  find_range<kThreads>(k, sh);
+  find_range<kThreads, C::kTwo>(k, sh);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   if ((mem & 1023u) != 0) {  // not by the launch's rules: nothing is read
