@@ -7,7 +7,7 @@
 // query heads, are one matrix Q of n G rows (row m is node m / G, head m % G).
 // A unit is (request, key-value head, block of 128 or 256 of those rows); it
 // reads the request's positions in tiles of 128.  The units' tiles, in order,
-// are one list, split evenly over the CTAs, one per SM.  A unit that several
+// are one list, split evenly by weight over the CTAs, one per SM.  A unit that several
 // worked on is joined in a second launch, in order.  (CTAs that take a request's
 // neighbouring blocks in step read each tile once from HBM, which is 2 to 3% of
 // the time where all requests have as many blocks, and loses a fifth where they
@@ -29,21 +29,22 @@
 // the positions that carry a row, and divided by the sum of the unrounded ones.
 //
 // What bounds it.  Few rows in bf16: the HBM (32 requests of 16k, 4 nodes, 64
-// heads over 8 of 128: 2.15 GB in 338 us, 6.4 TB/s of a copy's 6.8).  Many rows: a
-// step's chain of softmax and products (64 trees of 64 nodes over 4k-16k: 1.15 ms,
-// 1200 TFLOP/s; a chunk of 2048 behind 16k: 0.875 ms, 1340 TFLOP/s).  A pair of
+// heads over 8 of 128: 2.15 GB in 333 us, 6.5 TB/s of a copy's 6.8).  Many rows: a
+// step's chain of softmax and products (64 trees of 64 nodes over 4k-16k: 1.10 ms,
+// 1250 TFLOP/s; a chunk of 2048 behind 16k: 0.85 ms, 1380 TFLOP/s).  A pair of
 // steps takes 3700 cycles, of which the tensor cores work half: a softmax of 128
 // columns is 2000 (500 the largest, 1130 the exponentials, the rest waits and
 // stores), P V and the next Q K^T behind it 1500.  Neither shared memory (38%) nor
 // exponentials (26%) nor issue slots (35%) are full.  FP8: V's widening and the
 // issuing warp's waits, 1950 cycles a tile where the HBM's rate is 1460 (64 chains
-// of 4 over 16k-64k: 1.15-1.18 ms, 4.8 TB/s).  Short calls: the start, 8000 cycles
+// of 4 over 16k-64k: 1.16-1.18 ms, 4.8 TB/s).  Short calls: the start, 8000 cycles
 // until the first tile arrives, cold code, and the join (4 requests of 16 nodes
-// over 1k-4k: 32 us; one row over 16 positions: 11 us).
+// over 1k-4k: 27 us; one row over 16 positions: 10 us).
 //
 // Masks.  Only tiles that reach past the positions that all rows of a block see
 // have any: there a row's 128 bits come from its mask words, shifted to the
-// tile.  Values that some rows do not see must not meet their zeros as NaN or
+// tile, and a warp leaves out 32 positions that none of its rows sees and takes 32
+// that all see as any other (64 trees of 64 nodes: 5% less time).  Values that some rows do not see must not meet their zeros as NaN or
 // infinities: in those tiles everything that is not finite becomes 0 in shared
 // memory before the product, and at the end the rows that do see it add it.
 //
