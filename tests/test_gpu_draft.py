@@ -722,3 +722,19 @@ def test_draft_bookkeeping(draft):
     cache.companions.append(torch.zeros(8, 100, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="companions"):
         cache.draft(i32([1, 1]), i32(np.ones((2, 2))))
+
+
+@pytest.mark.parametrize("d,lens", [(64, [1000]), (128, [1000]), (256, [1000]), (128, [20000]), (128, [1001] * 160)])
+def test_attention_largest_fp8_values(draft, d, lens):
+    """The largest code under the largest scale, seen with the same weight by every position: units that several CTAs
+    share (one request) and whole ones (a request per CTA and more)."""
+    p = Drafted(lens, [1] * len(lens), 2, 1, d, FP8, seed=d)
+    p.q.zero_()
+    codes, scale = p.v[..., :64 * d].view(len(p.v), 1, 64, d), p.v[..., 64 * d:].view(torch.float32)
+    codes.fill_(0x7E)  # 448
+    codes[..., d // 2:] |= 0x80
+    codes[1::3, :, :, ::8] ^= 0x80  # (dims in which pages cancel)
+    scale.fill_(2.0 ** 60)
+    out, lse = p.run(draft)
+    assert torch.isfinite(out).all()
+    p.check(out, lse)

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       __syncthreads();
     }
     if (!live || way != 0) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = (l == 0.f ? 0.f : 1.f / l) * (k.a.c.fp8 ? draft::kTwo60 : 1.f);
     const int row = row0 + m, node = row / k.l.group;
     const int64_t t = first + node, qh = static_cast<int64_t>(p.head) * k.l.group + row - node * k.l.group;
     const bool none = l == 0.f;

@@ -70,8 +70,11 @@ constexpr int kKeys = 128;               // positions of a tile
 constexpr float kFar = 3.0e38f;          // references lie in [-kFar, kFar]
 constexpr float kSlack = 8.f;            // a logit over its reference
 constexpr int kTmem = 512, kColO = 256;  // score buffers at columns 0 and 128, then O
-// FP8: probabilities carry 2^52, so that with values of 2^-120 O is no smaller than the values by more than 2^-68
-constexpr float kLift = 52.f, kTwo120 = 1329227995784915872903807060280344576.f;
+// FP8: probabilities carry 2^52, so that with values of 2^-120 O is no smaller than the values by more than 2^-68.  A
+// probability is at most 2^8 and a value 480 x 2^60, so O stays below 2^9 per position and 2^40 for any number of them.
+// Only divided by the sum does it take all of 2^120: what several CTAs' parts are joined from carries 2^60 of it, too
+// little for an overflow and enough that nothing of O gets lost.
+constexpr float kLift = 52.f, kTwo120 = 1329227995784915872903807060280344576.f, kTwo60 = 1152921504606846976.f;
 
 struct Part {  // the unit that goes on past the end of a CTA's range; last < 0: none
   int32_t req, head, block, last;
@@ -86,7 +89,7 @@ struct Args {
   Layout l;
   Part* part;   // [ctas]
   float* stat;  // [2 ctas][block_rows][2]: reference (base 2) and sum
-  float* sum;   // [2 ctas][D / 4][block_rows][4]: neighbouring rows are neighbouring lanes
+  float* sum;   // [2 ctas][D / 4][block_rows][4]: neighbouring rows are neighbouring lanes; FP8: x 2^-60
 };
 
 template <int D_, bool kFp8_>
@@ -1304,7 +1307,7 @@ __device__ __forceinline__ void softmax(const Args& k, Shared& sh, Walk w, const
       if (both) d0 = g * (C::D / 2), d1 = d0 + C::D / 2;  // a half of the dims each
     }
     const bool whole = w.i0 == 0 && w.i1 == w.tiles;
-    const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (C::kFp8 ? kTwo120 : 1.f);  // O is 0 where the sum is
+    const float by = (whole && total != 0.f ? 1.f / total : 1.f) * (!C::kFp8 ? 1.f : whole ? kTwo120 : kTwo60);  // O is 0 where the sum is
     const int64_t slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0), qh = static_cast<int64_t>(w.head) * k.l.group + x0 - node * k.l.group;
     const int64_t t = w.q.first + node;
     const bool odd = !C::kFp8 && sh.odd[segment & 3] == static_cast<int>(segment);
