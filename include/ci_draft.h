@@ -88,10 +88,13 @@ CI_API int ci_draft_plan(const int32_t* length, const int32_t* count, const int3
  * positions, the second none.  A page id outside [0, num_pages) drops its
  * positions and sets CI_DEVERR_PAGE.
  *
- * Products are exact and accumulated in fp32; the softmax statistics are fp32;
- * the probabilities are rounded to bf16 for the product with the values (FP8:
- * with the value's scale in them) and divided by the sum of the unrounded ones;
- * out is rounded once.  Results do not depend on the order in which blocks run.
+ * Products are exact and accumulated in fp32; FP8: but for what is left out of a
+ * query's elements below 2^-13 m, at most 2^-21 m of each, m being the largest
+ * magnitude of its row and head, or 2^-119 if that is larger.  The softmax
+ * statistics are fp32; the probabilities are rounded to bf16 for the product with
+ * the values (FP8: with the value's scale in them) and divided by the sum of the
+ * unrounded ones; out is rounded once.  Results do not depend on the order in which
+ * blocks run.
  * Any finite logits; values |v| <= 2^80; FP8: scales finite, |scale| <= 2^60,
  * and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *

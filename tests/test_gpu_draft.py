@@ -738,3 +738,48 @@ def test_attention_largest_fp8_values(draft, d, lens):
     out, lse = p.run(draft)
     assert torch.isfinite(out).all()
     p.check(out, lse)
+
+
+def split_loss(q):
+    """What an FP8 call may leave out of a query's elements (float64 [..., d], bf16 values): nothing from 2^-13 of the
+    row's largest magnitude on, else at most 2^-21 of it."""
+    size = np.abs(q)
+    top = size.max(-1, keepdims=True)
+    return np.where(size >= 2.0 ** -13 * top, 0, np.minimum(size, 2.0 ** -21 * top))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("far", range(8, 19))
+def test_attention_fp8_queries_with_an_outlier(draft, d, far):
+    """One dim of the query is 2^far times as large as the others, and 0 in every key: the logits are the others'.  They
+    are alike, so that what each of them loses adds up."""
+    rng = np.random.default_rng(far)
+    p = Drafted([300], [16], 4, 1, d, FP8, seed=far)
+    codes = torch.from_numpy(rng.integers(0x30, 0x40, (len(p.k), 1, 64, d)).astype(np.uint8))  # 0.5 .. 1.875
+    codes[..., 0] = 0
+    p.k[..., :64 * d] = codes.view(len(p.k), 1, 64 * d)
+    p.k[..., 64 * d:].view(torch.float32).fill_(1.0)
+    small = 1 + torch.from_numpy(rng.integers(0, 128, (16, 4))).double() / 128  # 1 .. 2, exact in bf16
+    p.q = small[..., None].expand(16, 4, d).to(torch.bfloat16).contiguous()
+    p.q[..., 0] = 2.0 ** far
+    p.scale = 8.0 / d
+    out, lse = p.run(draft)
+    assert int(p.err) == 0
+    keys, vals = C.page_values(p.k.numpy(), d)[:, 0], C.page_values(p.v.numpy(), d)[:, 0]
+    table = p.table.numpy()
+    for i in range(16):
+        at = np.array(D.sees(300, 16, i, p.mask[i], len(p.k), table[0]))
+        k, v = keys[table[0, at // 64], at % 64], vals[table[0, at // 64], at % 64]
+        q = p.q[i].double().numpy()
+        x = p.scale * q @ k.T
+        # the logits' error: D products and the scales in fp32, and the split
+        dx = ((d + 8) * 2.0 ** -23 * p.scale * np.abs(q) @ np.abs(k).T + p.scale * split_loss(q) @ np.abs(k).T).max(-1)
+        z = np.log(np.exp(x - x.max(-1, keepdims=True)).sum(-1)) + x.max(-1)
+        w = np.exp(x - z[:, None])
+        n = len(at)
+        ztol = dx + (n + 64) * 2.0 ** -23 + 2.0 ** -21 * (np.abs(z) + 1)
+        assert (np.abs(lse[i].double().cpu().numpy() - z) <= ztol).all(), (i, np.abs(lse[i].double().cpu().numpy() - z).max())
+        want, mag = w @ v, w @ np.abs(v)
+        soft = 2 * np.expm1(dx) + (n + 64) * 2.0 ** -23
+        tol = 2.0 ** -8 * (np.abs(want) + mag) * (1 + 2.0 ** -6) + 2 * soft[:, None] * mag + 1e-30
+        assert (np.abs(out[i].double().cpu().numpy() - want) <= tol).all(), i

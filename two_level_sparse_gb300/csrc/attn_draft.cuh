@@ -49,11 +49,10 @@
 // memory before the product, and at the end the rows that do see it add it.
 //
 // FP8 pages.  Keys are multiplied as they are: the query, each row scaled by a
-// power of two to a largest magnitude in [2^7, 2^8), is the sum of two e4m3
-// numbers, exactly where an element is no smaller than 2^-10 of the row's largest,
-// else to 2^-18 of it.  Values widen to bf16 (x 2^-120) on the way from a ring of
-// raw tiles to the operands.  A position's scales join its logit and its
-// probability.
+// power of two, is the sum of an e4m3 and an e5m2 number, exactly where an element is
+// no smaller than 2^-13 of the row's largest, else within 2^-21 of that.  Values widen
+// to bf16 (x 2^-120) on the way from a ring of raw tiles to the operands.  A
+// position's scales join its logit and its probability.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -420,38 +419,40 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t next) {
 __device__ __forceinline__ uint64_t desc_rows(uint32_t addr, int row_bytes) {
   return row_bytes == 64 ? sdesc_k64_sw64(addr) : desc128(addr, 16);
 }
-// Instruction descriptor: M = 128, fp32 sums; bf16 or e4m3 operands, B MN-major or not.
+// Instruction descriptor: M = 128, fp32 sums; bf16 or e4m3 operands, B MN-major or not.  kE5m2: A is e5m2.
+constexpr uint32_t kE5m2 = 1u << 7;
 __host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          ((128u >> 4) << 24);
 }
 // N products issued by one lane (one election for all of them: the warp shares its
 // scheduler with the softmax's); step j reads the operands at a + S::a(j) and b +
-// S::b(j), in 16 bytes, or columns for an A in tensor memory.
-template <class S, int N, bool kE4m3>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// S::b(j), in 16 bytes, or columns for an A in tensor memory.  kFp8: the second half's
+// instruction descriptor is id2.
+template <class S, int N, bool kFp8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id2, uint32_t accumulate) {
   static_assert(N == 8 || N == 4, "");
-  if constexpr (kE4m3 && N == 8)
+  if constexpr (kFp8 && N == 8)
     asm volatile(
       "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
       "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %12;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
       "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %13;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
       "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %14;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::a(4)), "n"(S::a(5)), "n"(S::a(6)), "n"(S::a(7)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "n"(S::b(4)), "n"(S::b(5)), "n"(S::b(6)), "n"(S::b(7))
+      "add.s64 x, %1, %8;\n\tadd.s64 y, %2, %15;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %19, o;\n\t"
+      "add.s64 x, %1, %9;\n\tadd.s64 y, %2, %16;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %19, o;\n\t"
+      "add.s64 x, %1, %10;\n\tadd.s64 y, %2, %17;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %19, o;\n\t"
+      "add.s64 x, %1, %11;\n\tadd.s64 y, %2, %18;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %19, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::a(4)), "n"(S::a(5)), "n"(S::a(6)), "n"(S::a(7)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "n"(S::b(4)), "n"(S::b(5)), "n"(S::b(6)), "n"(S::b(7)), "r"(id2)
       : "memory");
-  else if constexpr (kE4m3)
+  else if constexpr (kFp8)
     asm volatile(
       "{\n\t.reg .pred p, e, o;\n\t.reg .b64 x;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 o, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
       "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %8;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t"
-      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3))
+      "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %11, o;\n\t"
+      "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %11, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(S::a(1)), "n"(S::a(2)), "n"(S::a(3)), "n"(S::b(1)), "n"(S::b(2)), "n"(S::b(3)), "r"(id2)
       : "memory");
   else if constexpr (N == 8)
     asm volatile(
@@ -660,14 +661,26 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3(uint32_t x) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
   return r;
 }
+__device__ __forceinline__ uint32_t f16x2_to_e5m2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ __half2 e4m3x2_to_f16(uint32_t x) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
   return *reinterpret_cast<const __half2*>(&r);
 }
 // The rows of Q: row m of the request's matrix is node m / G.  FP8: each row
-// scaled by a power of two, 1 / factor, and split into two e4m3 numbers per
-// element, one tile of each.
+// scaled by a power of two, 1 / factor, and split into an e4m3 and an e5m2 number
+// per element, one tile of each.  A bf16 element has eight bits: e4m3 has the leading
+// four, and what is left is at most eight of its last place, three bits and a sign,
+// which is what e5m2 has, with a smallest step of 2^-16 where e4m3's is 2^-9.  With the
+// largest in [2^7, 2^8) that is exact from 2^-13 of the largest on, else within 2^-21
+// of it (all bf16 values tried; with e4m3 for both, from 2^-9 on, and 2^-17).  Larger
+// elements' leading bits in e5m2 would allow a largest in [2^11, 2^12), exact from 2^-17
+// on and within 2^-25: seven operations per pair more, and 3 to 12% of a call's time
+// (32 requests of 16k, 64 nodes 1085 -> 1135 us, a prompt of 9001 1.95 -> 2.19 ms).
 template <class C>
 __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const Segment& s, const Buffers& b,
                                              float (*factor)[128], int tid) {
@@ -733,11 +746,11 @@ __device__ __forceinline__ void prep_queries(const Args& k, const Walk& w, const
       const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);  // 2^up, -120 <= up <= 126
       down[x] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // (f16 has the scaled elements exactly, down to 2^-32 of the largest)
+      for (int i = 0; i < 4; ++i) {  // (f16 has the scaled elements exactly, down to 2^-32 of the largest, and the differences)
         const uint32_t y = attn::f16x2(bf16_lo(u[x][i]) * f, bf16_hi(u[x][i]) * f);
         uint32_t h = f16x2_to_e4m3(y);
         const __half2 less = __hsub2(*reinterpret_cast<const __half2*>(&y), e4m3x2_to_f16(h));
-        const uint32_t l = f16x2_to_e4m3(*reinterpret_cast<const uint32_t*>(&less));
+        const uint32_t l = f16x2_to_e5m2(*reinterpret_cast<const uint32_t*>(&less));
         if (e == 255) h = 0x7F7F;  // a row that is not finite: NaN
         hi[x][i >> 1] |= h << (16 * (i & 1)), lo[x][i >> 1] |= l << (16 * (i & 1));
       }
@@ -882,13 +895,13 @@ __device__ __forceinline__ void prepare(const Args& k, Shared& sh, Walk w, const
 
 // ------------------------------------------------------------------ products
 // Steps of Q K^T: 32 bytes of the rows at a time, blocks of 128 bytes of all rows;
-// e4m3: the query's two parts in turn.
+// FP8: with the query's e4m3 parts, then with its e5m2 parts.
 template <class C>
 struct ScoreSteps {
-  static constexpr int kCount = C::D / 16;  // e4m3: half as many, twice
-  __host__ __device__ static constexpr int e(int j) { return C::kFp8 ? j >> 1 : j; }
+  static constexpr int kCount = C::D / 16;  // FP8: half as many, twice
+  __host__ __device__ static constexpr int e(int j) { return C::kFp8 ? j % (kCount / 2) : j; }
   __host__ __device__ static constexpr int a(int j) {
-    return (C::kFp8 && (j & 1) ? 128 * C::D / 16 : 0) + (e(j) >> 2) * (128 * 128 / 16) + (e(j) & 3) * 2;
+    return (C::kFp8 && j >= kCount / 2 ? 128 * C::D / 16 : 0) + (e(j) >> 2) * (128 * 128 / 16) + (e(j) & 3) * 2;
   }
   __host__ __device__ static constexpr int b(int j) { return (e(j) >> 2) * (C::kSlotKeys * 128 / 16) + (e(j) & 3) * 2; }
 };
@@ -936,8 +949,9 @@ __device__ __forceinline__ void products(const Args& k, Shared& sh, Walk w, cons
         const uint32_t d = tmem + 128 * (i & 1) + x * C::kSlotKeys;
         using S = ScoreSteps<C>;
         constexpr int kSteps = S::kCount > 8 ? 8 : S::kCount;
-        mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, 0);
-        if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kIdQ, 1);  // (a step's offsets repeat)
+        constexpr uint32_t kId2 = C::kFp8 ? kIdQ | kE5m2 : kIdQ;
+        mma_ss<S, kSteps, C::kFp8>(d, da, db, kIdQ, S::kCount > 8 ? kIdQ : kId2, 0);
+        if (S::kCount > 8) mma_ss<S, kSteps, C::kFp8>(d, da + S::a(8), db + S::b(8), kId2, kId2, 1);  // (a step's offsets repeat)
         if (x == C::kParts - 1) mma_commit_elect(&sh.s_full[i & 1]);
         if (last) mma_commit_elect(&sh.empty[slot]);
         if (++slot == C::kLoads) slot = 0;
