@@ -131,3 +131,28 @@ def test_drafts_that_do_not_fit(cache):
     assert d.cache_pos[:5].tolist() == [60, 61, 62, 63, -1]
     path, kept, after = c.commit(d, torch.ones(10, dtype=torch.int32))
     assert kept.tolist() == [0, 4] and after.tolist() == [-1, 1] and c.length.tolist() == [128, 64]
+
+
+def test_a_refused_draft_leaves_no_pages(cache, monkeypatch):
+    from two_level_sparse_gb300 import paged
+
+    c = cache(requests=3, max_pages=4, num_pages=6)
+    c.grow(i32(60, 0, 128))
+    before = c.page_table.clone(), c.ref_count.clone()
+    plan = paged.drafts.ci_draft_plan
+
+    def refuses(*args, **kw):
+        raise TypeError("token must be torch.int32, got torch.int64")
+
+    tokens = torch.ones(3, 9, dtype=torch.int32)
+    monkeypatch.setattr(paged.drafts, "ci_draft_plan", refuses)
+    for _ in range(3):  # (each would take four of the last three pages)
+        with pytest.raises(TypeError, match="token"):
+            c.draft(i32(9, 9, 9), tokens.long())
+        assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])
+    monkeypatch.setattr(paged.drafts, "ci_draft_plan", plan)
+    with pytest.raises(RuntimeError):  # no tensor has so many rows
+        c.draft(i32(9, 9, 9), tokens, rows=-1)
+    assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])
+    c.drop(c.draft(i32(9, 9, 9), tokens))
+    assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])

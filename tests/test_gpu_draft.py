@@ -783,3 +783,23 @@ def test_attention_fp8_queries_with_an_outlier(draft, d, far):
         soft = 2 * np.expm1(dx) + (n + 64) * 2.0 ** -23
         tol = 2.0 ** -8 * (np.abs(want) + mag) * (1 + 2.0 ** -6) + 2 * soft[:, None] * mag + 1e-30
         assert (np.abs(out[i].double().cpu().numpy() - want) <= tol).all(), i
+
+
+def test_refused_drafts_leave_no_pages(draft):
+    """What the plan refuses was allocated already: it goes back, and a draft with what is right finds it."""
+    from two_level_sparse_gb300.paged import PagedCache
+
+    cache = PagedCache(1, 3, 4, 8, 1, 64)
+    cache.grow(i32([60, 0, 120]))
+    before = cache.page_table.clone(), cache.ref_count.clone()
+    count, token, parent = i32([9, 9, 9]), i32(np.ones((3, 9))), i32(random_trees(np.random.default_rng(0), [9] * 3, 9))
+    for bad in (dict(token=token.long()), dict(token=token.cpu()), dict(token=token.t().contiguous().t()),
+                dict(parent=parent.long()), dict(parent=parent[:, :8].contiguous()), dict(parent=parent[:2]),
+                dict(count=count.long()), dict(count=count[:1]), dict(rows=-1)):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            cache.draft(**{**dict(count=count, token=token, parent=parent), **bad})
+        assert torch.equal(cache.page_table, before[0]) and torch.equal(cache.ref_count, before[1]), bad
+    d = cache.draft(count, token, parent)
+    assert (d.cache_pos >= 0).all() and int(cache.dev_err) == 0
+    cache.drop(d)
+    assert torch.equal(cache.page_table, before[0]) and torch.equal(cache.ref_count, before[1])

@@ -196,12 +196,16 @@ class PagedCache:
         ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
         fits = (count >= 0) & (count <= max_nodes) & (count <= self._limit() - self.length)
         end = self.length + torch.where(fits, count, 0)
-        ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, end, dev_err=self.dev_err)
         d = Draft(parent, max_nodes, ints(requests + 1), ints(rows), ints(rows),
                   None if parent is None else ints(rows, (max_nodes + 31) // 32), ints(rows), end)
-        drafts.ci_draft_plan(self.length, count, parent, self.page_table, self.ref_count.shape[0], d.req_start,
-                             d.positions, d.cache_pos, mask=d.mask, token=token, row_token=d.token,
-                             dev_err=self.dev_err)
+        ops.ci_pages_alloc(self.page_table, self.ref_count, self.length, end, dev_err=self.dev_err)
+        try:
+            drafts.ci_draft_plan(self.length, count, parent, self.page_table, self.ref_count.shape[0], d.req_start,
+                                 d.positions, d.cache_pos, mask=d.mask, token=token, row_token=d.token,
+                                 dev_err=self.dev_err)
+        except BaseException:  # what the call refuses leaves no pages behind the lengths
+            drafts.ci_pages_trim(self.page_table, self.ref_count, end, self.length, dev_err=self.dev_err)
+            raise
         self._open = d
         return d
 
