@@ -144,7 +144,8 @@ CI_API int ci_draft_accept(const int32_t* req_start, const int32_t* length, cons
  * (row_bytes 2 D and no scales, or D and 4) and every index-K pool (one head;
  * 128 or 64, and 4).  pools, heads, row_bytes, scale_bytes: HOST arrays of
  * 1 <= num_pools <= 160 entries, read before the call returns; pools 16-byte
- * aligned, row_bytes a multiple of 16 (at most 2^20), scale_bytes 0 or 4.
+ * aligned and disjoint (CI_ERR_SHAPE otherwise: a pool that is there twice would be
+ * moved twice), row_bytes a multiple of 16 (at most 2^20), scale_bytes 0 or 4.
  */
 CI_API int ci_slots_move(uint8_t* const* pools, const int32_t* heads, const int32_t* row_bytes,
                          const int32_t* scale_bytes, int32_t num_pools, int64_t num_pages, const int32_t* page_table,

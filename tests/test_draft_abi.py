@@ -120,6 +120,25 @@ def test_move_and_trim_refusals(draft):
     assert trim(P, -1, 4, P, 8, P, P, None, None) == SHAPE
 
 
+def test_move_refuses_pools_that_share_bytes(draft):
+    page = 2 * 64 * (256 + 4)  # of a pool of two heads
+    i32 = ctypes.c_int32
+    def status(*starts, pages=8):  # noqa: E306
+        n = len(starts)
+        return draft.lib.ci_slots_move((ctypes.c_void_p * n)(*starts), (i32 * n)(*[2] * n), (i32 * n)(*[256] * n),
+                                       (i32 * n)(*[4] * n), n, pages, P, 0, 4, None, P, 16, None, None, None)
+
+    assert status(P, P + 8 * page, P + 16 * page) == OK
+    assert status(P + 16 * page, P, P + 8 * page) == OK
+    assert status(P, P) == SHAPE
+    assert status(P + 8 * page, P, P + 8 * page) == SHAPE
+    assert status(P, P + 8 * page - 16) == SHAPE
+    assert status(P + 8 * page - 16, P + 32 * page, P) == SHAPE
+    assert status(*[P + 8 * page * i for i in range(160)]) == OK
+    assert status(*[P + 8 * page * (i % 159) for i in range(160)]) == SHAPE
+    assert status(P, P + 8 * page, pages=2 ** 31 - 1) == SHAPE
+
+
 def test_binding_refuses_what_it_can_see(draft):
     i32 = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):  # not on the GPU

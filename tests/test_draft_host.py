@@ -156,3 +156,18 @@ def test_a_refused_draft_leaves_no_pages(cache, monkeypatch):
     assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])
     c.drop(c.draft(i32(9, 9, 9), tokens))
     assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])
+
+
+def test_companions_that_layers_share_are_moved_once(cache):
+    c = cache(requests=1, max_pages=2, num_pages=2)
+    shared = torch.randint(0, 256, (2, 8448), dtype=torch.int32).to(torch.uint8)
+    c.companions += [shared, torch.zeros(2, 4352, dtype=torch.uint8), shared[:, None], shared]
+    c.grow(i32(10))
+    parent = i32(-1, 0, 0, 1, 2, 4).view(1, 6)
+    d = c.draft(i32(6), i32(0, 1, 2, 3, 4, 5).view(1, 6), parent)
+    was = shared.clone()
+    path, kept, _ = c.commit(d, i32(2, 0, 4, 0, 5, 0))
+    assert path[0, :int(kept)].tolist() == [0, 2, 4, 5]
+    page, row = int(c.page_table[0, 0]), lambda t, at: t[page, 128 * at:128 * at + 128]
+    for at, node in enumerate([0, 2, 4, 5]):
+        assert torch.equal(row(shared, 10 + at), row(was, 10 + node))

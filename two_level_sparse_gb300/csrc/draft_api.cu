@@ -1,5 +1,7 @@
 // The C ABI declared in include/ci_draft.h: host-side argument checks, then
 // the kernel launches.  No allocation, no synchronization.
+#include <algorithm>
+
 #include "../../include/ci_draft.h"
 #include "ci_internal.h"
 #include "draft_internal.h"
@@ -20,6 +22,22 @@ int check_heads(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0) return CI_ERR_SHAPE;
   if (num_q_heads > 65536 || num_q_heads / num_kv_heads > 128) return CI_ERR_RANGE;
   return CI_OK;
+}
+
+struct Span {  // of a pool's bytes
+  uint64_t begin, end;
+};
+Span span_of(const uint8_t* pool, uint64_t page_bytes, uint64_t num_pages) {
+  constexpr uint64_t kMost = UINT64_MAX / 2;
+  const uint64_t begin = reinterpret_cast<uintptr_t>(pool);
+  return {begin, begin + (num_pages > 0 && page_bytes > kMost / num_pages ? kMost : page_bytes * num_pages)};
+}
+// Whether two of them share bytes.
+bool overlap(Span* spans, int n) {
+  std::sort(spans, spans + n, [](const Span& x, const Span& y) { return x.begin < y.begin; });
+  for (int i = 1; i < n; ++i)
+    if (spans[i].begin < spans[i - 1].end) return true;
+  return false;
 }
 
 }  // namespace
@@ -111,13 +129,16 @@ int ci_slots_move(uint8_t* const* pools, const int32_t* heads, const int32_t* ro
   if (num_pools < 1 || num_pools > ci::kMaxPools || path_stride > CI_DRAFT_MAX_NODES) return CI_ERR_RANGE;
   if (!pools || !heads || !row_bytes || !scale_bytes) return CI_ERR_NULL;
   ci::MoveArgs a{};
+  Span spans[ci::kMaxPools];
   for (int i = 0; i < num_pools; ++i) {
     if (!pools[i]) return CI_ERR_NULL;
     if (heads[i] < 1 || row_bytes[i] < 16 || row_bytes[i] > (1 << 20) || heads[i] > (1 << 16)) return CI_ERR_RANGE;
     if (scale_bytes[i] != 0 && scale_bytes[i] != 4) return CI_ERR_UNSUPPORTED;
     if (!aligned(pools[i], 16) || row_bytes[i] % 16 != 0) return CI_ERR_ALIGN;
     a.pool[i] = pools[i], a.heads[i] = heads[i], a.row_bytes[i] = row_bytes[i], a.scale_bytes[i] = scale_bytes[i];
+    spans[i] = span_of(pools[i], static_cast<uint64_t>(heads[i]) * CI_PAGE * (row_bytes[i] + scale_bytes[i]), num_pages);
   }
+  if (overlap(spans, num_pools)) return CI_ERR_SHAPE;
   if (num_req == 0) return CI_OK;
   if (!length || !path || !count || (max_pages > 0 && !page_table)) return CI_ERR_NULL;
   a.num_pools = num_pools, a.num_pages = num_pages, a.page_table = page_table, a.num_req = num_req,

@@ -166,17 +166,19 @@ class PagedCache:
                            dev_err=self.dev_err, stream=stream, **kw)
         return out
 
-    def _pool_forms(self):
-        """Bytes of a position's row and of its scale, of every pool that a commit moves entries in."""
+    def _moved_pools(self):
+        """The pools that a commit moves entries in, each once (layers may share an index pool), and the bytes of a
+        position's row and of its scale in them."""
         fp8 = ops.cache_format(self.k[0], self.head_dim) == ops.CACHE_FP8
-        own = (self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)
-        forms = [own] * (2 * self.k.shape[0])
-        for p in self.companions:
+        pools = [*self.k, *self.v]
+        forms = [(self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)] * len(pools)
+        for p in {p.data_ptr(): p for p in self.companions}.values():
             row = p.shape[-1] // ops.PAGE - 4
             if p.dim() not in (2, 3) or row not in (64, 128) or p.shape[-1] != ops.PAGE * (row + 4):
                 raise ValueError("drafts need companions that are index-K pools: [num_pages, 8448 or 4352]")
+            pools.append(p)
             forms.append((row, 4))
-        return forms
+        return pools, forms
 
     def _is_open(self, draft):
         if self._open is not draft:
@@ -188,7 +190,7 @@ class PagedCache:
         most so many (None: requests * max_nodes).  A count or a length that does not fit counts as no tokens, a token
         for which the pages run out is kept nowhere and not accepted; both are in ``dev_err``."""
         self._closed()
-        self._pool_forms()
+        self._moved_pools()
         requests, max_nodes = token.shape
         if not 1 <= max_nodes <= drafts.MAX_NODES:
             raise ValueError(f"a tree has 1 to {drafts.MAX_NODES} nodes at most")
@@ -242,7 +244,7 @@ class PagedCache:
         path, kept, after, length = ints(requests, draft.max_nodes), ints(requests), ints(requests), ints(requests)
         drafts.ci_draft_accept(draft.req_start, self.length, draft.parent, draft.token, target, path, kept, after, length,
                                cache_pos=draft.cache_pos, dev_err=self.dev_err)
-        pools, forms = [*self.k, *self.v, *self.companions], self._pool_forms()
+        pools, forms = self._moved_pools()
         for at in range(0, len(pools), ops.MAX_POOLS):
             part = slice(at, at + ops.MAX_POOLS)
             drafts.ci_slots_move(pools[part], *zip(*forms[part]), self.page_table, self.length, path, kept,
