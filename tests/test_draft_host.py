@@ -171,3 +171,27 @@ def test_companions_that_layers_share_are_moved_once(cache):
     page, row = int(c.page_table[0, 0]), lambda t, at: t[page, 128 * at:128 * at + 128]
     for at, node in enumerate([0, 2, 4, 5]):
         assert torch.equal(row(shared, 10 + at), row(was, 10 + node))
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(2, 8448, dtype=torch.uint8), torch.zeros(4, 8448, dtype=torch.uint8),
+                                 torch.zeros(3, 8448), torch.zeros(3, 8448, dtype=torch.uint8, device="meta"),
+                                 torch.zeros(8448, 3, dtype=torch.uint8).t(), torch.zeros(3, 8192, dtype=torch.uint8)])
+def test_companions_are_looked_at_before_anything_happens(cache, bad):
+    c = cache(requests=1, max_pages=3, num_pages=3)
+    c.grow(i32(64))
+    before = c.page_table.clone(), c.ref_count.clone()
+    tokens = torch.ones(1, 3, dtype=torch.int32)
+    c.companions.append(bad)
+    with pytest.raises(ValueError, match="companions"):
+        c.draft(i32(3), tokens)
+    assert torch.equal(c.page_table, before[0]) and torch.equal(c.ref_count, before[1])
+    c.companions.pop()
+    d = c.draft(i32(3), tokens)
+    c.companions.append(bad)
+    keys = c.k.clone()
+    with pytest.raises(ValueError, match="companions"):  # the draft stays open, nothing has moved
+        c.commit(d, torch.ones(3, dtype=torch.int32))
+    assert torch.equal(c.k, keys) and c.length.tolist() == [64]
+    c.companions.pop()
+    assert c.commit(d, torch.ones(3, dtype=torch.int32))[1].tolist() == [3] and c.length.tolist() == [67]
+    consistent(c)

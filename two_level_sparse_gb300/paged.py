@@ -172,10 +172,13 @@ class PagedCache:
         fp8 = ops.cache_format(self.k[0], self.head_dim) == ops.CACHE_FP8
         pools = [*self.k, *self.v]
         forms = [(self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)] * len(pools)
+        num_pages = self.ref_count.shape[0]
         for p in {p.data_ptr(): p for p in self.companions}.values():
             row = p.shape[-1] // ops.PAGE - 4
-            if p.dim() not in (2, 3) or row not in (64, 128) or p.shape[-1] != ops.PAGE * (row + 4):
-                raise ValueError("drafts need companions that are index-K pools: [num_pages, 8448 or 4352]")
+            if (p.dim() not in (2, 3) or row not in (64, 128) or p.shape[-1] != ops.PAGE * (row + 4) or p.shape[0] != num_pages
+                    or p.dtype != torch.uint8 or p.device != self.k.device or not p.is_contiguous()):
+                raise ValueError("drafts need companions that are index-K pools on the cache's device: contiguous uint8 "
+                                 f"[{num_pages}, 8448 or 4352]")
             pools.append(p)
             forms.append((row, 4))
         return pools, forms
@@ -239,12 +242,12 @@ class PagedCache:
         Returns (path [requests, max_nodes], the kept nodes, -1 behind them; their number; the token behind the
         last one, -1 where nothing was drafted)."""
         self._is_open(draft)
+        pools, forms = self._moved_pools()  # (refused, if at all, before any entry moves)
         requests = self.length.shape[0]
         ints = lambda *shape: torch.empty(shape, dtype=_I32, device=self.length.device)  # noqa: E731
         path, kept, after, length = ints(requests, draft.max_nodes), ints(requests), ints(requests), ints(requests)
         drafts.ci_draft_accept(draft.req_start, self.length, draft.parent, draft.token, target, path, kept, after, length,
                                cache_pos=draft.cache_pos, dev_err=self.dev_err)
-        pools, forms = self._moved_pools()
         for at in range(0, len(pools), ops.MAX_POOLS):
             part = slice(at, at + ops.MAX_POOLS)
             drafts.ci_slots_move(pools[part], *zip(*forms[part]), self.page_table, self.length, path, kept,
