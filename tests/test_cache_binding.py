@@ -152,3 +152,18 @@ def test_workspace_goes_by_the_heads(cache, d, hkv):
         if d == 128 and 16 < group <= 32:
             heads = 64  # lists of positions take the kernel of many heads
         assert 0 <= got - heads * part * sms <= 32 * sms + 16, group
+
+
+def test_captured_calls_keep_no_workspace(cache, pools_asked, monkeypatch):
+    """A call on a stream that is being captured, whichever is the current one, has memory of its own."""
+    from two_level_sparse_gb300 import paged
+
+    c = host_cache(1, 2, 2, 4, 2, 64)
+    q = dev(2, 8, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(paged, "_capturing", lambda stream: stream is SIDE)
+    for _ in range(2):
+        pools_asked.clear()
+        c.attend(0, q, 0, dev(2), out=q, stream=SIDE)
+        assert len(pools_asked) == 1 and pools_asked[0][1] is SIDE and not c._workspace
+    c.attend(0, q, 0, dev(2), out=q)
+    assert len(c._workspace) == 1

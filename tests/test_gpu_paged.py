@@ -267,3 +267,52 @@ def test_nan_reaches_the_reader(cache, hq, what, fmt):
         assert out[1:, :hq // 2].isnan().all()
     else:
         assert out[1:, :hq // 2, 5].isnan().all()
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_captured_calls_have_workspaces_of_their_own(drafted):
+    """Two graphs of PagedCache's attention, captured on one stream, replayed at the same time on two and beside eager
+    calls on the first: each gives what it gives alone.  The capturing stream need not be the current one."""
+    from two_level_sparse_gb300.paged import PagedCache
+
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    cache = PagedCache(1, 4, 40, 170, 2, 128)
+    cache.grow(i32([2500, 2000, 1500, 2400]))
+    for pool in (cache.k, cache.v):
+        pool.view(torch.bfloat16).copy_(torch.randn(pool.view(torch.bfloat16).shape, device="cuda", generator=gen))
+    d = cache.draft(i32([3] * 4), i32([[1] * 3] * 4)) if drafted else None
+    rows = 12 if drafted else 4
+    qs = [torch.randn(rows, 16, 128, device="cuda", generator=gen).bfloat16() for _ in range(3)]
+    outs = [torch.empty_like(q) for q in qs]
+
+    def call(q, out, stream):
+        if drafted:
+            cache.attend_draft(0, q, d, out=out, stream=stream)
+        else:
+            cache.attend(0, q, DEC, cache.length, out=out, stream=stream)
+
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    want = []
+    for q, out in zip(qs, outs):
+        call(q, out, streams[0])
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    kept = {k: v.data_ptr() for k, v in cache._workspace.items()}
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph, stream=streams[0]):
+            with torch.cuda.stream(streams[2] if i else streams[0]):
+                call(qs[i], outs[i], streams[0])
+    assert {k: v.data_ptr() for k, v in cache._workspace.items()} == kept
+    for out in outs:
+        out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for graph, stream in zip(graphs, streams[1:]):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        call(qs[2], outs[2], streams[0])
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)

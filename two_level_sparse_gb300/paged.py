@@ -50,6 +50,16 @@ class Draft:
     end: torch.Tensor            # [requests]: the positions that there are pages for until the step ends
 
 
+def _capturing(stream):
+    """Whether ``stream`` (None: the current one) is being captured into a graph."""
+    if not torch.cuda.is_initialized():
+        return False
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class PagedCache:
     """``layers`` attention layers' keys and values for ``requests`` requests
     of up to ``64 * max_pages`` positions, in ``num_pages`` pages (every
@@ -151,18 +161,27 @@ class PagedCache:
                                    self.v[layer], self.page_table, layout, dev_err=self.dev_err, stream=stream, **kw)
         return q_out
 
+    def _work(self, what, heads, stream, device, size):
+        """The workspace of a call on ``stream``, kept for the next: calls on two streams may overlap, and a call's rows
+        do not change its ``size()``.  None, for one of the call's own, where the stream is being captured: graphs may
+        run at the same time, and beside the stream's other calls."""
+        on = stream if stream is not None else torch.cuda.current_stream(device)
+        if _capturing(stream):
+            return None
+        key = (what, heads, on.cuda_stream)
+        if key not in self._workspace:
+            self._workspace[key] = ops.empty_on(stream, (size(),), torch.uint8, device)
+        return self._workspace[key]
+
     def attend(self, layer, q, layout, seq_len, max_len=None, scale=None, pos=None, out=None, stream=None, **kw):
         """Attention of q [rows, heads, head_dim] over the cache or over ``pos``."""
         rows, heads, d = q.shape
         out = ops.empty_on(stream, q.shape, q.dtype, q.device) if out is None else out
-        on = stream if stream is not None else torch.cuda.current_stream(q.device)
-        key = (heads, on.cuda_stream)  # calls on two streams may overlap; the rows do not change the size
-        if key not in self._workspace:
-            n = ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d)
-            self._workspace[key] = ops.empty_on(stream, (n,), torch.uint8, q.device)
+        workspace = self._work("attend", heads, stream, q.device,
+                               lambda: ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d))
         max_len = ops.PAGE * self.page_table.shape[1] if max_len is None else max_len
         ops.ci_attn_decode(q, self.k[layer], self.v[layer], self.page_table, layout, seq_len, max_len,
-                           d ** -0.5 if scale is None else scale, out, pos=pos, workspace=self._workspace[key],
+                           d ** -0.5 if scale is None else scale, out, pos=pos, workspace=workspace,
                            dev_err=self.dev_err, stream=stream, **kw)
         return out
 
@@ -223,14 +242,8 @@ class PagedCache:
             out = ops.empty_on(stream, q.shape, q.dtype, q.device)
             with torch.cuda.stream(stream):
                 out.zero_()
-        workspace = None  # a captured call's is the graph's own: graphs may run at the same time
-        if not torch.cuda.is_current_stream_capturing():
-            on = stream if stream is not None else torch.cuda.current_stream(q.device)
-            key = ("draft", heads, on.cuda_stream)
-            n = drafts.attn_draft_workspace_bytes(draft.max_nodes, heads, self.k.shape[2], d)
-            if key not in self._workspace or self._workspace[key].numel() < n:
-                self._workspace[key] = ops.empty_on(stream, (n,), torch.uint8, q.device)
-            workspace = self._workspace[key]
+        workspace = self._work("draft", heads, stream, q.device, lambda: drafts.attn_draft_workspace_bytes(
+            draft.max_nodes, heads, self.k.shape[2], d))
         drafts.ci_attn_draft(q, self.k[layer], self.v[layer], self.page_table, draft.req_start, self.length, self._limit(),
                              draft.max_nodes, d ** -0.5 if scale is None else scale, out, mask=draft.mask,
                              workspace=workspace, dev_err=self.dev_err, stream=stream, **kw)
