@@ -99,11 +99,13 @@ CI_API int ci_draft_plan(const int32_t* length, const int32_t* count, const int3
  * and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *
  * max_len <= 64 * max_pages; max_rows >= 0: no request has more rows;
- * mask_words >= 1 (ignored for NULL).  rows * G < 2^31, and with B = min(num_req * ceil(max_rows *
- * G / 128), ceil(rows * G / 128) + num_req), G = num_q_heads / num_kv_heads:
- * num_kv_heads * B * (max_len / 128 + 1) < 2^31.
+ * mask_words >= 1 (ignored for NULL).  rows * G < 2^31, G = num_q_heads /
+ * num_kv_heads, and with B = min(num_req * ceil(max_rows * G / 128),
+ * ceil(rows * G / 128) + num_req): num_kv_heads * B * (max_len / 128 + 1) < 2^31.
  * ws: at least ci_attn_draft_workspace_bytes() bytes, 16-byte aligned, of any
- * content; one call's use of it ends with the call's work on the stream.
+ * content; one call's use of it ends with the call's work on the stream.  Its size
+ * is two blocks of rows' sums per SM, 40 MB for heads of 128 (20 and 40 for 64 and
+ * 256), and goes by head_dim alone: max_rows, checked to be >= 0, does not change it.
  */
 CI_API int64_t ci_attn_draft_workspace_bytes(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads,
                                              int32_t head_dim);

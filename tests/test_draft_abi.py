@@ -193,3 +193,14 @@ def test_oracle_path_and_moves():
     assert [int(out[table[0, s // 64], 0, 2 * (s % 64)]) for s in (62, 63, 64, 65)] == [10, 12, 14, 13]
     t, ref = D.trim(np.array([[2, 0, 1]]), np.array([1, 1, 2]), [190], [64])
     assert t.tolist() == [[2, -1, -1]] and ref.tolist() == [0, 0, 2]
+
+
+def test_workspace_goes_by_the_head_size(draft):
+    """Two blocks (of 256 rows; 128 with D = 256) of sums and two statistics per SM, whatever the rows and heads."""
+    n = draft.attn_draft_workspace_bytes
+    for d, rows in ((64, 256), (128, 256), (256, 128)):
+        got = {n(m, hq, hkv, d) for m in (0, 1, 77, 10 ** 6) for hq, hkv in ((1, 1), (64, 8), (128, 1))}
+        assert len(got) == 1
+        block = 2 * rows * (d + 2) * 4
+        sms = got.pop() // block
+        assert 0 <= n(1, 8, 8, d) - sms * block <= 16 * sms + 16

@@ -81,7 +81,7 @@ def ci_draft_plan(length, count, parent, page_table, num_pages, req_start, posit
 
 
 def attn_draft_workspace_bytes(max_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    """Of ci_attn_draft, for requests of up to ``max_rows`` rows."""
+    """Of ci_attn_draft.  It goes by ``head_dim`` alone; the others are checked."""
     n = lib.ci_attn_draft_workspace_bytes(max_rows, num_q_heads, num_kv_heads, head_dim)
     if n < 0:
         raise CIError("ci_attn_draft_workspace_bytes", n)
