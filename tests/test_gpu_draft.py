@@ -803,3 +803,42 @@ def test_refused_drafts_leave_no_pages(draft):
     assert (d.cache_pos >= 0).all() and int(cache.dev_err) == 0
     cache.drop(d)
     assert torch.equal(cache.page_table, before[0]) and torch.equal(cache.ref_count, before[1])
+
+
+@pytest.mark.parametrize("bad", ["none", "source", "behind the pool", "destination", "not moved", "all"])
+@pytest.mark.parametrize("req,most", [(1, 70), (5, 64), (30, 200)])
+def test_move_reports_pages(draft, req, most, bad):
+    """CI_DEVERR_PAGE where a position that moves has no page at one of its ends, and only there; it stays as it is."""
+    rng = np.random.default_rng(req + most)
+    gen = torch.Generator().manual_seed(req)
+    length = rng.integers(0, 200, req)
+    length[0] = 60
+    table, pages = make_table(gen, [int(n) + most for n in length])
+    table = table.numpy().copy()
+    count, path = np.zeros(req, int), np.full((req, most), -1)
+    for r in range(req):
+        path[r, :8] = [0, 1, 4, 5, 9, 30, most - 2, most - 1]
+        count[r] = 8
+    # of the first request: positions 60, 61 stay; 64, 65, 69, 90, 58 + most, 59 + most go to 62 .. 67
+    if bad in ("source", "all"):
+        table[0, (60 + most - 1) // 64] = -1
+    if bad == "behind the pool":
+        table[0, (60 + most - 1) // 64] = pages
+    if bad in ("destination", "all"):
+        table[0, 0] = -5
+    if bad == "not moved":
+        table[0, (60 + most - 1) // 64], count[0] = -1, 2  # (the first two stay where they are)
+    if bad == "all":
+        table[:] = np.where(rng.random(table.shape) < 0.3, pages + 3, table)
+    err = 0
+    for r in range(req):
+        for d in range(count[r]):
+            ends = (length[r] + path[r, d], length[r] + d)
+            if ends[0] != ends[1] and any(not 0 <= table[r, s // 64] < pages for s in ends):
+                err = PAGE_ERR
+    assert err == (0 if bad in ("none", "not moved") else PAGE_ERR)
+    pool = torch.randint(0, 256, (pages, 2, 64 * 20), generator=gen, dtype=torch.int32).to(torch.uint8)
+    got, bits = pool.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    draft.ci_slots_move([got], 16, 4, i32(table), i32(length), i32(path), i32(count), dev_err=bits)
+    np.testing.assert_array_equal(got.cpu().numpy(), D.move(pool.numpy(), 16, 4, table, length, path, count))
+    assert int(bits) == err
