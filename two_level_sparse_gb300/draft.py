@@ -2,7 +2,8 @@
 
 Argument marshalling only, like ``cache``, whose conventions hold: pools are
 uint8 [num_pages, kv_heads, bytes], ids and lengths int32, and a call runs on
-``stream`` (None: the current one of its tensors' device).
+``stream`` (None: the current one of its tensors' device, which has to be the
+current device).
 
 Trees are ``parent`` [requests, nodes] (None: chains); node 0 of a request is
 the token that it goes on with.
@@ -14,8 +15,8 @@ from array import array
 
 import torch
 
-from .cache import (_BF16, _F32, _F32T, _I32, _I32T, _I64, _P, _U8, MAX_POOLS, PAGE, _check, _dev, _heads,  # noqa: F401
-                    _ints, _numel, _on, _pools, _table, empty_on)
+from .cache import (_F32, _F32T, _I32, _I32T, _I64, _P, _U8, MAX_POOLS, PAGE, _check, _dev, _heads, _on, _pools,
+                    empty_on)
 from .ci import CIError, lib
 
 MAX_NODES = 256
@@ -38,21 +39,35 @@ for _name, _argtypes in SIGNATURES.items():
 _current_device = torch._C._cuda_getDevice  # torch.cuda.current_device(), without the check that CUDA is up
 
 
-def _shape(t, shape, name):
-    """The device pointer of a contiguous int32 GPU tensor of the shape (None: NULL)."""
+def _at(t, name):
+    """The device of a call's first tensor: the current one, which the launch goes to.  The others are compared with it."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must live on the GPU")
+    if at != _current_device():
+        raise ValueError(f"{name} must live on the current device")
+    return at
+
+
+def _here(t, at, dtype, name):
+    """The device pointer of a contiguous tensor of the type on device ``at`` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != at or not t.is_contiguous():
+        _dev(t, dtype, name)  # says what is wrong
+        raise ValueError(f"{name} must live on the current device")
+    return t.data_ptr()
+
+
+def _shape(t, shape, at, name):
+    """_here for an int32 tensor of the shape."""
     if t is None:
         return None
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype is not _I32T or not t.is_cuda or not t.is_contiguous():
-        return _dev(t, _I32T, name)  # says what is wrong
+    if t.dtype is not _I32T or t.get_device() != at or not t.is_contiguous():
+        return _here(t, at, _I32T, name)
     return t.data_ptr()
-
-
-def _here(t, name):
-    """The launch goes to the current device: the tensors have to be there."""
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} must live on the current device")
 
 
 def ci_draft_plan(length, count, parent, page_table, num_pages, req_start, positions, cache_pos, mask=None, token=None,
@@ -70,13 +85,13 @@ def ci_draft_plan(length, count, parent, page_table, num_pages, req_start, posit
     if (token is None) != (row_token is None):
         raise ValueError("token and row_token come together")
     words = 0 if mask is None else mask.shape[1]
-    args = [_shape(length, (num_req,), "length"), _shape(count, (num_req,), "count"),
-            _shape(parent, (num_req, max_nodes), "parent"), _shape(token, (num_req, max_nodes), "token"), num_req, max_nodes, _ints(page_table, "page_table"),
-            max_pages, num_pages, rows, _shape(req_start, (num_req + 1,), "req_start"),
-            _shape(positions, (rows,), "positions"), _shape(cache_pos, (rows,), "cache_pos"),
-            _shape(mask, (rows, words), "mask"), words, _shape(row_token, (rows,), "row_token"),
-            _dev(dev_err, _I32T, "dev_err"), _on(stream, page_table)]
-    _here(page_table, "page_table")
+    at, of_rows = _at(page_table, "page_table"), (rows,)
+    args = [_shape(length, (num_req,), at, "length"), _shape(count, (num_req,), at, "count"),
+            _shape(parent, (num_req, max_nodes), at, "parent"), _shape(token, (num_req, max_nodes), at, "token"), num_req,
+            max_nodes, _here(page_table, at, _I32T, "page_table"), max_pages, num_pages, rows,
+            _shape(req_start, (num_req + 1,), at, "req_start"), _shape(positions, of_rows, at, "positions"),
+            _shape(cache_pos, of_rows, at, "cache_pos"), _shape(mask, (rows, words), at, "mask"), words,
+            _shape(row_token, of_rows, at, "row_token"), _here(dev_err, at, _I32T, "dev_err"), _on(stream, page_table)]
     _check("ci_draft_plan", lib.ci_draft_plan(*args))
 
 
@@ -104,20 +119,23 @@ def ci_attn_draft(q, k_pool, v_pool, page_table, req_start, length, max_len, max
     kp, vp, num_pages, hkv, fmt = _pools(k_pool, v_pool, d)
     num_req, max_pages = page_table.shape
     words = 0 if mask is None else mask.shape[1]
-    mp = _shape(mask, (rows, words), "mask")
+    at = _at(q, "q")
+    for t, name in ((out, "out"), (k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t.get_device() != at:
+            raise ValueError(f"{name} must live on the current device")
+    mp = _shape(mask, (rows, words), at, "mask")
     if mask is not None and rows and not words:
         raise ValueError("mask needs a word per row")
-    starts = _shape(req_start, (num_req + 1,), "req_start")
-    lens = _shape(length, (num_req,), "length")
+    starts = _shape(req_start, (num_req + 1,), at, "req_start")
+    lens = _shape(length, (num_req,), at, "length")
     if lse is not None and tuple(lse.shape) != (rows, hq):
         raise ValueError(f"lse must be [{rows}, {hq}]")
-    _here(q, "q")
     if workspace is None:
         workspace = empty_on(stream, (attn_draft_workspace_bytes(max_rows, hq, hkv, d),), _U8, q.device)
     status = lib.ci_attn_draft(
-        qp, q_stride, rows, hq, hkv, d, scale, kp, vp, num_pages, fmt, _ints(page_table, "page_table"), num_req,
-        max_pages, starts, lens, max_len, max_rows, mp, words, op, out_stride, _dev(lse, _F32T, "lse"),
-        _dev(workspace, _U8, "workspace"), workspace.numel(), _dev(dev_err, _I32T, "dev_err"), _on(stream, q))
+        qp, q_stride, rows, hq, hkv, d, scale, kp, vp, num_pages, fmt, _here(page_table, at, _I32T, "page_table"), num_req,
+        max_pages, starts, lens, max_len, max_rows, mp, words, op, out_stride, _here(lse, at, _F32T, "lse"),
+        _here(workspace, at, _U8, "workspace"), workspace.numel(), _here(dev_err, at, _I32T, "dev_err"), _on(stream, q))
     if status:
         _check("ci_attn_draft", status)
 
@@ -128,14 +146,13 @@ def ci_draft_accept(req_start, length, parent, row_token, target, path, accepted
     its choice behind each row (see include/ci_draft.h)."""
     num_req, max_nodes = path.shape
     rows = row_token.shape[0]
-    args = [_shape(req_start, (num_req + 1,), "req_start"), _shape(length, (num_req,), "length"),
-            _shape(parent, (num_req, max_nodes), "parent"), num_req, max_nodes, rows,
-            _shape(row_token, (rows,), "row_token"), _shape(target, (rows,), "target"),
-            _shape(cache_pos, (rows,), "cache_pos"), _ints(path, "path"),
-            _shape(accepted, (num_req,), "accepted"), _shape(next, (num_req,), "next"),
-            _shape(new_len, (num_req,), "new_len"), _dev(dev_err, _I32T, "dev_err"),
-            _on(stream, path)]
-    _here(path, "path")
+    at, of_rows, of_req = _at(path, "path"), (rows,), (num_req,)
+    args = [_shape(req_start, (num_req + 1,), at, "req_start"), _shape(length, of_req, at, "length"),
+            _shape(parent, (num_req, max_nodes), at, "parent"), num_req, max_nodes, rows,
+            _shape(row_token, of_rows, at, "row_token"), _shape(target, of_rows, at, "target"),
+            _shape(cache_pos, of_rows, at, "cache_pos"), _here(path, at, _I32T, "path"),
+            _shape(accepted, of_req, at, "accepted"), _shape(next, of_req, at, "next"),
+            _shape(new_len, of_req, at, "new_len"), _here(dev_err, at, _I32T, "dev_err"), _on(stream, path)]
     _check("ci_draft_accept", lib.ci_draft_accept(*args))
 
 
@@ -152,13 +169,17 @@ def ci_slots_move(pools, row_bytes, scale_bytes, page_table, length, path, count
     scales = array("i", [scale_bytes]) * n if isinstance(scale_bytes, int) else array("i", scale_bytes)
     if len(rows) != n or len(scales) != n:
         raise ValueError("row_bytes and scale_bytes: a number, or one for each pool")
+    num_req, max_pages = page_table.shape
+    if path.dim() != 2 or path.shape[0] != num_req:
+        raise ValueError(f"path must be [{num_req}, n]")
+    at = _at(path, "path")
     if isinstance(pools, torch.Tensor):
-        base, shapes = _dev(pools, _U8, "pools"), [pools.shape[1:]]
+        base, shapes = _here(pools, at, _U8, "pools"), [pools.shape[1:]]
         step = pools.numel() // n
         ptrs = array("Q", range(base, base + n * step, step) if step else [base] * n)
     else:
         shapes = [p.shape for p in pools]
-        ptrs = array("Q", [_dev(p, _U8, "pools") for p in pools])
+        ptrs = array("Q", [_here(p, at, _U8, "pools") for p in pools])
     num_pages = shapes[0][0]
     heads = array("i")
     for shape, row, scale in {(shape, row, scale): None for shape, row, scale in
@@ -166,21 +187,18 @@ def ci_slots_move(pools, row_bytes, scale_bytes, page_table, length, path, count
         if len(shape) not in (2, 3) or shape[0] != num_pages or shape[-1] != PAGE * (row + scale):
             raise ValueError(f"a pool must be [{num_pages}, heads, {PAGE * (row + scale)}], got {list(shape)}")
     heads.extend([shape[1] if len(shape) == 3 else 1 for shape in shapes] * (n // len(shapes)))
-    num_req, max_pages = page_table.shape
-    if path.dim() != 2 or path.shape[0] != num_req:
-        raise ValueError(f"path must be [{num_req}, n]")
-    _here(path, "path")
     _check("ci_slots_move", lib.ci_slots_move(
         ptrs.buffer_info()[0], heads.buffer_info()[0], rows.buffer_info()[0], scales.buffer_info()[0], n, num_pages,
-        _ints(page_table, "page_table"), num_req, max_pages, _shape(length, (num_req,), "length"),
-        _ints(path, "path"), path.shape[1], _shape(count, (num_req,), "count"), _dev(dev_err, _I32T, "dev_err"),
-        _on(stream, path)))
+        _here(page_table, at, _I32T, "page_table"), num_req, max_pages, _shape(length, (num_req,), at, "length"),
+        _here(path, at, _I32T, "path"), path.shape[1], _shape(count, (num_req,), at, "count"),
+        _here(dev_err, at, _I32T, "dev_err"), _on(stream, path)))
 
 
 def ci_pages_trim(page_table, ref_count, old_len, new_len, dev_err=None, stream=None):
     """The pages behind new_len released, where a request had old_len positions (see include/ci_draft.h)."""
-    num_req = page_table.shape[0]
-    old, new = _shape(old_len, (num_req,), "old_len"), _shape(new_len, (num_req,), "new_len")
-    _here(page_table, "page_table")
-    _check("ci_pages_trim", lib.ci_pages_trim(*_table(page_table, ref_count), old, new, _dev(dev_err, _I32T, "dev_err"),
-                                              _on(stream, page_table)))
+    num_req, max_pages = page_table.shape
+    at = _at(page_table, "page_table")
+    _check("ci_pages_trim", lib.ci_pages_trim(
+        _here(page_table, at, _I32T, "page_table"), num_req, max_pages, _here(ref_count, at, _I32T, "ref_count"),
+        ref_count.shape[0], _shape(old_len, (num_req,), at, "old_len"), _shape(new_len, (num_req,), at, "new_len"),
+        _here(dev_err, at, _I32T, "dev_err"), _on(stream, page_table)))
