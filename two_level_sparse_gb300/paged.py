@@ -161,46 +161,49 @@ class PagedCache:
                                    self.v[layer], self.page_table, layout, dev_err=self.dev_err, stream=stream, **kw)
         return q_out
 
-    def _work(self, what, heads, stream, device, size):
+    def _work(self, what, q, stream, size):
         """The workspace of a call on ``stream``, kept for the next: calls on two streams may overlap, and a call's rows
         do not change its ``size()``.  None, for one of the call's own, where the stream is being captured: graphs may
         run at the same time, and beside the stream's other calls."""
-        on = stream if stream is not None else torch.cuda.current_stream(device)
         if _capturing(stream):
             return None
-        key = (what, heads, on.cuda_stream)
-        if key not in self._workspace:
-            self._workspace[key] = ops.empty_on(stream, (size(),), torch.uint8, device)
-        return self._workspace[key]
+        key = (what, q.shape[1], ops._on(stream, q))
+        kept = self._workspace.get(key)
+        if kept is None:
+            kept = self._workspace[key] = ops.empty_on(stream, (size(),), torch.uint8, q.device)
+        return kept
 
     def attend(self, layer, q, layout, seq_len, max_len=None, scale=None, pos=None, out=None, stream=None, **kw):
         """Attention of q [rows, heads, head_dim] over the cache or over ``pos``."""
         rows, heads, d = q.shape
         out = ops.empty_on(stream, q.shape, q.dtype, q.device) if out is None else out
-        workspace = self._work("attend", heads, stream, q.device,
-                               lambda: ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d))
+        workspace = self._work("attend", q, stream, lambda: ops.attn_workspace_bytes(rows, heads, self.k.shape[2], d))
         max_len = ops.PAGE * self.page_table.shape[1] if max_len is None else max_len
         ops.ci_attn_decode(q, self.k[layer], self.v[layer], self.page_table, layout, seq_len, max_len,
                            d ** -0.5 if scale is None else scale, out, pos=pos, workspace=workspace,
                            dev_err=self.dev_err, stream=stream, **kw)
         return out
 
-    def _moved_pools(self):
-        """The pools that a commit moves entries in, each once (layers may share an index pool), and the bytes of a
-        position's row and of its scale in them."""
-        fp8 = ops.cache_format(self.k[0], self.head_dim) == ops.CACHE_FP8
-        pools = [*self.k, *self.v]
-        forms = [(self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)] * len(pools)
-        num_pages = self.ref_count.shape[0]
-        for p in {p.data_ptr(): p for p in self.companions}.values():
+    def _moved_companions(self):
+        """The companions, each once (layers may share an index pool), and the bytes of a position's row and of its
+        scale in them."""
+        pools = list({p.data_ptr(): p for p in self.companions}.values())
+        num_pages, device, forms = self.ref_count.shape[0], self.k.device, []
+        for p in pools:
             row = p.shape[-1] // ops.PAGE - 4
             if (p.dim() not in (2, 3) or row not in (64, 128) or p.shape[-1] != ops.PAGE * (row + 4) or p.shape[0] != num_pages
-                    or p.dtype != torch.uint8 or p.device != self.k.device or not p.is_contiguous()):
+                    or p.dtype != torch.uint8 or p.device != device or not p.is_contiguous()):
                 raise ValueError("drafts need companions that are index-K pools on the cache's device: contiguous uint8 "
                                  f"[{num_pages}, 8448 or 4352]")
-            pools.append(p)
             forms.append((row, 4))
         return pools, forms
+
+    def _moved_pools(self):
+        """The pools that a commit moves entries in, and their forms."""
+        fp8 = ops.cache_format(self.k[0], self.head_dim) == ops.CACHE_FP8
+        companions, forms = self._moved_companions()
+        own = [*self.k, *self.v]
+        return own + companions, [(self.head_dim, 4) if fp8 else (2 * self.head_dim, 0)] * len(own) + forms
 
     def _is_open(self, draft):
         if self._open is not draft:
@@ -212,7 +215,7 @@ class PagedCache:
         most so many (None: requests * max_nodes).  A count or a length that does not fit counts as no tokens, a token
         for which the pages run out is kept nowhere and not accepted; both are in ``dev_err``."""
         self._closed()
-        self._moved_pools()
+        self._moved_companions()
         requests, max_nodes = token.shape
         if not 1 <= max_nodes <= drafts.MAX_NODES:
             raise ValueError(f"a tree has 1 to {drafts.MAX_NODES} nodes at most")
@@ -242,7 +245,7 @@ class PagedCache:
             out = ops.empty_on(stream, q.shape, q.dtype, q.device)
             with torch.cuda.stream(stream):
                 out.zero_()
-        workspace = self._work("draft", heads, stream, q.device, lambda: drafts.attn_draft_workspace_bytes(
+        workspace = self._work("draft", q, stream, lambda: drafts.attn_draft_workspace_bytes(
             draft.max_nodes, heads, self.k.shape[2], d))
         drafts.ci_attn_draft(q, self.k[layer], self.v[layer], self.page_table, draft.req_start, self.length, self._limit(),
                              draft.max_nodes, d ** -0.5 if scale is None else scale, out, mask=draft.mask,
