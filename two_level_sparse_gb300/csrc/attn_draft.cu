@@ -22,10 +22,13 @@ Layout layout_of(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
 //   m = max m_i;  l = sum l_i 2^(m_i - m);  out = sum o_i 2^(m_i - m) / l.
 // CTA (x, y) takes the unit that begins in CTA x and goes on, and every
 // gridDim.y-th run of its (row, four dims); neighbouring lanes have neighbouring
-// rows.  Many parts are dealt to four warps, whose sums are added in order.  Bound
-// by latency (the parts sit in L2): a pass over fewer (row, four dims) costs more
-// than a few parts one after another.  4 requests of 16 nodes, 6 parts: four warps
-// 34 us the whole call, one 30; one request of 256k, 38 parts: 16 warps 235, four 220.
+// rows.  More than 32 parts are dealt to four warps, whose sums are added in order.
+// Bound by latency (the parts sit in L2): a pass over fewer (row, four dims) costs
+// more than a few parts one after another.  Whole calls with one warp and with four:
+// 4 requests of 16 nodes, 6 parts, 27 and 30 us; one request of 64k of 128 rows, 10,
+// 25, 38 and 152 parts, 102 / 104, 62 / 61, 57 / 54 and 71 / 65 us; of 480 rows 219 /
+// 226, 106 / 109, 81 / 82 and 86 / 82.  (Of 32 rows four are as fast with 10, 96 / 95,
+// and faster from 15 on, 69 / 67; 54 / 26 with 152.)
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Args k) {
   __shared__ float sums[kJoinWarps][32][7];

@@ -26,27 +26,40 @@
 // The reference m of a row is the largest logit of its first tile, raised where
 // a later one passes it by 8 (in base 2): probabilities are at most 2^8, and O
 // is rescaled only then.  P is rounded to bf16, an error of its size of 2^-9 for
-// the positions that carry a row, and divided by the sum of the unrounded ones.
+// the positions that carry a row, and divided by the sum of the unrounded ones (by
+// that of the rounded ones, in bf16: error against 64 bits, two norms, 0.00198 for
+// 0.00205, of which 0.00166 is the result's own rounding, and 1 to 4% more time; FP8:
+// a probability is rounded with its value's scale in it, and the sum is without).
 //
 // What bounds it.  Few rows in bf16: the HBM (32 requests of 16k, 4 nodes, 64
-// heads over 8 of 128: 2.15 GB in 333 us, 6.5 TB/s of a copy's 6.8).  Many rows: a
-// step's chain of softmax and products (64 trees of 64 nodes over 4k-16k: 1.10 ms,
-// 1250 TFLOP/s; a chunk of 2048 behind 16k: 0.85 ms, 1380 TFLOP/s).  A pair of
-// steps takes 3700 cycles, of which the tensor cores work half: a softmax of 128
-// columns is 2000 (500 the largest, 1130 the exponentials, the rest waits and
-// stores), P V and the next Q K^T behind it 1500.  Neither shared memory (38%) nor
-// exponentials (26%) nor issue slots (35%) are full.  FP8: V's widening and the
-// issuing warp's waits, 1950 cycles a tile where the HBM's rate is 1460 (64 chains
-// of 4 over 16k-64k: 1.16-1.18 ms, 4.8 TB/s).  Short calls: the start, 8000 cycles
-// until the first tile arrives, cold code, and the join (4 requests of 16 nodes
-// over 1k-4k: 27 us; one row over 16 positions: 10 us).
+// heads over 8 of 128: 2.15 GB in 330 to 335 us, 6.4 to 6.5 TB/s of a
+// copy's 6.7).  Many rows: a
+// step's chain of softmax and products (64 trees of 64 nodes over 4k-16k: 1.10 ms in
+// short runs, 1.21 where the clock settles under load, 1130 TFLOP/s; a chunk of 2048
+// behind 16k: 0.85 and 0.90 ms, 1300 TFLOP/s).  A pair of steps takes 3700 cycles, of
+// which the tensor cores work half: a softmax of 128 columns is 2000 (500 the largest,
+// 1130 the exponentials, the rest waits and stores), P V and the next Q K^T behind it
+// 1500.  Neither shared memory (40%) nor exponentials (27%) nor issue slots (39%) are
+// full.  FP8: V's widening and the issuing warp's waits, 1950 cycles a tile where the HBM's rate is 1460 (64 chains
+// of 4 over 16k-64k: 1.16 to 1.23 ms, 4.5 TB/s); with many rows the scales, 96 reads
+// of 16 bytes from shared memory per row and tile that bf16 has not (a chunk of 1024
+// behind 8192: 1.6 times bf16's instructions, shared memory at 71%, where bf16 has
+// 40, and 1.35 times its time).  Short calls: the start, 8000 cycles until the first
+// tile arrives, cold code, and the join (4 requests of 16 nodes over 1k-4k: 27 us; one
+// row over 16 positions: 10 us).  Chains of many rows: the search for the CTA's range
+// walks a request's blocks one after another, 28 us of 0.86 ms with the 64 blocks of
+// 2048 tokens of 8 heads, 0.82 of 2.1 ms with the 2048 of 8192 tokens of 64 heads.
+//
+// Where FP8's loops come to lie counts, too: 64 to 256 instructions that never run,
+// put in front of V's widening, took up to 7% more time, 512 none.
 //
 // Masks.  Only tiles that reach past the positions that all rows of a block see
 // have any: there a row's 128 bits come from its mask words, shifted to the
 // tile, and a warp leaves out 32 positions that none of its rows sees and takes 32
-// that all see as any other (64 trees of 64 nodes: 5% less time).  Values that some rows do not see must not meet their zeros as NaN or
-// infinities: in those tiles everything that is not finite becomes 0 in shared
-// memory before the product, and at the end the rows that do see it add it.
+// that all see as any other (64 trees of 64 nodes: 5% less time).  Values that some
+// rows do not see must not meet their zeros as NaN or infinities: in those tiles
+// everything that is not finite becomes 0 in shared memory before the product, and at
+// the end the rows that do see it add it.
 //
 // FP8 pages.  Keys are multiplied as they are: the query, each row scaled by a
 // power of two, is the sum of an e4m3 and an e5m2 number, exactly where an element is
