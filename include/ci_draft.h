@@ -93,8 +93,9 @@ CI_API int ci_draft_plan(const int32_t* length, const int32_t* count, const int3
  * magnitude of its row and head, or 2^-119 if that is larger.  The softmax
  * statistics are fp32; the probabilities are rounded to bf16 for the product with
  * the values (FP8: with the value's scale in them) and divided by the sum of the
- * unrounded ones; out is rounded once.  Results do not depend on the order in which
- * blocks run.
+ * unrounded ones; out is rounded once.  FP8: a position's part of out is kept in
+ * steps of 2^-81, what lies below is lost.  Results do not depend on the order in
+ * which blocks run.
  * Any finite logits; values |v| <= 2^80; FP8: scales finite, |scale| <= 2^60,
  * and a value's NaN code (0x7F, 0xFF) reads as +-480 * scale.
  *

@@ -842,3 +842,12 @@ def test_move_reports_pages(draft, req, most, bad):
     draft.ci_slots_move([got], 16, 4, i32(table), i32(length), i32(path), i32(count), dev_err=bits)
     np.testing.assert_array_equal(got.cpu().numpy(), D.move(pool.numpy(), 16, 4, table, length, path, count))
     assert int(bits) == err
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+def test_attention_fp8_queries_with_a_large_dim(draft, kind, d):
+    """One dim of every query 64 times as large, over keys like any: logits as close as without it."""
+    p = Drafted([300, 0, 1, 700], [20, 5, 1, 9], 16, 2, d, FP8, kind, seed=d, gain=0.3)
+    p.q[..., 37] *= 64
+    p.check(*p.run(draft))
