@@ -851,3 +851,29 @@ def test_attention_fp8_queries_with_a_large_dim(draft, kind, d):
     p = Drafted([300, 0, 1, 700], [20, 5, 1, 9], 16, 2, d, FP8, kind, seed=d, gain=0.3)
     p.q[..., 37] *= 64
     p.check(*p.run(draft))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("far", [-110, -118, -119, -121, -126, -130])
+def test_attention_fp8_tiny_queries(draft, far, d):
+    """Queries of about 2^far under a scale that makes ordinary logits of them: off by what is left out of elements, at
+    most 2^-21 of the row's largest or of 2^-119."""
+    p = Drafted([200, 3], [6, 2], 4, 1, d, FP8, "chain", seed=-far)
+    p.q = (p.q.double() * 2.0 ** far).to(torch.bfloat16)
+    p.scale = 2.0 ** (-far - 4) if far > -123 else 2.0 ** 119
+    out, lse = p.run(draft)
+    assert int(p.err) == 0
+    kv, table = C.page_values(p.k.numpy(), d), p.table.numpy()
+    for r in range(2):
+        for i in range(p.nodes[r]):
+            t, at = p.starts[r] + i, np.arange(p.lens[r] + i + 1)
+            k = kv[table[r, at // 64], 0, at % 64]
+            q = p.q[t].double().numpy()
+            x = p.scale * q @ k.T
+            size = p.scale * np.abs(q) @ np.abs(k).T
+            top = np.maximum(np.abs(q).max(-1, keepdims=True), 2.0 ** -119)
+            left = np.where(np.abs(q) >= 2.0 ** -13 * top, 0, 2.0 ** -21 * top)
+            dx = ((d + 8) * 2.0 ** -23 * size + p.scale * left @ np.abs(k).T).max(-1)
+            z = np.log(np.exp(x - x.max(-1, keepdims=True)).sum(-1)) + x.max(-1)
+            ztol = dx + (len(at) + 64) * 2.0 ** -23 + 2.0 ** -21 * (np.abs(z) + 1)
+            assert (np.abs(lse[t].double().cpu().numpy() - z) <= ztol).all(), (r, i)
